@@ -31,7 +31,8 @@
  *    are fp32 [B, H, S].
  *  - LSE is the natural log of sum_j exp(scale * q . k_j) over visible keys
  *    (scale included); -inf for a row with no visible key.
- *  - causal: key j is visible to query i iff j <= i (requires Sq == Sk).
+ *  - causal: key j is visible to query i iff j <= i (requires Sq == Sk). The
+ *    attn_window_* calls have a mask, and shared K/V heads, of their own.
  *  - All tensor pointers are DEVICE pointers owned by the caller; the library
  *    keeps no pointer after a call returns and allocates nothing.
  *  - stream is a cudaStream_t (NULL = legacy default stream). Every compute
@@ -39,8 +40,8 @@
  *    reaches that point.
  *  - Device pointers of the attention calls must be 16-byte aligned and
  *    strides multiples of 8 elements (16 bytes), as required by the
- *    tensor-memory-access (TMA) unit; lcb_rope and lcb_cross_entropy state
- *    their own, weaker rules.
+ *    tensor-memory-access (TMA) unit; lcb_rope, lcb_rope_axes and
+ *    lcb_cross_entropy state their own, weaker rules.
  *  - Return value: LCB_OK or a negative LCB_ERR_* code; nothing is launched on
  *    an argument error. With the environment variable LCB_CHECKED=1 every call
  *    synchronises its stream and reports LCB_ERR_TIMEOUT if a kernel's
@@ -365,6 +366,91 @@ int lcb_cross_entropy(void* logits, const long long* labels, float* loss, float*
  */
 int lcb_rope(const void* x, void* y, int B, int S, int H, int D, double theta, long long pos0, int inverse,
              long long row_stride, long long batch_stride, void* stream);
+
+/*
+ * lcb_rope_axes — rotary position embedding with several position axes (time,
+ * height, width of image and video tokens), beside lcb_rope: y = RoPE(x) on
+ * bf16 [B, S, H, D=128] views (x and y share row/batch strides in elements;
+ * 4-byte aligned; x == y allowed). Pair k couples features k and k + 64 and
+ * turns by pos[a][b][s] * theta^(-2k/128) at token (b, s), a = pair_axis[k]
+ * (HOST array of 64 axis numbers in [0, n_axes)). pos: DEVICE int32
+ * (pos_bytes 4) or int64 (8), any sign, element (a, b, s) at
+ * a*pos_axis_stride + b*pos_batch_stride + s*pos_row_stride (batch stride 0:
+ * one set of positions for every sequence). inverse = 1 turns the other way
+ * (the transpose: it maps dQ, dK of rotated tensors back). Angles are reduced
+ * in 64-bit integer arithmetic (|pos| up to 2^40, as far as fp64 frequencies
+ * go), rotated in fp32, rounded to bf16 once.
+ */
+int lcb_rope_axes(const void* x, void* y, int B, int S, int H, int D, double theta, const void* pos, int pos_bytes,
+                  int n_axes, const int* pair_axis, long long pos_axis_stride, long long pos_batch_stride,
+                  long long pos_row_stride, int inverse, long long row_stride, long long batch_stride, void* stream);
+
+/*
+ * Attention with a sliding window and sinks. Query row i stands at position
+ * p = q_pos0 + i; key j (0 <= j < Sk) is visible to it iff
+ *     j <= p  and  (p - j < window  or  j < sinks):
+ * the last `window` keys up to and including its own position, and the first
+ * `sinks` keys of the sequence. A row that sees nothing (p < 0, or every key
+ * out of its window) has O = 0, LSE = -inf and no part in any gradient.
+ * window >= Sk + Sq is causal attention. Heads: q has H, k and v have Hkv with
+ * Hkv | H; query head h reads K/V head h / (H / Hkv).
+ * Sizes: Sq, Sk, |q_pos0| <= 2^28; window >= 1, sinks >= 0; D = 128.
+ * Pointers 16-byte aligned, strides in elements, multiples of 8; k and v share
+ * strides, o and dO share strides, dk and dv share strides; outputs must not
+ * overlap themselves or other arguments.
+ * Infinities and NaN: a score hidden by the mask is dropped whatever its value.
+ * In v (and in q, k, dO of the backward) a non-finite row spreads to the rows
+ * of the same 128 x 128 tile (16 keys in attn_window_decode) that do not see
+ * it, since 0 * NaN is NaN in the products. Keys at or past Sk or lens[b] are
+ * never read.
+ *
+ * attn_window_fwd — O (bf16 [B, Sq, H, D]) and LSE (fp32, natural log, scale
+ * included). Deterministic.
+ */
+int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv, int Sq,
+                    int Sk, int D, int window, int sinks, long long q_pos0, float scale, long long q_row_stride,
+                    long long q_batch_stride, long long kv_row_stride, long long kv_batch_stride,
+                    long long o_row_stride, long long o_batch_stride, long long lse_head_stride,
+                    long long lse_batch_stride, void* stream);
+
+/* Bytes of device workspace attn_window_bwd needs for these sizes: Delta, the
+ * tiled fp32 dQ accumulator, and fp32 dK/dV partials of key tiles whose queries
+ * are dealt to several CTAs; 0 for sizes that attn_window_bwd refuses, or with
+ * an empty side. */
+size_t attn_window_bwd_workspace_bytes(int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                                       long long q_pos0);
+
+/*
+ * attn_window_bwd — gradients of attn_window_fwd by recomputation, from its o
+ * and lse and the upstream dO: dq [B, Sq, H, D], dk, dv [B, Sk, Hkv, D], bf16,
+ * overwritten (keys that no query sees: 0). dk and dv sum over the query heads
+ * that share a K/V head, and are deterministic; dq's fp32 summation order is
+ * not fixed, as attn_bwd's. workspace: device memory of at least
+ * attn_window_bwd_workspace_bytes(), 16-byte aligned, contents ignored; calls
+ * that may overlap on the GPU need workspaces of their own.
+ */
+int attn_window_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                    void* dq, void* dk, void* dv, int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                    long long q_pos0, float scale, long long q_row_stride, long long q_batch_stride,
+                    long long kv_row_stride, long long kv_batch_stride, long long o_row_stride,
+                    long long o_batch_stride, long long lse_head_stride, long long lse_batch_stride,
+                    long long dq_row_stride, long long dq_batch_stride, long long dkv_row_stride,
+                    long long dkv_batch_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * attn_window_decode — the serving form: the T newest tokens of each sequence
+ * against its K/V cache. q, o: [B, T, H, D]; k, v: caches [B, Smax, Hkv, D] of
+ * which sequence b has filled lens[b] rows, the T newest tokens' among them
+ * (lens: DEVICE int32 [B], values clamped to [0, Smax], so a captured graph
+ * replays with the lengths of the moment); token t stands at position
+ * lens[b] - T + t. Each visible cache row is read once for all query rows of
+ * its head up to 16 of them (T * H / Hkv). Deterministic, no workspace.
+ */
+int attn_window_decode(const void* q, const void* k, const void* v, const int* lens, void* o, float* lse, int B, int H,
+                       int Hkv, int T, int Smax, int D, int window, int sinks, float scale, long long q_row_stride,
+                       long long q_batch_stride, long long kv_row_stride, long long kv_batch_stride,
+                       long long o_row_stride, long long o_batch_stride, long long lse_head_stride,
+                       long long lse_batch_stride, void* stream);
 
 /*
  * lcb_permute_rows — row gather/scatter on the device, used to move a

@@ -7,6 +7,9 @@ Public calls (all run in this library's CUDA kernels):
   dq_tiles_zeros / dq_tiles_zero_ / dq_untile (the one-pass backward's tiled dQ accumulator),
   attn_lse_merge, zigzag_schedule, ring_schedule, permute_rows, cast_f32_bf16,
   rope (rotary position embedding with a raised base, and its inverse),
+  attn_window_fwd / attn_window_bwd (sliding window with sinks, shared K/V heads),
+  attn_window_decode (its form for the newest tokens against a K/V cache),
+  rope_axes (rotary positions with several axes, and the inverse),
   cross_entropy (the loss head with an in-place backward),
   zigzag_attention_fwd / zigzag_attention_bwd (the one-device zigzag ring),
   ulysses_all_to_all, ulysses_attention_fwd / ulysses_attention_bwd (Ulysses
@@ -32,6 +35,10 @@ from ._lib import (  # noqa: F401
     attn_fwd_ex,
     attn_fwd_group,
     attn_lse_merge,
+    attn_window_bwd,
+    attn_window_bwd_workspace_bytes,
+    attn_window_decode,
+    attn_window_fwd,
     cast_f32_bf16,
     cross_entropy,
     dq_tiles_zero_,
@@ -41,6 +48,8 @@ from ._lib import (  # noqa: F401
     permute_rows,
     ring_schedule,
     rope,
+    rope_axes,
+    rope_pair_axes,
     selftest_bounded_wait,
     set_wait_limit_ns,
     take_device_status,

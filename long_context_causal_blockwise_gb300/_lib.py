@@ -81,6 +81,15 @@ _SIGNATURES = {
     "ring_schedule": ([_I, _I, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(LcbTask)], _I),
     "lcb_cross_entropy": ([_P, _P, _P, _P, _P, _I, _I, _LL, _I, _I, _P], _I),
     "lcb_rope": ([_P, _P, _I, _I, _I, _I, ctypes.c_double, _LL, _I, _LL, _LL, _P], _I),
+    "lcb_rope_axes": ([_P, _P, _I, _I, _I, _I, ctypes.c_double, _P, _I, _I, ctypes.POINTER(ctypes.c_int), _LL, _LL, _LL,
+                       _I, _LL, _LL, _P], _I),
+    "attn_window_fwd": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _LL, _F, _LL, _LL, _LL, _LL, _LL, _LL, _LL,
+                         _LL, _P], _I),
+    "attn_window_bwd_workspace_bytes": ([_I, _I, _I, _I, _I, _I, _I, _I, _LL], _SZ),
+    "attn_window_bwd": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _LL, _F, _LL, _LL, _LL, _LL,
+                         _LL, _LL, _LL, _LL, _LL, _LL, _LL, _LL, _P, _SZ, _P], _I),
+    "attn_window_decode": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _LL, _LL, _LL, _LL, _LL, _LL, _LL,
+                            _LL, _P], _I),
     "lcb_permute_rows": ([_P, _P, _P, _I, _LL, _P], _I),
     "lcb_scatter_rows": ([_P, _P, _P, _I, _LL, _P], _I),
     "lcb_cast_f32_bf16": ([_P, _P, _LL, _P], _I),
@@ -483,6 +492,178 @@ def rope(x, theta, pos0=0, inverse=False, out=None):
         raise ValueError("x and out must share strides")
     _check("lcb_rope", load().lcb_rope(_ptr(x), _ptr(out), B, S, H, D, float(theta), int(pos0), int(inverse), r, b,
                                        _stream(x)))
+    return out
+
+
+# ------------------------------------------------------------------ window and sinks
+
+def _on_device(name, dev, *tensors):
+    """Every tensor on `dev`, which must be the current CUDA device (kernels launch there)."""
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a CUDA device")
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: tensors on {dev}, which is not the current device")
+
+
+def _window_shapes(name, q, k, v):
+    """(B, Sq, H, D, Sk, Hkv, q strides, k/v strides) of a windowed-attention call."""
+    qr, qb = _bshd(q, "q")
+    kr, kb = _bshd(k, "k")
+    B, Sq, H, D = q.shape
+    Bk, Sk, Hkv, Dk = k.shape
+    if _bshd(v, "v") != (kr, kb) and Sk:
+        raise ValueError("k and v must share strides")
+    if v.shape != k.shape or Bk != B or Dk != D or Hkv < 1 or H % Hkv:
+        raise ValueError(f"{name}: k and v must be [B, Sk, Hkv, D] with Hkv dividing q's H, "
+                         f"got {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    return B, Sq, H, D, Sk, Hkv, qr, qb, kr, kb
+
+
+def _window_out(q, o, lse):
+    """Given or fresh (o, lse) of q's shape, with their strides."""
+    B, S, H, D = q.shape
+    o = torch.empty((B, S, H, D), dtype=q.dtype, device=q.device) if o is None else o
+    lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse is None else lse
+    if o.shape != q.shape or lse.shape != (B, H, S):
+        raise ValueError("o must have q's shape and lse [B, H, S]")
+    return o, lse, *_bshd(o, "o"), *_bhs_any(lse, "lse")
+
+
+def _bhs_any(t, name):
+    """Strides of an fp32 [B, H, S] view; a length of one says nothing of its last stride."""
+    if t.dim() == 3 and t.shape[2] <= 1 and t.is_cuda and t.dtype == torch.float32:
+        return t.stride(1), t.stride(0)
+    return _bhs(t, name)
+
+
+def attn_window_fwd(q, k, v, window, sinks=0, q_pos0=None, scale=None, o=None, lse=None):
+    """Attention with a sliding window and sinks; returns (o bf16, lse fp32 [B, H, Sq]).
+
+    q [B, Sq, H, 128], k and v [B, Sk, Hkv, 128] bf16 views (Hkv divides H:
+    query head h reads K/V head h // (H // Hkv)). The query of row i, at
+    position p = q_pos0 + i, sees the keys j <= p with p - j < window and, among
+    those, the first `sinks` whatever their distance. q_pos0=None puts the
+    queries at the end of the keys (Sk - Sq: self-attention, or the next chunk
+    of a prompt against its cache). A row that sees nothing gives 0 and -inf."""
+    B, Sq, H, D, Sk, Hkv, qr, qb, kr, kb = _window_shapes("attn_window_fwd", q, k, v)
+    o, lse, orr, ob, lh, lb = _window_out(q, o, lse)
+    _on_device("attn_window_fwd", q.device, k, v, o, lse)
+    _check("attn_window_fwd", load().attn_window_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Sk, D, _window(window),
+        _window(sinks), Sk - Sq if q_pos0 is None else int(q_pos0), D ** -0.5 if scale is None else float(scale), qr,
+        qb, kr, kb, orr, ob, lh, lb, _stream(q)))
+    return o, lse
+
+
+def _window(n):
+    """A window or sink count for the C ABI: more than 2^30 keys is all of them."""
+    return max(-1, min(int(n), 1 << 30))
+
+
+def attn_window_bwd_workspace_bytes(B, H, Hkv, Sq, Sk, window, sinks=0, q_pos0=None, D=128):
+    return int(load().attn_window_bwd_workspace_bytes(B, H, Hkv, Sq, Sk, D, _window(window), _window(sinks),
+                                                      Sk - Sq if q_pos0 is None else int(q_pos0)))
+
+
+def attn_window_bwd(q, k, v, o, lse, do, window, sinks=0, q_pos0=None, scale=None, dq=None, dk=None, dv=None,
+                    workspace=None):
+    """Gradients of attn_window_fwd (its o and lse, upstream do); returns (dq, dk, dv) bf16.
+
+    o and do share strides. dk and dv are [B, Sk, Hkv, 128], summed over the
+    query heads of each K/V head. workspace: uint8 of
+    attn_window_bwd_workspace_bytes (None: allocated here)."""
+    B, Sq, H, D, Sk, Hkv, qr, qb, kr, kb = _window_shapes("attn_window_bwd", q, k, v)
+    if o.shape != q.shape or do.shape != q.shape or lse.shape != (B, H, Sq):
+        raise ValueError("o and do must have q's shape and lse [B, H, Sq]")
+    orr, ob = _bshd(o, "o")
+    if _bshd(do, "do") != (orr, ob) and Sq:
+        raise ValueError("o and do must share strides")
+    lh, lb = _bhs_any(lse, "lse")
+    dev = q.device
+    dq = torch.empty((B, Sq, H, D), dtype=q.dtype, device=dev) if dq is None else dq
+    dk = torch.empty((B, Sk, Hkv, D), dtype=q.dtype, device=dev) if dk is None else dk
+    dv = torch.empty((B, Sk, Hkv, D), dtype=q.dtype, device=dev) if dv is None else dv
+    if dq.shape != q.shape or dk.shape != k.shape or dv.shape != k.shape:
+        raise ValueError("dq must have q's shape, dk and dv k's")
+    dqr, dqb = _bshd(dq, "dq")
+    dkr, dkb = _bshd(dk, "dk")
+    if _bshd(dv, "dv") != (dkr, dkb) and Sk:
+        raise ValueError("dk and dv must share strides")
+    pos0 = Sk - Sq if q_pos0 is None else int(q_pos0)
+    if workspace is None:
+        n = attn_window_bwd_workspace_bytes(B, H, Hkv, Sq, Sk, window, sinks, pos0, D)
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on_device("attn_window_bwd", dev, k, v, o, lse, do, dq, dk, dv, workspace)
+    _check("attn_window_bwd", load().attn_window_bwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Sq, Sk, D, _window(window), _window(sinks), pos0,
+        D ** -0.5 if scale is None else float(scale), qr, qb, kr, kb, orr, ob, lh, lb, dqr, dqb, dkr, dkb,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(q)))
+    return dq, dk, dv
+
+
+def attn_window_decode(q, k_cache, v_cache, lens, window, sinks=0, scale=None, o=None, lse=None):
+    """The T newest tokens of each sequence against its K/V cache; returns (o, lse fp32 [B, H, T]).
+
+    q [B, T, H, 128]; caches [B, Smax, Hkv, 128], of which sequence b has filled
+    lens[b] rows (CUDA int32 [B]), the newest tokens' own among them: token t
+    stands at position lens[b] - T + t. Window, sinks and heads as in
+    attn_window_fwd. Cache rows at or past lens[b] are not read."""
+    B, T, H, D, Smax, Hkv, qr, qb, kr, kb = _window_shapes("attn_window_decode", q, k_cache, v_cache)
+    if lens.dtype != torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous int32 [B] tensor")
+    o, lse, orr, ob, lh, lb = _window_out(q, o, lse)
+    _on_device("attn_window_decode", q.device, k_cache, v_cache, lens, o, lse)
+    _check("attn_window_decode", load().attn_window_decode(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv,
+        T, Smax, D, _window(window), _window(sinks), D ** -0.5 if scale is None else float(scale), qr, qb, kr, kb, orr,
+        ob, lh, lb, _stream(q)))
+    return o, lse
+
+
+def rope_pair_axes(sections, interleaved=False):
+    """The axis of each of the 64 feature pairs: sections[a] pairs for axis a,
+    one axis after another, or (interleaved) dealt to the axes in turn while
+    they have pairs left."""
+    sections = [int(n) for n in sections]
+    if not sections or min(sections) < 0 or sum(sections) != 64:
+        raise ValueError("sections must be non-negative counts of feature pairs that add up to 64")
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    return [a for i in range(max(sections)) for a, n in enumerate(sections) if i < n]
+
+
+_PAIR_AXES = {}  # (sections, interleaved) -> the C array of rope_pair_axes
+
+
+def rope_axes(x, theta, pos, sections, inverse=False, interleaved=False, out=None):
+    """RoPE with several position axes of a bf16 [B, S, H, 128] view; out=None rotates in place.
+
+    pos: int32 or int64, [axes, S] (the same positions for every sequence) or
+    [axes, B, S]. sections: how many of the 64 feature pairs each axis has
+    (rope_pair_axes says which); pair k turns by its axis' position times
+    theta^(-2k/128). inverse=True applies the transpose."""
+    key = (tuple(sections), bool(interleaved))
+    arr = _PAIR_AXES.get(key)
+    if arr is None:
+        arr = _PAIR_AXES[key] = (ctypes.c_int * 64)(*rope_pair_axes(*key))
+    r, b = _bshd(x, "x")
+    B, S, H, D = x.shape
+    out = x if out is None else out
+    if out.shape != x.shape or _bshd(out, "out") != (r, b):
+        raise ValueError("x and out must share shape and strides")
+    if pos.dtype not in (torch.int32, torch.int64) or tuple(pos.shape) not in ((len(key[0]), S), (len(key[0]), B, S)):
+        raise ValueError("pos must be int32 or int64 [axes, S] or [axes, B, S]")
+    pb = pos.stride(1) if pos.dim() == 3 else 0
+    _on_device("rope_axes", x.device, pos, out)
+    _check("lcb_rope_axes", load().lcb_rope_axes(
+        x.data_ptr(), out.data_ptr(), B, S, H, D, float(theta), pos.data_ptr(), pos.element_size(), len(key[0]), arr,
+        pos.stride(0), pb, pos.stride(-1), int(inverse), r, b, _stream(x)))
     return out
 
 

@@ -97,6 +97,13 @@ int finish(int rc, cudaStream_t stream) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether no two rows of `row` elements of a [B, rows] view share an element
+// (an output written by many CTAs), one batch after another or interleaved.
+bool rows_apart(int B, int rows, long long row, long long rs, long long bs) {
+  if (rs < 0 || bs < 0 || rs >= (1LL << 38) || bs >= (1LL << 38)) return false;
+  if (rows > 1 && rs < row) return false;
+  return B == 1 || bs >= (rows - 1) * rs + row || (bs >= row && (rows == 1 || rs >= (B - 1) * bs + row));
+}
 bool stride_ok(long long s) { return s >= 0 && (s % 8) == 0 && s < (1LL << 38); }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -755,6 +762,250 @@ int lcb_rope(const void* x, void* y, int B, int S, int H, int D, double theta, l
   for (int k = 0; k < D / 2; ++k) fr.f[k] = std::pow(theta, -2.0 * k / D);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return finish(launch_rope(x, y, B, S, H, row_stride, batch_stride, pos0, inverse, fr, st), st);
+}
+
+int lcb_rope_axes(const void* x, void* y, int B, int S, int H, int D, double theta, const void* pos, int pos_bytes,
+                  int n_axes, const int* pair_axis, long long pos_axis_stride, long long pos_batch_stride,
+                  long long pos_row_stride, int inverse, long long row_stride, long long batch_stride, void* stream) {
+  if (B < 1 || H < 1 || S < 0) return LCB_ERR_ARG;
+  if (D != kHeadDim || (pos_bytes != 4 && pos_bytes != 8)) return LCB_ERR_UNSUPPORTED;
+  if (!(theta > 0.0) || !std::isfinite(theta) || (inverse != 0 && inverse != 1)) return LCB_ERR_ARG;
+  if (n_axes < 1 || n_axes > 64 || !pair_axis) return LCB_ERR_ARG;
+  RopeAxes ax;
+  for (int k = 0; k < D / 2; ++k) {
+    if (pair_axis[k] < 0 || pair_axis[k] >= n_axes) return LCB_ERR_ARG;
+    ax.axis[k] = static_cast<unsigned char>(pair_axis[k]);
+    // turns per unit of position, modulo one: a whole turn changes nothing
+    const double turns = std::pow(theta, -2.0 * k / D) / 6.283185307179586476925286766559;
+    ax.turn[k] = static_cast<unsigned long long>(std::ldexp(turns - std::floor(turns), 64));
+  }
+  if (S == 0) return LCB_OK;
+  if (!x || !y || (reinterpret_cast<uintptr_t>(x) & 3u) || (reinterpret_cast<uintptr_t>(y) & 3u)) return LCB_ERR_ARG;
+  if (!pos || (reinterpret_cast<uintptr_t>(pos) & static_cast<uintptr_t>(pos_bytes - 1))) return LCB_ERR_ARG;
+  if (pos_axis_stride < 0 || pos_batch_stride < 0 || pos_row_stride < 0) return LCB_ERR_ARG;
+  if (row_stride % 2 || batch_stride % 2 || !rows_apart(B, S, static_cast<long long>(H) * D, row_stride, batch_stride))
+    return LCB_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(launch_rope_axes(x, y, B, S, H, row_stride, batch_stride, pos, pos_bytes, pos_axis_stride,
+                                 pos_batch_stride, pos_row_stride, inverse, ax, st),
+                st);
+}
+
+// Sizes, window and scale shared by the windowed-attention calls; fills `w`.
+static int prep_window(WindowShape* w, int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                       long long q_pos0, float scale) {
+  if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Sq < 0 || Sk < 0) return LCB_ERR_ARG;
+  if (D != kHeadDim) return LCB_ERR_UNSUPPORTED;
+  if (window < 1 || sinks < 0 || !(scale > 0.f) || !std::isfinite(scale)) return LCB_ERR_ARG;
+  if (Sq > kWindowMaxRows || Sk > kWindowMaxRows || q_pos0 > kWindowMaxRows || q_pos0 < -kWindowMaxRows)
+    return LCB_ERR_ARG;
+  w->Sq = Sq;
+  w->Sk = Sk;
+  w->pos0 = static_cast<int>(q_pos0);
+  w->window = std::min(window, kWindowMaxWindow);
+  w->sinks = std::min(sinks, Sk);
+  return LCB_OK;
+}
+
+// A bf16 input [B, rows, heads, 128] for TMA or 16-byte loads.
+static bool window_input(const void* p, long long rs, long long bs, int heads) {
+  return p && aligned16(p) && stride_ok(rs) && stride_ok(bs) && rs >= static_cast<long long>(heads) * kHeadDim;
+}
+// A bf16 output: its rows also lie apart from one another.
+static bool window_output(const void* p, long long rs, long long bs, int B, int rows, int heads) {
+  return p && aligned16(p) && stride_ok(rs) && stride_ok(bs) &&
+         rows_apart(B, rows, static_cast<long long>(heads) * kHeadDim, rs, bs);
+}
+
+static WindowSplit split_args(const void* q, const void* k, const void* v, const int* lens, void* o, float* lse, int B,
+                              int H, int Hkv, int T, const WindowShape& w, float scale, long long q_row_stride,
+                              long long q_batch_stride, long long kv_row_stride, long long kv_batch_stride,
+                              long long o_row_stride, long long o_batch_stride, long long lse_head_stride,
+                              long long lse_batch_stride) {
+  WindowSplit a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.lens = lens;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.q_rs = q_row_stride;
+  a.q_bs = q_batch_stride;
+  a.kv_rs = kv_row_stride;
+  a.kv_bs = kv_batch_stride;
+  a.o_rs = o_row_stride;
+  a.o_bs = o_batch_stride;
+  a.l_hs = lse_head_stride;
+  a.l_bs = lse_batch_stride;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.T = T;
+  a.Sk = w.Sk;
+  a.pos0 = w.pos0;
+  a.window = w.window;
+  a.sinks = w.sinks;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.row_tiles = a.cluster = 1;
+  return a;
+}
+
+int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv, int Sq,
+                    int Sk, int D, int window, int sinks, long long q_pos0, float scale, long long q_row_stride,
+                    long long q_batch_stride, long long kv_row_stride, long long kv_batch_stride,
+                    long long o_row_stride, long long o_batch_stride, long long lse_head_stride,
+                    long long lse_batch_stride, void* stream) {
+  WindowShape w;
+  int rc = prep_window(&w, B, H, Hkv, Sq, Sk, D, window, sinks, q_pos0, scale);
+  if (rc != LCB_OK) return rc;
+  if (Sq == 0) return LCB_OK;
+  if (!window_output(o, o_row_stride, o_batch_stride, B, Sq, H) || !lse || lse_head_stride < 0 || lse_batch_stride < 0)
+    return LCB_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (Sk == 0)
+    return finish(launch_fill_empty(o, 0, o_row_stride, o_batch_stride, lse, lse_head_stride, lse_batch_stride, B, H,
+                                    Sq, st),
+                  st);
+  if (!window_input(q, q_row_stride, q_batch_stride, H) || !window_input(k, kv_row_stride, kv_batch_stride, Hkv) ||
+      !window_input(v, kv_row_stride, kv_batch_stride, Hkv))
+    return LCB_ERR_ARG;
+  // Query rows that fit one 16-row tile of the split kernel go there: a
+  // 128-row tile would be mostly padding, and one CTA a head would walk the
+  // whole window.
+  if (static_cast<long long>(Sq) * (H / Hkv) <= 16)
+    return finish(launch_window_split(split_args(q, k, v, nullptr, o, lse, B, H, Hkv, Sq, w, scale, q_row_stride,
+                                                 q_batch_stride, kv_row_stride, kv_batch_stride, o_row_stride,
+                                                 o_batch_stride, lse_head_stride, lse_batch_stride),
+                                      st),
+                  st);
+  WindowFwd a;
+  a.q = {q, q_row_stride, q_batch_stride};
+  a.k = {k, kv_row_stride, kv_batch_stride};
+  a.v = {v, kv_row_stride, kv_batch_stride};
+  a.o = o;
+  a.lse = lse;
+  a.o_row_stride = o_row_stride;
+  a.o_batch_stride = o_batch_stride;
+  a.lse_head_stride = lse_head_stride;
+  a.lse_batch_stride = lse_batch_stride;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.w = w;
+  a.scale = scale;
+  if ((rc = dev_status(&a.st)) != LCB_OK) return rc;
+  return finish(launch_window_fwd(a, st), st);
+}
+
+int attn_window_decode(const void* q, const void* k, const void* v, const int* lens, void* o, float* lse, int B, int H,
+                       int Hkv, int T, int Smax, int D, int window, int sinks, float scale, long long q_row_stride,
+                       long long q_batch_stride, long long kv_row_stride, long long kv_batch_stride,
+                       long long o_row_stride, long long o_batch_stride, long long lse_head_stride,
+                       long long lse_batch_stride, void* stream) {
+  WindowShape w;
+  int rc = prep_window(&w, B, H, Hkv, T, Smax, D, window, sinks, 0, scale);
+  if (rc != LCB_OK) return rc;
+  if (T == 0) return LCB_OK;
+  if (!window_output(o, o_row_stride, o_batch_stride, B, T, H) || !lse || lse_head_stride < 0 || lse_batch_stride < 0)
+    return LCB_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (Smax == 0)
+    return finish(launch_fill_empty(o, 0, o_row_stride, o_batch_stride, lse, lse_head_stride, lse_batch_stride, B, H,
+                                    T, st),
+                  st);
+  if (!lens || (reinterpret_cast<uintptr_t>(lens) & 3u)) return LCB_ERR_ARG;
+  if (!window_input(q, q_row_stride, q_batch_stride, H) || !window_input(k, kv_row_stride, kv_batch_stride, Hkv) ||
+      !window_input(v, kv_row_stride, kv_batch_stride, Hkv))
+    return LCB_ERR_ARG;
+  return finish(launch_window_split(split_args(q, k, v, lens, o, lse, B, H, Hkv, T, w, scale, q_row_stride,
+                                               q_batch_stride, kv_row_stride, kv_batch_stride, o_row_stride,
+                                               o_batch_stride, lse_head_stride, lse_batch_stride),
+                                    st),
+                st);
+}
+
+// Workspace of attn_window_bwd: Delta [B, H, Sq], the tiled dQ accumulator and
+// the runs' dK/dV partials, each at a 256-byte boundary.
+size_t attn_window_bwd_workspace_bytes(int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                                       long long q_pos0) {
+  WindowShape w;
+  if (prep_window(&w, B, H, Hkv, Sq, Sk, D, window, sinks, q_pos0, 1.f) != LCB_OK) return 0;
+  if (Sq == 0 || Sk == 0) return 0;
+  return delta_bytes(B, H, Sq) + static_cast<size_t>(B) * H * dq_tiles(Sq) * kDqTileFloats * sizeof(float) +
+         static_cast<size_t>(plan_window_bwd(w, B, H, Hkv).slots) * 2 * kDqTileFloats * sizeof(float);
+}
+
+int attn_window_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                    void* dq, void* dk, void* dv, int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                    long long q_pos0, float scale, long long q_row_stride, long long q_batch_stride,
+                    long long kv_row_stride, long long kv_batch_stride, long long o_row_stride,
+                    long long o_batch_stride, long long lse_head_stride, long long lse_batch_stride,
+                    long long dq_row_stride, long long dq_batch_stride, long long dkv_row_stride,
+                    long long dkv_batch_stride, void* workspace, size_t ws_bytes, void* stream) {
+  WindowShape w;
+  int rc = prep_window(&w, B, H, Hkv, Sq, Sk, D, window, sinks, q_pos0, scale);
+  if (rc != LCB_OK) return rc;
+  if (Sq == 0 && Sk == 0) return LCB_OK;
+  if (Sq > 0 && !window_output(dq, dq_row_stride, dq_batch_stride, B, Sq, H)) return LCB_ERR_ARG;
+  if (Sk > 0 && (!window_output(dk, dkv_row_stride, dkv_batch_stride, B, Sk, Hkv) ||
+                 !window_output(dv, dkv_row_stride, dkv_batch_stride, B, Sk, Hkv)))
+    return LCB_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long HD = static_cast<long long>(H) * kHeadDim, KD = static_cast<long long>(Hkv) * kHeadDim;
+  if (Sq == 0 || Sk == 0) {  // one side empty: the other's gradients are 0
+    for (int b = 0; b < B; ++b) {
+      char* rows[3] = {static_cast<char*>(dq), static_cast<char*>(dk), static_cast<char*>(dv)};
+      for (int g = Sq == 0 ? 1 : 0; g < (Sq == 0 ? 3 : 1); ++g) {
+        const long long rs = g ? dkv_row_stride : dq_row_stride, bs = g ? dkv_batch_stride : dq_batch_stride;
+        if (cudaMemset2DAsync(rows[g] + 2 * b * bs, 2 * rs, 0, 2 * (g ? KD : HD), g ? Sk : Sq, st) != cudaSuccess)
+          return LCB_ERR_CUDA;
+      }
+    }
+    return finish(LCB_OK, st);
+  }
+  if (!window_input(q, q_row_stride, q_batch_stride, H) || !window_input(o, o_row_stride, o_batch_stride, H) ||
+      !window_input(dO, o_row_stride, o_batch_stride, H) || !window_input(k, kv_row_stride, kv_batch_stride, Hkv) ||
+      !window_input(v, kv_row_stride, kv_batch_stride, Hkv))
+    return LCB_ERR_ARG;
+  if (!lse || lse_head_stride < 0 || lse_batch_stride < 0) return LCB_ERR_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      ws_bytes < attn_window_bwd_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks, q_pos0))
+    return LCB_ERR_ARG;
+  WindowBwd a;
+  const size_t acc_bytes = static_cast<size_t>(B) * H * dq_tiles(Sq) * kDqTileFloats * sizeof(float);
+  float* delta = static_cast<float*>(workspace);
+  a.q = {q, q_row_stride, q_batch_stride};
+  a.k = {k, kv_row_stride, kv_batch_stride};
+  a.v = {v, kv_row_stride, kv_batch_stride};
+  a.dO = {dO, o_row_stride, o_batch_stride};
+  a.lse = lse;
+  a.delta = delta;
+  a.lse_head_stride = lse_head_stride;
+  a.lse_batch_stride = lse_batch_stride;
+  a.delta_head_stride = Sq;
+  a.delta_batch_stride = static_cast<long long>(H) * Sq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dkv_row_stride = dkv_row_stride;
+  a.dkv_batch_stride = dkv_batch_stride;
+  a.dq_tiles = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta_bytes(B, H, Sq));
+  a.dq_tile_head_stride = dq_tiles(Sq) * kDqTileFloats;
+  a.dq_tile_batch_stride = a.dq_tile_head_stride * H;
+  a.partial = reinterpret_cast<float*>(reinterpret_cast<char*>(a.dq_tiles) + acc_bytes);
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.w = w;
+  a.scale = scale;
+  if ((rc = dev_status(&a.st)) != LCB_OK) return rc;
+  rc = launch_bwd_preprocess(o, dO, o_row_stride, o_batch_stride, delta, a.delta_head_stride, a.delta_batch_stride, B,
+                             H, Sq, st);
+  if (rc != LCB_OK) return rc;
+  if (cudaMemsetAsync(a.dq_tiles, 0, acc_bytes, st) != cudaSuccess) return LCB_ERR_CUDA;
+  if ((rc = launch_window_bwd(a, st)) != LCB_OK) return rc;
+  return finish(launch_dq_untile(a.dq_tiles, a.dq_tile_head_stride, a.dq_tile_batch_stride, dq, dq_row_stride,
+                                 dq_batch_stride, B, H, Sq, st),
+                st);
 }
 
 int lcb_selftest_bounded_wait(void* stream) {

@@ -1,0 +1,510 @@
+// Backward of attention with a sliding window and sinks, key/value heads
+// shared by groups of query heads, in one pass.
+//
+// With P_ij = exp(scale q_i.k_j - LSE_i) on the visible pairs, 0 elsewhere, and
+// dP_ij = dO_i.v_j, Delta_i = dO_i.O_i:
+//   dS = P (dP - Delta),  dV_j = sum_i P_ij dO_i,  dK_j = scale sum_i dS_ij q_i,
+//   dQ_i = scale sum_j dS_ij k_j,
+// the sums over i running over all query heads that share the K/V head.
+//
+// The tile machinery is that of the full one-pass backward: a CTA owns 128
+// keys, keeps dK and dV in TMEM, and for each (query head, query tile) pair
+// forms S^T and dP^T, then dV += P^T dO, dK += dS^T Q and the partial dQ =
+// dS K, added into a tiled fp32 accumulator in L2 (half of its columns by bulk
+// reductions from shared memory, half by vector reductions from registers: dQ's
+// summation order is not fixed). What the window adds: the pairs of a key tile
+// are those whose rows reach it, for every query head of the group, so the
+// shared heads' gradients are summed in the same TMEM accumulators; a pair
+// needs the per-element mask only where the diagonal, the window's far edge,
+// the last sink or the last key cuts it.
+//
+// A tile that holds sinks is seen by every later query: its list is as long as
+// the sequence, and with few K/V heads its CTA would outlast the grid. Long
+// lists are cut into runs, a CTA each, whose dK and dV go to fp32 partials that
+// a second kernel sums in run order (so dK and dV stay deterministic).
+//
+// TMEM: S^T [0,128) (P^T bf16 over it), dP^T [128,256) (then the dQ partial),
+// dV [256,384), dK [384,512). Shared memory: K, V, a two-slot Q ring, one dO
+// slot, dS^T, two 16 KB staging slots for dQ blocks, row statistics.
+// Warps 0-15 compute, 16 TMA producer, 17 MMA issuer, 18 dQ reducer.
+#include <algorithm>
+
+#include "attn_bwd_tile.cuh"
+#include "attn_window.cuh"
+
+namespace lcb {
+namespace {
+
+struct WinParams {
+  const float* lse;
+  const float* delta;
+  long long l_hs, l_bs;  // LSE strides
+  long long d_hs, d_bs;  // Delta strides
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  long long g_rs, g_bs;
+  float* dq_acc;
+  long long dq_hs, dq_bs;  // its head and batch strides (floats)
+  float* partial;
+  int B, H, Hkv;
+  WindowShape w;
+  WindowBwdPlan plan;
+  float scale, scale_log2;
+  DevStatus st;
+};
+
+__global__ void __launch_bounds__(kFuThreads, 1)
+    attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                           const __grid_constant__ WinParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  Bars* bars = reinterpret_cast<Bars*>(smem + kFuSmBar);
+  volatile int* abort_flag = &bars->abort;
+  const int warp = static_cast<int>(warp_id());
+  const int lane = static_cast<int>(lane_id());
+  constexpr uint32_t kWhere = 6u << 24;
+
+  // Work item: the sink tiles' runs come first (the longest lists), then the
+  // other key tiles, head by head, so that the CTAs running together read the
+  // query tiles and add into the dQ tiles of one stretch of a few heads.
+  const bool sink = static_cast<long long>(blockIdx.x) < p.plan.sink_ctas;
+  const int local = static_cast<int>(blockIdx.x) - (sink ? 0 : static_cast<int>(p.plan.sink_ctas));
+  const int segs = sink ? p.plan.sink_segs : p.plan.segs;
+  const int tiles = sink ? p.plan.sink_tiles : p.plan.key_tiles - p.plan.sink_tiles;
+  const int seg = local % segs;
+  const int kt = (local / segs) % tiles + (sink ? 0 : p.plan.sink_tiles);
+  const int bh = local / segs / tiles;
+  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int G = p.H / p.Hkv;
+  const QueryTiles qt = query_tiles(p.w, kt);
+  const int per = qt.hi - qt.lo;
+  const int all = G * per;
+  const int run = (all + segs - 1) / segs;
+  const int s0 = min(all, seg * run);
+  const int n = min(all, s0 + run) - s0;  // pairs of this CTA: s0 .. s0 + n - 1 of the list, head-major
+  auto head_of = [&](int i) { return hk * G + (s0 + i) / per; };
+  auto tile_of = [&](int i) { return qt.lo + (s0 + i) % per; };
+
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->stg_full[x], 128);
+      mbar_init(&bars->stg_free[x], 1);
+    }
+  }
+  const uint32_t tbase = start(bars, kKvStages, 1, warp);  // its barrier fence covers the inits above
+  const uint32_t tS = tbase, tDP = tbase + 128, tDV = tbase + 256, tDK = tbase + 384;
+  const uint32_t tDQ = tDP;
+
+  if (warp == kProducerWarp) {
+    if (lane == 0 && n > 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_do);
+      const uint64_t pol = l2_policy_evict_last();
+      mbar_arrive_expect_tx(&bars->fixed_full, 2 * kTileBytes);
+      load_tile(smem + kFuSmK, &tm_k, &bars->fixed_full, hk * kD, kt * kT, b, pol);
+      load_tile(smem + kFuSmV, &tm_v, &bars->fixed_full, hk * kD, kt * kT, b, pol);
+      int i = 0;
+      bool ok = true;
+      for (; i < n && ok; ++i) {
+        const int s = i % kKvStages;
+        const uint32_t ph = static_cast<uint32_t>(i / kKvStages) & 1u;
+        const uint32_t dph = static_cast<uint32_t>(i) & 1u;  // one dO slot
+        const int x0 = head_of(i) * kD, row = tile_of(i) * kT;
+        ok = mbar_wait(&bars->ring_empty[s], ph ^ 1u, abort_flag, p.st, kWhere | (1u << 16));
+        if (!ok) break;
+        mbar_arrive_expect_tx(&bars->ring_full[s], kTileBytes);
+        load_tile(smem + kFuSmQ + s * kTileBytes, &tm_q, &bars->ring_full[s], x0, row, b, pol);
+        ok = mbar_wait(&bars->do_empty[0], dph ^ 1u, abort_flag, p.st, kWhere | (11u << 16));
+        if (!ok) break;
+        mbar_arrive_expect_tx(&bars->do_full[0], kTileBytes);
+        load_tile(smem + kFuSmDo, &tm_do, &bars->do_full[0], x0, row, b, pol);
+      }
+      if (!ok) {
+        // Every copy already issued lands before the CTA can exit.
+        drain_wait(&bars->fixed_full, 0, p.st.limit);
+        for (int k2 = max(0, i - kKvStages); k2 <= i && k2 < n; ++k2)
+          drain_wait(&bars->ring_full[k2 % kKvStages], static_cast<uint32_t>(k2 / kKvStages) & 1u, p.st.limit);
+        for (int k2 = max(0, i - 1); k2 <= i && k2 < n; ++k2)
+          drain_wait(&bars->do_full[0], static_cast<uint32_t>(k2) & 1u, p.st.limit);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && n > 0) {
+      const uint32_t id_s = idesc_bf16(kT, kT, false, false);  // scores: both operands K-major
+      const uint32_t id_g = idesc_bf16(kT, kD, false, true);   // dK, dV: B MN-major
+      const uint32_t id_q = idesc_bf16(kT, kD, true, true);    // dQ: A (dS) and B (K) MN-major
+      const uint32_t sK = sbase + kFuSmK, sV = sbase + kFuSmV, sDs = sbase + kFuSmDs, sDo = sbase + kFuSmDo;
+      auto q_slot = [&](int i) { return sbase + kFuSmQ + (i % kKvStages) * kTileBytes; };
+      auto wait_q = [&](int i) {
+        const bool r = mbar_wait(&bars->ring_full[i % kKvStages], static_cast<uint32_t>(i / kKvStages) & 1u,
+                                 abort_flag, p.st, kWhere | (3u << 16));
+        tc_fence_after();
+        return r;
+      };
+      auto wait_do = [&](int i) {
+        const bool r = mbar_wait(&bars->do_full[0], static_cast<uint32_t>(i) & 1u, abort_flag, p.st,
+                                 kWhere | (12u << 16));
+        tc_fence_after();
+        return r;
+      };
+      bool ok = mbar_wait(&bars->fixed_full, 0, abort_flag, p.st, kWhere | (2u << 16));
+      if (ok) ok = wait_q(0);
+      if (ok) {
+        mma_ss_tile(tS, sK, q_slot(0), id_s, false);  // S^T(0) = K Q_0^T
+        tc_commit(&bars->s_full);
+      }
+      if (ok) ok = wait_do(0);
+      if (ok) {
+        mma_ss_tile(tDP, sV, sDo, id_s, false);  // dP^T(0) = V dO_0^T
+        tc_commit(&bars->dp_full);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const uint32_t ph = static_cast<uint32_t>(i) & 1u;
+        ok = mbar_wait(&bars->pt_full, ph, abort_flag, p.st, kWhere | (4u << 16));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ddo = sdesc_sw128(sDo, kColHalf, 1024);
+        // dV += P^T(i) dO_i; P^T K-step kk (queries 16kk..16kk+15) sits at columns 32(kk/2) + 8(kk%2)
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t a = tS + 32 * (kk >> 1) + 8 * (kk & 1);
+          mma_ts(tDV, a, sdesc_advance(ddo, kk * 2048), id_g, (i > 0 || kk > 0));
+        }
+        tc_commit(&bars->do_empty[0]);  // the dO slot may take dO(i+1)
+        if (i + 1 < n) {
+          ok = wait_q(i + 1);
+          if (!ok) break;
+          mma_ss_tile(tS, sK, q_slot(i + 1), id_s, false);  // S^T(i+1), after dV read P^T(i)
+          tc_commit(&bars->s_full);
+        }
+        // dS^T(i) is in shared memory; every compute thread loaded dP^T(i) before arriving
+        ok = mbar_wait(&bars->p_full, ph, abort_flag, p.st, kWhere | (13u << 16));
+        if (!ok) break;
+        tc_fence_after();
+        mma_ss_tile_mnmn(tDQ, sDs, sK, id_q);  // dQ(i) = dS(i) K
+        tc_commit(&bars->dq_full);
+        mma_ss_tile_mn(tDK, sDs, q_slot(i), id_g, i > 0);  // dK += dS^T(i) Q_i
+        tc_commit(&bars->ds_free);
+        tc_commit(&bars->ring_empty[i % kKvStages]);
+        if (i + 1 < n) {
+          ok = wait_do(i + 1);
+          if (ok) ok = mbar_wait(&bars->dq_free, ph, abort_flag, p.st, kWhere | (8u << 16));
+          if (!ok) break;
+          tc_fence_after();
+          mma_ss_tile(tDP, sV, sDo, id_s, false);  // dP^T(i+1), over the read dQ(i)
+          tc_commit(&bars->dp_full);
+        }
+      }
+      if (ok) tc_commit(&bars->acc_full);
+      tc_commit(&bars->mma_done);
+      drain_wait(&bars->mma_done, 0, p.st.limit);
+    }
+    __syncwarp();
+  } else if (warp == kFuReduceWarp) {
+    // Adds the two staged 16 KB dQ blocks of each pair (columns 0-63) into the
+    // accumulator and frees each slot once read.
+    if (lane == 0 && n > 0) {
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const uint32_t ph = static_cast<uint32_t>(i) & 1u;
+        float* tile = p.dq_acc + b * p.dq_bs + head_of(i) * p.dq_hs + static_cast<long long>(tile_of(i)) * (kT * kD);
+        ok = mbar_wait(&bars->stg_full[0], ph, abort_flag, p.st, kWhere | (14u << 16));
+        if (!ok) break;
+        bulk_reduce_add_f32(tile, sbase + kFuSmStg, kDqBlock);
+        bulk_commit();
+        ok = mbar_wait(&bars->stg_full[1], ph, abort_flag, p.st, kWhere | (14u << 16));
+        if (!ok) break;
+        bulk_reduce_add_f32(tile + kDqBlock / 4, sbase + kFuSmStg + kDqBlock, kDqBlock);
+        bulk_commit();
+        bulk_wait_read<1>();
+        mbar_arrive(&bars->stg_free[0]);
+        bulk_wait_read<0>();
+        mbar_arrive(&bars->stg_free[1]);
+      }
+      bulk_wait_all();  // every reduction issued has completed
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- compute
+    const int x = warp >> 2;            // this warpgroup's query columns [32x, 32x + 32)
+    const int row = threadIdx.x & 127;  // key row of S^T/dP^T/dV/dK, query row of dQ: the TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint8_t* ds_tile = smem + kFuSmDs;
+    uint8_t* stg_row = smem + kFuSmStg + (x & 1) * kDqBlock + row * 128;  // used by warpgroups 0 and 1
+    // This warpgroup's 32 query statistics of the current tile, published by
+    // every warp of the group (same values) and read back as broadcast float4s.
+    // Each array is rewritten only after a barrier that every reader of its
+    // previous values has passed (s_full(s) needs all of phase 1 of pair s-1
+    // done; dp_full(i) needs dq_free(i-1), which follows phase 2 of pair i-1).
+    float* l2s = reinterpret_cast<float*>(smem + kFuSmStats) + 32 * x;
+    float* sds = reinterpret_cast<float*>(smem + kFuSmStats) + 128 + 32 * x;
+    const int j0 = kt * kT, j = j0 + row;
+    const bool key_ok = j < p.w.Sk;  // a zero-filled row past the last key: P must be 0
+    const float c = p.scale_log2;
+    float rl = 0.f, rd = 0.f;  // raw LSE and Delta of the next pair, query 32x + lane of its tile
+    auto fetch_stats = [&](int i) {
+      const int h = head_of(i), q = tile_of(i) * kT + 32 * x + lane;
+      rl = q < p.w.Sq ? __ldg(p.lse + b * p.l_bs + h * p.l_hs + q) : -INFINITY;
+      rd = q < p.w.Sq ? __ldg(p.delta + b * p.d_bs + h * p.d_hs + q) : 0.f;
+    };
+    if (n > 0) fetch_stats(0);
+    bool ok = true;
+    // Step s runs phase 2 of pair s-1, phase 1 of pair s, then phase 3 of pair
+    // s-1: P^T(s) is computed while the tensor pipe runs dQ(s-1) and dK(s-1).
+    // dS carries the softmax scale (dS' = scale * P (dP - Delta)).
+    float pv[32];    // P^T of the pair between its phases 1 and 2
+    float sd = 0.f;  // -scale * Delta of that pair
+    const float scl = p.scale;
+    for (int s = 0; s <= n && ok; ++s) {
+      if (s > 0) {
+        // Phase 2: dS'^T = P^T (scale dP^T - scale Delta), rounded to bf16 (half a step, 2^-9 of each value,
+        // of either sign) into shared memory for dK and dQ.
+        const int i = s - 1;
+        const uint32_t ph = static_cast<uint32_t>(i) & 1u;
+        ok = warp_all(mbar_wait(&bars->dp_full, ph, abort_flag, p.st, kWhere | (6u << 16)));
+        if (!ok) break;
+        tc_fence_after();
+        sds[lane] = sd;
+        __syncwarp();
+        uint32_t dk[16];
+        {
+          uint32_t dp[32];
+          tmem_ld_x32(tDP + lane_off + 32 * x, dp);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 d = *reinterpret_cast<const float4*>(sds + e);
+            float t0, t1, u0, u1;
+            ffma2(t0, t1, __uint_as_float(dp[e]), __uint_as_float(dp[e + 1]), scl, scl, d.x, d.y);
+            fmul2(u0, u1, pv[e], pv[e + 1], t0, t1);
+            dk[e >> 1] = pack_bf16x2(u0, u1);
+            ffma2(t0, t1, __uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3]), scl, scl, d.z, d.w);
+            fmul2(u0, u1, pv[e + 2], pv[e + 3], t0, t1);
+            dk[(e >> 1) + 1] = pack_bf16x2(u0, u1);
+          }
+        }
+        if (i > 0) {
+          ok = warp_all(mbar_wait(&bars->ds_free, ph ^ 1u, abort_flag, p.st, kWhere | (9u << 16)));
+          if (!ok) break;
+        }
+        st_tile_quarter_row(ds_tile, row, x, dk);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full);  // also: dP^T(i) is in registers, its columns may take dQ(i)
+      }
+      if (s < n) {
+        // Phase 1: P^T(s), into this warpgroup's own S^T columns (already read by it).
+        const int p0 = p.w.pos0 + tile_of(s) * kT;  // position of the pair's first query
+        const float l2v = (rl == -INFINITY) ? -INFINITY : -rl * kLog2e;  // fetched a step ago
+        sd = -p.scale * rd;
+        if (s + 1 < n) fetch_stats(s + 1);
+        ok = warp_all(mbar_wait(&bars->s_full, static_cast<uint32_t>(s) & 1u, abort_flag, p.st, kWhere | (5u << 16)));
+        if (!ok) break;
+        tc_fence_after();
+        l2s[lane] = l2v;
+        __syncwarp();
+        const bool whole = j0 + kT - 1 <= p0 && j0 + kT <= p.w.Sk &&
+                           (p0 + kT - 1 - j0 < p.w.window || j0 + kT <= p.w.sinks);
+        {
+          uint32_t sv[32];
+          tmem_ld_x32(tS + lane_off + 32 * x, sv);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(l2s + e);
+            float x0, x1;
+            ffma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), c, c, m.x, m.y);
+            pv[e] = ex2_approx(x0);
+            pv[e + 1] = ex2_approx(x1);
+            ffma2(x0, x1, __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]), c, c, m.z, m.w);
+            pv[e + 2] = ex2_approx(x0);
+            pv[e + 3] = ex2_approx(x1);
+          }
+          if (!whole) {
+            // queries 32x + e with e in [from, to] of this tile see key j
+            const int at = p0 + 32 * x;
+            const int from = j - at;
+            const int to = !key_ok ? -1 : (j < p.w.sinks ? 31 : j + (p.w.window - 1) - at);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e < from || e > to) pv[e] = 0.f;
+          }
+        }
+        {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) pk[e >> 1] = pack_bf16x2(pv[e], pv[e + 1]);
+          tmem_st_x16_nowait(tS + lane_off + 32 * x, pk);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->pt_full);  // dV(s) and S^T(s+1) may go
+      }
+      if (s > 0) {
+        // Phase 3: row `row` of dQ(i) (TMEM lane = query row), columns [32x, 32x + 32), added into the accumulator.
+        const int i = s - 1;
+        const uint32_t ph = static_cast<uint32_t>(i) & 1u;
+        ok = warp_all(mbar_wait(&bars->dq_full, ph, abort_flag, p.st, kWhere | (7u << 16)));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t g[32];
+        tmem_ld_x32(tDQ + lane_off + 32 * x, g);
+        tc_fence_before();
+        mbar_arrive(&bars->dq_free);
+        if (x < 2) {
+          if (i > 0)
+            ok = warp_all(mbar_wait(&bars->stg_free[x], ph ^ 1u, abort_flag, p.st, kWhere | (15u << 16)));
+          if (!ok) break;
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch)
+            *reinterpret_cast<uint4*>(stg_row + ((ch ^ (row & 7)) << 4)) =
+                make_uint4(g[4 * ch], g[4 * ch + 1], g[4 * ch + 2], g[4 * ch + 3]);
+          fence_proxy_async_smem();
+          mbar_arrive(&bars->stg_full[x]);
+        } else {
+          float* tile = p.dq_acc + b * p.dq_bs + head_of(i) * p.dq_hs + static_cast<long long>(tile_of(i)) * (kT * kD);
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch)
+            red_add_v4(tile + 8192 + ((8 * (x - 2) + ch) * 128 + row) * 4, g[4 * ch], g[4 * ch + 1], g[4 * ch + 2],
+                       g[4 * ch + 3]);
+        }
+      }
+    }
+    // Epilogue: warpgroups 0/1 write dV columns [0,64)/[64,128), 2/3 write dK: bf16 rows, or this run's partial.
+    const bool parts = segs > 1;
+    const bool valid = parts || key_ok;
+    const int half = x & 1;
+    const long long slot = static_cast<long long>(local) + (!sink && p.plan.split(true) ? p.plan.sink_ctas : 0);
+    void* gdst;
+    long long off;
+    if (parts) {
+      gdst = p.partial;
+      off = (slot * 2 + (x < 2 ? 1 : 0)) * (kT * kD) + row * kD + 64 * half;
+    } else {
+      gdst = x < 2 ? p.dv : p.dk;
+      off = b * p.g_bs + static_cast<long long>(j) * p.g_rs + hk * kD + 64 * half;
+    }
+    const int mode = parts ? LCB_GRAD_F32_STORE : LCB_GRAD_BF16;
+    const uint32_t tacc = (x < 2 ? tDV : tDK) + lane_off + 64 * half;
+    if (n == 0) {
+      if (valid) store_zero(gdst, off, 64, mode);
+    } else if (ok) {
+      ok = warp_all(mbar_wait(&bars->acc_full, 0, abort_flag, p.st, kWhere | (10u << 16)));
+      if (ok) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t a[32];
+          tmem_ld_x32(tacc + ch * 32, a);
+          if (valid) store_grad_chunk(gdst, off + ch * 32, a, 1.f, mode);
+        }
+      }
+    }
+  }
+  teardown(tbase, warp);
+}
+
+// dK and dV of the split key tiles: their runs' fp32 partials, summed in run
+// order and rounded once. A CTA of 256 threads takes 16 rows of one tile's dK
+// or dV, a thread eight columns of a row.
+__global__ void __launch_bounds__(256) window_sum_runs_kernel(const __grid_constant__ WinParams p, int first_tile,
+                                                              int tiles, int segs, long long first_slot) {
+  int id = static_cast<int>(blockIdx.x);
+  const int part = id % 16;  // 8 groups of rows, dK then dV
+  id /= 16;
+  const int kt = first_tile + id % tiles;
+  const int bh = id / tiles;
+  const int row = (part & 7) * 16 + static_cast<int>(threadIdx.x >> 4), col = (threadIdx.x & 15) * 8;
+  const int j = kt * kT + row;
+  if (j >= p.w.Sk) return;
+  const float* src = p.partial +
+                     ((first_slot + static_cast<long long>(id) * segs) * 2 + (part >> 3)) * (kT * kD) + row * kD + col;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
+  for (int s = 0; s < segs; ++s, src += 2 * kT * kD) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(src)), v = __ldg(reinterpret_cast<const float4*>(src) + 1);
+    a = make_float4(a.x + u.x, a.y + u.y, a.z + u.z, a.w + u.w);
+    c = make_float4(c.x + v.x, c.y + v.y, c.z + v.z, c.w + v.w);
+  }
+  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  __nv_bfloat16* dst = (part >> 3) ? p.dv : p.dk;
+  *reinterpret_cast<uint4*>(dst + b * p.g_bs + static_cast<long long>(j) * p.g_rs + hk * kD + col) =
+      make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(c.x, c.y), pack_bf16x2(c.z, c.w));
+}
+
+}  // namespace
+
+WindowBwdPlan plan_window_bwd(const WindowShape& w, int B, int H, int Hkv) {
+  WindowBwdPlan pl = {};
+  const long long heads = static_cast<long long>(B) * Hkv, G = H / Hkv;
+  pl.key_tiles = (w.Sk + kT - 1) / kT;
+  pl.sink_tiles = std::min(pl.key_tiles, (w.sinks + kT - 1) / kT);
+  long long pairs = 0, longest = 0, longest_sink = 0;
+  for (int kt = 0; kt < pl.key_tiles; ++kt) {
+    const QueryTiles q = query_tiles(w, kt);
+    const long long n = G * (q.hi - q.lo);
+    pairs += n * heads;
+    (kt < pl.sink_tiles ? longest_sink : longest) = std::max(kt < pl.sink_tiles ? longest_sink : longest, n);
+  }
+  // A run is long enough for its fixed cost (loading K and V, writing dK and
+  // dV: about two pairs' time) and short enough that about three of them could
+  // follow one another on every SM.
+  const long long run = std::max<long long>(8, (pairs + 152 * 3 - 1) / (152 * 3));
+  pl.segs = static_cast<int>(std::max<long long>(1, (longest + run - 1) / run));
+  pl.sink_segs = static_cast<int>(std::max<long long>(1, (longest_sink + run - 1) / run));
+  pl.sink_ctas = heads * pl.sink_tiles * pl.sink_segs;
+  const long long rest = heads * (pl.key_tiles - pl.sink_tiles) * pl.segs;
+  pl.ctas = pl.sink_ctas + rest;
+  pl.slots = (pl.sink_segs > 1 ? pl.sink_ctas : 0) + (pl.segs > 1 ? rest : 0);
+  return pl;
+}
+
+int launch_window_bwd(const WindowBwd& a, cudaStream_t stream) {
+  CUtensorMap tk, tv, tq, tdo;
+  int rc;
+  if ((rc = make_tma_map_bf16(&tk, a.k, a.B, a.w.Sk, a.Hkv * kD, kT)) != 0) return rc;
+  if ((rc = make_tma_map_bf16(&tv, a.v, a.B, a.w.Sk, a.Hkv * kD, kT)) != 0) return rc;
+  if ((rc = make_tma_map_bf16(&tq, a.q, a.B, a.w.Sq, a.H * kD, kT)) != 0) return rc;
+  if ((rc = make_tma_map_bf16(&tdo, a.dO, a.B, a.w.Sq, a.H * kD, kT)) != 0) return rc;
+  static DeviceOnce smem_set;
+  if ((rc = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(attn_window_bwd_kernel), kFuSmem)) != 0)
+    return rc;
+  WinParams p;
+  p.lse = a.lse;
+  p.delta = a.delta;
+  p.l_hs = a.lse_head_stride;
+  p.l_bs = a.lse_batch_stride;
+  p.d_hs = a.delta_head_stride;
+  p.d_bs = a.delta_batch_stride;
+  p.dk = static_cast<__nv_bfloat16*>(a.dk);
+  p.dv = static_cast<__nv_bfloat16*>(a.dv);
+  p.g_rs = a.dkv_row_stride;
+  p.g_bs = a.dkv_batch_stride;
+  p.dq_acc = a.dq_tiles;
+  p.dq_hs = a.dq_tile_head_stride;
+  p.dq_bs = a.dq_tile_batch_stride;
+  p.partial = a.partial;
+  p.B = a.B;
+  p.H = a.H;
+  p.Hkv = a.Hkv;
+  p.w = a.w;
+  p.plan = plan_window_bwd(a.w, a.B, a.H, a.Hkv);
+  p.scale = a.scale;
+  p.scale_log2 = a.scale * kLog2e;
+  p.st = a.st;
+  if (p.plan.ctas > 0x7fffffffLL / 16) return -1;
+  attn_window_bwd_kernel<<<static_cast<unsigned>(p.plan.ctas), kFuThreads, kFuSmem, stream>>>(tk, tv, tq, tdo, p);
+  if (cudaGetLastError() != cudaSuccess) return -4;
+  const int heads = a.B * a.Hkv, rest = p.plan.key_tiles - p.plan.sink_tiles;
+  if (p.plan.split(true))
+    window_sum_runs_kernel<<<static_cast<unsigned>(heads * p.plan.sink_tiles * 16), 256, 0, stream>>>(
+        p, 0, p.plan.sink_tiles, p.plan.sink_segs, 0);
+  if (p.plan.split(false) && rest > 0)
+    window_sum_runs_kernel<<<static_cast<unsigned>(heads * rest * 16), 256, 0, stream>>>(
+        p, p.plan.sink_tiles, rest, p.plan.segs, p.plan.split(true) ? p.plan.sink_ctas : 0);
+  return cudaGetLastError() == cudaSuccess ? 0 : -4;
+}
+
+}  // namespace lcb

@@ -2,9 +2,11 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "attn_window.cuh"
 #include "common.cuh"
 #include "device_once.h"
 
@@ -123,5 +125,64 @@ struct RopeFreqs {
 // y = RoPE(x) (inverse: the transpose) on bf16 [B, S, H, 128] views sharing strides.
 int launch_rope(const void* x, void* y, int B, int S, int H, long long row_stride, long long batch_stride,
                 long long pos0, int inverse, const RopeFreqs& fr, cudaStream_t stream);
+
+// RoPE with several position axes: pair k turns by pos[axis[k]] * turn[k] / 2^64 turns.
+struct RopeAxes {
+  unsigned long long turn[64];
+  unsigned char axis[64];
+};
+// y = RoPE(x) with positions pos[axis][b][s] (int32 or int64 by pos_bytes; strides in elements).
+int launch_rope_axes(const void* x, void* y, int B, int S, int H, long long row_stride, long long batch_stride,
+                     const void* pos, int pos_bytes, long long pos_axis_stride, long long pos_batch_stride,
+                     long long pos_row_stride, int inverse, const RopeAxes& ax, cudaStream_t stream);
+
+// Windowed attention (attn_window.cuh says what is visible); strides in elements.
+struct WindowFwd {
+  RowView q, k, v;
+  void* o;
+  float* lse;
+  long long o_row_stride, o_batch_stride, lse_head_stride, lse_batch_stride;
+  int B, H, Hkv;
+  WindowShape w;
+  float scale;
+  DevStatus st;
+};
+int launch_window_fwd(const WindowFwd& a, cudaStream_t stream);  // Sq, Sk > 0
+
+struct WindowBwd {
+  RowView q, k, v, dO;
+  const float* lse;
+  const float* delta;
+  long long lse_head_stride, lse_batch_stride, delta_head_stride, delta_batch_stride;
+  void* dk;
+  void* dv;
+  long long dkv_row_stride, dkv_batch_stride;
+  float* dq_tiles;  // zeroed tiled accumulator, added into
+  long long dq_tile_head_stride, dq_tile_batch_stride;
+  float* partial;  // plan.slots * 2 * 128 * 128 floats
+  int B, H, Hkv;
+  WindowShape w;
+  float scale;
+  DevStatus st;
+};
+WindowBwdPlan plan_window_bwd(const WindowShape& w, int B, int H, int Hkv);
+int launch_window_bwd(const WindowBwd& a, cudaStream_t stream);  // Sq, Sk > 0
+
+// Windowed attention of T query rows per head, keys split over a cluster. lens
+// (device, may be null): keys of each sequence, queries at its last T
+// positions; null: Sk keys, queries from pos0 on.
+struct WindowSplit {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const int* lens;
+  __nv_bfloat16* o;
+  float* lse;
+  long long q_rs, q_bs, kv_rs, kv_bs, o_rs, o_bs, l_hs, l_bs;
+  int B, H, Hkv, T, Sk, pos0, window, sinks;
+  float scale_log2;
+  int row_tiles, cluster;  // set by the launch
+};
+int launch_window_split(WindowSplit p, cudaStream_t stream);
 
 }  // namespace lcb
