@@ -496,47 +496,88 @@ def rope(x, theta, pos0=0, inverse=False, out=None):
 
 
 # ------------------------------------------------------------------ window and sinks
+#
+# A serving step makes these calls by the hundred, each a few microseconds of
+# GPU work: the checks read a tensor's shape and strides once, and the stream
+# and device come as plain integers.
 
-def _on_device(name, dev, *tensors):
-    """Every tensor on `dev`, which must be the current CUDA device (kernels launch there)."""
-    if dev.type != "cuda":
+_BF16 = torch.bfloat16
+
+
+def _fn(name):
+    return getattr(_LIB or load(), name)
+
+
+def _rows(t, name):
+    """(shape, row stride, batch stride) of a bf16 [B, S, H, D] view with dense heads. The stride of a dimension of
+    length one says nothing; it is taken as that of a dense tensor."""
+    if t.dtype is not _BF16 or t.dim() != 4:
+        raise ValueError(f"{name} must be a bf16 [B, S, H, D] view, got {t.dtype} {tuple(t.shape)}")
+    shape, (bs, rs, hs, ds) = t.shape, t.stride()
+    B, S, H, D = shape
+    if ds != 1 and D > 1 or hs != D and H > 1:
+        raise ValueError(f"{name}: heads must be dense within a row")
+    if S <= 1:
+        rs = H * D
+    return shape, rs, bs if B > 1 else 0
+
+
+def _stats(t, name, shape):
+    """(head stride, batch stride) of an fp32 [B, H, S] view."""
+    if t.dtype is not torch.float32 or t.shape != shape:
+        raise ValueError(f"{name} must be an fp32 [B, H, S] view of {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    bs, hs, ss = t.stride()
+    if ss != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dim")
+    return hs, bs
+
+
+def _raw_stream(name, *tensors):
+    """The current stream of the tensors' device, which must be one, a CUDA device, and the current one (kernels launch
+    there)."""
+    dev = tensors[0].get_device()
+    if dev < 0:
         raise ValueError(f"{name}: tensors must be on a CUDA device")
     for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: tensors on {dev}, which is not the current device")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}, not on one CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name}: tensors on {tensors[0].device}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _window_shapes(name, q, k, v):
-    """(B, Sq, H, D, Sk, Hkv, q strides, k/v strides) of a windowed-attention call."""
-    qr, qb = _bshd(q, "q")
-    kr, kb = _bshd(k, "k")
-    B, Sq, H, D = q.shape
-    Bk, Sk, Hkv, Dk = k.shape
-    if _bshd(v, "v") != (kr, kb) and Sk:
-        raise ValueError("k and v must share strides")
-    if v.shape != k.shape or Bk != B or Dk != D or Hkv < 1 or H % Hkv:
+def _window_inputs(name, q, k, v):
+    """q's shape and strides, k's shape, the strides of k and v, of a windowed-attention call."""
+    qs, qr, qb = _rows(q, "q")
+    ks, kr, kb = _rows(k, "k")
+    vs, vr, vb = _rows(v, "v")
+    if vs != ks or ks[0] != qs[0] or ks[3] != qs[3] or ks[2] < 1 or qs[2] % ks[2]:
         raise ValueError(f"{name}: k and v must be [B, Sk, Hkv, D] with Hkv dividing q's H, "
-                         f"got {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
-    return B, Sq, H, D, Sk, Hkv, qr, qb, kr, kb
+                         f"got {tuple(qs)}, {tuple(ks)}, {tuple(vs)}")
+    if (vr, vb) != (kr, kb) and ks[1]:
+        raise ValueError("k and v must share strides")
+    return qs, qr, qb, ks, kr, kb
 
 
-def _window_out(q, o, lse):
-    """Given or fresh (o, lse) of q's shape, with their strides."""
-    B, S, H, D = q.shape
-    o = torch.empty((B, S, H, D), dtype=q.dtype, device=q.device) if o is None else o
-    lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse is None else lse
-    if o.shape != q.shape or lse.shape != (B, H, S):
-        raise ValueError("o must have q's shape and lse [B, H, S]")
-    return o, lse, *_bshd(o, "o"), *_bhs_any(lse, "lse")
+def _window_out(q, shape, o, lse):
+    """Given or fresh (o, lse) for queries of `shape`, with their strides."""
+    B, S, H, D = shape
+    if o is None:
+        o, orr, ob = torch.empty(shape, dtype=_BF16, device=q.device), H * D, S * H * D
+    else:
+        os_, orr, ob = _rows(o, "o")
+        if os_ != shape:
+            raise ValueError("o must have q's shape")
+    if lse is None:
+        lse, lh, lb = torch.empty((B, H, S), dtype=torch.float32, device=q.device), S, H * S
+    else:
+        lh, lb = _stats(lse, "lse", (B, H, S))
+    return o, lse, orr, ob, lh, lb
 
 
-def _bhs_any(t, name):
-    """Strides of an fp32 [B, H, S] view; a length of one says nothing of its last stride."""
-    if t.dim() == 3 and t.shape[2] <= 1 and t.is_cuda and t.dtype == torch.float32:
-        return t.stride(1), t.stride(0)
-    return _bhs(t, name)
+def _count(n):
+    """A window or sink count for the C ABI: more than 2^30 keys is all of them."""
+    return max(-1, min(int(n), 1 << 30))
 
 
 def attn_window_fwd(q, k, v, window, sinks=0, q_pos0=None, scale=None, o=None, lse=None):
@@ -548,23 +589,20 @@ def attn_window_fwd(q, k, v, window, sinks=0, q_pos0=None, scale=None, o=None, l
     those, the first `sinks` whatever their distance. q_pos0=None puts the
     queries at the end of the keys (Sk - Sq: self-attention, or the next chunk
     of a prompt against its cache). A row that sees nothing gives 0 and -inf."""
-    B, Sq, H, D, Sk, Hkv, qr, qb, kr, kb = _window_shapes("attn_window_fwd", q, k, v)
-    o, lse, orr, ob, lh, lb = _window_out(q, o, lse)
-    _on_device("attn_window_fwd", q.device, k, v, o, lse)
-    _check("attn_window_fwd", load().attn_window_fwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Sk, D, _window(window),
-        _window(sinks), Sk - Sq if q_pos0 is None else int(q_pos0), D ** -0.5 if scale is None else float(scale), qr,
-        qb, kr, kb, orr, ob, lh, lb, _stream(q)))
+    qs, qr, qb, ks, kr, kb = _window_inputs("attn_window_fwd", q, k, v)
+    B, Sq, H, D = qs
+    Sk = ks[1]
+    o, lse, orr, ob, lh, lb = _window_out(q, qs, o, lse)
+    stream = _raw_stream("attn_window_fwd", q, k, v, o, lse)
+    _check("attn_window_fwd", _fn("attn_window_fwd")(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, ks[2], Sq, Sk, D, _count(window),
+        _count(sinks), Sk - Sq if q_pos0 is None else int(q_pos0), D ** -0.5 if scale is None else float(scale), qr,
+        qb, kr, kb, orr, ob, lh, lb, stream))
     return o, lse
 
 
-def _window(n):
-    """A window or sink count for the C ABI: more than 2^30 keys is all of them."""
-    return max(-1, min(int(n), 1 << 30))
-
-
 def attn_window_bwd_workspace_bytes(B, H, Hkv, Sq, Sk, window, sinks=0, q_pos0=None, D=128):
-    return int(load().attn_window_bwd_workspace_bytes(B, H, Hkv, Sq, Sk, D, _window(window), _window(sinks),
+    return int(load().attn_window_bwd_workspace_bytes(B, H, Hkv, Sq, Sk, D, _count(window), _count(sinks),
                                                       Sk - Sq if q_pos0 is None else int(q_pos0)))
 
 
@@ -575,22 +613,24 @@ def attn_window_bwd(q, k, v, o, lse, do, window, sinks=0, q_pos0=None, scale=Non
     o and do share strides. dk and dv are [B, Sk, Hkv, 128], summed over the
     query heads of each K/V head. workspace: uint8 of
     attn_window_bwd_workspace_bytes (None: allocated here)."""
-    B, Sq, H, D, Sk, Hkv, qr, qb, kr, kb = _window_shapes("attn_window_bwd", q, k, v)
-    if o.shape != q.shape or do.shape != q.shape or lse.shape != (B, H, Sq):
-        raise ValueError("o and do must have q's shape and lse [B, H, Sq]")
-    orr, ob = _bshd(o, "o")
-    if _bshd(do, "do") != (orr, ob) and Sq:
+    qs, qr, qb, ks, kr, kb = _window_inputs("attn_window_bwd", q, k, v)
+    B, Sq, H, D = qs
+    Sk, Hkv = ks[1], ks[2]
+    os_, orr, ob = _rows(o, "o")
+    ds_, dor, dob = _rows(do, "do")
+    if os_ != qs or ds_ != qs:
+        raise ValueError("o and do must have q's shape")
+    if (dor, dob) != (orr, ob) and Sq:
         raise ValueError("o and do must share strides")
-    lh, lb = _bhs_any(lse, "lse")
+    lh, lb = _stats(lse, "lse", (B, H, Sq))
     dev = q.device
-    dq = torch.empty((B, Sq, H, D), dtype=q.dtype, device=dev) if dq is None else dq
-    dk = torch.empty((B, Sk, Hkv, D), dtype=q.dtype, device=dev) if dk is None else dk
-    dv = torch.empty((B, Sk, Hkv, D), dtype=q.dtype, device=dev) if dv is None else dv
-    if dq.shape != q.shape or dk.shape != k.shape or dv.shape != k.shape:
+    dq = torch.empty(qs, dtype=_BF16, device=dev) if dq is None else dq
+    dk = torch.empty(ks, dtype=_BF16, device=dev) if dk is None else dk
+    dv = torch.empty(ks, dtype=_BF16, device=dev) if dv is None else dv
+    (dqs, dqr, dqb), (dks, dkr, dkb), (dvs, dvr, dvb) = _rows(dq, "dq"), _rows(dk, "dk"), _rows(dv, "dv")
+    if dqs != qs or dks != ks or dvs != ks:
         raise ValueError("dq must have q's shape, dk and dv k's")
-    dqr, dqb = _bshd(dq, "dq")
-    dkr, dkb = _bshd(dk, "dk")
-    if _bshd(dv, "dv") != (dkr, dkb) and Sk:
+    if (dvr, dvb) != (dkr, dkb) and Sk:
         raise ValueError("dk and dv must share strides")
     pos0 = Sk - Sq if q_pos0 is None else int(q_pos0)
     if workspace is None:
@@ -598,12 +638,12 @@ def attn_window_bwd(q, k, v, o, lse, do, window, sinks=0, q_pos0=None, scale=Non
         workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _on_device("attn_window_bwd", dev, k, v, o, lse, do, dq, dk, dv, workspace)
-    _check("attn_window_bwd", load().attn_window_bwd(
+    stream = _raw_stream("attn_window_bwd", q, k, v, o, lse, do, dq, dk, dv, workspace)
+    _check("attn_window_bwd", _fn("attn_window_bwd")(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
-        dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Sq, Sk, D, _window(window), _window(sinks), pos0,
+        dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Sq, Sk, D, _count(window), _count(sinks), pos0,
         D ** -0.5 if scale is None else float(scale), qr, qb, kr, kb, orr, ob, lh, lb, dqr, dqb, dkr, dkb,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(q)))
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream))
     return dq, dk, dv
 
 
@@ -614,15 +654,16 @@ def attn_window_decode(q, k_cache, v_cache, lens, window, sinks=0, scale=None, o
     lens[b] rows (CUDA int32 [B]), the newest tokens' own among them: token t
     stands at position lens[b] - T + t. Window, sinks and heads as in
     attn_window_fwd. Cache rows at or past lens[b] are not read."""
-    B, T, H, D, Smax, Hkv, qr, qb, kr, kb = _window_shapes("attn_window_decode", q, k_cache, v_cache)
-    if lens.dtype != torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
+    qs, qr, qb, ks, kr, kb = _window_inputs("attn_window_decode", q, k_cache, v_cache)
+    B, T, H, D = qs
+    if lens.dtype is not torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
         raise ValueError("lens must be a contiguous int32 [B] tensor")
-    o, lse, orr, ob, lh, lb = _window_out(q, o, lse)
-    _on_device("attn_window_decode", q.device, k_cache, v_cache, lens, o, lse)
-    _check("attn_window_decode", load().attn_window_decode(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv,
-        T, Smax, D, _window(window), _window(sinks), D ** -0.5 if scale is None else float(scale), qr, qb, kr, kb, orr,
-        ob, lh, lb, _stream(q)))
+    o, lse, orr, ob, lh, lb = _window_out(q, qs, o, lse)
+    stream = _raw_stream("attn_window_decode", q, k_cache, v_cache, lens, o, lse)
+    _check("attn_window_decode", _fn("attn_window_decode")(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, ks[2],
+        T, ks[1], D, _count(window), _count(sinks), D ** -0.5 if scale is None else float(scale), qr, qb, kr, kb, orr,
+        ob, lh, lb, stream))
     return o, lse
 
 
@@ -652,18 +693,20 @@ def rope_axes(x, theta, pos, sections, inverse=False, interleaved=False, out=Non
     arr = _PAIR_AXES.get(key)
     if arr is None:
         arr = _PAIR_AXES[key] = (ctypes.c_int * 64)(*rope_pair_axes(*key))
-    r, b = _bshd(x, "x")
-    B, S, H, D = x.shape
-    out = x if out is None else out
-    if out.shape != x.shape or _bshd(out, "out") != (r, b):
+    shape, r, b = _rows(x, "x")
+    if out is None:
+        out = x
+    elif _rows(out, "out") != (shape, r, b):
         raise ValueError("x and out must share shape and strides")
-    if pos.dtype not in (torch.int32, torch.int64) or tuple(pos.shape) not in ((len(key[0]), S), (len(key[0]), B, S)):
+    B, S, H, D = shape
+    n = len(key[0])
+    ps = pos.stride()
+    if pos.dtype not in (torch.int32, torch.int64) or pos.shape != (n, S) and pos.shape != (n, B, S):
         raise ValueError("pos must be int32 or int64 [axes, S] or [axes, B, S]")
-    pb = pos.stride(1) if pos.dim() == 3 else 0
-    _on_device("rope_axes", x.device, pos, out)
-    _check("lcb_rope_axes", load().lcb_rope_axes(
-        x.data_ptr(), out.data_ptr(), B, S, H, D, float(theta), pos.data_ptr(), pos.element_size(), len(key[0]), arr,
-        pos.stride(0), pb, pos.stride(-1), int(inverse), r, b, _stream(x)))
+    stream = _raw_stream("rope_axes", x, pos, out)
+    _check("lcb_rope_axes", _fn("lcb_rope_axes")(
+        x.data_ptr(), out.data_ptr(), B, S, H, D, theta, pos.data_ptr(), pos.element_size(), n, arr, ps[0],
+        ps[1] if len(ps) == 3 else 0, ps[-1], bool(inverse), r, b, stream))
     return out
 
 

@@ -31,6 +31,7 @@
 
 #include "attn_bwd_tile.cuh"
 #include "attn_window.cuh"
+#include "mma_warp.cuh"
 
 namespace lcb {
 namespace {
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kFuThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   Bars* bars = reinterpret_cast<Bars*>(smem + kFuSmBar);
   volatile int* abort_flag = &bars->abort;
-  const int warp = static_cast<int>(warp_id());
+  const int warp = static_cast<int>(uniform(warp_id()));
   const int lane = static_cast<int>(lane_id());
   constexpr uint32_t kWhere = 6u << 24;
 
@@ -134,74 +135,89 @@ __global__ void __launch_bounds__(kFuThreads, 1)
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && n > 0) {
+    // All lanes walk the loop, one elected lane issues.
+    if (n > 0) {
+      const uint32_t one = elect_one();
+      const uint32_t tm = uniform(tbase);
+      const uint32_t uS = tm, uDP = tm + 128, uDV = tm + 256, uDK = tm + 384, uDQ = uDP;
       const uint32_t id_s = idesc_bf16(kT, kT, false, false);  // scores: both operands K-major
       const uint32_t id_g = idesc_bf16(kT, kD, false, true);   // dK, dV: B MN-major
       const uint32_t id_q = idesc_bf16(kT, kD, true, true);    // dQ: A (dS) and B (K) MN-major
-      const uint32_t sK = sbase + kFuSmK, sV = sbase + kFuSmV, sDs = sbase + kFuSmDs, sDo = sbase + kFuSmDo;
-      auto q_slot = [&](int i) { return sbase + kFuSmQ + (i % kKvStages) * kTileBytes; };
-      auto wait_q = [&](int i) {
-        const bool r = mbar_wait(&bars->ring_full[i % kKvStages], static_cast<uint32_t>(i / kKvStages) & 1u,
-                                 abort_flag, p.st, kWhere | (3u << 16));
+      // operands as read K-major (rows) and MN-major (columns)
+      const uint64_t k_rows = sdesc_sw128(sbase + kFuSmK, 16, 1024), k_cols = sdesc_sw128(sbase + kFuSmK, kColHalf, 1024);
+      const uint64_t v_rows = sdesc_sw128(sbase + kFuSmV, 16, 1024);
+      const uint64_t q_rows = sdesc_sw128(sbase + kFuSmQ, 16, 1024), q_cols = sdesc_sw128(sbase + kFuSmQ, kColHalf, 1024);
+      const uint64_t do_rows = sdesc_sw128(sbase + kFuSmDo, 16, 1024),
+                     do_cols = sdesc_sw128(sbase + kFuSmDo, kColHalf, 1024);
+      const uint64_t ds_rows = sdesc_sw128(sbase + kFuSmDs, 16, 1024),
+                     ds_cols = sdesc_sw128(sbase + kFuSmDs, kColHalf, 1024);
+      auto slot = [&](int i) { return static_cast<uint32_t>(i & 1) * kTileBytes; };
+      auto scores = [&](uint32_t d, uint64_t da, uint64_t db) {  // D = A B^T, both K-major
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kColHalf + (kk & 3) * 32;
+          mma_ss_if(d, sdesc_advance(da, off), sdesc_advance(db, off), id_s, kk > 0, one);
+        }
+      };
+      auto wait = [&](uint64_t* bar, uint32_t ph, uint32_t id) {
+        const bool r = mbar_wait_warp(bar, ph, abort_flag, p.st, kWhere | (id << 16));
         tc_fence_after();
         return r;
       };
-      auto wait_do = [&](int i) {
-        const bool r = mbar_wait(&bars->do_full[0], static_cast<uint32_t>(i) & 1u, abort_flag, p.st,
-                                 kWhere | (12u << 16));
-        tc_fence_after();
-        return r;
-      };
-      bool ok = mbar_wait(&bars->fixed_full, 0, abort_flag, p.st, kWhere | (2u << 16));
+      auto wait_q = [&](int i) { return wait(&bars->ring_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, 3u); };
+      auto wait_do = [&](int i) { return wait(&bars->do_full[0], static_cast<uint32_t>(i) & 1u, 12u); };
+      static_assert(kKvStages == 2, "the Q ring's slot is the pair's parity");
+      bool ok = wait(&bars->fixed_full, 0, 2u);
       if (ok) ok = wait_q(0);
       if (ok) {
-        mma_ss_tile(tS, sK, q_slot(0), id_s, false);  // S^T(0) = K Q_0^T
-        tc_commit(&bars->s_full);
+        scores(uS, k_rows, q_rows);  // S^T(0) = K Q_0^T
+        tc_commit_if(&bars->s_full, one);
       }
       if (ok) ok = wait_do(0);
       if (ok) {
-        mma_ss_tile(tDP, sV, sDo, id_s, false);  // dP^T(0) = V dO_0^T
-        tc_commit(&bars->dp_full);
+        scores(uDP, v_rows, do_rows);  // dP^T(0) = V dO_0^T
+        tc_commit_if(&bars->dp_full, one);
       }
       for (int i = 0; i < n && ok; ++i) {
-        const uint32_t ph = static_cast<uint32_t>(i) & 1u;
-        ok = mbar_wait(&bars->pt_full, ph, abort_flag, p.st, kWhere | (4u << 16));
+        const uint32_t ph = static_cast<uint32_t>(i) & 1u, acc = i > 0 ? 1u : 0u;
+        ok = wait(&bars->pt_full, ph, 4u);
         if (!ok) break;
-        tc_fence_after();
-        const uint64_t ddo = sdesc_sw128(sDo, kColHalf, 1024);
         // dV += P^T(i) dO_i; P^T K-step kk (queries 16kk..16kk+15) sits at columns 32(kk/2) + 8(kk%2)
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t a = tS + 32 * (kk >> 1) + 8 * (kk & 1);
-          mma_ts(tDV, a, sdesc_advance(ddo, kk * 2048), id_g, (i > 0 || kk > 0));
-        }
-        tc_commit(&bars->do_empty[0]);  // the dO slot may take dO(i+1)
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_if(uDV, uS + 32 * (kk >> 1) + 8 * (kk & 1), sdesc_advance(do_cols, kk * 2048), id_g,
+                    kk > 0 ? 1u : acc, one);
+        tc_commit_if(&bars->do_empty[0], one);  // the dO slot may take dO(i+1)
         if (i + 1 < n) {
           ok = wait_q(i + 1);
           if (!ok) break;
-          mma_ss_tile(tS, sK, q_slot(i + 1), id_s, false);  // S^T(i+1), after dV read P^T(i)
-          tc_commit(&bars->s_full);
+          scores(uS, k_rows, sdesc_advance(q_rows, slot(i + 1)));  // S^T(i+1), after dV read P^T(i)
+          tc_commit_if(&bars->s_full, one);
         }
         // dS^T(i) is in shared memory; every compute thread loaded dP^T(i) before arriving
-        ok = mbar_wait(&bars->p_full, ph, abort_flag, p.st, kWhere | (13u << 16));
+        ok = wait(&bars->p_full, ph, 13u);
         if (!ok) break;
-        tc_fence_after();
-        mma_ss_tile_mnmn(tDQ, sDs, sK, id_q);  // dQ(i) = dS(i) K
-        tc_commit(&bars->dq_full);
-        mma_ss_tile_mn(tDK, sDs, q_slot(i), id_g, i > 0);  // dK += dS^T(i) Q_i
-        tc_commit(&bars->ds_free);
-        tc_commit(&bars->ring_empty[i % kKvStages]);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // dQ(i) = dS(i) K
+          mma_ss_if(uDQ, sdesc_advance(ds_cols, kk * 2048), sdesc_advance(k_cols, kk * 2048), id_q, kk > 0, one);
+        tc_commit_if(&bars->dq_full, one);
+        const uint64_t qi = sdesc_advance(q_cols, slot(i));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // dK += dS^T(i) Q_i
+          mma_ss_if(uDK, sdesc_advance(ds_rows, (kk >> 2) * kColHalf + (kk & 3) * 32), sdesc_advance(qi, kk * 2048),
+                    id_g, kk > 0 ? 1u : acc, one);
+        tc_commit_if(&bars->ds_free, one);
+        tc_commit_if(&bars->ring_empty[i & 1], one);
         if (i + 1 < n) {
           ok = wait_do(i + 1);
-          if (ok) ok = mbar_wait(&bars->dq_free, ph, abort_flag, p.st, kWhere | (8u << 16));
+          if (ok) ok = wait(&bars->dq_free, ph, 8u);
           if (!ok) break;
-          tc_fence_after();
-          mma_ss_tile(tDP, sV, sDo, id_s, false);  // dP^T(i+1), over the read dQ(i)
-          tc_commit(&bars->dp_full);
+          scores(uDP, v_rows, do_rows);  // dP^T(i+1), over the read dQ(i)
+          tc_commit_if(&bars->dp_full, one);
         }
       }
-      if (ok) tc_commit(&bars->acc_full);
-      tc_commit(&bars->mma_done);
+      if (ok) tc_commit_if(&bars->acc_full, one);
+      tc_commit_if(&bars->mma_done, one);
       drain_wait(&bars->mma_done, 0, p.st.limit);
     }
     __syncwarp();

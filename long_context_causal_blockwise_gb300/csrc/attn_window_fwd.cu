@@ -8,7 +8,10 @@
 // of a head as two 128-row tiles that ping-pong, so the tensor core works on
 // one while the softmax warps work on the other; K and V stream by TMA through
 // a four-slot ring; S and O live in TMEM, P goes back over S as the second
-// product's A operand; the running maximum is raised lazily (by more than 2^8).
+// product's A operand; the running maximum m is raised lazily, only when a score
+// passes it by more than 32 in base 2. O / l is exact for any m; P then stays
+// below 2^32, l below 2^61 and O below 2^61 max |v|, and what falls under
+// 2^-126 is 2^-126 of a term that is there.
 // What the window adds: a CTA streams only the key tiles that one of its rows
 // can see (the sink tiles, then the window's), each query tile skips those of
 // them that it does not see itself, and a tile needs the per-element mask only
@@ -29,6 +32,7 @@
 
 #include "attn_window.cuh"
 #include "lcb_internal.h"
+#include "mma_warp.cuh"
 
 namespace lcb {
 namespace {
@@ -37,17 +41,20 @@ constexpr int kBM = 128;
 constexpr int kBN = 128;
 constexpr int kD = 128;
 constexpr int kStages = 4;
-constexpr int kThreads = 320;
+constexpr int kThreads = 320;  // 8 softmax warps, producer, MMA issuer
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
 constexpr uint32_t kTileBytes = kBN * kD * 2;  // 32 KB, two 16 KB halves of 64 columns
 constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kSmQ = 0;
 constexpr uint32_t kSmKV = 2 * kTileBytes;
 constexpr uint32_t kSmBar = kSmKV + kStages * kTileBytes;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kHeadGroup = 4;              // (b, h) pairs whose query blocks interleave in the CTA order
+constexpr float kRescaleThreshold = 32.0f;  // log2 units
+constexpr int kHeadGroup = 4;              // (b, h) pairs whose query blocks interleave in the item order
+constexpr int kSms = 152;
 
 struct Bars {
-  uint64_t q_full;
+  uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kStages];
   uint64_t kv_empty[kStages];
   uint64_t s_full[2];
@@ -63,7 +70,7 @@ struct Params {
   __nv_bfloat16* o;
   float* lse;
   long long o_rs, o_bs, l_hs, l_bs;
-  int B, H, G;
+  int B, H, G, items;
   WindowShape w;
   float scale_log2;
   DevStatus st;
@@ -73,15 +80,33 @@ constexpr uint32_t kWhere = 5u << 24;  // kernel id of timeout reports
 
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
-// The visits of a CTA's two query tiles: `all` is the stream of key tiles that
-// either one sees; query tile t takes part in visit i iff its own list has it.
+// Item k of the grid's work: 256 query rows from q0 of head h of batch b.
+// (b, h) pairs go in groups of kHeadGroup, a group's items latest query block
+// first with its heads interleaved: neighbours in time share K/V tiles in L2
+// (heads of one K/V head, blocks of one window).
+struct Item {
+  int b, h, q0;
+};
+
+__device__ __forceinline__ Item item_of(const Params& p, int k) {
+  const int nq = (p.w.Sq + 2 * kBM - 1) / (2 * kBM);
+  const int group = k / (nq * kHeadGroup);
+  const int g0 = group * kHeadGroup;
+  const int gsz = min(kHeadGroup, p.B * p.H - g0);
+  const int within = k - group * nq * kHeadGroup;
+  const int bh = g0 + within % gsz;
+  return {bh / p.H, bh % p.H, (nq - 1 - within / gsz) * 2 * kBM};
+}
+
+// The visits of an item's two query tiles: `all` is the stream of key tiles that
+// either one sees; query tile t takes part in visits [0, sinks[t]) and
+// [from[t], to[t]) of the n.
 struct Visits {
   KeyTiles all, own[2];
-  int n, last[2];  // visits of the stream; the last one of each query tile (-1: none)
-  __device__ __forceinline__ bool active(int t, int i) const {
-    const int kt = all.tile(i);
-    return i < n && (kt < own[t].ns || (kt >= own[t].lo && kt < own[t].hi));
-  }
+  int n, sinks[2], from[2], to[2];
+  __device__ __forceinline__ bool any(int t) const { return own[t].count() > 0; }
+  __device__ __forceinline__ bool active(int t, int i) const { return i < sinks[t] || (i >= from[t] && i < to[t]); }
+  __device__ __forceinline__ int last(int t) const { return to[t] > from[t] ? to[t] - 1 : sinks[t] - 1; }
 };
 
 __device__ __forceinline__ Visits visits(const WindowShape& w, int q0) {
@@ -90,44 +115,42 @@ __device__ __forceinline__ Visits visits(const WindowShape& w, int q0) {
   v.n = v.all.count();
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    v.own[t] = key_tiles(w, q0 + t * kBM, kBM);
-    const int kt = v.own[t].hi > v.own[t].lo ? v.own[t].hi - 1 : v.own[t].ns - 1;  // its last key tile
-    v.last[t] = kt < 0 ? -1 : (kt < v.all.ns ? kt : v.all.ns + kt - v.all.lo);
+    const KeyTiles k = v.own[t] = key_tiles(w, q0 + t * kBM, kBM);
+    auto visit = [&](int kt) { return kt <= v.all.ns ? kt : v.all.ns + kt - v.all.lo; };  // kt in the stream
+    v.sinks[t] = visit(k.ns);
+    v.from[t] = visit(k.lo);
+    v.to[t] = visit(k.hi);
+    if (k.ns == k.lo) v.sinks[t] = v.to[t];  // one stretch
   }
   return v;
 }
 
+// The columns of key tile kt that query tile `own` can use: all of a window
+// tile's, a sink tile's up to the last sink. The second product runs over
+// these alone, in steps of 16.
+__device__ __forceinline__ int used_columns(const WindowShape& w, const KeyTiles& own, int kt) {
+  return kt < own.ns ? min(kBN, w.sinks - kt * kBN) : kBN;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     attn_window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                           const __grid_constant__ CUtensorMap tm_v, const Params p) {
+                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   Bars* bars = reinterpret_cast<Bars*>(smem + kSmBar);
   volatile int* abort_flag = &bars->abort;
-  const int warp = static_cast<int>(warp_id());
+  const int warp = static_cast<int>(uniform(warp_id()));
   const int lane = static_cast<int>(lane_id());
 
-  // (b, h) pairs go in groups of kHeadGroup, a group's CTAs latest query block
-  // first with its heads interleaved: neighbours in time share K/V tiles in L2
-  // (heads of one K/V head, blocks of one window), and the short first blocks
-  // of the sequence end the grid.
-  const int nq = (p.w.Sq + 2 * kBM - 1) / (2 * kBM);
-  const int group = static_cast<int>(blockIdx.x) / (nq * kHeadGroup);
-  const int g0 = group * kHeadGroup;
-  const int gsz = min(kHeadGroup, p.B * p.H - g0);
-  const int within = static_cast<int>(blockIdx.x) - group * nq * kHeadGroup;
-  const int bh = g0 + within % gsz;
-  const int b = bh / p.H, h = bh % p.H;
-  const int q0 = (nq - 1 - within / gsz) * 2 * kBM;
-
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->kv_full[s], 1);
       mbar_init(&bars->kv_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_full[t], 1);
+      mbar_init(&bars->q_empty[t], 1);
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->p_full[t], 128);
       mbar_init(&bars->o_full[t], 1);
@@ -136,11 +159,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bars->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kProducerWarp && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -150,218 +173,254 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = bars->tmem_base;
 
-  if (warp == 8) {
+  // Every role walks the same items; barrier phases carry on from one to the
+  // next (ring slots by a running count, the others by one count per query tile).
+  if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
-    const Visits v = visits(p.w, q0);
-    if (lane == 0 && v.n > 0) {
+    if (lane == 0) {
       const uint64_t pol = l2_policy_evict_last();
-      const int xq = h * kD, xk = (h / p.G) * kD;
-      const uint32_t tiles = (v.last[0] >= 0 ? 1u : 0u) + (v.last[1] >= 0 ? 1u : 0u);
-      mbar_arrive_expect_tx(&bars->q_full, tiles * kTileBytes);
-      for (int t = 0; t < 2; ++t) {
-        if (v.last[t] < 0) continue;
-        for (int half = 0; half < 2; ++half)
-          tma_load_3d(smem + kSmQ + t * kTileBytes + half * kHalfBytes, &tm_q, &bars->q_full, xq + half * 64,
-                      q0 + t * kBM, b);
-      }
-      int it = 0;
+      int it = 0;              // K and V tiles loaded
+      uint32_t nq[2] = {0, 0};  // Q tiles loaded
       bool ok = true;
-      for (int i = 0; i < v.n && ok; ++i) {
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int slot = it % kStages;
-          const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
-          if (!mbar_wait(&bars->kv_empty[slot], ph ^ 1u, abort_flag, p.st, kWhere | (1u << 16))) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&bars->kv_full[slot], kTileBytes);
-          const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
+      for (int k = static_cast<int>(blockIdx.x); k < p.items && ok; k += static_cast<int>(gridDim.x)) {
+        const Item w = item_of(p, k);
+        const Visits v = visits(p.w, w.q0);
+        const int xq = w.h * kD, xk = (w.h / p.G) * kD;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (!v.any(t)) continue;
+          ok = mbar_wait(&bars->q_empty[t], (nq[t] & 1u) ^ 1u, abort_flag, p.st, kWhere | (7u << 16));
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars->q_full[t], kTileBytes);
           for (int half = 0; half < 2; ++half)
-            tma_load_3d_hint(smem + kSmKV + slot * kTileBytes + half * kHalfBytes, map, &bars->kv_full[slot],
-                             xk + half * 64, v.all.tile(i) * kBN, b, pol);
+            tma_load_3d(smem + kSmQ + t * kTileBytes + half * kHalfBytes, &tm_q, &bars->q_full[t], xq + half * 64,
+                        w.q0 + t * kBM, w.b);
+          ++nq[t];
+        }
+        for (int i = 0; i < v.n && ok; ++i) {
+          for (int kv = 0; kv < 2; ++kv, ++it) {
+            const int slot = it % kStages;
+            const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
+            if (!mbar_wait(&bars->kv_empty[slot], ph ^ 1u, abort_flag, p.st, kWhere | (1u << 16))) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&bars->kv_full[slot], kTileBytes);
+            const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
+            for (int half = 0; half < 2; ++half)
+              tma_load_3d_hint(smem + kSmKV + slot * kTileBytes + half * kHalfBytes, map, &bars->kv_full[slot],
+                               xk + half * 64, v.all.tile(i) * kBN, w.b, pol);
+          }
         }
       }
       if (!ok) {
         // Let every copy already issued land before the CTA can exit.
-        drain_wait(&bars->q_full, 0, p.st.limit);
-        for (int k = max(0, it - kStages); k < it; ++k)
-          drain_wait(&bars->kv_full[k % kStages], static_cast<uint32_t>(k / kStages) & 1u, p.st.limit);
+        for (int t = 0; t < 2; ++t)
+          if (nq[t] > 0) drain_wait(&bars->q_full[t], (nq[t] - 1) & 1u, p.st.limit);
+        for (int j = max(0, it - kStages); j < it; ++j)
+          drain_wait(&bars->kv_full[j % kStages], static_cast<uint32_t>(j / kStages) & 1u, p.st.limit);
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    const Visits v = visits(p.w, q0);
-    if (lane == 0 && v.n > 0) {
-      const uint32_t idesc_qk = idesc_bf16(kBM, kBN, false, false);
-      const uint32_t idesc_pv = idesc_bf16(kBM, kD, false, true);
-      auto issue_qk = [&](int t, int slot) {
-        const uint64_t qa = sdesc_sw128(sbase + kSmQ + t * kTileBytes, 16, 1024);
-        const uint64_t kb = sdesc_sw128(sbase + kSmKV + slot * kTileBytes, 16, 1024);
+    // All lanes walk the loop, one elected lane issues.
+    const uint32_t one = elect_one();
+    const uint32_t tm = uniform(tbase);
+    const uint32_t idesc_qk = idesc_bf16(kBM, kBN, false, false);
+    const uint32_t idesc_pv = idesc_bf16(kBM, kD, false, true);
+    const uint64_t q_desc = sdesc_sw128(sbase + kSmQ, 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(sbase + kSmKV, 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(sbase + kSmKV + kTileBytes, kHalfBytes, 1024);
+    // Visit g of the CTA has K in ring slot 2 (g & 1) and V in the slot after it.
+    auto issue_qk = [&](int t, uint32_t g) {
+      const uint64_t qa = sdesc_advance(q_desc, t * kTileBytes), kb = sdesc_advance(k_desc, (g & 1u) * 2 * kTileBytes);
 #pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-          mma_ss(tbase + t * 128, sdesc_advance(qa, off), sdesc_advance(kb, off), idesc_qk, kk > 0);
-        }
-        tc_commit(&bars->s_full[t]);
-      };
-      auto issue_pv = [&](int t, int slot, bool acc) {
-        const uint64_t vb = sdesc_sw128(sbase + kSmKV + slot * kTileBytes, kHalfBytes, 1024);
+      for (int kk = 0; kk < kD / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+        mma_ss_if(tm + t * 128, sdesc_advance(qa, off), sdesc_advance(kb, off), idesc_qk, kk > 0, one);
+      }
+      tc_commit_if(&bars->s_full[t], one);
+    };
+    auto issue_pv = [&](int t, uint32_t g, uint32_t acc, int cols) {
+      const uint64_t vb = sdesc_advance(v_desc, (g & 1u) * 2 * kTileBytes);
+      if (cols == kBN) {
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
-          mma_ts(tbase + 256 + t * 128, tbase + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv,
-                 (acc || kk > 0));
-      };
-      auto wait_kv = [&](int it) {
-        const bool r = mbar_wait(&bars->kv_full[it % kStages], static_cast<uint32_t>(it / kStages) & 1u, abort_flag,
-                                 p.st, kWhere | (3u << 16));
-        tc_fence_after();
-        return r;
-      };
-      int done[2] = {0, 0};  // products P V issued per query tile
-      bool ok = mbar_wait(&bars->q_full, 0, abort_flag, p.st, kWhere | (2u << 16));
-      if (ok) ok = wait_kv(0);
-      if (ok) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (v.active(t, 0)) issue_qk(t, 0);
-        tc_commit(&bars->kv_empty[0]);
+          mma_ts_if(tm + 256 + t * 128, tm + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv,
+                    kk > 0 ? 1u : acc, one);
+      } else {
+#pragma unroll 1
+        for (int kk = 0; kk * 16 < cols; ++kk)
+          mma_ts_if(tm + 256 + t * 128, tm + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv,
+                    kk > 0 ? 1u : acc, one);
       }
-      for (int i = 0; i < v.n && ok; ++i) {
-        const int itV = 2 * i + 1, itK = 2 * i + 2;
-        const int sV = itV % kStages, sK = itK % kStages;
-        ok = wait_kv(itV);
+    };
+    auto wait_kv = [&](uint32_t g, int v) {
+      const bool r = mbar_wait_warp(&bars->kv_full[2 * (g & 1u) + v], (g >> 1) & 1u, abort_flag, p.st,
+                                    kWhere | (3u << 16));
+      tc_fence_after();
+      return r;
+    };
+    uint32_t g = 0;  // visits of the items before, and of this one
+    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    bool ok = true;
+    for (int k = static_cast<int>(blockIdx.x); k < p.items && ok; k += static_cast<int>(gridDim.x)) {
+      const Item w = item_of(p, k);
+      const Visits v = visits(p.w, w.q0);
+      if (v.n == 0) continue;
+      uint32_t acc[2] = {0, 0};
+      ok = wait_kv(g, 0);
+      // First products. S_t is free: the previous item's last P V of tile t was issued before.
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || !v.any(t)) continue;
+        ok = mbar_wait_warp(&bars->q_full[t], q_phase[t], abort_flag, p.st, kWhere | (2u << 16));
+        if (!ok) continue;
+        q_phase[t] ^= 1u;
+        tc_fence_after();
+        if (v.active(t, 0)) {
+          issue_qk(t, g);
+          if (v.last(t) == 0) tc_commit_if(&bars->q_empty[t], one);
+        }
+      }
+      if (!ok) break;
+      tc_commit_if(&bars->kv_empty[2 * (g & 1u)], one);
+      for (int i = 0; i < v.n && ok; ++i, ++g) {
+        ok = wait_kv(g, 1);
         if (!ok) break;
         bool k_ready = false;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok) continue;
           if (v.active(t, i)) {
-            ok = mbar_wait(&bars->p_full[t], static_cast<uint32_t>(done[t]) & 1u, abort_flag, p.st,
-                           kWhere | (4u << 16));
+            // P is in TMEM; for an item's first visit its rows have also read the previous item's O
+            ok = mbar_wait_warp(&bars->p_full[t], p_phase[t], abort_flag, p.st, kWhere | (4u << 16));
             if (!ok) continue;
+            p_phase[t] ^= 1u;
             tc_fence_after();
-            issue_pv(t, sV, done[t] > 0);
-            ++done[t];
-            if (i == v.last[t]) tc_commit(&bars->o_full[t]);
+            issue_pv(t, g, acc[t], used_columns(p.w, v.own[t], v.all.tile(i)));
+            acc[t] = 1;
+            if (i == v.last(t)) tc_commit_if(&bars->o_full[t], one);
           }
           if (v.active(t, i + 1)) {  // S over P once the product above has read it (issue order)
             if (!k_ready) {
-              ok = wait_kv(itK);
+              ok = wait_kv(g + 1, 0);
               if (!ok) continue;
               k_ready = true;
             }
-            issue_qk(t, sK);
+            issue_qk(t, g + 1);
+            if (i + 1 == v.last(t)) tc_commit_if(&bars->q_empty[t], one);
           }
         }
         if (!ok) break;
-        tc_commit(&bars->kv_empty[sV]);
-        if (i + 1 < v.n) tc_commit(&bars->kv_empty[sK]);
+        tc_commit_if(&bars->kv_empty[2 * (g & 1u) + 1], one);
+        if (i + 1 < v.n) tc_commit_if(&bars->kv_empty[2 * ((g + 1) & 1u)], one);
       }
-      // Every MMA issued must finish before TMEM is released.
-      tc_commit(&bars->mma_done);
-      drain_wait(&bars->mma_done, 0, p.st.limit);
     }
+    // Every MMA issued must finish before TMEM is released.
+    tc_commit_if(&bars->mma_done, one);
+    drain_wait(&bars->mma_done, 0, p.st.limit);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2;
     const int row = threadIdx.x & 127;
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tbase + t * 128 + lane_off;
-    const uint32_t tO = tbase + 256 + t * 128 + lane_off;
-    const int qi = q0 + t * kBM + row;
-    const int pos = p.w.pos0 + qi;
-    const int p_first = p.w.pos0 + q0 + t * kBM, p_last = p_first + kBM - 1;
+    const uint32_t tS = tbase + t * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tO = tS + 256;
     const float c = p.scale_log2;
-    float m = -INFINITY, l = 0.f;
+    uint32_t s_phase = 0, o_phase = 0;
     bool ok = true;
-    const KeyTiles own = key_tiles(p.w, q0 + t * kBM, kBM);
-    const int cnt = own.count();
-    for (int i = 0; i < cnt; ++i) {
-      ok = warp_all(mbar_wait(&bars->s_full[t], static_cast<uint32_t>(i) & 1u, abort_flag, p.st,
-                              kWhere | (5u << 16)));
+    for (int k = static_cast<int>(blockIdx.x); k < p.items; k += static_cast<int>(gridDim.x)) {
+      const int q0 = item_of(p, k).q0 + t * kBM;
+      const KeyTiles own = key_tiles(p.w, q0, kBM);
+      const int cnt = own.count();
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < cnt; ++i, s_phase ^= 1u) {
+        ok = warp_all(mbar_wait(&bars->s_full[t], s_phase, abort_flag, p.st, kWhere | (5u << 16)));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+        tmem_ld_x128(tS, s);
+        const int kbase = own.tile(i) * kBN;
+        const int p_first = p.w.pos0 + q0;
+        const bool whole = kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
+                           (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks);
+        if (!whole) {
+          // The mask cuts this tile: the row sees columns [from, to], and those before `sink` up to `to`.
+          const int pos = p_first + row;
+          const int to = min(pos, p.w.Sk - 1) - kbase;
+          const int from = pos - p.w.window + 1 - kbase;
+          const int sink = p.w.sinks - kbase;
+          if (sink > 0) {
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (e > to || (e < from && e >= sink)) s[e] = __float_as_uint(-INFINITY);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (e > to || e < from) s[e] = __float_as_uint(-INFINITY);
+          }
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; e += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            m4[u] = fmax3(m4[u], __uint_as_float(s[e + 2 * u]), __uint_as_float(s[e + 2 * u + 1]));
+        const float m_new = fmaxf(m, fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c);
+        const bool fresh = m == -INFINITY;  // nothing seen so far: O and l are 0, whatever the maximum
+        const bool resc = !fresh && m_new > m + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, resc)) {
+          // O in pieces of 16 columns: beside the 128 scores, larger ones would not fit the registers
+          const float alpha = resc ? ex2_approx(m - m_new) : 1.0f;
+#pragma unroll 1
+          for (int ch = 0; ch < 8; ++ch) {
+            uint32_t o[16];
+            tmem_ld_x16(tO + ch * 16, o);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+            tmem_st_x16(tO + ch * 16, o);
+          }
+          if (resc) l *= alpha;
+        }
+        if (fresh || resc) m = m_new;
+        // P is rounded to bf16 for the second product (half a step, 2^-9 of each weight, of either sign); l sums it
+        // in fp32.
+        const float neg_m = (m == -INFINITY) ? 0.f : -m;
+        float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            const int e = 64 * hf + 2 * u;
+            float x0, x1;
+            ffma2(x0, x1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), c, c, neg_m, neg_m);
+            const float p0 = ex2_approx(x0);
+            const float p1 = ex2_approx(x1);
+            if (u & 1)
+              fadd2(sb0, sb1, sb0, sb1, p0, p1);
+            else
+              fadd2(sa0, sa1, sa0, sa1, p0, p1);
+            pk[u] = pack_bf16x2(p0, p1);
+          }
+          tmem_st_x32(tS + 32 * hf, pk);
+        }
+        l += (sa0 + sb0) + (sa1 + sb1);
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[t]);
+      }
+      if (ok && cnt > 0) {
+        ok = warp_all(mbar_wait(&bars->o_full[t], o_phase, abort_flag, p.st, kWhere | (6u << 16)));
+        o_phase ^= 1u;
+      }
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[128];
-      tmem_ld_x128(tS, s);
-      const int kbase = own.tile(i) * kBN;
-      const bool whole = kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
-                         (p_last - kbase < p.w.window || kbase + kBN <= p.w.sinks);
-      if (!whole) {
-        // columns [from, to] are visible, and those before `sink` up to `to`
-        const int to = min(pos, p.w.Sk - 1) - kbase;
-        const int from = pos - p.w.window + 1 - kbase;
-        const int sink = p.w.sinks - kbase;
-        if (sink > 0) {
-#pragma unroll
-          for (int cc = 0; cc < 128; ++cc)
-            if (cc > to || (cc < from && cc >= sink)) s[cc] = __float_as_uint(-INFINITY);
-        } else {
-#pragma unroll
-          for (int cc = 0; cc < 128; ++cc)
-            if (cc > to || cc < from) s[cc] = __float_as_uint(-INFINITY);
-        }
-      }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int cc = 0; cc < 128; cc += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          m4[k] = fmax3(m4[k], __uint_as_float(s[cc + 2 * k]), __uint_as_float(s[cc + 2 * k + 1]));
-      const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-      const float m_new = fmaxf(m, mx * c);
-      if (i == 0) {
-        m = m_new;
-      } else {
-        const bool resc = m_new > m + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, resc)) {
-          const float alpha = resc ? ex2_approx(m - m_new) : 1.0f;
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t o[32];
-            tmem_ld_x32(tO + ch * 32, o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st_x32(tO + ch * 32, o);
-          }
-          if (resc) {
-            l *= alpha;
-            m = m_new;
-          }
-        }
-      }
-      const float neg_m = (m == -INFINITY) ? 0.f : -m;
-      // P is rounded to bf16 for the second product (half a step, 2^-9 of each weight, of either sign); l keeps fp32
-      float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int e = 64 * hf + 2 * k;
-          float x0, x1;
-          ffma2(x0, x1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), c, c, neg_m, neg_m);
-          const float p0 = ex2_approx(x0);
-          const float p1 = ex2_approx(x1);
-          if (k & 1)
-            fadd2(sb0, sb1, sb0, sb1, p0, p1);
-          else
-            fadd2(sa0, sa1, sa0, sa1, p0, p1);
-          pk[k] = pack_bf16x2(p0, p1);
-        }
-        tmem_st_x32(tS + 32 * hf, pk);
-      }
-      l += (sa0 + sb0) + (sa1 + sb1);
-      tc_fence_before();
-      mbar_arrive(&bars->p_full[t]);
-    }
-    if (ok && cnt > 0) ok = warp_all(mbar_wait(&bars->o_full[t], 0, abort_flag, p.st, kWhere | (6u << 16)));
-    if (ok) {
-      tc_fence_after();
+      const Item w = item_of(p, k);
+      const int qi = w.q0 + t * kBM + row;
       const bool valid = qi < p.w.Sq;
       const float inv_l = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* dst = p.o + b * p.o_bs + static_cast<long long>(qi) * p.o_rs + h * kD;
+      __nv_bfloat16* dst = p.o + w.b * p.o_bs + static_cast<long long>(qi) * p.o_rs + w.h * kD;
 #pragma unroll
       for (int ch = 0; ch < 4; ++ch) {
         uint32_t o[32];
@@ -369,28 +428,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_x32(tO + ch * 32, o);
         } else {  // no key for any row of this tile: O was never formed
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
         }
         if (valid) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(o[k]) * inv_l, __uint_as_float(o[k + 1]) * inv_l);
-            w.y = pack_bf16x2(__uint_as_float(o[k + 2]) * inv_l, __uint_as_float(o[k + 3]) * inv_l);
-            w.z = pack_bf16x2(__uint_as_float(o[k + 4]) * inv_l, __uint_as_float(o[k + 5]) * inv_l);
-            w.w = pack_bf16x2(__uint_as_float(o[k + 6]) * inv_l, __uint_as_float(o[k + 7]) * inv_l);
-            *reinterpret_cast<uint4*>(dst + ch * 32 + k) = w;
+          for (int j = 0; j < 32; j += 8) {
+            uint4 u;
+            u.x = pack_bf16x2(__uint_as_float(o[j]) * inv_l, __uint_as_float(o[j + 1]) * inv_l);
+            u.y = pack_bf16x2(__uint_as_float(o[j + 2]) * inv_l, __uint_as_float(o[j + 3]) * inv_l);
+            u.z = pack_bf16x2(__uint_as_float(o[j + 4]) * inv_l, __uint_as_float(o[j + 5]) * inv_l);
+            u.w = pack_bf16x2(__uint_as_float(o[j + 6]) * inv_l, __uint_as_float(o[j + 7]) * inv_l);
+            *reinterpret_cast<uint4*>(dst + ch * 32 + j) = u;
           }
         }
       }
       if (valid)
-        p.lse[b * p.l_bs + h * p.l_hs + qi] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+        p.lse[w.b * p.l_bs + w.h * p.l_hs + qi] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+      tc_fence_before();  // O is read: the next item's first P V (after this tile's next p_full) may overwrite it
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
@@ -420,9 +480,11 @@ int launch_window_fwd(const WindowFwd& a, cudaStream_t stream) {
   p.w = a.w;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.st = a.st;
-  const long long grid = static_cast<long long>((a.w.Sq + 2 * kBM - 1) / (2 * kBM)) * a.B * a.H;
-  if (grid > 0x7fffffffLL) return -1;
-  attn_window_fwd_kernel<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(tq, tk, tv, p);
+  const long long items = static_cast<long long>((a.w.Sq + 2 * kBM - 1) / (2 * kBM)) * a.B * a.H;
+  if (items > 0x7fffffffLL - kSms) return -1;
+  p.items = static_cast<int>(items);
+  attn_window_fwd_kernel<<<static_cast<unsigned>(std::min<long long>(items, kSms)), kThreads, kSmemBytes, stream>>>(
+      tq, tk, tv, p);
   return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 

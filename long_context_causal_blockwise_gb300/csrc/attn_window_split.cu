@@ -29,6 +29,8 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 
 #include "lcb_internal.h"
 
@@ -38,10 +40,8 @@ namespace lcb {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kKeys = 16;            // keys per warp step
-constexpr int kMaxCluster = 16;
+constexpr int kKeys = 16;  // keys per warp step
+constexpr int kMaxCluster = 16;  // above 8 the size is not portable, but allowed on request
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum is raised lazily, P stays <= 256
 
@@ -71,13 +71,20 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
 // Weight of a partial with maximum m in a sum with maximum M >= m (both -inf: the partial is empty, or NaN).
 __device__ __forceinline__ float weight(float m, float M) { return m == M ? 1.f : ex2_approx(m - M); }
 
-// NT: 8-row tiles of query rows (1 or 2).
-template <int NT>
-__global__ void __launch_bounds__(kThreads) window_split_kernel(const __grid_constant__ WindowSplit p) {
+// A CTA's shared memory: its warps' partials, joined into slot 0, cM and cL.
+template <int kRows, int kWarps>
+struct Partials {
+  float O[kWarps][kRows][kD];
+  float M[kWarps][kRows], L[kWarps][kRows];
+  float cM[kRows], cL[kRows];
+};
+
+// NT: 8-row tiles of query rows (1 or 2); kWarps: warps of a CTA.
+template <int NT, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) window_split_kernel(const __grid_constant__ WindowSplit p) {
   constexpr int kRows = 8 * NT;
-  __shared__ __align__(16) float sO[kWarps][kRows][kD];
-  __shared__ float sM[kWarps][kRows], sL[kWarps][kRows];
-  __shared__ float cM[kRows], cL[kRows];
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  auto& [sO, sM, sL, cM, cL] = *reinterpret_cast<Partials<kRows, kWarps>*>(smem_raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % p.cluster;
@@ -319,33 +326,106 @@ __global__ void __launch_bounds__(kThreads) window_split_kernel(const __grid_con
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-template <int NT>
-int launch(const WindowSplit& p, long long grid, cudaStream_t stream) {
-  const void* fn = reinterpret_cast<const void*>(window_split_kernel<NT>);
-  if (p.cluster > 8) {  // above the portable cluster size
+template <int NT, int kWarps>
+struct Form {
+  static constexpr int kSmem = sizeof(Partials<8 * NT, kWarps>);
+  static const void* fn() { return reinterpret_cast<const void*>(window_split_kernel<NT, kWarps>); }
+
+  static cudaLaunchConfig_t config(cudaLaunchAttribute* at, int cluster, long long tiles, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * cluster));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    at->id = cudaLaunchAttributeClusterDimension;
+    at->val.clusterDim.x = static_cast<unsigned>(cluster);
+    at->val.clusterDim.y = 1;
+    at->val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cfg;
+  }
+
+  // Per device context: clusters above 8 CTAs and this form's shared memory allowed.
+  static int allow() {
     static DeviceOnce once;
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) return -4;
-    const int rc = once.run(
+    return once.run(
         dev, current_context_id(),
-        [&] {
-          return cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess ? 0 : -4;
+        [] {
+          return cudaFuncSetAttribute(fn(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                         cudaFuncSetAttribute(fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
+                     ? 0
+                     : -4;
         },
         -4);
-    if (rc != 0) return rc;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, window_split_kernel<NT>, p) == cudaSuccess ? 0 : -4;
+
+  // Clusters of this size that the GPU holds at once (a property of the device model, asked for once), or 0.
+  static int resident(int cluster) {
+    static std::atomic<int> known[kMaxCluster + 1];  // 0: not asked yet; n + 1
+    int n = known[cluster].load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchAttribute at;
+      const cudaLaunchConfig_t cfg = config(&at, cluster, 1, nullptr);
+      int got = 0;
+      if (cudaOccupancyMaxActiveClusters(&got, fn(), &cfg) != cudaSuccess) {
+        cudaGetLastError();  // such clusters do not fit: not an error of the call
+        got = 0;
+      }
+      known[cluster].store(n = got + 1, std::memory_order_relaxed);
+    }
+    return n - 1;
+  }
+
+  // The largest cluster with which all tiles are resident at once, every warp having a step; 0 if none.
+  static int one_wave(long long tiles, long long steps) {
+    for (int c = static_cast<int>(std::min<long long>(kMaxCluster, std::max<long long>(1, steps / kWarps))); c > 0; --c)
+      if (resident(c) >= tiles) return c;
+    return 0;
+  }
+
+  static int launch(const WindowSplit& p, long long tiles, cudaStream_t stream) {
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = config(&at, p.cluster, tiles, stream);
+    return cudaLaunchKernelEx(&cfg, window_split_kernel<NT, kWarps>, p) == cudaSuccess ? 0 : -4;
+  }
+};
+
+// How many CTAs and warps share a tile's keys. All CTAs resident at once beats
+// any second wave, and more warps in flight beat fewer: of the forms with 2, 4
+// and 8 warps a CTA take the one that puts most warps on the GPU in one wave
+// (the smaller CTA where they tie: it fills the SMs more evenly). Four 32K-key
+// windows x 40 heads, us by cluster of two-warp CTAs: 4: 388, 5: 363, 6 (a
+// second wave): 459; one 2K-key window x 32 heads: two warps x 16: 12.3, four
+// warps x 12: 10.8, four x 16 (a second wave): 18.
+template <int NT>
+int launch_rows(WindowSplit& p, long long tiles, long long steps, cudaStream_t stream) {
+  int rc;
+  if ((rc = Form<NT, 2>::allow()) != 0 || (rc = Form<NT, 4>::allow()) != 0 || (rc = Form<NT, 8>::allow()) != 0)
+    return rc;
+  const int c2 = Form<NT, 2>::one_wave(tiles, steps), c4 = Form<NT, 4>::one_wave(tiles, steps),
+            c8 = Form<NT, 8>::one_wave(tiles, steps);
+  if (2 * c2 >= 4 * c4 && 2 * c2 >= 8 * c8) {
+    p.cluster = std::max(1, c2);
+    if (c2 == 0) {
+      // More tiles than fit at once: the cluster (up to 8) whose last wave is fullest.
+      double best = 0;
+      for (int c = 1; c <= 8 && 2 * c <= std::max<long long>(2, steps); ++c) {
+        const double waves = static_cast<double>(tiles) / std::max(1, Form<NT, 2>::resident(c));
+        const double full = waves / std::ceil(waves);
+        if (full > best + 0.02) best = full, p.cluster = c;
+      }
+    }
+    return Form<NT, 2>::launch(p, tiles, stream);
+  }
+  if (4 * c4 >= 8 * c8) {
+    p.cluster = c4;
+    return Form<NT, 4>::launch(p, tiles, stream);
+  }
+  p.cluster = c8;
+  return Form<NT, 8>::launch(p, tiles, stream);
 }
 
 }  // namespace
@@ -356,15 +436,10 @@ int launch_window_split(WindowSplit p, cudaStream_t stream) {
   p.row_tiles = (R + rows - 1) / rows;
   // Most keys that a row tile can see, from the host's side of the sizes.
   const long long seen = std::min<long long>(p.Sk, static_cast<long long>(p.window) + p.T - 1 + p.sinks);
-  const long long tiles = static_cast<long long>(p.B) * p.Hkv * p.row_tiles;
-  // CTAs per tile: while there are fewer than eight CTAs an SM, and each keeps two steps a warp.
-  p.cluster = 1;
-  while (p.cluster < kMaxCluster && tiles * p.cluster < 152 * 8 && seen > 2LL * p.cluster * 2 * kKeys * kWarps)
-    p.cluster *= 2;
-  const long long grid = tiles * p.cluster;
-  if (grid > 0x7fffffffLL) return -1;
-  if (grid == 0) return 0;
-  return rows == 8 ? launch<1>(p, grid, stream) : launch<2>(p, grid, stream);
+  const long long tiles = static_cast<long long>(p.B) * p.Hkv * p.row_tiles, steps = (seen + kKeys - 1) / kKeys;
+  if (tiles > 0x7fffffffLL / kMaxCluster) return -1;
+  if (tiles == 0) return 0;
+  return rows == 8 ? launch_rows<1>(p, tiles, steps, stream) : launch_rows<2>(p, tiles, steps, stream);
 }
 
 }  // namespace lcb
