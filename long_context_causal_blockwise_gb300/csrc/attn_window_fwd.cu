@@ -19,10 +19,17 @@
 // it. Work is 4 * 128 flops a visible pair plus the hidden part of the cut
 // tiles, at most two per query tile and edge.
 //
-//   warp 8      TMA producer
-//   warp 9      MMA issuer (one thread), owner of the TMEM allocation
+// A CTA stays and walks over its share of the (head, 256 rows) items, each role
+// on its own: the producer loads and the tensor core starts the next item while
+// the epilogue warps still write the last one's O, so an item's start and end
+// hide behind its neighbours (8K tokens, window 1024: 158 us with the epilogue
+// in the softmax warps, 168 with a CTA per item).
+//
 //   warps 0-3   softmax of query tile 0 (thread = query row = TMEM lane)
 //   warps 4-7   softmax of query tile 1
+//   warps 8-11  epilogue of both
+//   warp 12     TMA producer
+//   warp 13     MMA issuer, owner of the TMEM allocation (14 and 15 fill the warpgroup)
 //
 // TMEM (512 columns x 128 lanes, fp32): S_0 [0,128), S_1 [128,256),
 // O_0 [256,384), O_1 [384,512).
@@ -41,16 +48,22 @@ constexpr int kBM = 128;
 constexpr int kBN = 128;
 constexpr int kD = 128;
 constexpr int kStages = 4;
-constexpr int kThreads = 320;  // 8 softmax warps, producer, MMA issuer
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
+constexpr int kThreads = 512;  // four warpgroups
+constexpr int kEpilogueWarp = 8;
+constexpr int kProducerWarp = 12;
+constexpr int kMmaWarp = 13;
+// Registers a thread: the block is launched with 128 each; the softmax
+// warpgroups' 128 scores want more, and 2 * 168 + 2 * 88 = 4 * 128.
+constexpr int kSoftmaxRegs = 168;
+constexpr int kOtherRegs = 88;
 constexpr uint32_t kTileBytes = kBN * kD * 2;  // 32 KB, two 16 KB halves of 64 columns
 constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kSmQ = 0;
 constexpr uint32_t kSmKV = 2 * kTileBytes;
-constexpr uint32_t kSmBar = kSmKV + kStages * kTileBytes;
+constexpr uint32_t kSmRow = kSmKV + kStages * kTileBytes;  // (m, l) of each query row
+constexpr uint32_t kSmBar = kSmRow + 2 * kBM * 8;
 constexpr float kRescaleThreshold = 32.0f;  // log2 units
-constexpr int kHeadGroup = 4;              // (b, h) pairs whose query blocks interleave in the item order
+constexpr long long kGroupBytes = 80LL << 20;  // K and V of the windows that a group of heads keeps in L2
 constexpr int kSms = 152;
 
 struct Bars {
@@ -59,7 +72,8 @@ struct Bars {
   uint64_t kv_empty[kStages];
   uint64_t s_full[2];
   uint64_t p_full[2];
-  uint64_t o_full[2];
+  uint64_t o_full[2], o_free[2];
+  uint64_t row_full[2], row_free[2];  // (m, l) of a finished query tile
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
@@ -70,7 +84,7 @@ struct Params {
   __nv_bfloat16* o;
   float* lse;
   long long o_rs, o_bs, l_hs, l_bs;
-  int B, H, G, items;
+  int B, H, G, items, head_group;
   WindowShape w;
   float scale_log2;
   DevStatus st;
@@ -78,24 +92,27 @@ struct Params {
 
 constexpr uint32_t kWhere = 5u << 24;  // kernel id of timeout reports
 
-__device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
-
 // Item k of the grid's work: 256 query rows from q0 of head h of batch b.
-// (b, h) pairs go in groups of kHeadGroup, a group's items latest query block
-// first with its heads interleaved: neighbours in time share K/V tiles in L2
-// (heads of one K/V head, blocks of one window).
+// (b, h) pairs go in groups (as many as keep their windows' K and V in L2), a
+// group's items query block by query block with its heads interleaved. Blocks
+// come latest first, and first to last in every other group counted from the
+// end: where the window spans much of the sequence later blocks cost more, and
+// CTA c, which takes items c, c + 152, ..., then meets no jump between groups
+// and ends on the cheap ones.
 struct Item {
   int b, h, q0;
 };
 
 __device__ __forceinline__ Item item_of(const Params& p, int k) {
   const int nq = (p.w.Sq + 2 * kBM - 1) / (2 * kBM);
-  const int group = k / (nq * kHeadGroup);
-  const int g0 = group * kHeadGroup;
-  const int gsz = min(kHeadGroup, p.B * p.H - g0);
-  const int within = k - group * nq * kHeadGroup;
+  const int group = k / (nq * p.head_group);
+  const int g0 = group * p.head_group;
+  const int gsz = min(p.head_group, p.B * p.H - g0);
+  const int within = k - group * nq * p.head_group;
   const int bh = g0 + within % gsz;
-  return {bh / p.H, bh % p.H, (nq - 1 - within / gsz) * 2 * kBM};
+  const int at = within / gsz;
+  const int groups = (p.B * p.H + p.head_group - 1) / p.head_group;
+  return {bh / p.H, bh % p.H, ((groups - group) & 1 ? nq - 1 - at : at) * 2 * kBM};
 }
 
 // The visits of an item's two query tiles: `all` is the stream of key tiles that
@@ -132,6 +149,127 @@ __device__ __forceinline__ int used_columns(const WindowShape& w, const KeyTiles
   return kt < own.ns ? min(kBN, w.sinks - kt * kBN) : kBN;
 }
 
+// Raises the running maximum m to m_new where that passes it by more than the
+// threshold, and rescales l and O (TMEM, 256 columns after S) with it. A row
+// that has seen nothing yet takes m_new as it is: its l and O are 0.
+__device__ __forceinline__ void raise_max(uint32_t tS, float& m, float& l, float m_new) {
+  const bool fresh = m == -INFINITY;
+  const bool resc = !fresh && m_new > m + kRescaleThreshold;
+  if (__any_sync(0xffffffffu, resc)) {
+    // O in pieces of 16 columns: beside the 128 scores, larger ones would not fit the registers
+    const float alpha = resc ? ex2_approx(m - m_new) : 1.0f;
+#pragma unroll 1
+    for (int ch = 0; ch < 8; ++ch) {
+      uint32_t o[16];
+      tmem_ld_x16(tS + 256 + ch * 16, o);
+#pragma unroll
+      for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+      tmem_st_x16(tS + 256 + ch * 16, o);
+    }
+    if (resc) l *= alpha;
+  }
+  if (fresh || resc) m = m_new;
+}
+
+// P of 16 pairs of scores (bf16 pairs into pk), their sum into (s0, s1). P is
+// rounded to bf16 for the second product (half a step, 2^-9 of each weight, of
+// either sign); the sum is fp32.
+__device__ __forceinline__ void weights(const uint32_t* s, uint32_t* pk, float c, float neg_m, float& s0, float& s1) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    float x0, x1;
+    ffma2(x0, x1, __uint_as_float(s[2 * u]), __uint_as_float(s[2 * u + 1]), c, c, neg_m, neg_m);
+    const float p0 = ex2_approx(x0);
+    const float p1 = ex2_approx(x1);
+    fadd2(s0, s1, s0, s1, p0, p1);
+    pk[u] = pack_bf16x2(p0, p1);
+  }
+}
+
+// One score tile of a row, all of it visible: P over S in TMEM, m and l brought up.
+__device__ __forceinline__ void softmax_whole(uint32_t tS, float c, float& m, float& l) {
+  uint32_t s[128];
+  tmem_ld_x64(tS, *reinterpret_cast<uint32_t(*)[64]>(s));
+  tmem_ld_x64(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(s + 64));
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 128; e += 8)
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      m4[u] = fmax3(m4[u], __uint_as_float(s[e + 2 * u]), __uint_as_float(s[e + 2 * u + 1]));
+  raise_max(tS, m, l, fmaxf(m, fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c));
+  const float neg_m = (m == -INFINITY) ? 0.f : -m;
+  float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t pk[32];
+    weights(s + 64 * hf, pk, c, neg_m, sa0, sa1);
+    weights(s + 64 * hf + 32, pk + 16, c, neg_m, sb0, sb1);
+    tmem_st_x32(tS + 32 * hf, pk);
+  }
+  l += (sa0 + sb0) + (sa1 + sb1);
+}
+
+// Bits [0, n) of a word.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
+// The same for a tile that the mask cuts: the row sees columns [from, to], and
+// those before `sink` up to `to`; the second product reads columns [0, used).
+// Columns go in halves of 64 with a bit for each visible one, read twice from
+// TMEM (for the maximum, then for P, which overwrites columns that were read
+// before); a half that no row of the warp sees costs only its zeros. Loops over
+// halves rather than 128 masked registers: with three cut tiles among ten (8K
+// tokens, window 1024) the unrolled form took 193 us where the whole kernel
+// without any mask took 122.
+__device__ __forceinline__ void softmax_cut(uint32_t tS, float c, float& m, float& l, int from, int to, int sink,
+                                            int used) {
+  auto seen = [&](int ch) { return low_bits(to + 1 - ch) & (~low_bits(from - ch) | low_bits(sink - ch)); };
+  auto masked = [&](uint32_t (&s)[64], int ch) {
+    tmem_ld_x64(tS + ch, s);
+    const uint32_t see[2] = {seen(ch), seen(ch + 32)};
+#pragma unroll
+    for (int k = 0; k < 64; ++k)
+      if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = __float_as_uint(-INFINITY);
+  };
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int ch = 0; ch < used; ch += 64) {
+    if (!__any_sync(0xffffffffu, seen(ch) | seen(ch + 32))) continue;
+    uint32_t s[64];
+    masked(s, ch);
+    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 64; e += 8)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        m4[u] = fmax3(m4[u], __uint_as_float(s[e + 2 * u]), __uint_as_float(s[e + 2 * u + 1]));
+    mx = fmaxf(mx, fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])));
+  }
+  raise_max(tS, m, l, fmaxf(m, mx * c));
+  const float neg_m = (m == -INFINITY) ? 0.f : -m;
+  float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+#pragma unroll 1
+  for (int ch = 0; ch < used; ch += 64) {
+    uint32_t pk[32];
+    if (__any_sync(0xffffffffu, seen(ch) | seen(ch + 32))) {
+      uint32_t s[64];
+      masked(s, ch);
+      weights(s, pk, c, neg_m, sa0, sa1);
+      weights(s + 32, pk + 16, c, neg_m, sb0, sb1);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) pk[k] = 0u;
+    }
+    tmem_st_x32_nowait(tS + ch / 2, pk);
+  }
+  tmem_wait_st();
+  l += (sa0 + sb0) + (sa1 + sb1);
+}
+
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     attn_window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
@@ -154,6 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->p_full[t], 128);
       mbar_init(&bars->o_full[t], 1);
+      mbar_init(&bars->o_free[t], 128);
+      mbar_init(&bars->row_full[t], 128);
+      mbar_init(&bars->row_free[t], 128);
     }
     mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
@@ -175,160 +316,227 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Every role walks the same items; barrier phases carry on from one to the
   // next (ring slots by a running count, the others by one count per query tile).
-  if (warp == kProducerWarp) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_last();
-      int it = 0;              // K and V tiles loaded
-      uint32_t nq[2] = {0, 0};  // Q tiles loaded
+  if (warp >= kProducerWarp) {
+    regs_down();
+    if (warp == kProducerWarp) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        const uint64_t pol = l2_policy_evict_last();
+        int it = 0;              // K and V tiles loaded
+        uint32_t nq[2] = {0, 0};  // Q tiles loaded
+        bool ok = true;
+        for (int k = static_cast<int>(blockIdx.x); k < p.items && ok; k += static_cast<int>(gridDim.x)) {
+          const Item w = item_of(p, k);
+          const Visits v = visits(p.w, w.q0);
+          const int xq = w.h * kD, xk = (w.h / p.G) * kD;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (!v.any(t)) continue;
+            ok = mbar_wait_inline(&bars->q_empty[t], (nq[t] & 1u) ^ 1u, abort_flag, p.st, kWhere | (7u << 16));
+            if (!ok) break;
+            mbar_arrive_expect_tx(&bars->q_full[t], kTileBytes);
+            for (int half = 0; half < 2; ++half)
+              tma_load_3d(smem + kSmQ + t * kTileBytes + half * kHalfBytes, &tm_q, &bars->q_full[t], xq + half * 64,
+                          w.q0 + t * kBM, w.b);
+            ++nq[t];
+          }
+          for (int i = 0; i < v.n && ok; ++i) {
+            for (int kv = 0; kv < 2; ++kv, ++it) {
+              const int slot = it % kStages;
+              const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
+              if (!mbar_wait_inline(&bars->kv_empty[slot], ph ^ 1u, abort_flag, p.st, kWhere | (1u << 16))) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx(&bars->kv_full[slot], kTileBytes);
+              const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
+              for (int half = 0; half < 2; ++half)
+                tma_load_3d_hint(smem + kSmKV + slot * kTileBytes + half * kHalfBytes, map, &bars->kv_full[slot],
+                                 xk + half * 64, v.all.tile(i) * kBN, w.b, pol);
+            }
+          }
+        }
+        if (!ok) {
+          // Let every copy already issued land before the CTA can exit.
+          for (int t = 0; t < 2; ++t)
+            if (nq[t] > 0) drain_wait(&bars->q_full[t], (nq[t] - 1) & 1u, p.st.limit);
+          for (int j = max(0, it - kStages); j < it; ++j)
+            drain_wait(&bars->kv_full[j % kStages], static_cast<uint32_t>(j / kStages) & 1u, p.st.limit);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ MMA issuer
+      // All lanes walk the loop, one elected lane issues.
+      const uint32_t one = elect_one();
+      const uint32_t tm = uniform(tbase);
+      const uint32_t idesc_qk = idesc_bf16(kBM, kBN, false, false);
+      const uint32_t idesc_pv = idesc_bf16(kBM, kD, false, true);
+      const uint64_t q_desc = sdesc_sw128(sbase + kSmQ, 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(sbase + kSmKV, 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(sbase + kSmKV + kTileBytes, kHalfBytes, 1024);
+      // Visit g of the CTA has K in ring slot 2 (g & 1) and V in the slot after it.
+      auto issue_qk = [&](int t, uint32_t g) {
+        const uint64_t qa = sdesc_advance(q_desc, t * kTileBytes), kb = sdesc_advance(k_desc, (g & 1u) * 2 * kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+          mma_ss_if(tm + t * 128, sdesc_advance(qa, off), sdesc_advance(kb, off), idesc_qk, kk > 0, one);
+        }
+        tc_commit_if(&bars->s_full[t], one);
+      };
+      auto issue_pv = [&](int t, uint32_t g, uint32_t acc, int cols) {
+        const uint64_t vb = sdesc_advance(v_desc, (g & 1u) * 2 * kTileBytes);
+        if (cols == kBN) {
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            mma_ts_if(tm + 256 + t * 128, tm + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv,
+                      kk > 0 ? 1u : acc, one);
+        } else {
+#pragma unroll 1
+          for (int kk = 0; kk * 16 < cols; ++kk)
+            mma_ts_if(tm + 256 + t * 128, tm + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv,
+                      kk > 0 ? 1u : acc, one);
+        }
+      };
+      auto wait_kv = [&](uint32_t g, int v) {
+        const bool r = mbar_wait_warp(&bars->kv_full[2 * (g & 1u) + v], (g >> 1) & 1u, abort_flag, p.st,
+                                      kWhere | (3u << 16));
+        tc_fence_after();
+        return r;
+      };
+      uint32_t g = 0;  // visits of the items before, and of this one
+      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
       bool ok = true;
       for (int k = static_cast<int>(blockIdx.x); k < p.items && ok; k += static_cast<int>(gridDim.x)) {
         const Item w = item_of(p, k);
         const Visits v = visits(p.w, w.q0);
-        const int xq = w.h * kD, xk = (w.h / p.G) * kD;
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (!v.any(t)) continue;
-          ok = mbar_wait(&bars->q_empty[t], (nq[t] & 1u) ^ 1u, abort_flag, p.st, kWhere | (7u << 16));
-          if (!ok) break;
-          mbar_arrive_expect_tx(&bars->q_full[t], kTileBytes);
-          for (int half = 0; half < 2; ++half)
-            tma_load_3d(smem + kSmQ + t * kTileBytes + half * kHalfBytes, &tm_q, &bars->q_full[t], xq + half * 64,
-                        w.q0 + t * kBM, w.b);
-          ++nq[t];
-        }
-        for (int i = 0; i < v.n && ok; ++i) {
-          for (int kv = 0; kv < 2; ++kv, ++it) {
-            const int slot = it % kStages;
-            const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
-            if (!mbar_wait(&bars->kv_empty[slot], ph ^ 1u, abort_flag, p.st, kWhere | (1u << 16))) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(&bars->kv_full[slot], kTileBytes);
-            const CUtensorMap* map = kv == 0 ? &tm_k : &tm_v;
-            for (int half = 0; half < 2; ++half)
-              tma_load_3d_hint(smem + kSmKV + slot * kTileBytes + half * kHalfBytes, map, &bars->kv_full[slot],
-                               xk + half * 64, v.all.tile(i) * kBN, w.b, pol);
+        if (v.n == 0) continue;
+        uint32_t acc[2] = {0, 0};
+        ok = wait_kv(g, 0);
+        // First products. S_t is free: the previous item's last P V of tile t was issued before.
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || !v.any(t)) continue;
+          ok = mbar_wait_warp(&bars->q_full[t], q_phase[t], abort_flag, p.st, kWhere | (2u << 16));
+          if (!ok) continue;
+          q_phase[t] ^= 1u;
+          tc_fence_after();
+          if (v.active(t, 0)) {
+            issue_qk(t, g);
+            if (v.last(t) == 0) tc_commit_if(&bars->q_empty[t], one);
           }
         }
+        if (!ok) break;
+        tc_commit_if(&bars->kv_empty[2 * (g & 1u)], one);
+        for (int i = 0; i < v.n && ok; ++i, ++g) {
+          ok = wait_kv(g, 1);
+          if (!ok) break;
+          bool k_ready = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok) continue;
+            if (v.active(t, i)) {
+              ok = mbar_wait_warp(&bars->p_full[t], p_phase[t], abort_flag, p.st, kWhere | (4u << 16));
+              if (!ok) continue;
+              p_phase[t] ^= 1u;
+              if (acc[t] == 0) {  // the first P V of an item writes over O: the previous one's has been read
+                ok = mbar_wait_warp(&bars->o_free[t], o_phase[t] ^ 1u, abort_flag, p.st, kWhere | (8u << 16));
+                if (!ok) continue;
+                o_phase[t] ^= 1u;
+              }
+              tc_fence_after();
+              issue_pv(t, g, acc[t], used_columns(p.w, v.own[t], v.all.tile(i)));
+              acc[t] = 1;
+              if (i == v.last(t)) tc_commit_if(&bars->o_full[t], one);
+            }
+            if (v.active(t, i + 1)) {  // S over P once the product above has read it (issue order)
+              if (!k_ready) {
+                ok = wait_kv(g + 1, 0);
+                if (!ok) continue;
+                k_ready = true;
+              }
+              issue_qk(t, g + 1);
+              if (i + 1 == v.last(t)) tc_commit_if(&bars->q_empty[t], one);
+            }
+          }
+          if (!ok) break;
+          tc_commit_if(&bars->kv_empty[2 * (g & 1u) + 1], one);
+          if (i + 1 < v.n) tc_commit_if(&bars->kv_empty[2 * ((g + 1) & 1u)], one);
+        }
       }
-      if (!ok) {
-        // Let every copy already issued land before the CTA can exit.
-        for (int t = 0; t < 2; ++t)
-          if (nq[t] > 0) drain_wait(&bars->q_full[t], (nq[t] - 1) & 1u, p.st.limit);
-        for (int j = max(0, it - kStages); j < it; ++j)
-          drain_wait(&bars->kv_full[j % kStages], static_cast<uint32_t>(j / kStages) & 1u, p.st.limit);
-      }
+      // Every MMA issued must finish before TMEM is released.
+      tc_commit_if(&bars->mma_done, one);
+      drain_wait(&bars->mma_done, 0, p.st.limit);
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    // All lanes walk the loop, one elected lane issues.
-    const uint32_t one = elect_one();
-    const uint32_t tm = uniform(tbase);
-    const uint32_t idesc_qk = idesc_bf16(kBM, kBN, false, false);
-    const uint32_t idesc_pv = idesc_bf16(kBM, kD, false, true);
-    const uint64_t q_desc = sdesc_sw128(sbase + kSmQ, 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(sbase + kSmKV, 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(sbase + kSmKV + kTileBytes, kHalfBytes, 1024);
-    // Visit g of the CTA has K in ring slot 2 (g & 1) and V in the slot after it.
-    auto issue_qk = [&](int t, uint32_t g) {
-      const uint64_t qa = sdesc_advance(q_desc, t * kTileBytes), kb = sdesc_advance(k_desc, (g & 1u) * 2 * kTileBytes);
-#pragma unroll
-      for (int kk = 0; kk < kD / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-        mma_ss_if(tm + t * 128, sdesc_advance(qa, off), sdesc_advance(kb, off), idesc_qk, kk > 0, one);
-      }
-      tc_commit_if(&bars->s_full[t], one);
-    };
-    auto issue_pv = [&](int t, uint32_t g, uint32_t acc, int cols) {
-      const uint64_t vb = sdesc_advance(v_desc, (g & 1u) * 2 * kTileBytes);
-      if (cols == kBN) {
-#pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          mma_ts_if(tm + 256 + t * 128, tm + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv,
-                    kk > 0 ? 1u : acc, one);
-      } else {
-#pragma unroll 1
-        for (int kk = 0; kk * 16 < cols; ++kk)
-          mma_ts_if(tm + 256 + t * 128, tm + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv,
-                    kk > 0 ? 1u : acc, one);
-      }
-    };
-    auto wait_kv = [&](uint32_t g, int v) {
-      const bool r = mbar_wait_warp(&bars->kv_full[2 * (g & 1u) + v], (g >> 1) & 1u, abort_flag, p.st,
-                                    kWhere | (3u << 16));
-      tc_fence_after();
-      return r;
-    };
-    uint32_t g = 0;  // visits of the items before, and of this one
-    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+  } else if (warp >= kEpilogueWarp) {
+    // ------------------------------------------------------------ epilogue
+    regs_down();
+    // O of a finished query tile out of TMEM while the softmax warps are on the next item.
+    const int row = 32 * (warp - kEpilogueWarp) + lane;
+    const uint32_t tO = tbase + 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    uint32_t phase[2] = {0, 0};
     bool ok = true;
     for (int k = static_cast<int>(blockIdx.x); k < p.items && ok; k += static_cast<int>(gridDim.x)) {
       const Item w = item_of(p, k);
-      const Visits v = visits(p.w, w.q0);
-      if (v.n == 0) continue;
-      uint32_t acc[2] = {0, 0};
-      ok = wait_kv(g, 0);
-      // First products. S_t is free: the previous item's last P V of tile t was issued before.
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (!ok || !v.any(t)) continue;
-        ok = mbar_wait_warp(&bars->q_full[t], q_phase[t], abort_flag, p.st, kWhere | (2u << 16));
         if (!ok) continue;
-        q_phase[t] ^= 1u;
-        tc_fence_after();
-        if (v.active(t, 0)) {
-          issue_qk(t, g);
-          if (v.last(t) == 0) tc_commit_if(&bars->q_empty[t], one);
-        }
-      }
-      if (!ok) break;
-      tc_commit_if(&bars->kv_empty[2 * (g & 1u)], one);
-      for (int i = 0; i < v.n && ok; ++i, ++g) {
-        ok = wait_kv(g, 1);
-        if (!ok) break;
-        bool k_ready = false;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        const int qi = w.q0 + t * kBM + row;
+        const bool valid = qi < p.w.Sq;
+        const bool any = key_tiles(p.w, w.q0 + t * kBM, kBM).count() > 0;  // else O was never formed
+        float m = -INFINITY, l = 0.f;
+        if (any) {
+          ok = mbar_wait_warp(&bars->row_full[t], phase[t], abort_flag, p.st, kWhere | (10u << 16));
           if (!ok) continue;
-          if (v.active(t, i)) {
-            // P is in TMEM; for an item's first visit its rows have also read the previous item's O
-            ok = mbar_wait_warp(&bars->p_full[t], p_phase[t], abort_flag, p.st, kWhere | (4u << 16));
-            if (!ok) continue;
-            p_phase[t] ^= 1u;
-            tc_fence_after();
-            issue_pv(t, g, acc[t], used_columns(p.w, v.own[t], v.all.tile(i)));
-            acc[t] = 1;
-            if (i == v.last(t)) tc_commit_if(&bars->o_full[t], one);
-          }
-          if (v.active(t, i + 1)) {  // S over P once the product above has read it (issue order)
-            if (!k_ready) {
-              ok = wait_kv(g + 1, 0);
-              if (!ok) continue;
-              k_ready = true;
+          const float2 r = reinterpret_cast<const float2*>(smem + kSmRow)[t * kBM + row];
+          m = r.x;
+          l = r.y;
+          mbar_arrive(&bars->row_free[t]);
+          ok = mbar_wait_warp(&bars->o_full[t], phase[t], abort_flag, p.st, kWhere | (6u << 16));
+          if (!ok) continue;
+          phase[t] ^= 1u;
+          tc_fence_after();
+        }
+        const float inv_l = l == 0.f ? 0.f : 1.f / l;
+        __nv_bfloat16* dst = p.o + w.b * p.o_bs + static_cast<long long>(qi) * p.o_rs + w.h * kD;
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t o[32];
+          if (any) {
+            tmem_ld_x32(tO + t * 128 + ch * 32, o);
+            if (ch == 3) {
+              tc_fence_before();
+              mbar_arrive(&bars->o_free[t]);  // the next item's P V may write over O
             }
-            issue_qk(t, g + 1);
-            if (i + 1 == v.last(t)) tc_commit_if(&bars->q_empty[t], one);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0u;
+          }
+          if (valid) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint4 u;
+              u.x = pack_bf16x2(__uint_as_float(o[j]) * inv_l, __uint_as_float(o[j + 1]) * inv_l);
+              u.y = pack_bf16x2(__uint_as_float(o[j + 2]) * inv_l, __uint_as_float(o[j + 3]) * inv_l);
+              u.z = pack_bf16x2(__uint_as_float(o[j + 4]) * inv_l, __uint_as_float(o[j + 5]) * inv_l);
+              u.w = pack_bf16x2(__uint_as_float(o[j + 6]) * inv_l, __uint_as_float(o[j + 7]) * inv_l);
+              *reinterpret_cast<uint4*>(dst + ch * 32 + j) = u;
+            }
           }
         }
-        if (!ok) break;
-        tc_commit_if(&bars->kv_empty[2 * (g & 1u) + 1], one);
-        if (i + 1 < v.n) tc_commit_if(&bars->kv_empty[2 * ((g + 1) & 1u)], one);
+        if (valid)
+          p.lse[w.b * p.l_bs + w.h * p.l_hs + qi] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
       }
     }
-    // Every MMA issued must finish before TMEM is released.
-    tc_commit_if(&bars->mma_done, one);
-    drain_wait(&bars->mma_done, 0, p.st.limit);
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int t = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t tS = tbase + t * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t tO = tS + 256;
     const float c = p.scale_log2;
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0, row_phase = 0;
     bool ok = true;
     for (int k = static_cast<int>(blockIdx.x); k < p.items; k += static_cast<int>(gridDim.x)) {
       const int q0 = item_of(p, k).q0 + t * kBM;
@@ -336,115 +544,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt = own.count();
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < cnt; ++i, s_phase ^= 1u) {
-        ok = warp_all(mbar_wait(&bars->s_full[t], s_phase, abort_flag, p.st, kWhere | (5u << 16)));
+        ok = mbar_wait_warp(&bars->s_full[t], s_phase, abort_flag, p.st, kWhere | (5u << 16));
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[128];
-        tmem_ld_x128(tS, s);
         const int kbase = own.tile(i) * kBN;
         const int p_first = p.w.pos0 + q0;
-        const bool whole = kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
-                           (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks);
-        if (!whole) {
+        if (kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
+            (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks)) {
+          softmax_whole(tS, c, m, l);
+        } else {
           // The mask cuts this tile: the row sees columns [from, to], and those before `sink` up to `to`.
           const int pos = p_first + row;
-          const int to = min(pos, p.w.Sk - 1) - kbase;
-          const int from = pos - p.w.window + 1 - kbase;
-          const int sink = p.w.sinks - kbase;
-          if (sink > 0) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e > to || (e < from && e >= sink)) s[e] = __float_as_uint(-INFINITY);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e > to || e < from) s[e] = __float_as_uint(-INFINITY);
-          }
+          softmax_cut(tS, c, m, l, pos - p.w.window + 1 - kbase, min(pos, p.w.Sk - 1) - kbase, p.w.sinks - kbase,
+                      used_columns(p.w, own, own.tile(i)));
         }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < 128; e += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            m4[u] = fmax3(m4[u], __uint_as_float(s[e + 2 * u]), __uint_as_float(s[e + 2 * u + 1]));
-        const float m_new = fmaxf(m, fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c);
-        const bool fresh = m == -INFINITY;  // nothing seen so far: O and l are 0, whatever the maximum
-        const bool resc = !fresh && m_new > m + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, resc)) {
-          // O in pieces of 16 columns: beside the 128 scores, larger ones would not fit the registers
-          const float alpha = resc ? ex2_approx(m - m_new) : 1.0f;
-#pragma unroll 1
-          for (int ch = 0; ch < 8; ++ch) {
-            uint32_t o[16];
-            tmem_ld_x16(tO + ch * 16, o);
-#pragma unroll
-            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
-            tmem_st_x16(tO + ch * 16, o);
-          }
-          if (resc) l *= alpha;
-        }
-        if (fresh || resc) m = m_new;
-        // P is rounded to bf16 for the second product (half a step, 2^-9 of each weight, of either sign); l sums it
-        // in fp32.
-        const float neg_m = (m == -INFINITY) ? 0.f : -m;
-        float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int u = 0; u < 32; ++u) {
-            const int e = 64 * hf + 2 * u;
-            float x0, x1;
-            ffma2(x0, x1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), c, c, neg_m, neg_m);
-            const float p0 = ex2_approx(x0);
-            const float p1 = ex2_approx(x1);
-            if (u & 1)
-              fadd2(sb0, sb1, sb0, sb1, p0, p1);
-            else
-              fadd2(sa0, sa1, sa0, sa1, p0, p1);
-            pk[u] = pack_bf16x2(p0, p1);
-          }
-          tmem_st_x32(tS + 32 * hf, pk);
-        }
-        l += (sa0 + sb0) + (sa1 + sb1);
         tc_fence_before();
         mbar_arrive(&bars->p_full[t]);
       }
-      if (ok && cnt > 0) {
-        ok = warp_all(mbar_wait(&bars->o_full[t], o_phase, abort_flag, p.st, kWhere | (6u << 16)));
-        o_phase ^= 1u;
+      if (ok && cnt > 0) {  // m and l to the epilogue warps, and on to the next item
+        ok = mbar_wait_warp(&bars->row_free[t], row_phase ^ 1u, abort_flag, p.st, kWhere | (9u << 16));
+        if (!ok) break;
+        row_phase ^= 1u;
+        reinterpret_cast<float2*>(smem + kSmRow)[t * kBM + row] = make_float2(m, l);
+        mbar_arrive(&bars->row_full[t]);
       }
       if (!ok) break;
-      tc_fence_after();
-      const Item w = item_of(p, k);
-      const int qi = w.q0 + t * kBM + row;
-      const bool valid = qi < p.w.Sq;
-      const float inv_l = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* dst = p.o + w.b * p.o_bs + static_cast<long long>(qi) * p.o_rs + w.h * kD;
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t o[32];
-        if (cnt > 0) {
-          tmem_ld_x32(tO + ch * 32, o);
-        } else {  // no key for any row of this tile: O was never formed
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
-        }
-        if (valid) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            uint4 u;
-            u.x = pack_bf16x2(__uint_as_float(o[j]) * inv_l, __uint_as_float(o[j + 1]) * inv_l);
-            u.y = pack_bf16x2(__uint_as_float(o[j + 2]) * inv_l, __uint_as_float(o[j + 3]) * inv_l);
-            u.z = pack_bf16x2(__uint_as_float(o[j + 4]) * inv_l, __uint_as_float(o[j + 5]) * inv_l);
-            u.w = pack_bf16x2(__uint_as_float(o[j + 6]) * inv_l, __uint_as_float(o[j + 7]) * inv_l);
-            *reinterpret_cast<uint4*>(dst + ch * 32 + j) = u;
-          }
-        }
-      }
-      if (valid)
-        p.lse[w.b * p.l_bs + w.h * p.l_hs + qi] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
-      tc_fence_before();  // O is read: the next item's first P V (after this tile's next p_full) may overwrite it
     }
   }
 
@@ -483,6 +607,9 @@ int launch_window_fwd(const WindowFwd& a, cudaStream_t stream) {
   const long long items = static_cast<long long>((a.w.Sq + 2 * kBM - 1) / (2 * kBM)) * a.B * a.H;
   if (items > 0x7fffffffLL - kSms) return -1;
   p.items = static_cast<int>(items);
+  const long long window_rows = std::min<long long>(a.w.Sk, static_cast<long long>(a.w.window) + a.w.sinks + 2 * kBM);
+  const long long kv_heads = std::max<long long>(1, kGroupBytes / (window_rows * 4 * kD));
+  p.head_group = static_cast<int>(std::min<long long>(static_cast<long long>(a.B) * a.H, kv_heads * p.G));
   attn_window_fwd_kernel<<<static_cast<unsigned>(std::min<long long>(items, kSms)), kThreads, kSmemBytes, stream>>>(
       tq, tk, tv, p);
   return cudaGetLastError() == cudaSuccess ? 0 : -4;

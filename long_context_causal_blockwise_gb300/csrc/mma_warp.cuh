@@ -21,11 +21,31 @@ __device__ __forceinline__ uint32_t elect_one() {
 // A value that all lanes hold, as one the compiler knows to be uniform.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// mbar_wait by all lanes; the same answer in each.
+// mbar_wait without a function call in the waiting path: a call keeps the
+// values around it in the registers of the calling convention, and does not
+// compile beside setmaxnreg.
+__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                 const DevStatus& st, uint32_t where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > st.limit) {
+      *abort_flag = 1;
+      if (atomicOr(st.words, DEV_TIMEOUT) == 0) {
+        st.words[1] = where | ((blockIdx.x & 0xffu)) | ((warp_id() & 0xffu) << 8);
+        st.words[2] = blockIdx.x;
+      }
+      return false;
+    }
+  }
+}
+
+// The same by all lanes of a warp, with the same answer in each.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                const DevStatus& st, uint32_t where) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait_slow(bar, parity, abort_flag, st, where));
+  return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, abort_flag, st, where));
 }
 
 __device__ __forceinline__ void tc_commit_if(uint64_t* bar, uint32_t elected) {
