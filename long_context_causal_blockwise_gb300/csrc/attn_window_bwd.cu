@@ -115,11 +115,11 @@ __global__ void __launch_bounds__(kFuThreads, 1)
         const uint32_t ph = static_cast<uint32_t>(i / kKvStages) & 1u;
         const uint32_t dph = static_cast<uint32_t>(i) & 1u;  // one dO slot
         const int x0 = head_of(i) * kD, row = tile_of(i) * kT;
-        ok = mbar_wait(&bars->ring_empty[s], ph ^ 1u, abort_flag, p.st, kWhere | (1u << 16));
+        ok = mbar_wait_inline(&bars->ring_empty[s], ph ^ 1u, abort_flag, p.st, kWhere | (1u << 16));
         if (!ok) break;
         mbar_arrive_expect_tx(&bars->ring_full[s], kTileBytes);
         load_tile(smem + kFuSmQ + s * kTileBytes, &tm_q, &bars->ring_full[s], x0, row, b, pol);
-        ok = mbar_wait(&bars->do_empty[0], dph ^ 1u, abort_flag, p.st, kWhere | (11u << 16));
+        ok = mbar_wait_inline(&bars->do_empty[0], dph ^ 1u, abort_flag, p.st, kWhere | (11u << 16));
         if (!ok) break;
         mbar_arrive_expect_tx(&bars->do_full[0], kTileBytes);
         load_tile(smem + kFuSmDo, &tm_do, &bars->do_full[0], x0, row, b, pol);
@@ -229,11 +229,11 @@ __global__ void __launch_bounds__(kFuThreads, 1)
       for (int i = 0; i < n && ok; ++i) {
         const uint32_t ph = static_cast<uint32_t>(i) & 1u;
         float* tile = p.dq_acc + b * p.dq_bs + head_of(i) * p.dq_hs + static_cast<long long>(tile_of(i)) * (kT * kD);
-        ok = mbar_wait(&bars->stg_full[0], ph, abort_flag, p.st, kWhere | (14u << 16));
+        ok = mbar_wait_inline(&bars->stg_full[0], ph, abort_flag, p.st, kWhere | (14u << 16));
         if (!ok) break;
         bulk_reduce_add_f32(tile, sbase + kFuSmStg, kDqBlock);
         bulk_commit();
-        ok = mbar_wait(&bars->stg_full[1], ph, abort_flag, p.st, kWhere | (14u << 16));
+        ok = mbar_wait_inline(&bars->stg_full[1], ph, abort_flag, p.st, kWhere | (14u << 16));
         if (!ok) break;
         bulk_reduce_add_f32(tile + kDqBlock / 4, sbase + kFuSmStg + kDqBlock, kDqBlock);
         bulk_commit();
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kFuThreads, 1)
         // of either sign) into shared memory for dK and dQ.
         const int i = s - 1;
         const uint32_t ph = static_cast<uint32_t>(i) & 1u;
-        ok = warp_all(mbar_wait(&bars->dp_full, ph, abort_flag, p.st, kWhere | (6u << 16)));
+        ok = mbar_wait_warp(&bars->dp_full, ph, abort_flag, p.st, kWhere | (6u << 16));
         if (!ok) break;
         tc_fence_after();
         sds[lane] = sd;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kFuThreads, 1)
           }
         }
         if (i > 0) {
-          ok = warp_all(mbar_wait(&bars->ds_free, ph ^ 1u, abort_flag, p.st, kWhere | (9u << 16)));
+          ok = mbar_wait_warp(&bars->ds_free, ph ^ 1u, abort_flag, p.st, kWhere | (9u << 16));
           if (!ok) break;
         }
         st_tile_quarter_row(ds_tile, row, x, dk);
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kFuThreads, 1)
         const float l2v = (rl == -INFINITY) ? -INFINITY : -rl * kLog2e;  // fetched a step ago
         sd = -p.scale * rd;
         if (s + 1 < n) fetch_stats(s + 1);
-        ok = warp_all(mbar_wait(&bars->s_full, static_cast<uint32_t>(s) & 1u, abort_flag, p.st, kWhere | (5u << 16)));
+        ok = mbar_wait_warp(&bars->s_full, static_cast<uint32_t>(s) & 1u, abort_flag, p.st, kWhere | (5u << 16));
         if (!ok) break;
         tc_fence_after();
         l2s[lane] = l2v;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kFuThreads, 1)
         // Phase 3: row `row` of dQ(i) (TMEM lane = query row), columns [32x, 32x + 32), added into the accumulator.
         const int i = s - 1;
         const uint32_t ph = static_cast<uint32_t>(i) & 1u;
-        ok = warp_all(mbar_wait(&bars->dq_full, ph, abort_flag, p.st, kWhere | (7u << 16)));
+        ok = mbar_wait_warp(&bars->dq_full, ph, abort_flag, p.st, kWhere | (7u << 16));
         if (!ok) break;
         tc_fence_after();
         uint32_t g[32];
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kFuThreads, 1)
         mbar_arrive(&bars->dq_free);
         if (x < 2) {
           if (i > 0)
-            ok = warp_all(mbar_wait(&bars->stg_free[x], ph ^ 1u, abort_flag, p.st, kWhere | (15u << 16)));
+            ok = mbar_wait_warp(&bars->stg_free[x], ph ^ 1u, abort_flag, p.st, kWhere | (15u << 16));
           if (!ok) break;
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch)
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kFuThreads, 1)
     if (n == 0) {
       if (valid) store_zero(gdst, off, 64, mode);
     } else if (ok) {
-      ok = warp_all(mbar_wait(&bars->acc_full, 0, abort_flag, p.st, kWhere | (10u << 16)));
+      ok = mbar_wait_warp(&bars->acc_full, 0, abort_flag, p.st, kWhere | (10u << 16));
       if (ok) {
         tc_fence_after();
 #pragma unroll 1
