@@ -924,15 +924,16 @@ int attn_window_decode(const void* q, const void* k, const void* v, const int* l
                 st);
 }
 
-// Workspace of attn_window_bwd: Delta [B, H, Sq], the tiled dQ accumulator and
-// the runs' dK/dV partials, each at a 256-byte boundary.
+// Workspace of attn_window_bwd: two row statistics and a 128 x 128 fp32 dQ tile
+// per (head, 128 queries), and the runs' dK/dV partials.
 size_t attn_window_bwd_workspace_bytes(int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks,
                                        long long q_pos0) {
   WindowShape w;
   if (prep_window(&w, B, H, Hkv, Sq, Sk, D, window, sinks, q_pos0, 1.f) != LCB_OK) return 0;
   if (Sq == 0 || Sk == 0) return 0;
-  return delta_bytes(B, H, Sq) + static_cast<size_t>(B) * H * dq_tiles(Sq) * kDqTileFloats * sizeof(float) +
-         static_cast<size_t>(plan_window_bwd(w, B, H, Hkv).slots) * 2 * kDqTileFloats * sizeof(float);
+  return (static_cast<size_t>(B) * H * dq_tiles(Sq) * (2 * 128 + kDqTileFloats) +
+          static_cast<size_t>(plan_window_bwd(w, B, H, Hkv).slots) * 2 * kDqTileFloats) *
+         sizeof(float);
 }
 
 int attn_window_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
@@ -972,40 +973,29 @@ int attn_window_bwd(const void* q, const void* k, const void* v, const void* o, 
       ws_bytes < attn_window_bwd_workspace_bytes(B, H, Hkv, Sq, Sk, D, window, sinks, q_pos0))
     return LCB_ERR_ARG;
   WindowBwd a;
-  const size_t acc_bytes = static_cast<size_t>(B) * H * dq_tiles(Sq) * kDqTileFloats * sizeof(float);
-  float* delta = static_cast<float*>(workspace);
   a.q = {q, q_row_stride, q_batch_stride};
   a.k = {k, kv_row_stride, kv_batch_stride};
   a.v = {v, kv_row_stride, kv_batch_stride};
+  a.o = {o, o_row_stride, o_batch_stride};
   a.dO = {dO, o_row_stride, o_batch_stride};
   a.lse = lse;
-  a.delta = delta;
   a.lse_head_stride = lse_head_stride;
   a.lse_batch_stride = lse_batch_stride;
-  a.delta_head_stride = Sq;
-  a.delta_batch_stride = static_cast<long long>(H) * Sq;
+  a.dq = dq;
   a.dk = dk;
   a.dv = dv;
+  a.dq_row_stride = dq_row_stride;
+  a.dq_batch_stride = dq_batch_stride;
   a.dkv_row_stride = dkv_row_stride;
   a.dkv_batch_stride = dkv_batch_stride;
-  a.dq_tiles = reinterpret_cast<float*>(static_cast<char*>(workspace) + delta_bytes(B, H, Sq));
-  a.dq_tile_head_stride = dq_tiles(Sq) * kDqTileFloats;
-  a.dq_tile_batch_stride = a.dq_tile_head_stride * H;
-  a.partial = reinterpret_cast<float*>(reinterpret_cast<char*>(a.dq_tiles) + acc_bytes);
+  a.workspace = static_cast<float*>(workspace);
   a.B = B;
   a.H = H;
   a.Hkv = Hkv;
   a.w = w;
   a.scale = scale;
   if ((rc = dev_status(&a.st)) != LCB_OK) return rc;
-  rc = launch_bwd_preprocess(o, dO, o_row_stride, o_batch_stride, delta, a.delta_head_stride, a.delta_batch_stride, B,
-                             H, Sq, st);
-  if (rc != LCB_OK) return rc;
-  if (cudaMemsetAsync(a.dq_tiles, 0, acc_bytes, st) != cudaSuccess) return LCB_ERR_CUDA;
-  if ((rc = launch_window_bwd(a, st)) != LCB_OK) return rc;
-  return finish(launch_dq_untile(a.dq_tiles, a.dq_tile_head_stride, a.dq_tile_batch_stride, dq, dq_row_stride,
-                                 dq_batch_stride, B, H, Sq, st),
-                st);
+  return finish(launch_window_bwd(a, st), st);
 }
 
 int lcb_selftest_bounded_wait(void* stream) {

@@ -210,9 +210,6 @@ __device__ __forceinline__ void softmax_whole(uint32_t tS, float c, float& m, fl
   l += (sa0 + sb0) + (sa1 + sb1);
 }
 
-// Bits [0, n) of a word.
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
-
 // The same for a tile that the mask cuts: the row sees columns [from, to], and
 // those before `sink` up to `to`; the second product reads columns [0, used).
 // Columns go in halves of 64 with a bit for each visible one, read twice from

@@ -150,16 +150,14 @@ struct WindowFwd {
 int launch_window_fwd(const WindowFwd& a, cudaStream_t stream);  // Sq, Sk > 0
 
 struct WindowBwd {
-  RowView q, k, v, dO;
+  RowView q, k, v, o, dO;
   const float* lse;
-  const float* delta;
-  long long lse_head_stride, lse_batch_stride, delta_head_stride, delta_batch_stride;
+  long long lse_head_stride, lse_batch_stride;
+  void* dq;
   void* dk;
   void* dv;
-  long long dkv_row_stride, dkv_batch_stride;
-  float* dq_tiles;  // zeroed tiled accumulator, added into
-  long long dq_tile_head_stride, dq_tile_batch_stride;
-  float* partial;  // plan.slots * 2 * 128 * 128 floats
+  long long dq_row_stride, dq_batch_stride, dkv_row_stride, dkv_batch_stride;
+  float* workspace;  // row statistics, tiled dQ accumulator, dK/dV partials (attn_window_bwd_workspace_bytes)
   int B, H, Hkv;
   WindowShape w;
   float scale;

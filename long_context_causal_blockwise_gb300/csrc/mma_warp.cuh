@@ -18,6 +18,9 @@ __device__ __forceinline__ uint32_t elect_one() {
   return e;
 }
 
+// Bits [0, n) of a word.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
 // A value that all lanes hold, as one the compiler knows to be uniform.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 

@@ -158,11 +158,12 @@ def test_rope_axes_refusals():
     assert call(S=0) == _lib.LCB_OK
 
 
-def test_workspace_covers_delta_dq_and_partials():
+def test_workspace_covers_statistics_dq_and_partials():
     n = lcb.attn_window_bwd_workspace_bytes
-    assert n(1, 2, 2, 300, 300, 64) == 2560 + 2 * 3 * 65536  # Delta (2400 B to a multiple of 256), dQ tiles
+    tile = 65536 + 1024  # an fp32 dQ tile and two row statistics
+    assert n(1, 2, 2, 300, 300, 64) == 2 * 3 * tile
     # a sink tile seen by all of a long sequence: its list is cut into runs, each with an fp32 dK and dV
-    base = 4 * 65536 * 4 + 4 * 512 * 65536
+    base = 4 * 512 * tile
     assert n(1, 4, 1, 65536, 65536, 128, 0) == base
     more = n(1, 4, 1, 65536, 65536, 128, 4) - base
     assert more > 0 and more % (2 * 65536) == 0
