@@ -504,22 +504,21 @@ def rope(x, theta, pos0=0, inverse=False, out=None):
 _BF16 = torch.bfloat16
 
 
-def _fn(name):
-    return getattr(_LIB or load(), name)
-
-
 def _rows(t, name):
     """(shape, row stride, batch stride) of a bf16 [B, S, H, D] view with dense heads. The stride of a dimension of
     length one says nothing; it is taken as that of a dense tensor."""
-    if t.dtype is not _BF16 or t.dim() != 4:
-        raise ValueError(f"{name} must be a bf16 [B, S, H, D] view, got {t.dtype} {tuple(t.shape)}")
-    shape, (bs, rs, hs, ds) = t.shape, t.stride()
+    shape = t.shape
+    if t.dtype is not _BF16 or len(shape) != 4:
+        raise ValueError(f"{name} must be a bf16 [B, S, H, D] view, got {t.dtype} {tuple(shape)}")
     B, S, H, D = shape
+    if t.is_contiguous():
+        return shape, H * D, S * H * D
+    bs, rs, hs, ds = t.stride()
     if ds != 1 and D > 1 or hs != D and H > 1:
         raise ValueError(f"{name}: heads must be dense within a row")
     if S <= 1:
         rs = H * D
-    return shape, rs, bs if B > 1 else 0
+    return shape, rs, bs if B > 1 else S * H * D
 
 
 def _stats(t, name, shape):
@@ -532,17 +531,16 @@ def _stats(t, name, shape):
     return hs, bs
 
 
-def _raw_stream(name, *tensors):
-    """The current stream of the tensors' device, which must be one, a CUDA device, and the current one (kernels launch
-    there)."""
-    dev = tensors[0].get_device()
+def _raw_stream(name, dev, tensors):
+    """The current stream of device `dev` (tensor.get_device()), which must be the current CUDA device (kernels launch
+    there) and hold all tensors."""
     if dev < 0:
         raise ValueError(f"{name}: tensors must be on a CUDA device")
     for t in tensors:
         if t.get_device() != dev:
-            raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}, not on one CUDA device")
+            raise ValueError(f"{name}: tensors must be on one CUDA device")
     if dev != torch.cuda.current_device():
-        raise ValueError(f"{name}: tensors on {tensors[0].device}, which is not the current device")
+        raise ValueError(f"{name}: tensors on cuda:{dev}, which is not the current device")
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
@@ -554,7 +552,7 @@ def _window_inputs(name, q, k, v):
     if vs != ks or ks[0] != qs[0] or ks[3] != qs[3] or ks[2] < 1 or qs[2] % ks[2]:
         raise ValueError(f"{name}: k and v must be [B, Sk, Hkv, D] with Hkv dividing q's H, "
                          f"got {tuple(qs)}, {tuple(ks)}, {tuple(vs)}")
-    if (vr, vb) != (kr, kb) and ks[1]:
+    if (vr != kr or vb != kb) and ks[1]:
         raise ValueError("k and v must share strides")
     return qs, qr, qb, ks, kr, kb
 
@@ -575,9 +573,13 @@ def _window_out(q, shape, o, lse):
     return o, lse, orr, ob, lh, lb
 
 
+_MOST = 1 << 30
+
+
 def _count(n):
     """A window or sink count for the C ABI: more than 2^30 keys is all of them."""
-    return max(-1, min(int(n), 1 << 30))
+    n = int(n)
+    return n if 0 <= n <= _MOST else (_MOST if n > 0 else -1)
 
 
 def attn_window_fwd(q, k, v, window, sinks=0, q_pos0=None, scale=None, o=None, lse=None):
@@ -593,11 +595,13 @@ def attn_window_fwd(q, k, v, window, sinks=0, q_pos0=None, scale=None, o=None, l
     B, Sq, H, D = qs
     Sk = ks[1]
     o, lse, orr, ob, lh, lb = _window_out(q, qs, o, lse)
-    stream = _raw_stream("attn_window_fwd", q, k, v, o, lse)
-    _check("attn_window_fwd", _fn("attn_window_fwd")(
+    stream = _raw_stream("attn_window_fwd", q.get_device(), (k, v, o, lse))
+    rc = (_LIB or load()).attn_window_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, ks[2], Sq, Sk, D, _count(window),
         _count(sinks), Sk - Sq if q_pos0 is None else int(q_pos0), D ** -0.5 if scale is None else float(scale), qr,
-        qb, kr, kb, orr, ob, lh, lb, stream))
+        qb, kr, kb, orr, ob, lh, lb, stream)
+    if rc:
+        _check("attn_window_fwd", rc)
     return o, lse
 
 
@@ -638,12 +642,14 @@ def attn_window_bwd(q, k, v, o, lse, do, window, sinks=0, q_pos0=None, scale=Non
         workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    stream = _raw_stream("attn_window_bwd", q, k, v, o, lse, do, dq, dk, dv, workspace)
-    _check("attn_window_bwd", _fn("attn_window_bwd")(
+    stream = _raw_stream("attn_window_bwd", q.get_device(), (k, v, o, lse, do, dq, dk, dv, workspace))
+    rc = (_LIB or load()).attn_window_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
         dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Sq, Sk, D, _count(window), _count(sinks), pos0,
         D ** -0.5 if scale is None else float(scale), qr, qb, kr, kb, orr, ob, lh, lb, dqr, dqb, dkr, dkb,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream))
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+    if rc:
+        _check("attn_window_bwd", rc)
     return dq, dk, dv
 
 
@@ -659,11 +665,13 @@ def attn_window_decode(q, k_cache, v_cache, lens, window, sinks=0, scale=None, o
     if lens.dtype is not torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
         raise ValueError("lens must be a contiguous int32 [B] tensor")
     o, lse, orr, ob, lh, lb = _window_out(q, qs, o, lse)
-    stream = _raw_stream("attn_window_decode", q, k_cache, v_cache, lens, o, lse)
-    _check("attn_window_decode", _fn("attn_window_decode")(
+    stream = _raw_stream("attn_window_decode", q.get_device(), (k_cache, v_cache, lens, o, lse))
+    rc = (_LIB or load()).attn_window_decode(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, ks[2],
         T, ks[1], D, _count(window), _count(sinks), D ** -0.5 if scale is None else float(scale), qr, qb, kr, kb, orr,
-        ob, lh, lb, stream))
+        ob, lh, lb, stream)
+    if rc:
+        _check("attn_window_decode", rc)
     return o, lse
 
 
@@ -699,14 +707,16 @@ def rope_axes(x, theta, pos, sections, inverse=False, interleaved=False, out=Non
     elif _rows(out, "out") != (shape, r, b):
         raise ValueError("x and out must share shape and strides")
     B, S, H, D = shape
-    n = len(key[0])
-    ps = pos.stride()
-    if pos.dtype not in (torch.int32, torch.int64) or pos.shape != (n, S) and pos.shape != (n, B, S):
+    n, dtype, ps = len(key[0]), pos.dtype, pos.shape
+    if (dtype is not torch.int32 and dtype is not torch.int64) or ps != (n, S) and ps != (n, B, S):
         raise ValueError("pos must be int32 or int64 [axes, S] or [axes, B, S]")
-    stream = _raw_stream("rope_axes", x, pos, out)
-    _check("lcb_rope_axes", _fn("lcb_rope_axes")(
-        x.data_ptr(), out.data_ptr(), B, S, H, D, theta, pos.data_ptr(), pos.element_size(), n, arr, ps[0],
-        ps[1] if len(ps) == 3 else 0, ps[-1], bool(inverse), r, b, stream))
+    ps = pos.stride()
+    stream = _raw_stream("rope_axes", x.get_device(), (pos, out))
+    rc = (_LIB or load()).lcb_rope_axes(
+        x.data_ptr(), out.data_ptr(), B, S, H, D, theta, pos.data_ptr(), 4 if dtype is torch.int32 else 8, n, arr,
+        ps[0], ps[1] if len(ps) == 3 else 0, ps[-1], bool(inverse), r, b, stream)
+    if rc:
+        _check("lcb_rope_axes", rc)
     return out
 
 

@@ -771,13 +771,20 @@ int lcb_rope_axes(const void* x, void* y, int B, int S, int H, int D, double the
   if (D != kHeadDim || (pos_bytes != 4 && pos_bytes != 8)) return LCB_ERR_UNSUPPORTED;
   if (!(theta > 0.0) || !std::isfinite(theta) || (inverse != 0 && inverse != 1)) return LCB_ERR_ARG;
   if (n_axes < 1 || n_axes > 64 || !pair_axis) return LCB_ERR_ARG;
-  RopeAxes ax;
-  for (int k = 0; k < D / 2; ++k) {
+  // The 64 powers cost more than the launch: a thread keeps those of the base it used last.
+  static thread_local RopeAxes ax;
+  static thread_local double ax_theta = 0.0;
+  if (ax_theta != theta) {
+    for (int k = 0; k < kHeadDim / 2; ++k) {
+      // turns per unit of position, modulo one: a whole turn changes nothing
+      const double turns = std::pow(theta, -2.0 * k / kHeadDim) / 6.283185307179586476925286766559;
+      ax.turn[k] = static_cast<unsigned long long>(std::ldexp(turns - std::floor(turns), 64));
+    }
+    ax_theta = theta;
+  }
+  for (int k = 0; k < kHeadDim / 2; ++k) {
     if (pair_axis[k] < 0 || pair_axis[k] >= n_axes) return LCB_ERR_ARG;
     ax.axis[k] = static_cast<unsigned char>(pair_axis[k]);
-    // turns per unit of position, modulo one: a whole turn changes nothing
-    const double turns = std::pow(theta, -2.0 * k / D) / 6.283185307179586476925286766559;
-    ax.turn[k] = static_cast<unsigned long long>(std::ldexp(turns - std::floor(turns), 64));
   }
   if (S == 0) return LCB_OK;
   if (!x || !y || (reinterpret_cast<uintptr_t>(x) & 3u) || (reinterpret_cast<uintptr_t>(y) & 3u)) return LCB_ERR_ARG;

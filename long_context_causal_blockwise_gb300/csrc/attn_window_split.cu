@@ -370,7 +370,7 @@ struct Form {
       cudaLaunchAttribute at;
       const cudaLaunchConfig_t cfg = config(&at, cluster, 1, nullptr);
       int got = 0;
-      if (cudaOccupancyMaxActiveClusters(&got, fn(), &cfg) != cudaSuccess) {
+      if (allow() != 0 || cudaOccupancyMaxActiveClusters(&got, fn(), &cfg) != cudaSuccess) {
         cudaGetLastError();  // such clusters do not fit: not an error of the call
         got = 0;
       }
@@ -387,6 +387,8 @@ struct Form {
   }
 
   static int launch(const WindowSplit& p, long long tiles, cudaStream_t stream) {
+    const int rc = allow();
+    if (rc != 0) return rc;
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t cfg = config(&at, p.cluster, tiles, stream);
     return cudaLaunchKernelEx(&cfg, window_split_kernel<NT, kWarps>, p) == cudaSuccess ? 0 : -4;
@@ -402,9 +404,6 @@ struct Form {
 // warps x 12: 10.8, four x 16 (a second wave): 18.
 template <int NT>
 int launch_rows(WindowSplit& p, long long tiles, long long steps, cudaStream_t stream) {
-  int rc;
-  if ((rc = Form<NT, 2>::allow()) != 0 || (rc = Form<NT, 4>::allow()) != 0 || (rc = Form<NT, 8>::allow()) != 0)
-    return rc;
   const int c2 = Form<NT, 2>::one_wave(tiles, steps), c4 = Form<NT, 4>::one_wave(tiles, steps),
             c8 = Form<NT, 8>::one_wave(tiles, steps);
   if (2 * c2 >= 4 * c4 && 2 * c2 >= 8 * c8) {
