@@ -829,6 +829,57 @@ def run_rope(args):
     return 0
 
 
+def run_window(args):
+    """Times windowed attention with sinks at the headline shape's heads and length (B1 H32 S32768, window 4096, 4
+    sinks): forward and backward, and the single-token form for a batch of four against 32K windows; prints one JSON
+    line (not the headline bench line). FLOPs are those of the visible pairs (forward 4 D, backward 10 D)."""
+    import torch
+
+    import long_context_causal_blockwise_gb300 as lcb
+
+    Sw, Hw, W, sinks = 32768, 32, 4096, 4
+    dev = torch.device("cuda", 0)
+    lcb.load()
+    g = torch.Generator(device=dev).manual_seed(0)
+    q, k, v, do = (torch.randn(1, Sw, Hw, D, generator=g, device=dev).to(torch.bfloat16) for _ in range(4))
+
+    def timed(fn, steps):
+        for _ in range(max(3, args.warmup)):
+            fn()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(steps):
+            fn()
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / steps
+
+    steps = max(3, min(args.steps, 20))
+    o, lse = lcb.attn_window_fwd(q, k, v, W, sinks)
+    ws = torch.empty(lcb.attn_window_bwd_workspace_bytes(1, Hw, Hw, Sw, Sw, W, sinks), dtype=torch.uint8, device=dev)
+    grads = [torch.empty_like(q) for _ in range(3)]
+    t_fwd = timed(lambda: lcb.attn_window_fwd(q, k, v, W, sinks, o=o, lse=lse), steps)
+    t_bwd = timed(lambda: lcb.attn_window_bwd(q, k, v, o, lse, do, W, sinks, dq=grads[0], dk=grads[1], dv=grads[2],
+                                              workspace=ws), steps)
+    seen = lambda p: min(p + 1, W) + min(sinks, max(0, p - W + 1))  # noqa: E731
+    pairs = Hw * sum(seen(p) for p in range(Sw))
+    del grads, ws
+    Bd, Hd, Wd, Smax = 4, 40, 32768, 40000
+    kc, vc = (torch.randn(Bd, Smax, Hd, D, generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+    qd = torch.randn(Bd, 1, Hd, D, generator=g, device=dev).to(torch.bfloat16)
+    lens = torch.full((Bd,), Smax, dtype=torch.int32, device=dev)
+    t_dec = timed(lambda: lcb.attn_window_decode(qd, kc, vc, lens, Wd, sinks), steps)
+    nb = Bd * Hd * (Wd + sinks) * D * 4 + Bd * Hd * (4 * D + 4)
+    pk = load_peaks()
+    print(json.dumps({
+        "metric": f"windowed attention, B1 H{Hw} S{Sw} D{D}, window {W}, {sinks} sinks; decode B{Bd} H{Hd}, window {Wd}",
+        "fwd_ms": t_fwd, "fwd_tflops": 4 * D * pairs / t_fwd / 1e9, "bwd_ms": t_bwd,
+        "bwd_tflops": 10 * D * pairs / t_bwd / 1e9, "decode_ms": t_dec, **hbm_fields("decode_", nb, t_dec, pk),
+        "inputs": "larger than L2; no flush"}), flush=True)
+    return 0
+
+
 def run_merge(args):
     """Times the stand-alone LSE merge (attn_lse_merge) of one bf16 block into
     the fp32 accumulator, 16384 rows x 32 heads x 128 (the ring step's merge at
@@ -937,6 +988,8 @@ def main():
                     help="time the cross-entropy loss head (V=32000, 32768 tokens)")
     ap.add_argument("--rope", action="store_true",
                     help="time the RoPE kernel on a [1, 524288, 32, 128] tensor")
+    ap.add_argument("--window", action="store_true",
+                    help="time windowed attention with sinks (forward, backward, decode)")
     ap.add_argument("--zigzag", action="store_true",
                     help="time the one-device zigzag ring (S=131072, P=8) against monolithic attention")
     ap.add_argument("--ulysses", action="store_true",
@@ -948,6 +1001,8 @@ def main():
         return run_zigzag(args)
     if args.rope:
         return run_rope(args)
+    if args.window:
+        return run_window(args)
     if args.merge:
         return run_merge(args)
     if args.ulysses:

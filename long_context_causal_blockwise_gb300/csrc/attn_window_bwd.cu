@@ -37,12 +37,80 @@
 // Warps 0-15 compute, 16 TMA producer, 17 MMA issuer, 18 dQ reducer.
 #include <algorithm>
 
-#include "attn_bwd_tile.cuh"
 #include "attn_window.cuh"
+#include "lcb_attn.h"
+#include "lcb_internal.h"
 #include "mma_warp.cuh"
 
 namespace lcb {
 namespace {
+
+constexpr int kT = 128;  // rows of every tile
+constexpr int kD = 128;
+constexpr int kCompute = 512;  // compute threads: warps 0-15
+constexpr int kProducerWarp = 16;
+constexpr int kMmaWarp = 17;
+constexpr int kReduceWarp = 18;
+constexpr int kThreads = 608;
+constexpr uint32_t kTileBytes = kT * kD * 2;   // 32 KB: two 16 KB boxes of 128 rows x 64 columns
+constexpr uint32_t kColHalf = kTileBytes / 2;  // column-half stride of a tile
+constexpr uint32_t kDqBlock = 128 * 32 * 4;    // one staged dQ block: 128 rows x 32 columns fp32
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Loads one 128-row tile (two 64-column boxes) of `map` at row `row`.
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int x0, int row, int b,
+                                          uint64_t pol) {
+  tma_load_3d_hint(dst, map, bar, x0, row, b, pol);
+  tma_load_3d_hint(dst + kColHalf, map, bar, x0 + 64, row, b, pol);
+}
+
+// Writes 32 bf16 values (16 packed words) as columns [32q, 32q+32) of row `r`
+// of a 128 x 128 K-major tile with 128-byte swizzle (the layout TMA produces).
+__device__ __forceinline__ void st_tile_quarter_row(uint8_t* tile, int r, int q, const uint32_t (&w)[16]) {
+  uint8_t* rowp = tile + (q >> 1) * kColHalf + r * 128;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int ch = 4 * (q & 1) + c;
+    *reinterpret_cast<uint4*>(rowp + ((ch ^ (r & 7)) << 4)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
+}
+
+// Stores 32 columns of a gradient row, fp32 accumulator values, as bf16 or as they are.
+__device__ __forceinline__ void store_row(void* base, long long off, const uint32_t (&a)[32], bool f32) {
+  if (f32) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(base) + off);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dst[i] = make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + off);
+    auto pair = [&](int i) { return pack_bf16x2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])); };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pair(8 * i), pair(8 * i + 2), pair(8 * i + 4), pair(8 * i + 6));
+  }
+}
+
+__device__ __forceinline__ void bulk_reduce_add_f32(float* gdst, uint32_t ssrc, uint32_t bytes) {
+  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(gdst), "r"(ssrc),
+               "r"(bytes)
+               : "memory");
+}
+// Adds four floats at gaddr (16-byte aligned) in L2, fire and forget.
+__device__ __forceinline__ void red_add_v4(float* gaddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(gaddr), "f"(__uint_as_float(a)),
+               "f"(__uint_as_float(b)), "f"(__uint_as_float(c)), "f"(__uint_as_float(d))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 struct WinBars {
   uint64_t fixed_full;             // K and V are in place
@@ -150,7 +218,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-__global__ void __launch_bounds__(kFuThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_window_bwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                            const __grid_constant__ WinParams p) {
@@ -342,7 +410,7 @@ __global__ void __launch_bounds__(kFuThreads, 1)
       drain_wait(&bars->mma_done, 0, p.st.limit);
     }
     __syncwarp();
-  } else if (warp == kFuReduceWarp) {
+  } else if (warp == kReduceWarp) {
     // Adds the two staged 16 KB dQ blocks of each pair (columns 0-63) into the
     // accumulator and frees each slot once read.
     if (lane == 0 && n > 0) {
@@ -509,24 +577,29 @@ __global__ void __launch_bounds__(kFuThreads, 1)
       gdst = quarter < 2 ? p.dv : p.dk;
       off = b * p.g_bs + static_cast<long long>(j) * p.g_rs + hk * kD + 64 * half;
     }
-    const int mode = parts ? LCB_GRAD_F32_STORE : LCB_GRAD_BF16;
     const uint32_t tacc = (quarter < 2 ? tDV : tDK) + lane_off + 64 * half;
-    if (n == 0) {
-      if (valid) store_zero(gdst, off, 64, mode);
-    } else if (ok) {
-      ok = mbar_wait_warp(&bars->acc_full, 0, abort_flag, p.st, kWhere | (10u << 16));
-      if (ok) {
-        tc_fence_after();
+    if (n > 0 && ok) ok = mbar_wait_warp(&bars->acc_full, 0, abort_flag, p.st, kWhere | (10u << 16));
+    if (ok) {
+      tc_fence_after();
 #pragma unroll 1
-        for (int ch = 0; ch < 2; ++ch) {
-          uint32_t a[32];
+      for (int ch = 0; ch < 2; ++ch) {
+        uint32_t a[32];
+        if (n > 0) {
           tmem_ld_x32(tacc + ch * 32, a);
-          if (valid) store_grad_chunk(gdst, off + ch * 32, a, 1.f, mode);
+        } else {  // no query sees these keys
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = 0u;
         }
+        if (valid) store_row(gdst, off + ch * 32, a, parts);
       }
     }
   }
-  teardown(tbase, warp);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
 }
 
 // After the pass: dQ from its tiled fp32 accumulator to bf16 rows (the first
@@ -655,7 +728,7 @@ int launch_window_bwd(const WindowBwd& a, cudaStream_t stream) {
   if (p.plan.ctas > 0x7fffffffLL || dq_blocks + sink_blocks + rest_blocks > 0x7fffffffLL) return -1;
   const long long rows = static_cast<long long>(a.B) * p.q_tiles * kT;
   window_bwd_prep_kernel<<<static_cast<unsigned>(std::min<long long>(rows / 8, 152LL * 16)), 256, 0, stream>>>(p);
-  attn_window_bwd_kernel<<<static_cast<unsigned>(p.plan.ctas), kFuThreads, kWinSmem, stream>>>(tk, tv, tq, tdo, p);
+  attn_window_bwd_kernel<<<static_cast<unsigned>(p.plan.ctas), kThreads, kWinSmem, stream>>>(tk, tv, tq, tdo, p);
   window_bwd_finish_kernel<<<static_cast<unsigned>(dq_blocks + sink_blocks + rest_blocks), 256, 0, stream>>>(
       p, static_cast<int>(dq_blocks), static_cast<int>(sink_blocks));
   return cudaGetLastError() == cudaSuccess ? 0 : -4;

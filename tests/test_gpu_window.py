@@ -160,6 +160,67 @@ def test_gradient_against_differences():
         assert abs(got - diff) <= 8 * 3 * 2.0 ** -8 * np.sqrt((to64(g) ** 2 * d ** 2).sum()) + 1e-5 * abs(diff)
 
 
+@pytest.mark.parametrize("B,H,Hkv,Sq,Sk,window,sinks,pos0", [
+    (2, 40, 8, 300, 300, 90, 4, None),     # 160 blocks of 256 query rows: some CTAs walk over two
+    (1, 64, 64, 600, 500, 64, 3, -200),    # ... and some of their blocks see nothing
+    (1, 48, 16, 1030, 700, 200, 0, 400),   # a last block of six rows, rows past every key
+])
+def test_more_blocks_than_sms(B, H, Hkv, Sq, Sk, window, sinks, pos0):
+    """A CTA's second and third block: barrier phases carried over, blocks without keys in between."""
+    q, k, v, do = _rand(Sq, (B, Sq, H, D), (B, Sk, Hkv, D), (B, Sk, Hkv, D), (B, Sq, H, D))
+    _check(q, k, v, window, sinks, pos0, do)
+
+
+def test_broadcast_keys_of_a_batch():
+    """One K/V for every sequence of the batch (batch stride 0): as with copies, gradients per sequence."""
+    q, k, v, do = _rand(12, (3, 300, 4, D), (1, 300, 2, D), (1, 300, 2, D), (3, 300, 4, D))
+    kx, vx = k.expand(3, -1, -1, -1), v.expand(3, -1, -1, -1)
+    a = _check(q, kx, vx, 100, 4, None, do)
+    b = _check(q, kx.contiguous(), vx.contiguous(), 100, 4, None, do)
+    assert all(torch.equal(x, y) for x, y in zip(a[:2] + a[3:], b[:2] + b[3:]))
+    lens = torch.tensor([300, 17, 0], dtype=torch.int32, device="cuda")
+    _decode_check(q[:, :1], kx, vx, lens, 100, 4)
+
+
+def test_wide_window_agrees_with_attn_fwd():
+    """A window over everything is causal attention: the two kernels within both their roundings."""
+    q, k, v = _rand(13, (1, 1000, 3, D), (1, 1000, 3, D), (1, 1000, 3, D))
+    o, lse = lcb.attn_window_fwd(q, k, v, 1000)
+    o2, lse2 = lcb.attn_fwd(q, k, v)
+    torch.cuda.synchronize()
+    assert (lse - lse2).abs().max() <= 1e-5 * lse.abs().max()
+    assert (o.float() - o2.float()).abs().max() <= 4 * 2.0 ** -8 * v.float().abs().max()
+
+
+def test_two_captured_graphs_interleaved():
+    """Two graphs of the whole training pass, each with buffers of its own, replayed in turn and on two streams."""
+    runs = []
+    for seed in (14, 15):
+        t = _rand(seed, (1, 500, 4, D), (1, 500, 2, D), (1, 500, 2, D), (1, 500, 4, D))
+        ws = torch.empty(lcb.attn_window_bwd_workspace_bytes(1, 4, 2, 500, 500, 70, 4), dtype=torch.uint8, device="cuda")
+
+        def step(t=t, ws=ws):
+            o, lse = lcb.attn_window_fwd(*t[:3], 70, 4)
+            return (o, lse, *lcb.attn_window_bwd(*t[:3], o, lse, t[3], 70, 4, workspace=ws))
+        want = [x.clone() for x in step()]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        runs.append((graph, out, want, torch.cuda.Stream(), step))  # step keeps its inputs alive
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, _, _, stream, _ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _, _ in runs:
+        for i, (x, y) in enumerate(zip(out, want)):
+            if i == 2:  # dQ: an fp32 sum in no fixed order, then one rounding: within one bf16 step of either
+                assert (x.float() - y.float()).abs().max() <= 2.0 ** -7 * y.float().abs().max()
+            else:
+                assert torch.equal(x, y)
+
+
 def test_side_stream_and_graph_replay():
     """On a stream of its own; then forward and backward captured once and replayed with other inputs."""
     q, k, v, do = _rand(9, (1, 300, 4, D), (1, 300, 2, D), (1, 300, 2, D), (1, 300, 4, D))
