@@ -26,11 +26,16 @@
 // TMEM: S^T [0,128) (P^T bf16 over it), dP^T [128,256) (then the dQ partial),
 // dV [256,384), dK [384,512).
 //
-// The five products read 288 KB of shared memory a pair, TMA, dS and the dQ
-// staging write and read another 130 KB: at 128 bytes a clock that is 3300
-// clocks of the 4700 that a pair takes, so shared memory bounds the kernel
-// (two groups of eight warps on alternate pairs, which shortens the chain of
-// dependent steps, measured 8% slower: more statistics reads a pair).
+// What bounds it: 32K tokens x 32 heads, window 4096, take 4.45 ms: 4330 clocks
+// a pair of which the products need 2560, at 1.96 GHz under the 1.4 kW cap. By
+// time stamps the compute warps are busy or in short waits throughout (dS 780
+// clocks, P 830, the dQ export 1040 to 1380, waits 1400). None of these moved
+// it: two groups of eight warps on alternate pairs (8% slower), the dQ export
+// in warps of its own (4% slower), -LSE added by the tensor core as one more
+// K step (no change), the last steps of dK after the next dP^T (13% slower: the
+// one dS buffer then waits for them), Q and dO freed and loaded by halves (no
+// change). Waits without a function call, which had cost spills: 6.62 -> 6.21
+// ms with the forward.
 //
 // Shared memory: K, V, a two-slot Q ring with the row statistics of its tile,
 // one dO slot, dS^T, two 16 KB staging blocks for dQ.

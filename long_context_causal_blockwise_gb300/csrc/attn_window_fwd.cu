@@ -22,8 +22,18 @@
 // A CTA stays and walks over its share of the (head, 256 rows) items, each role
 // on its own: the producer loads and the tensor core starts the next item while
 // the epilogue warps still write the last one's O, so an item's start and end
-// hide behind its neighbours (8K tokens, window 1024: 158 us with the epilogue
-// in the softmax warps, 168 with a CTA per item).
+// hide behind its neighbours.
+//
+// What bounds it: the tensor core, fed from shared memory. With the softmax
+// taken out, 131 visits of the 1000-row chunk below take 163 us: 80 clocks a
+// 128 x 128 x 16 product where the pipe alone needs 64. Measured on the way
+// (us; 8K tokens x 32 heads, window 1024 / a 1000-row chunk of a 64K context,
+// window 16384): 192 / 237 with a CTA per item and one thread issuing the
+// products, 165 / 192 with the warp issuing them together (the descriptors stay
+// in uniform registers), 140 / 193 with the epilogue in warps of its own and
+// cut tiles in small loops, 128 / 178 with the maximum looked for only where a
+// tile's sum says so. Splitting a row's columns over two warps (16 softmax
+// warps) changed nothing.
 //
 //   warps 0-3   softmax of query tile 0 (thread = query row = TMEM lane)
 //   warps 4-7   softmax of query tile 1
@@ -186,54 +196,37 @@ __device__ __forceinline__ void weights(const uint32_t* s, uint32_t* pk, float c
   }
 }
 
-// One score tile of a row, all of it visible: P over S in TMEM, m and l brought up.
-__device__ __forceinline__ void softmax_whole(uint32_t tS, float c, float& m, float& l) {
-  uint32_t s[128];
-  tmem_ld_x64(tS, *reinterpret_cast<uint32_t(*)[64]>(s));
-  tmem_ld_x64(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(s + 64));
-  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int e = 0; e < 128; e += 8)
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      m4[u] = fmax3(m4[u], __uint_as_float(s[e + 2 * u]), __uint_as_float(s[e + 2 * u + 1]));
-  raise_max(tS, m, l, fmaxf(m, fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c));
-  const float neg_m = (m == -INFINITY) ? 0.f : -m;
-  float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    uint32_t pk[32];
-    weights(s + 64 * hf, pk, c, neg_m, sa0, sa1);
-    weights(s + 64 * hf + 32, pk + 16, c, neg_m, sb0, sb1);
-    tmem_st_x32(tS + 32 * hf, pk);
+// The columns of a score tile that a row sees: [from, to], and those before
+// `sink` up to `to`. A bit for each of the 32 from column ch on.
+struct Seen {
+  int from, to, sink;
+  __device__ __forceinline__ uint32_t word(int ch) const {
+    return low_bits(to + 1 - ch) & (~low_bits(from - ch) | low_bits(sink - ch));
   }
-  l += (sa0 + sb0) + (sa1 + sb1);
+};
+
+// 64 scores from column ch on, the hidden ones -inf.
+__device__ __forceinline__ void load_seen(uint32_t (&s)[64], uint32_t tS, int ch, const Seen& v) {
+  tmem_ld_x64(tS + ch, s);
+  const uint32_t see[2] = {v.word(ch), v.word(ch + 32)};
+#pragma unroll
+  for (int k = 0; k < 64; ++k)
+    if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = __float_as_uint(-INFINITY);
 }
 
-// The same for a tile that the mask cuts: the row sees columns [from, to], and
-// those before `sink` up to `to`; the second product reads columns [0, used).
-// Columns go in halves of 64 with a bit for each visible one, read twice from
-// TMEM (for the maximum, then for P, which overwrites columns that were read
-// before); a half that no row of the warp sees costs only its zeros. Loops over
-// halves rather than 128 masked registers: with three cut tiles among ten (8K
-// tokens, window 1024) the unrolled form took 193 us where the whole kernel
-// without any mask took 122.
-__device__ __forceinline__ void softmax_cut(uint32_t tS, float c, float& m, float& l, int from, int to, int sink,
-                                            int used) {
-  auto seen = [&](int ch) { return low_bits(to + 1 - ch) & (~low_bits(from - ch) | low_bits(sink - ch)); };
-  auto masked = [&](uint32_t (&s)[64], int ch) {
-    tmem_ld_x64(tS + ch, s);
-    const uint32_t see[2] = {seen(ch), seen(ch + 32)};
-#pragma unroll
-    for (int k = 0; k < 64; ++k)
-      if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = __float_as_uint(-INFINITY);
-  };
+// A score tile in two passes: the maximum first, raised if it has to be, then P
+// over S in TMEM, l brought up. The second product reads columns [0, used).
+// Columns go in halves of 64, read again for the second pass (P overwrites only
+// columns that were read before); a half that no row of the warp sees costs
+// only its zeros. Kept small: it runs for the first tile of a row and where the
+// one-pass forms below give up.
+__device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m, float& l, const Seen v, int used) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int ch = 0; ch < used; ch += 64) {
-    if (!__any_sync(0xffffffffu, seen(ch) | seen(ch + 32))) continue;
+    if (!__any_sync(0xffffffffu, v.word(ch) | v.word(ch + 32))) continue;
     uint32_t s[64];
-    masked(s, ch);
+    load_seen(s, tS, ch, v);
     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int e = 0; e < 64; e += 8)
@@ -248,9 +241,9 @@ __device__ __forceinline__ void softmax_cut(uint32_t tS, float c, float& m, floa
 #pragma unroll 1
   for (int ch = 0; ch < used; ch += 64) {
     uint32_t pk[32];
-    if (__any_sync(0xffffffffu, seen(ch) | seen(ch + 32))) {
+    if (__any_sync(0xffffffffu, v.word(ch) | v.word(ch + 32))) {
       uint32_t s[64];
-      masked(s, ch);
+      load_seen(s, tS, ch, v);
       weights(s, pk, c, neg_m, sa0, sa1);
       weights(s + 32, pk + 16, c, neg_m, sb0, sb1);
     } else {
@@ -261,6 +254,61 @@ __device__ __forceinline__ void softmax_cut(uint32_t tS, float c, float& m, floa
   }
   tmem_wait_st();
   l += (sa0 + sb0) + (sa1 + sb1);
+}
+
+// The one-pass forms take P against the maximum as it stands, without looking
+// for a new one: the tile's row sum tells afterwards whether a score was too far
+// above it (some P over 2^32 makes a sum over 2^32; none makes one up to 2^39 at
+// most). Then, or at a NaN, S is still in place and the two passes run.
+// False: nothing was done.
+constexpr float kMostSum = 549755813888.f;  // 2^39
+
+// All 128 columns visible.
+__device__ __forceinline__ bool softmax_whole(uint32_t tS, float c, float m, float& l) {
+  uint32_t s[128], pk[64];
+  tmem_ld_x64(tS, *reinterpret_cast<uint32_t(*)[64]>(s));
+  tmem_ld_x64(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(s + 64));
+  float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (q & 1)
+      weights(s + 32 * q, pk + 16 * q, c, -m, sb0, sb1);
+    else
+      weights(s + 32 * q, pk + 16 * q, c, -m, sa0, sa1);
+  }
+  const float sum = (sa0 + sb0) + (sa1 + sb1);
+  if (!__all_sync(0xffffffffu, sum <= kMostSum)) return false;
+  tmem_st_x32_nowait(tS, *reinterpret_cast<uint32_t(*)[32]>(pk));
+  tmem_st_x32_nowait(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+  tmem_wait_st();
+  l += sum;
+  return true;
+}
+
+// A tile that the mask cuts.
+__device__ __forceinline__ bool softmax_cut(uint32_t tS, float c, float m, float& l, const Seen v, int used) {
+  uint32_t pk[64];
+  float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t* pks = pk + 32 * half;
+    if (64 * half < used && __any_sync(0xffffffffu, v.word(64 * half) | v.word(64 * half + 32))) {
+      uint32_t s[64];
+      load_seen(s, tS, 64 * half, v);
+      weights(s, pks, c, -m, sa0, sa1);
+      weights(s + 32, pks + 16, c, -m, sb0, sb1);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) pks[k] = 0u;
+    }
+  }
+  const float sum = (sa0 + sb0) + (sa1 + sb1);
+  if (!__all_sync(0xffffffffu, sum <= kMostSum)) return false;
+  tmem_st_x32_nowait(tS, *reinterpret_cast<uint32_t(*)[32]>(pk));
+  if (used > 64) tmem_st_x32_nowait(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+  tmem_wait_st();
+  l += sum;
+  return true;
 }
 
 __device__ __forceinline__ void regs_down() {
@@ -546,15 +594,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int kbase = own.tile(i) * kBN;
         const int p_first = p.w.pos0 + q0;
-        if (kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
-            (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks)) {
-          softmax_whole(tS, c, m, l);
-        } else {
-          // The mask cuts this tile: the row sees columns [from, to], and those before `sink` up to `to`.
-          const int pos = p_first + row;
-          softmax_cut(tS, c, m, l, pos - p.w.window + 1 - kbase, min(pos, p.w.Sk - 1) - kbase, p.w.sinks - kbase,
-                      used_columns(p.w, own, own.tile(i)));
+        const int pos = p_first + row;
+        const Seen v = {pos - p.w.window + 1 - kbase, min(pos, p.w.Sk - 1) - kbase, p.w.sinks - kbase};
+        const int used = used_columns(p.w, own, own.tile(i));
+        bool done = false;
+        if (!__any_sync(0xffffffffu, m == -INFINITY)) {
+          if (kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
+              (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks))
+            done = softmax_whole(tS, c, m, l);
+          else
+            done = softmax_cut(tS, c, m, l, v, used);
         }
+        if (!done) softmax_two_pass(tS, c, m, l, v, used);
         tc_fence_before();
         mbar_arrive(&bars->p_full[t]);
       }
