@@ -9,9 +9,10 @@
 // one while the softmax warps work on the other; K and V stream by TMA through
 // a four-slot ring; S and O live in TMEM, P goes back over S as the second
 // product's A operand; the running maximum m is raised lazily, only when a score
-// passes it by more than 32 in base 2. O / l is exact for any m; P then stays
-// below 2^32, l below 2^61 and O below 2^61 max |v|, and what falls under
-// 2^-126 is 2^-126 of a term that is there.
+// passes it by 32 to 39 in base 2. O / l is exact for any m; P stays below 2^39,
+// l below 2^60 and O below 2^60 max |v|, and what falls under 2^-126 is 2^-126
+// of a term that is there.
+//
 // What the window adds: a CTA streams only the key tiles that one of its rows
 // can see (the sink tiles, then the window's), each query tile skips those of
 // them that it does not see itself, and a tile needs the per-element mask only
