@@ -106,6 +106,16 @@ bool rows_apart(int B, int rows, long long row, long long rs, long long bs) {
 }
 bool stride_ok(long long s) { return s >= 0 && (s % 8) == 0 && s < (1LL << 38); }
 
+// A bf16 input [B, rows, heads, 128] for TMA or 16-byte loads.
+bool window_input(const void* p, long long rs, long long bs, int heads) {
+  return p && aligned16(p) && stride_ok(rs) && stride_ok(bs) && rs >= static_cast<long long>(heads) * kHeadDim;
+}
+// A bf16 output: its rows also lie apart from one another.
+bool window_output(const void* p, long long rs, long long bs, int B, int rows, int heads) {
+  return p && aligned16(p) && stride_ok(rs) && stride_ok(bs) &&
+         rows_apart(B, rows, static_cast<long long>(heads) * kHeadDim, rs, bs);
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -155,6 +165,20 @@ int set_smem_limit_once(DeviceOnce& once, const void* kernel, int bytes) {
       dev, current_context_id(),
       [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess
+                   ? LCB_OK
+                   : LCB_ERR_CUDA;
+      },
+      LCB_ERR_CUDA);
+}
+
+int allow_clusters_once(DeviceOnce& once, const void* kernel, int bytes) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return LCB_ERR_CUDA;
+  return once.run(
+      dev, current_context_id(),
+      [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess
                    ? LCB_OK
                    : LCB_ERR_CUDA;
       },
@@ -812,16 +836,6 @@ static int prep_window(WindowShape* w, int B, int H, int Hkv, int Sq, int Sk, in
   w->window = std::min(window, kWindowMaxWindow);
   w->sinks = std::min(sinks, Sk);
   return LCB_OK;
-}
-
-// A bf16 input [B, rows, heads, 128] for TMA or 16-byte loads.
-static bool window_input(const void* p, long long rs, long long bs, int heads) {
-  return p && aligned16(p) && stride_ok(rs) && stride_ok(bs) && rs >= static_cast<long long>(heads) * kHeadDim;
-}
-// A bf16 output: its rows also lie apart from one another.
-static bool window_output(const void* p, long long rs, long long bs, int B, int rows, int heads) {
-  return p && aligned16(p) && stride_ok(rs) && stride_ok(bs) &&
-         rows_apart(B, rows, static_cast<long long>(heads) * kHeadDim, rs, bs);
 }
 
 static WindowSplit split_args(const void* q, const void* k, const void* v, const int* lens, void* o, float* lse, int B,

@@ -346,20 +346,9 @@ struct Form {
     return cfg;
   }
 
-  // Per device context: clusters above 8 CTAs and this form's shared memory allowed.
   static int allow() {
     static DeviceOnce once;
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return -4;
-    return once.run(
-        dev, current_context_id(),
-        [] {
-          return cudaFuncSetAttribute(fn(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                         cudaFuncSetAttribute(fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
-                     ? 0
-                     : -4;
-        },
-        -4);
+    return allow_clusters_once(once, fn(), kSmem);
   }
 
   // Clusters of this size that the GPU holds at once (a property of the device model, asked for once), or 0.

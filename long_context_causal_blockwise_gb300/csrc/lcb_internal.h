@@ -34,6 +34,9 @@ unsigned long long current_context_id();
 // attributes belong to a device context). Returns 0, or LCB_ERR_CUDA.
 int set_smem_limit_once(DeviceOnce& once, const void* kernel, int bytes);
 
+// The same for a kernel launched in clusters, which may have up to 16 CTAs (8 is the portable limit).
+int allow_clusters_once(DeviceOnce& once, const void* kernel, int bytes);
+
 // One block of a forward launch (rows relative to the shared tensors).
 struct FwdTask {
   int q_off, q_len, k_off, k_len, causal, o_mode;  // o_mode: 0 bf16, 1 fp32, 2 merge into fp32 (O, LSE)
