@@ -399,10 +399,10 @@ int lcb_rope_axes(const void* x, void* y, int B, int S, int H, int D, double the
  * strides, o and dO share strides, dk and dv share strides; outputs must not
  * overlap themselves or other arguments.
  * Infinities and NaN: a score hidden by the mask is dropped whatever its value.
- * In v (and in q, k, dO of the backward) a non-finite row spreads to the rows
- * of the same 128 x 128 tile (16 keys in attn_window_decode) that do not see
- * it, since 0 * NaN is NaN in the products. Keys at or past Sk or lens[b] are
- * never read.
+ * In v (and in q, k, dO of the backward) a non-finite row spreads to rows that
+ * do not see it but share a tile with it (128 x 128 at most; the sizes decide),
+ * since 0 * NaN is NaN in the products. Keys at or past Sk or lens[b] are never
+ * read.
  *
  * attn_window_fwd — O (bf16 [B, Sq, H, D]) and LSE (fp32, natural log, scale
  * included). Deterministic.

@@ -890,10 +890,7 @@ int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float*
   if (!window_input(q, q_row_stride, q_batch_stride, H) || !window_input(k, kv_row_stride, kv_batch_stride, Hkv) ||
       !window_input(v, kv_row_stride, kv_batch_stride, Hkv))
     return LCB_ERR_ARG;
-  // Query rows that fit one 16-row tile of the split kernel go there: a
-  // 128-row tile would be mostly padding, and one CTA a head would walk the
-  // whole window.
-  if (static_cast<long long>(Sq) * (H / Hkv) <= 16)
+  if (window_split_pays(B, H, Hkv, w))
     return finish(launch_window_split(split_args(q, k, v, nullptr, o, lse, B, H, Hkv, Sq, w, scale, q_row_stride,
                                                  q_batch_stride, kv_row_stride, kv_batch_stride, o_row_stride,
                                                  o_batch_stride, lse_head_stride, lse_batch_stride),

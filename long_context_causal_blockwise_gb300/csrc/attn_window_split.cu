@@ -32,6 +32,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "attn_window.cuh"
 #include "lcb_internal.h"
 
 namespace cg = cooperative_groups;
@@ -40,6 +41,7 @@ namespace lcb {
 namespace {
 
 constexpr int kD = 128;
+constexpr int kSms = 152;
 constexpr int kKeys = 16;  // keys per warp step
 constexpr int kMaxCluster = 16;  // above 8 the size is not portable, but allowed on request
 constexpr float kLn2 = 0.69314718055994531f;
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_split_kernel(const __grid_
           float mx = fmaxf(s[nt][e], s[nt][2 + e]);
 #pragma unroll
           for (int w = 4; w < 32; w *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          mx = fmaxf(mx, m[nt][e]);
+          mx = mx > m[nt][e] + kRescaleThreshold ? mx : m[nt][e];  // each row for itself: no other row's keys change its bits
           const float a = weight(m[nt][e], mx);
           m[nt][e] = mx;
           l[nt][e] *= a;
@@ -398,9 +400,13 @@ int launch_rows(WindowSplit& p, long long tiles, long long steps, cudaStream_t s
   if (2 * c2 >= 4 * c4 && 2 * c2 >= 8 * c8) {
     p.cluster = std::max(1, c2);
     if (c2 == 0) {
-      // More tiles than fit at once: the cluster (up to 8) whose last wave is fullest.
+      // More tiles than fit at once. A wave costs a start of some 4 us, so one
+      // CTA a tile; or, where each still has 32 steps and that hides under the
+      // others' loads, the cluster (up to 8) whose last wave is fullest. us by
+      // cluster 1, 2, 3, 4, 8: 2048 tiles of 129 steps 347, 324, 321, 347, 369;
+      // of 17 steps 55, 61, 66, 81, 126; 4096 of 5 steps 45, 63, 80, 100, 194.
       double best = 0;
-      for (int c = 1; c <= 8 && 2 * c <= std::max<long long>(2, steps); ++c) {
+      for (int c = 1; c <= 8 && (c == 1 || c * 32 <= steps); ++c) {
         const double waves = static_cast<double>(tiles) / std::max(1, Form<NT, 2>::resident(c));
         const double full = waves / std::ceil(waves);
         if (full > best + 0.02) best = full, p.cluster = c;
@@ -417,6 +423,33 @@ int launch_rows(WindowSplit& p, long long tiles, long long steps, cudaStream_t s
 }
 
 }  // namespace
+
+// Query rows of one 16-row tile per K/V head always come here. For more, two
+// estimates in us, fitted to 190 forwards (1 to 2500 query rows, 1 to 40 heads,
+// G from 1 to 8, windows of 16 to 16384; the slower form is picked in one of
+// ten of them, by 20% at most). This kernel: a start, each row tile's own, and
+// its tensor work, whose keys feed 16 rows from registers. The 128-row tiles of
+// attn_window_fwd: a CTA walks the visits of 256 query rows of one head. us,
+// this kernel / tiles:
+//   H 32, Hkv 8, window 16384:  8 tokens 38 / 158, 32 tokens 91 / 160, 64 tokens 173 / 160
+//   H 32, Hkv 32, window 1024: 32 tokens 13 / 19, 128 tokens 27 / 20
+//   H 4, Hkv 4, window 4096:  256 tokens 26 / 53
+// More row tiles than the GPU holds at once do not pay: 1024 of 256 keys take
+// 64, 512 take 19.
+bool window_split_pays(int B, int H, int Hkv, const WindowShape& w) {
+  const int G = H / Hkv;
+  const long long rows = static_cast<long long>(w.Sq) * G;
+  if (rows <= 16) return true;
+  const double row_tiles = static_cast<double>(B) * Hkv * ((rows + 15) / 16);
+  if (row_tiles > 4 * kSms) return false;
+  const double reach = static_cast<double>(w.window) + w.sinks + (14 + G) / G + 1;  // keys that a row tile may see
+  const double keys = std::min(reach, std::max(0., std::min<double>(w.Sk, w.pos0 + 0.5 * w.Sq + 1)));
+  const double split_us = 6.4 + row_tiles * (7.8e-3 + 7.7e-5 * keys) + 7.3e-4 * std::min(keys, 4096.);
+  const int visits = key_tiles(w, (w.Sq - 1) / 256 * 256, 256).count();
+  const double waves = std::ceil(static_cast<double>(B) * H * ((w.Sq + 255) / 256) / kSms);
+  const double tiles_us = 0.6 + waves * (5.4 + 1.18 * visits);
+  return split_us < tiles_us;
+}
 
 int launch_window_split(WindowSplit p, cudaStream_t stream) {
   const int R = p.T * (p.H / p.Hkv);

@@ -185,5 +185,6 @@ struct WindowSplit {
   int row_tiles, cluster;  // set by the launch
 };
 int launch_window_split(WindowSplit p, cudaStream_t stream);
+bool window_split_pays(int B, int H, int Hkv, const WindowShape& w);  // for a forward without lens; Sq, Sk > 0
 
 }  // namespace lcb

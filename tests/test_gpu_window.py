@@ -62,6 +62,27 @@ def test_fwd_bwd_vs_oracle(B, H, Hkv, Sq, Sk, window, sinks, pos0):
     _check(q, k, v, window, sinks, pos0, do)
 
 
+@pytest.mark.parametrize("B,H,Hkv,Sq,Sk,window,sinks,pos0", [c for c in CASES if c[3] * c[1] // c[2] > 16])
+def test_forward_in_128_row_tiles(B, H, Hkv, Sq, Sk, window, sinks, pos0):
+    """The same with so many heads (more than 608 tiles of 16 rows) that the keys are not split over a cluster."""
+    n = 608 // (B * Hkv * ((Sq * (H // Hkv) + 15) // 16)) + 1
+    q, k, v = _rand(Sq + Sk + window % 1000, (B, Sq, n * H, D), (B, Sk, n * Hkv, D), (B, Sk, n * Hkv, D))
+    _check(q, k, v, window, sinks, pos0)
+
+
+@pytest.mark.parametrize("H,Hkv,Sq,Sk,window", [(32, 8, 5, 9000, 8000), (8, 1, 33, 5000, 4000), (2, 2, 500, 3000, 2000),
+                                                (3, 1, 7, 2000, 1500), (40, 8, 30, 700, 700)])
+def test_forward_split_over_row_tiles(H, Hkv, Sq, Sk, window):
+    """More query rows than one 16-row tile, few enough heads that their keys are split over clusters all the same:
+    row tiles that begin inside a token's group of heads, a last tile with rows missing."""
+    q, k, v = _rand(Sk, (1, Sq, H, D), (1, Sk, Hkv, D), (1, Sk, Hkv, D))
+    a = _check(q, k, v, window, 3, None)
+    b = lcb.attn_window_fwd(q, k, v, window, 3)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    _check(q, k, v, window, 0, Sk - 2 * Sq)  # the chunk before the last keys
+    _check(q, k, v, 20, 3, Sk + 5)  # its window past the keys for the last rows
+
+
 @pytest.mark.parametrize("H,Hkv,Sq", [(1, 1, 1), (1, 1, 16), (8, 1, 2), (8, 8, 16), (16, 1, 1), (12, 1, 1), (6, 2, 5)])
 def test_few_rows_forward(H, Hkv, Sq):
     """Up to 16 query rows a K/V head: the keys split over a cluster of CTAs."""
@@ -71,18 +92,20 @@ def test_few_rows_forward(H, Hkv, Sq):
         _check(q, k, v, window, sinks, pos0, name=f"Sk {Sk} window {window}")
 
 
-def test_large_scores_and_sharp_rows():
+@pytest.mark.parametrize("H", [2, 20])
+def test_large_scores_and_sharp_rows(H):
     """Scores of hundreds (the running maximum moves by more than 2^8 between tiles), and one key that takes all."""
-    q, k, v, do = _rand(5, (1, 500, 2, D), (1, 500, 2, D), (1, 500, 2, D), (1, 500, 2, D))
+    q, k, v, do = _rand(5, *[(1, 500, H, D)] * 4)
     k *= torch.linspace(0.1, 6, 500, device="cuda")[None, :, None, None].to(k.dtype)
     q *= 4
     _check(q, k, v, 200, 4, None, do)
 
 
-def test_scores_of_minus_infinity_and_hidden_nan_keys():
+@pytest.mark.parametrize("H", [1, 33])  # keys split over a cluster; 128-row tiles
+def test_scores_of_minus_infinity_and_hidden_nan_keys(H):
     """k = -inf towards a positive q gives visible scores of -inf (weight 0), the type's lowest value gives a score that
     no other key's weight survives next to; NaN in a hidden key's k touches no row."""
-    q, k, v = _rand(6, (1, 300, 1, D), (1, 300, 1, D), (1, 300, 1, D))
+    q, k, v = _rand(6, *[(1, 300, H, D)] * 3)
     q[:] = q.abs() + 0.1
     ref, lse = lcb.attn_window_fwd(q, k, v, 50)  # the same tiles: equal bits where nothing hidden gets in
     k2 = k.clone()
@@ -271,6 +294,14 @@ def test_decode_vs_oracle(H, Hkv, T, window, sinks):
         k[b, max(0, n):] = float("nan")
         v[b, max(0, n):] = float("nan")
     _decode_check(q, k, v, lens, window, sinks)
+
+
+@pytest.mark.parametrize("B,H,Hkv,T,Smax", [(37, 32, 32, 1, 70), (37, 32, 32, 1, 1500), (90, 16, 8, 5, 1100)])
+def test_decode_more_tiles_than_fit(B, H, Hkv, T, Smax):
+    """Batches whose tiles run in several waves, with short caches and with long ones."""
+    lens = Smax - 3 * torch.arange(B, dtype=torch.int32, device="cuda")
+    q, k, v = _rand(Smax, (B, T, H, D), (B, Smax, Hkv, D), (B, Smax, Hkv, D))
+    _decode_check(q, k, v, lens, 1400, 2)
 
 
 def test_decode_graph_follows_the_lengths():
