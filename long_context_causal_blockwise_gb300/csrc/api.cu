@@ -793,7 +793,7 @@ int lcb_rope_axes(const void* x, void* y, int B, int S, int H, int D, double the
                   long long pos_row_stride, int inverse, long long row_stride, long long batch_stride, void* stream) {
   if (B < 1 || H < 1 || S < 0) return LCB_ERR_ARG;
   if (D != kHeadDim || (pos_bytes != 4 && pos_bytes != 8)) return LCB_ERR_UNSUPPORTED;
-  if (!(theta > 0.0) || !std::isfinite(theta) || (inverse != 0 && inverse != 1)) return LCB_ERR_ARG;
+  if (!(theta >= 1e-300) || !std::isfinite(theta) || (inverse != 0 && inverse != 1)) return LCB_ERR_ARG;
   if (n_axes < 1 || n_axes > 64 || !pair_axis) return LCB_ERR_ARG;
   // The 64 powers cost more than the launch: a thread keeps those of the base it used last.
   static thread_local RopeAxes ax;

@@ -452,6 +452,7 @@ bool window_split_pays(int B, int H, int Hkv, const WindowShape& w) {
 }
 
 int launch_window_split(WindowSplit p, cudaStream_t stream) {
+  if (static_cast<long long>(p.T) * (p.H / p.Hkv) > kWindowMaxRows) return -1;
   const int R = p.T * (p.H / p.Hkv);
   const int rows = R <= 8 ? 8 : 16;
   p.row_tiles = (R + rows - 1) / rows;

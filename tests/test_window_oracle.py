@@ -150,7 +150,7 @@ def test_rope_axes_refusals():
     def call(x=FAKE, S=8, D=128, theta=1e6, pos=FAKE, pb=4, n=2, arr=axes, ps=(8, 0, 1), inverse=0, rs=256, bs=0, B=1):
         return lib.lcb_rope_axes(x, FAKE, B, S, 2, D, theta, pos, pb, n, arr, *ps, inverse, rs, bs, NUL)
     assert call(D=64) == UNSUP and call(pb=2) == UNSUP
-    for kw in (dict(theta=0.0), dict(theta=float("inf")), dict(n=1), dict(n=0), dict(n=65), dict(arr=None),
+    for kw in (dict(theta=0.0), dict(theta=1e-310), dict(theta=float("inf")), dict(n=1), dict(n=0), dict(n=65), dict(arr=None),
                dict(pos=NUL), dict(pos=ctypes.c_void_p(6)), dict(pos=ctypes.c_void_p(12), pb=8), dict(ps=(-1, 0, 1)),
                dict(inverse=2), dict(rs=255), dict(rs=128), dict(x=ctypes.c_void_p(2)), dict(B=2, bs=0),
                dict(B=2, bs=256)):
