@@ -25,6 +25,11 @@
 // the epilogue warps still write the last one's O, so an item's start and end
 // hide behind its neighbours.
 //
+// Where there are fewer items than half the SMs, a cluster of CTAs shares one:
+// each takes an equal run of its visits, O, m and l stay in shared memory, and
+// after the pass every CTA joins its share of the rows from all of them through
+// distributed shared memory.
+//
 // What bounds it: the tensor core, fed from shared memory. With the softmax
 // taken out, 131 visits of the 1000-row chunk below take 163 us: 80 clocks a
 // 128 x 128 x 16 product where the pipe alone needs 64. Measured on the way
@@ -44,13 +49,18 @@
 //
 // TMEM (512 columns x 128 lanes, fp32): S_0 [0,128), S_1 [128,256),
 // O_0 [256,384), O_1 [384,512).
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 
 #include "attn_window.cuh"
 #include "lcb_internal.h"
 #include "mma_warp.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace lcb {
 namespace {
@@ -76,6 +86,7 @@ constexpr uint32_t kSmBar = kSmRow + 2 * kBM * 8;
 constexpr float kRescaleThreshold = 32.0f;  // log2 units
 constexpr long long kGroupBytes = 80LL << 20;  // K and V of the windows that a group of heads keeps in L2
 constexpr int kSms = 152;
+constexpr int kMaxCluster = 16;  // above 8 the size is not portable, but allowed on request
 
 struct Bars {
   uint64_t q_full[2], q_empty[2];
@@ -95,7 +106,7 @@ struct Params {
   __nv_bfloat16* o;
   float* lse;
   long long o_rs, o_bs, l_hs, l_bs;
-  int B, H, G, items, head_group;
+  int B, H, G, items, head_group, parts;  // parts: CTAs of a cluster that share an item
   WindowShape w;
   float scale_log2;
   DevStatus st;
@@ -127,37 +138,60 @@ __device__ __forceinline__ Item item_of(const Params& p, int k) {
 }
 
 // The visits of an item's two query tiles: `all` is the stream of key tiles that
-// either one sees; query tile t takes part in visits [0, sinks[t]) and
-// [from[t], to[t]) of the n.
+// either one sees, of which [first, end) are this CTA's; query tile t takes part
+// in those before sinks[t] and those of [from[t], to[t]).
 struct Visits {
-  KeyTiles all, own[2];
-  int n, sinks[2], from[2], to[2];
-  __device__ __forceinline__ bool any(int t) const { return own[t].count() > 0; }
+  KeyTiles all;
+  int first, end, own_ns[2], sinks[2], from[2], to[2];
+  __device__ __forceinline__ bool any(int t) const { return last(t) >= first; }
   __device__ __forceinline__ bool active(int t, int i) const { return i < sinks[t] || (i >= from[t] && i < to[t]); }
   __device__ __forceinline__ int last(int t) const { return to[t] > from[t] ? to[t] - 1 : sinks[t] - 1; }
 };
 
-__device__ __forceinline__ Visits visits(const WindowShape& w, int q0) {
+// Key tile kt in the stream `all`.
+__device__ __forceinline__ int visit_of(const KeyTiles& all, int kt) { return kt <= all.ns ? kt : all.ns + kt - all.lo; }
+
+// The first of n visits that are part `part`'s.
+__device__ __forceinline__ int part_begin(int n, int part, int parts) {
+  return static_cast<int>(static_cast<long long>(n) * part / parts);
+}
+
+// How many of a query tile's own visits come before visit i of the stream.
+__device__ __forceinline__ int visits_before(const KeyTiles& all, const KeyTiles& own, int i) {
+  const int to = visit_of(all, own.hi);
+  if (own.ns == own.lo) return min(i, to);  // one stretch
+  return min(i, visit_of(all, own.ns)) + max(0, min(i, to) - visit_of(all, own.lo));
+}
+
+template <bool kParts>
+__device__ __forceinline__ Visits visits(const Params& p, int q0, int part) {
   Visits v;
-  v.all = key_tiles(w, q0, 2 * kBM);
-  v.n = v.all.count();
+  v.all = key_tiles(p.w, q0, 2 * kBM);
+  const int n = v.all.count();
+  v.first = kParts ? part_begin(n, part, p.parts) : 0;
+  v.end = kParts ? part_begin(n, part + 1, p.parts) : n;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const KeyTiles k = v.own[t] = key_tiles(w, q0 + t * kBM, kBM);
-    auto visit = [&](int kt) { return kt <= v.all.ns ? kt : v.all.ns + kt - v.all.lo; };  // kt in the stream
-    v.sinks[t] = visit(k.ns);
-    v.from[t] = visit(k.lo);
-    v.to[t] = visit(k.hi);
+    const KeyTiles k = key_tiles(p.w, q0 + t * kBM, kBM);
+    v.own_ns[t] = k.ns;
+    v.sinks[t] = visit_of(v.all, k.ns);
+    v.from[t] = visit_of(v.all, k.lo);
+    v.to[t] = visit_of(v.all, k.hi);
     if (k.ns == k.lo) v.sinks[t] = v.to[t];  // one stretch
+    if (kParts) {
+      v.sinks[t] = min(v.sinks[t], v.end);
+      v.from[t] = max(v.from[t], v.first);
+      v.to[t] = min(v.to[t], v.end);
+    }
   }
   return v;
 }
 
-// The columns of key tile kt that query tile `own` can use: all of a window
+// The columns of key tile kt that a query tile with own_ns sink tiles can use: all of a window
 // tile's, a sink tile's up to the last sink. The second product runs over
 // these alone, in steps of 16.
-__device__ __forceinline__ int used_columns(const WindowShape& w, const KeyTiles& own, int kt) {
-  return kt < own.ns ? min(kBN, w.sinks - kt * kBN) : kBN;
+__device__ __forceinline__ int used_columns(const WindowShape& w, int own_ns, int kt) {
+  return kt < own_ns ? min(kBN, w.sinks - kt * kBN) : kBN;
 }
 
 // Raises the running maximum m to m_new where that passes it by more than the
@@ -312,10 +346,17 @@ __device__ __forceinline__ bool softmax_cut(uint32_t tS, float c, float m, float
   return true;
 }
 
+// Piece `piece` (four floats) of a query row's O in shared memory, where parts are joined.
+__device__ __forceinline__ float4* part_o(uint8_t* smem, int row, int piece) {
+  return reinterpret_cast<float4*>(smem + kSmKV + row * (kD * 4) + ((piece ^ (row & 31)) << 4));
+}
+
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
 }
 
+// kParts: one item per cluster, its visits dealt to the cluster's CTAs.
+template <bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
@@ -360,6 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = bars->tmem_base;
 
+  const int part = kParts ? static_cast<int>(blockIdx.x) % p.parts : 0;
+  const int item0 = static_cast<int>(blockIdx.x) / (kParts ? p.parts : 1);
+  auto next_item = [&](int k) { return kParts ? p.items : k + static_cast<int>(gridDim.x); };
+
   // Every role walks the same items; barrier phases carry on from one to the
   // next (ring slots by a running count, the others by one count per query tile).
   if (warp >= kProducerWarp) {
@@ -371,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;              // K and V tiles loaded
         uint32_t nq[2] = {0, 0};  // Q tiles loaded
         bool ok = true;
-        for (int k = static_cast<int>(blockIdx.x); k < p.items && ok; k += static_cast<int>(gridDim.x)) {
+        for (int k = item0; k < p.items && ok; k = next_item(k)) {
           const Item w = item_of(p, k);
-          const Visits v = visits(p.w, w.q0);
+          const Visits v = visits<kParts>(p, w.q0, part);
           const int xq = w.h * kD, xk = (w.h / p.G) * kD;
           for (int t = 0; t < 2 && ok; ++t) {
             if (!v.any(t)) continue;
@@ -385,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           w.q0 + t * kBM, w.b);
             ++nq[t];
           }
-          for (int i = 0; i < v.n && ok; ++i) {
+          for (int i = v.first; i < v.end && ok; ++i) {
             for (int kv = 0; kv < 2; ++kv, ++it) {
               const int slot = it % kStages;
               const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
@@ -453,10 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;  // visits of the items before, and of this one
       uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
       bool ok = true;
-      for (int k = static_cast<int>(blockIdx.x); k < p.items && ok; k += static_cast<int>(gridDim.x)) {
+      for (int k = item0; k < p.items && ok; k = next_item(k)) {
         const Item w = item_of(p, k);
-        const Visits v = visits(p.w, w.q0);
-        if (v.n == 0) continue;
+        const Visits v = visits<kParts>(p, w.q0, part);
+        if (v.first == v.end) continue;
         uint32_t acc[2] = {0, 0};
         ok = wait_kv(g, 0);
         // First products. S_t is free: the previous item's last P V of tile t was issued before.
@@ -467,14 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) continue;
           q_phase[t] ^= 1u;
           tc_fence_after();
-          if (v.active(t, 0)) {
+          if (v.active(t, v.first)) {
             issue_qk(t, g);
-            if (v.last(t) == 0) tc_commit_if(&bars->q_empty[t], one);
+            if (v.last(t) == v.first) tc_commit_if(&bars->q_empty[t], one);
           }
         }
         if (!ok) break;
         tc_commit_if(&bars->kv_empty[2 * (g & 1u)], one);
-        for (int i = 0; i < v.n && ok; ++i, ++g) {
+        for (int i = v.first; i < v.end && ok; ++i, ++g) {
           ok = wait_kv(g, 1);
           if (!ok) break;
           bool k_ready = false;
@@ -491,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o_phase[t] ^= 1u;
               }
               tc_fence_after();
-              issue_pv(t, g, acc[t], used_columns(p.w, v.own[t], v.all.tile(i)));
+              issue_pv(t, g, acc[t], used_columns(p.w, v.own_ns[t], v.all.tile(i)));
               acc[t] = 1;
               if (i == v.last(t)) tc_commit_if(&bars->o_full[t], one);
             }
@@ -507,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           tc_commit_if(&bars->kv_empty[2 * (g & 1u) + 1], one);
-          if (i + 1 < v.n) tc_commit_if(&bars->kv_empty[2 * ((g + 1) & 1u)], one);
+          if (i + 1 < v.end) tc_commit_if(&bars->kv_empty[2 * ((g + 1) & 1u)], one);
         }
       }
       // Every MMA issued must finish before TMEM is released.
@@ -518,61 +563,90 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kEpilogueWarp) {
     // ------------------------------------------------------------ epilogue
     regs_down();
-    // O of a finished query tile out of TMEM while the softmax warps are on the next item.
     const int row = 32 * (warp - kEpilogueWarp) + lane;
     const uint32_t tO = tbase + 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    uint32_t phase[2] = {0, 0};
-    bool ok = true;
-    for (int k = static_cast<int>(blockIdx.x); k < p.items && ok; k += static_cast<int>(gridDim.x)) {
-      const Item w = item_of(p, k);
+    if constexpr (kParts) {
+      // This part's O, not divided by l yet, over the ring once nothing reads it any more, 16-byte pieces of a row
+      // exchanged by the row's number (a warp writes a column of pieces, and reads a row). (m, l) are there already.
+      const Visits v = visits<true>(p, item_of(p, item0).q0, part);
+      bool ok = true;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (!ok) continue;
-        const int qi = w.q0 + t * kBM + row;
-        const bool valid = qi < p.w.Sq;
-        const bool any = key_tiles(p.w, w.q0 + t * kBM, kBM).count() > 0;  // else O was never formed
-        float m = -INFINITY, l = 0.f;
-        if (any) {
-          ok = mbar_wait_warp(&bars->row_full[t], phase[t], abort_flag, p.st, kWhere | (10u << 16));
-          if (!ok) continue;
-          const float2 r = reinterpret_cast<const float2*>(smem + kSmRow)[t * kBM + row];
-          m = r.x;
-          l = r.y;
-          mbar_arrive(&bars->row_free[t]);
-          ok = mbar_wait_warp(&bars->o_full[t], phase[t], abort_flag, p.st, kWhere | (6u << 16));
-          if (!ok) continue;
-          phase[t] ^= 1u;
-          tc_fence_after();
-        }
-        const float inv_l = l == 0.f ? 0.f : 1.f / l;
-        __nv_bfloat16* dst = p.o + w.b * p.o_bs + static_cast<long long>(qi) * p.o_rs + w.h * kD;
+        if (v.any(t))
+          ok = ok && mbar_wait_warp(&bars->row_full[t], 0, abort_flag, p.st, kWhere | (10u << 16)) &&
+               mbar_wait_warp(&bars->o_full[t], 0, abort_flag, p.st, kWhere | (6u << 16));
+        else
+          reinterpret_cast<float2*>(smem + kSmRow)[t * kBM + row] = make_float2(-INFINITY, 0.f);
+      }
+      tc_fence_after();
 #pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || !v.any(t)) continue;
+#pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t o[32];
-          if (any) {
-            tmem_ld_x32(tO + t * 128 + ch * 32, o);
-            if (ch == 3) {
-              tc_fence_before();
-              mbar_arrive(&bars->o_free[t]);  // the next item's P V may write over O
-            }
-          } else {
+          tmem_ld_x32(tO + t * 128 + ch * 32, o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0u;
-          }
-          if (valid) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint4 u;
-              u.x = pack_bf16x2(__uint_as_float(o[j]) * inv_l, __uint_as_float(o[j + 1]) * inv_l);
-              u.y = pack_bf16x2(__uint_as_float(o[j + 2]) * inv_l, __uint_as_float(o[j + 3]) * inv_l);
-              u.z = pack_bf16x2(__uint_as_float(o[j + 4]) * inv_l, __uint_as_float(o[j + 5]) * inv_l);
-              u.w = pack_bf16x2(__uint_as_float(o[j + 6]) * inv_l, __uint_as_float(o[j + 7]) * inv_l);
-              *reinterpret_cast<uint4*>(dst + ch * 32 + j) = u;
-            }
-          }
+          for (int j = 0; j < 32; j += 4)
+            *part_o(smem, t * kBM + row, ch * 8 + j / 4) = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                                                                       __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
         }
-        if (valid)
-          p.lse[w.b * p.l_bs + w.h * p.l_hs + qi] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+      }
+    } else {
+      // O of a finished query tile out of TMEM while the softmax warps are on the next item.
+      uint32_t phase[2] = {0, 0};
+      bool ok = true;
+      for (int k = item0; k < p.items && ok; k = next_item(k)) {
+        const Item w = item_of(p, k);
+  #pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok) continue;
+          const int qi = w.q0 + t * kBM + row;
+          const bool valid = qi < p.w.Sq;
+          const bool any = key_tiles(p.w, w.q0 + t * kBM, kBM).count() > 0;  // else O was never formed
+          float m = -INFINITY, l = 0.f;
+          if (any) {
+            ok = mbar_wait_warp(&bars->row_full[t], phase[t], abort_flag, p.st, kWhere | (10u << 16));
+            if (!ok) continue;
+            const float2 r = reinterpret_cast<const float2*>(smem + kSmRow)[t * kBM + row];
+            m = r.x;
+            l = r.y;
+            mbar_arrive(&bars->row_free[t]);
+            ok = mbar_wait_warp(&bars->o_full[t], phase[t], abort_flag, p.st, kWhere | (6u << 16));
+            if (!ok) continue;
+            phase[t] ^= 1u;
+            tc_fence_after();
+          }
+          const float inv_l = l == 0.f ? 0.f : 1.f / l;
+          __nv_bfloat16* dst = p.o + w.b * p.o_bs + static_cast<long long>(qi) * p.o_rs + w.h * kD;
+  #pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t o[32];
+            if (any) {
+              tmem_ld_x32(tO + t * 128 + ch * 32, o);
+              if (ch == 3) {
+                tc_fence_before();
+                mbar_arrive(&bars->o_free[t]);  // the next item's P V may write over O
+              }
+            } else {
+  #pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = 0u;
+            }
+            if (valid) {
+  #pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                uint4 u;
+                u.x = pack_bf16x2(__uint_as_float(o[j]) * inv_l, __uint_as_float(o[j + 1]) * inv_l);
+                u.y = pack_bf16x2(__uint_as_float(o[j + 2]) * inv_l, __uint_as_float(o[j + 3]) * inv_l);
+                u.z = pack_bf16x2(__uint_as_float(o[j + 4]) * inv_l, __uint_as_float(o[j + 5]) * inv_l);
+                u.w = pack_bf16x2(__uint_as_float(o[j + 6]) * inv_l, __uint_as_float(o[j + 7]) * inv_l);
+                *reinterpret_cast<uint4*>(dst + ch * 32 + j) = u;
+              }
+            }
+          }
+          if (valid)
+            p.lse[w.b * p.l_bs + w.h * p.l_hs + qi] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+        }
       }
     }
   } else {
@@ -584,12 +658,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale_log2;
     uint32_t s_phase = 0, row_phase = 0;
     bool ok = true;
-    for (int k = static_cast<int>(blockIdx.x); k < p.items; k += static_cast<int>(gridDim.x)) {
+    for (int k = item0; k < p.items; k = next_item(k)) {
       const int q0 = item_of(p, k).q0 + t * kBM;
       const KeyTiles own = key_tiles(p.w, q0, kBM);
-      const int cnt = own.count();
+      int from = 0, to = own.count();  // of its visits, this CTA's
+      if constexpr (kParts) {
+        const KeyTiles all = key_tiles(p.w, q0 - t * kBM, 2 * kBM);
+        from = visits_before(all, own, part_begin(all.count(), part, p.parts));
+        to = visits_before(all, own, part_begin(all.count(), part + 1, p.parts));
+      }
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < cnt; ++i, s_phase ^= 1u) {
+      for (int i = from; i < to; ++i, s_phase ^= 1u) {
         ok = mbar_wait_warp(&bars->s_full[t], s_phase, abort_flag, p.st, kWhere | (5u << 16));
         if (!ok) break;
         tc_fence_after();
@@ -597,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p_first = p.w.pos0 + q0;
         const int pos = p_first + row;
         const Seen v = {pos - p.w.window + 1 - kbase, min(pos, p.w.Sk - 1) - kbase, p.w.sinks - kbase};
-        const int used = used_columns(p.w, own, own.tile(i));
+        const int used = used_columns(p.w, own.ns, own.tile(i));
         bool done = false;
         if (!__any_sync(0xffffffffu, m == -INFINITY)) {
           if (kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
@@ -610,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&bars->p_full[t]);
       }
-      if (ok && cnt > 0) {  // m and l to the epilogue warps, and on to the next item
+      if (ok && to > from) {  // m and l to the epilogue warps, and on to the next item
         ok = mbar_wait_warp(&bars->row_free[t], row_phase ^ 1u, abort_flag, p.st, kWhere | (9u << 16));
         if (!ok) break;
         row_phase ^= 1u;
@@ -627,6 +706,126 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
+  if constexpr (kParts) {
+    // Join the parts: row r = part + parts * i of the item's 256 here, i in turn by warp i % 16, lane = four features.
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const Item w = item_of(p, item0);
+    const int rows = (min(2 * kBM, p.w.Sq - w.q0) - part + p.parts - 1) / p.parts;  // this CTA's
+    float2* stats = reinterpret_cast<float2*>(smem + kSmRow);
+    float2* ml = reinterpret_cast<float2*>(smem + kSmQ);  // [rows][parts] of (m, l)
+    float* wt = reinterpret_cast<float*>(ml + 2 * kBM + kMaxCluster);  // and the parts' weights over the row's sum
+    const int pair = threadIdx.x, i = pair / p.parts, c = pair - i * p.parts;
+    if (i < rows) ml[pair] = *cluster.map_shared_rank(&stats[part + p.parts * i], c);
+    __syncthreads();
+    if (i < rows) {
+      const float2* row = ml + i * p.parts;
+      float M = -INFINITY, L = 0.f;
+      for (int e = 0; e < p.parts; ++e) M = fmaxf(M, row[e].x);
+      for (int e = 0; e < p.parts; ++e)
+        if (row[e].y != 0.f) L += row[e].y * (row[e].x == M ? 1.f : ex2_approx(row[e].x - M));
+      // negative: no weight in that part, and no O if none of its keys was visited
+      wt[pair] = row[c].y == 0.f ? -1.f : (row[c].x == M ? 1.f : ex2_approx(row[c].x - M)) / L;
+      if (c == 0)
+        p.lse[w.b * p.l_bs + w.h * p.l_hs + w.q0 + part + p.parts * i] =
+            L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+    }
+    __syncthreads();
+    const int pairs = (rows - warp + 15) / 16 * p.parts;  // (row, part) pairs of this warp, eight loads in flight
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    int li = warp, lc = 0, ai = warp, ac = 0;  // pair to load, pair to add
+    for (int n = 0; n < pairs; n += 8) {
+      float4 v[8];
+      float f[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        f[u] = n + u < pairs ? wt[li * p.parts + lc] : -1.f;
+        v[u] = f[u] < 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                          : *cluster.map_shared_rank(part_o(smem, part + p.parts * li, lane), lc);
+        if (++lc == p.parts) lc = 0, li += 16;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (n + u >= pairs) break;
+        if (!(f[u] < 0.f)) a = make_float4(a.x + f[u] * v[u].x, a.y + f[u] * v[u].y, a.z + f[u] * v[u].z, a.w + f[u] * v[u].w);
+        if (++ac == p.parts) {
+          uint2 o;
+          o.x = pack_bf16x2(a.x, a.y);
+          o.y = pack_bf16x2(a.z, a.w);
+          const long long qi = w.q0 + part + p.parts * ai;
+          *reinterpret_cast<uint2*>(p.o + w.b * p.o_bs + qi * p.o_rs + w.h * kD + lane * 4) = o;
+          a = make_float4(0.f, 0.f, 0.f, 0.f);
+          ac = 0;
+          ai += 16;
+        }
+      }
+    }
+    cluster.sync();  // no CTA leaves while another reads its shared memory
+  }
+}
+
+const void* parts_kernel() { return reinterpret_cast<const void*>(attn_window_fwd_kernel<true>); }
+
+int allow_parts() {
+  static DeviceOnce once;
+  return allow_clusters_once(once, parts_kernel(), kSmemBytes);
+}
+
+cudaLaunchConfig_t parts_config(cudaLaunchAttribute* at, int parts, long long items, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items * parts));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = static_cast<unsigned>(parts);
+  at->val.clusterDim.y = 1;
+  at->val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of this size that the GPU holds at once (a property of the device model, asked for once), or 0.
+int resident_clusters(int parts) {
+  static std::atomic<int> known[kMaxCluster + 1];  // 0: not asked yet; n + 1
+  int n = known[parts].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = parts_config(&at, parts, 1, nullptr);
+    int got = 0;
+    if (allow_parts() != 0 || cudaOccupancyMaxActiveClusters(&got, parts_kernel(), &cfg) != cudaSuccess) {
+      cudaGetLastError();  // such clusters do not fit: not an error of the call
+      got = 0;
+    }
+    known[parts].store(n = got + 1, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
+// Items, the parts that an item is dealt to, and an estimate of the time in us
+// from measurements at 4 to 64 items: a visit takes 1.2 where one query tile has
+// rows, 1.3 where both do, an item's start and end 5.4, a cluster and its join 5
+// or 9 more (64 or 128 KB of O a CTA through distributed shared memory). The
+// cluster, all of them resident at once, that promises most. us by parts 1, 2,
+// 4, 8, 12, 4 heads x 256 rows: window 16384 181, 108, 62, 40, 33; 2048 34, 27,
+// 21, 19, 19; 512 18, 18, 16, 15, 17.
+struct Plan {
+  long long items;
+  int parts;
+  double us;
+};
+
+Plan plan_of(const WindowShape& w, int B, int H) {
+  Plan d = {static_cast<long long>((w.Sq + 2 * kBM - 1) / (2 * kBM)) * B * H, 1, 0.};
+  const int visits = key_tiles(w, (w.Sq - 1) / (2 * kBM) * 2 * kBM, 2 * kBM).count();
+  const double visit_us = w.Sq > kBM ? 1.3 : 1.18;
+  d.us = 0.6 + std::ceil(static_cast<double>(d.items) / kSms) * (5.4 + (d.items > kSms ? 1.18 : visit_us) * visits);
+  for (int c = 2; c <= kMaxCluster && c * d.items <= kSms; ++c) {
+    const double us = (w.Sq > kBM ? 15. : 11.) + visit_us * ((visits + c - 1) / c);
+    if (us < d.us && resident_clusters(c) >= d.items) d.parts = c, d.us = us;
+  }
+  return d;
 }
 
 }  // namespace
@@ -637,9 +836,6 @@ int launch_window_fwd(const WindowFwd& a, cudaStream_t stream) {
   if ((rc = make_tma_map_bf16(&tq, a.q, a.B, a.w.Sq, a.H * kD, kBM)) != 0) return rc;
   if ((rc = make_tma_map_bf16(&tk, a.k, a.B, a.w.Sk, a.Hkv * kD, kBN)) != 0) return rc;
   if ((rc = make_tma_map_bf16(&tv, a.v, a.B, a.w.Sk, a.Hkv * kD, kBN)) != 0) return rc;
-  static DeviceOnce smem_set;
-  if ((rc = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(attn_window_fwd_kernel), kSmemBytes)) != 0)
-    return rc;
   Params p;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
@@ -653,15 +849,27 @@ int launch_window_fwd(const WindowFwd& a, cudaStream_t stream) {
   p.w = a.w;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.st = a.st;
-  const long long items = static_cast<long long>((a.w.Sq + 2 * kBM - 1) / (2 * kBM)) * a.B * a.H;
-  if (items > 0x7fffffffLL - kSms) return -1;
-  p.items = static_cast<int>(items);
+  const Plan plan = plan_of(a.w, a.B, a.H);
+  if (plan.items > 0x7fffffffLL - kSms) return -1;
+  p.items = static_cast<int>(plan.items);
+  p.parts = plan.parts;
   const long long window_rows = std::min<long long>(a.w.Sk, static_cast<long long>(a.w.window) + a.w.sinks + 2 * kBM);
   const long long kv_heads = std::max<long long>(1, kGroupBytes / (window_rows * 4 * kD));
   p.head_group = static_cast<int>(std::min<long long>(static_cast<long long>(a.B) * a.H, kv_heads * p.G));
-  attn_window_fwd_kernel<<<static_cast<unsigned>(std::min<long long>(items, kSms)), kThreads, kSmemBytes, stream>>>(
-      tq, tk, tv, p);
+  if (plan.parts > 1) {
+    if ((rc = allow_parts()) != 0) return rc;
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = parts_config(&at, plan.parts, plan.items, stream);
+    return cudaLaunchKernelEx(&cfg, attn_window_fwd_kernel<true>, tq, tk, tv, p) == cudaSuccess ? 0 : -4;
+  }
+  static DeviceOnce smem_set;
+  if ((rc = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(attn_window_fwd_kernel<false>), kSmemBytes)) != 0)
+    return rc;
+  attn_window_fwd_kernel<false>
+      <<<static_cast<unsigned>(std::min<long long>(plan.items, kSms)), kThreads, kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
+
+double window_tiles_us(const WindowShape& w, int B, int H) { return plan_of(w, B, H).us; }
 
 }  // namespace lcb

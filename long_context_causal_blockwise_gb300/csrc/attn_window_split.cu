@@ -445,10 +445,7 @@ bool window_split_pays(int B, int H, int Hkv, const WindowShape& w) {
   const double reach = static_cast<double>(w.window) + w.sinks + (14 + G) / G + 1;  // keys that a row tile may see
   const double keys = std::min(reach, std::max(0., std::min<double>(w.Sk, w.pos0 + 0.5 * w.Sq + 1)));
   const double split_us = 6.4 + row_tiles * (7.8e-3 + 7.7e-5 * keys) + 7.3e-4 * std::min(keys, 4096.);
-  const int visits = key_tiles(w, (w.Sq - 1) / 256 * 256, 256).count();
-  const double waves = std::ceil(static_cast<double>(B) * H * ((w.Sq + 255) / 256) / kSms);
-  const double tiles_us = 0.6 + waves * (5.4 + 1.18 * visits);
-  return split_us < tiles_us;
+  return split_us < window_tiles_us(w, B, H);
 }
 
 int launch_window_split(WindowSplit p, cudaStream_t stream) {

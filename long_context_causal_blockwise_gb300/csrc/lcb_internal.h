@@ -151,6 +151,7 @@ struct WindowFwd {
   DevStatus st;
 };
 int launch_window_fwd(const WindowFwd& a, cudaStream_t stream);  // Sq, Sk > 0
+double window_tiles_us(const WindowShape& w, int B, int H);      // estimate of its time
 
 struct WindowBwd {
   RowView q, k, v, o, dO;

@@ -70,6 +70,37 @@ def test_forward_in_128_row_tiles(B, H, Hkv, Sq, Sk, window, sinks, pos0):
     _check(q, k, v, window, sinks, pos0)
 
 
+@pytest.mark.parametrize("B,H,Hkv,Sq,Sk,window,sinks,pos0", [
+    (1, 8, 8, 300, 4000, 3500, 4, None),      # 16 blocks, clusters of nine or so
+    (2, 16, 2, 130, 5000, 4500, 300, None),
+    (1, 12, 12, 513, 2600, 2200, 0, 2000),    # a last block of one row
+    (1, 16, 4, 257, 3000, 2900, 0, 2990),     # later rows past the keys
+    (1, 16, 16, 400, 2500, 2300, 200, -150),  # rows that see nothing; so few keys that a block is one CTA's
+    (1, 5, 1, 700, 1500, 1400, 130, None),
+    (1, 10, 10, 100, 6000, 5900, 0, None),    # one query tile alone
+    (2, 6, 6, 200, 2300, 100, 2000, None),    # sinks in most parts, the window in the last
+])
+def test_forward_blocks_shared_by_a_cluster(B, H, Hkv, Sq, Sk, window, sinks, pos0):
+    """Few blocks of query rows and many keys: a cluster of CTAs shares a block, joined through shared memory."""
+    q, k, v = _rand(Sq + window, (B, Sq, H, D), (B, Sk, Hkv, D), (B, Sk, Hkv, D))
+    a = _check(q, k, v, window, sinks, pos0)
+    b = lcb.attn_window_fwd(q, k, v, window, sinks, pos0)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    # scores of hundreds, the largest anywhere; a key of -inf towards q has no weight, nor has a NaN key past the diagonal
+    q = 4 * q.abs()
+    k *= (0.1 + 6 * (torch.arange(Sk, device="cuda") * 617 % Sk) / Sk)[None, :, None, None].to(k.dtype)
+    k[:, Sk // 3] = torch.finfo(torch.bfloat16).min
+    _check(q, k, v, window, sinks, pos0)
+    want = lcb.attn_window_fwd(q, k, v, window, sinks, pos0)
+    k[:, Sk // 3] = float("-inf")
+    half = Sq // 64 * 32  # a warp's rows share the choice of how a tile is done
+    first = (Sk - Sq if pos0 is None else pos0) + half
+    if 0 <= first < Sk:
+        k[:, first:] = float("nan")  # rows of the first half do not see them
+    o, lse = lcb.attn_window_fwd(q, k, v, window, sinks, pos0)
+    assert torch.equal(o[:, :half], want[0][:, :half]) and torch.equal(lse[:, :, :half], want[1][:, :, :half])
+
+
 @pytest.mark.parametrize("H,Hkv,Sq,Sk,window", [(32, 8, 5, 9000, 8000), (8, 1, 33, 5000, 4000), (2, 2, 500, 3000, 2000),
                                                 (3, 1, 7, 2000, 1500), (40, 8, 30, 700, 700)])
 def test_forward_split_over_row_tiles(H, Hkv, Sq, Sk, window):
