@@ -140,10 +140,11 @@ __device__ __forceinline__ Item item_of(const Params& p, int k) {
 // The visits of an item's two query tiles: `all` is the stream of key tiles that
 // either one sees, of which [first, end) are this CTA's; query tile t takes part
 // in those before sinks[t] and those of [from[t], to[t]).
+template <bool kParts>
 struct Visits {
-  KeyTiles all;
-  int first, end, own_ns[2], sinks[2], from[2], to[2];
-  __device__ __forceinline__ bool any(int t) const { return last(t) >= first; }
+  KeyTiles all, own[2];
+  int first, end, sinks[2], from[2], to[2];
+  __device__ __forceinline__ bool any(int t) const { return kParts ? last(t) >= first : own[t].count() > 0; }
   __device__ __forceinline__ bool active(int t, int i) const { return i < sinks[t] || (i >= from[t] && i < to[t]); }
   __device__ __forceinline__ int last(int t) const { return to[t] > from[t] ? to[t] - 1 : sinks[t] - 1; }
 };
@@ -164,16 +165,15 @@ __device__ __forceinline__ int visits_before(const KeyTiles& all, const KeyTiles
 }
 
 template <bool kParts>
-__device__ __forceinline__ Visits visits(const Params& p, int q0, int part) {
-  Visits v;
+__device__ __forceinline__ Visits<kParts> visits(const Params& p, int q0, int part) {
+  Visits<kParts> v;
   v.all = key_tiles(p.w, q0, 2 * kBM);
   const int n = v.all.count();
   v.first = kParts ? part_begin(n, part, p.parts) : 0;
   v.end = kParts ? part_begin(n, part + 1, p.parts) : n;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const KeyTiles k = key_tiles(p.w, q0 + t * kBM, kBM);
-    v.own_ns[t] = k.ns;
+    const KeyTiles k = v.own[t] = key_tiles(p.w, q0 + t * kBM, kBM);
     v.sinks[t] = visit_of(v.all, k.ns);
     v.from[t] = visit_of(v.all, k.lo);
     v.to[t] = visit_of(v.all, k.hi);
@@ -401,11 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = bars->tmem_base;
 
-  const int part = kParts ? static_cast<int>(blockIdx.x) % p.parts : 0;
-  const int item0 = static_cast<int>(blockIdx.x) / (kParts ? p.parts : 1);
-  auto next_item = [&](int k) { return kParts ? p.items : k + static_cast<int>(gridDim.x); };
+  const int part = kParts ? static_cast<int>(blockIdx.x) : 0;  // of item blockIdx.y
 
-  // Every role walks the same items; barrier phases carry on from one to the
+  // Every role walks the same items (the loops' bounds are written out each time: held in variables they cost the
+  // issuing warp 6% of a long window's time); barrier phases carry on from one to the
   // next (ring slots by a running count, the others by one count per query tile).
   if (warp >= kProducerWarp) {
     regs_down();
@@ -416,9 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;              // K and V tiles loaded
         uint32_t nq[2] = {0, 0};  // Q tiles loaded
         bool ok = true;
-        for (int k = item0; k < p.items && ok; k = next_item(k)) {
+        for (int k = static_cast<int>(kParts ? blockIdx.y : blockIdx.x); k < p.items && ok;
+             k += kParts ? p.items : static_cast<int>(gridDim.x)) {
           const Item w = item_of(p, k);
-          const Visits v = visits<kParts>(p, w.q0, part);
+          const Visits<kParts> v = visits<kParts>(p, w.q0, part);
           const int xq = w.h * kD, xk = (w.h / p.G) * kD;
           for (int t = 0; t < 2 && ok; ++t) {
             if (!v.any(t)) continue;
@@ -498,9 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;  // visits of the items before, and of this one
       uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
       bool ok = true;
-      for (int k = item0; k < p.items && ok; k = next_item(k)) {
+      for (int k = static_cast<int>(kParts ? blockIdx.y : blockIdx.x); k < p.items && ok;
+           k += kParts ? p.items : static_cast<int>(gridDim.x)) {
         const Item w = item_of(p, k);
-        const Visits v = visits<kParts>(p, w.q0, part);
+        const Visits<kParts> v = visits<kParts>(p, w.q0, part);
         if (v.first == v.end) continue;
         uint32_t acc[2] = {0, 0};
         ok = wait_kv(g, 0);
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o_phase[t] ^= 1u;
               }
               tc_fence_after();
-              issue_pv(t, g, acc[t], used_columns(p.w, v.own_ns[t], v.all.tile(i)));
+              issue_pv(t, g, acc[t], used_columns(p.w, v.own[t].ns, v.all.tile(i)));
               acc[t] = 1;
               if (i == v.last(t)) tc_commit_if(&bars->o_full[t], one);
             }
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kParts) {
       // This part's O, not divided by l yet, over the ring once nothing reads it any more, 16-byte pieces of a row
       // exchanged by the row's number (a warp writes a column of pieces, and reads a row). (m, l) are there already.
-      const Visits v = visits<true>(p, item_of(p, item0).q0, part);
+      const Visits<kParts> v = visits<kParts>(p, item_of(p, static_cast<int>(blockIdx.y)).q0, part);
       bool ok = true;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -596,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // O of a finished query tile out of TMEM while the softmax warps are on the next item.
       uint32_t phase[2] = {0, 0};
       bool ok = true;
-      for (int k = item0; k < p.items && ok; k = next_item(k)) {
+      for (int k = static_cast<int>(kParts ? blockIdx.y : blockIdx.x); k < p.items && ok;
+           k += kParts ? p.items : static_cast<int>(gridDim.x)) {
         const Item w = item_of(p, k);
   #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -658,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale_log2;
     uint32_t s_phase = 0, row_phase = 0;
     bool ok = true;
-    for (int k = item0; k < p.items; k = next_item(k)) {
+    for (int k = static_cast<int>(kParts ? blockIdx.y : blockIdx.x); k < p.items;
+         k += kParts ? p.items : static_cast<int>(gridDim.x)) {
       const int q0 = item_of(p, k).q0 + t * kBM;
       const KeyTiles own = key_tiles(p.w, q0, kBM);
       int from = 0, to = own.count();  // of its visits, this CTA's
@@ -710,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Join the parts: row r = part + parts * i of the item's 256 here, i in turn by warp i % 16, lane = four features.
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    const Item w = item_of(p, item0);
+    const Item w = item_of(p, static_cast<int>(blockIdx.y));
     const int rows = (min(2 * kBM, p.w.Sq - w.q0) - part + p.parts - 1) / p.parts;  // this CTA's
     float2* stats = reinterpret_cast<float2*>(smem + kSmRow);
     float2* ml = reinterpret_cast<float2*>(smem + kSmQ);  // [rows][parts] of (m, l)
@@ -773,7 +776,7 @@ int allow_parts() {
 
 cudaLaunchConfig_t parts_config(cudaLaunchAttribute* at, int parts, long long items, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items * parts));
+  cfg.gridDim = dim3(static_cast<unsigned>(parts), static_cast<unsigned>(items));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
