@@ -38,7 +38,8 @@
 // products, 165 / 192 with the warp issuing them together (the descriptors stay
 // in uniform registers), 140 / 193 with the epilogue in warps of its own and
 // cut tiles in small loops, 128 / 178 with the maximum looked for only where a
-// tile's sum says so. Splitting a row's columns over two warps (16 softmax
+// tile's sum says so, 124 / 177 with that for a row's first tile too and items
+// decoded without the compiler's divisions. Splitting a row's columns over two warps (16 softmax
 // warps) changed nothing.
 //
 //   warps 0-3   softmax of query tile 0 (thread = query row = TMEM lane)
@@ -102,11 +103,31 @@ struct Bars {
 };
 constexpr uint32_t kSmemBytes = kSmBar + sizeof(Bars) + 1024;  // + alignment slack
 
+// Division of 0 <= n < 2^31 by d >= 1, d known to the host: with 2^(s-1) < d <=
+// 2^s and m = ceil(2^(31+s) / d) < 2^32, n m / 2^(31+s) exceeds n / d by less
+// than n / 2^(31+s) < 1 / d, too little to reach the next integer. (The item
+// decode below is between a CTA's items, where every cycle of it shows; the
+// compiler's own division takes some 100.)
+struct Divisor {
+  uint32_t d, m, s;
+  __host__ explicit Divisor(uint32_t by = 1) : d(by), s(0) {
+    while ((1ull << s) < by) ++s;
+    m = static_cast<uint32_t>(((1ull << (31 + s)) + by - 1) / by);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(n)) * m) >> (31 + s));
+  }
+};
+
 struct Params {
   __nv_bfloat16* o;
   float* lse;
   long long o_rs, o_bs, l_hs, l_bs;
-  int B, H, G, items, head_group, parts;  // parts: CTAs of a cluster that share an item
+  int H, items;
+  int parts;                             // CTAs of a cluster that share an item
+  int nq;                                // items of a head
+  int head_group, last_group, last_size;  // heads of a group; the last group, and its heads
+  Divisor by_h, by_g, by_group_items, by_group, by_last;  // H, H / Hkv, nq * head_group, head_group, last_size
   WindowShape w;
   float scale_log2;
   DevStatus st;
@@ -126,15 +147,13 @@ struct Item {
 };
 
 __device__ __forceinline__ Item item_of(const Params& p, int k) {
-  const int nq = (p.w.Sq + 2 * kBM - 1) / (2 * kBM);
-  const int group = k / (nq * p.head_group);
-  const int g0 = group * p.head_group;
-  const int gsz = min(p.head_group, p.B * p.H - g0);
-  const int within = k - group * nq * p.head_group;
-  const int bh = g0 + within % gsz;
-  const int at = within / gsz;
-  const int groups = (p.B * p.H + p.head_group - 1) / p.head_group;
-  return {bh / p.H, bh % p.H, ((groups - group) & 1 ? nq - 1 - at : at) * 2 * kBM};
+  const int group = p.by_group_items.div(k);
+  const int within = k - group * p.nq * p.head_group;
+  const bool last = group == p.last_group;  // it may be smaller
+  const int at = last ? p.by_last.div(within) : p.by_group.div(within);
+  const int bh = group * p.head_group + within - at * (last ? p.last_size : p.head_group);
+  const int b = p.by_h.div(bh);
+  return {b, bh - b * p.H, ((p.last_group - group) & 1 ? at : p.nq - 1 - at) * 2 * kBM};
 }
 
 // The visits of an item's two query tiles: `all` is the stream of key tiles that
@@ -150,7 +169,9 @@ struct Visits {
 };
 
 // Key tile kt in the stream `all`.
-__device__ __forceinline__ int visit_of(const KeyTiles& all, int kt) { return kt <= all.ns ? kt : all.ns + kt - all.lo; }
+__device__ __forceinline__ int visit_of(const KeyTiles& all, int kt) {
+  return kt <= all.ns ? kt : all.ns + kt - all.lo;
+}
 
 // The first of n visits that are part `part`'s.
 __device__ __forceinline__ int part_begin(int n, int part, int parts) {
@@ -253,9 +274,9 @@ __device__ __forceinline__ void load_seen(uint32_t (&s)[64], uint32_t tS, int ch
 // over S in TMEM, l brought up. The second product reads columns [0, used).
 // Columns go in halves of 64, read again for the second pass (P overwrites only
 // columns that were read before); a half that no row of the warp sees costs
-// only its zeros. Kept small: it runs for the first tile of a row and where the
-// one-pass forms below give up.
-__device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m, float& l, const Seen v, int used) {
+// only its zeros. Kept small: it runs where the one-pass forms below give up.
+__device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m, float& l, const Seen v, int used,
+                                                 bool keep_m) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int ch = 0; ch < used; ch += 64) {
@@ -270,7 +291,7 @@ __device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m,
         m4[u] = fmax3(m4[u], __uint_as_float(s[e + 2 * u]), __uint_as_float(s[e + 2 * u + 1]));
     mx = fmaxf(mx, fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])));
   }
-  raise_max(tS, m, l, fmaxf(m, mx * c));
+  raise_max(tS, m, l, keep_m ? m : fmaxf(m, mx * c));
   const float neg_m = (m == -INFINITY) ? 0.f : -m;
   float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
 #pragma unroll 1
@@ -294,12 +315,28 @@ __device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m,
 // The one-pass forms take P against the maximum as it stands, without looking
 // for a new one: the tile's row sum tells afterwards whether a score was too far
 // above it (some P over 2^32 makes a sum over 2^32; none makes one up to 2^39 at
-// most). Then, or at a NaN, S is still in place and the two passes run.
-// False: nothing was done.
-constexpr float kMostSum = 549755813888.f;  // 2^39
+// most). Then, or at a NaN, S is still in place and the two passes run. A row
+// that has seen nothing yet takes 0 for its maximum: right if its sum, of the
+// keys that it sees here, comes out neither that large nor under 2^-30, beside
+// which weights lost under 2^-126 are nothing. False: nothing was done.
+constexpr float kMostSum = 549755813888.f;           // 2^39
+constexpr float kLeastSum = 9.313225746154785e-10f;  // 2^-30
 
-// All 128 columns visible.
-__device__ __forceinline__ bool softmax_whole(uint32_t tS, float c, float m, float& l) {
+// Whether the weights that the warp's rows took against their m (0 if it was
+// -inf: it is set here) stand. `fine`: whether this row's do; if another's do
+// not, the two passes keep its m all the same, so that no row's bits depend on
+// another row's scores.
+__device__ __forceinline__ bool accept(float& m, float& l, float sum, bool sees, bool& fine) {
+  const bool fresh = m == -INFINITY && sees;
+  fine = sum <= kMostSum && (!fresh || sum >= kLeastSum);
+  if (fine && fresh) m = 0.f;
+  if (!__all_sync(0xffffffffu, fine)) return false;
+  l += sum;
+  return true;
+}
+
+// All 128 columns visible, every row of the warp with a maximum.
+__device__ __forceinline__ bool softmax_whole(uint32_t tS, float c, float m, float& l, bool& fine) {
   uint32_t s[128], pk[64];
   tmem_ld_x64(tS, *reinterpret_cast<uint32_t(*)[64]>(s));
   tmem_ld_x64(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(s + 64));
@@ -312,7 +349,8 @@ __device__ __forceinline__ bool softmax_whole(uint32_t tS, float c, float m, flo
       weights(s + 32 * q, pk + 16 * q, c, -m, sa0, sa1);
   }
   const float sum = (sa0 + sb0) + (sa1 + sb1);
-  if (!__all_sync(0xffffffffu, sum <= kMostSum)) return false;
+  fine = sum <= kMostSum;
+  if (!__all_sync(0xffffffffu, fine)) return false;
   tmem_st_x32_nowait(tS, *reinterpret_cast<uint32_t(*)[32]>(pk));
   tmem_st_x32_nowait(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
   tmem_wait_st();
@@ -321,28 +359,31 @@ __device__ __forceinline__ bool softmax_whole(uint32_t tS, float c, float m, flo
 }
 
 // A tile that the mask cuts.
-__device__ __forceinline__ bool softmax_cut(uint32_t tS, float c, float m, float& l, const Seen v, int used) {
+__device__ __forceinline__ bool softmax_cut(uint32_t tS, float c, float& m, float& l, const Seen v, int used,
+                                            bool& fine) {
   uint32_t pk[64];
+  const float neg_m = m == -INFINITY ? 0.f : -m;
+  bool sees = false;
   float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t* pks = pk + 32 * half;
-    if (64 * half < used && __any_sync(0xffffffffu, v.word(64 * half) | v.word(64 * half + 32))) {
+    const bool here = 64 * half < used && (v.word(64 * half) | v.word(64 * half + 32)) != 0;
+    sees |= here;
+    if (__any_sync(0xffffffffu, here)) {
       uint32_t s[64];
       load_seen(s, tS, 64 * half, v);
-      weights(s, pks, c, -m, sa0, sa1);
-      weights(s + 32, pks + 16, c, -m, sb0, sb1);
+      weights(s, pks, c, neg_m, sa0, sa1);
+      weights(s + 32, pks + 16, c, neg_m, sb0, sb1);
     } else {
 #pragma unroll
       for (int k = 0; k < 32; ++k) pks[k] = 0u;
     }
   }
-  const float sum = (sa0 + sb0) + (sa1 + sb1);
-  if (!__all_sync(0xffffffffu, sum <= kMostSum)) return false;
+  if (!accept(m, l, (sa0 + sb0) + (sa1 + sb1), sees, fine)) return false;
   tmem_st_x32_nowait(tS, *reinterpret_cast<uint32_t(*)[32]>(pk));
   if (used > 64) tmem_st_x32_nowait(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
   tmem_wait_st();
-  l += sum;
   return true;
 }
 
@@ -404,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int part = kParts ? static_cast<int>(blockIdx.x) : 0;  // of item blockIdx.y
 
   // Every role walks the same items (the loops' bounds are written out each time: held in variables they cost the
-  // issuing warp 6% of a long window's time); barrier phases carry on from one to the
-  // next (ring slots by a running count, the others by one count per query tile).
+  // issuing warp 6% of a long window's time); barrier phases carry on from one to
+  // the next (ring slots by a running count, the others by one count per query tile).
   if (warp >= kProducerWarp) {
     regs_down();
     if (warp == kProducerWarp) {
@@ -419,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
              k += kParts ? p.items : static_cast<int>(gridDim.x)) {
           const Item w = item_of(p, k);
           const Visits<kParts> v = visits<kParts>(p, w.q0, part);
-          const int xq = w.h * kD, xk = (w.h / p.G) * kD;
+          const int xq = w.h * kD, xk = p.by_g.div(w.h) * kD;
           for (int t = 0; t < 2 && ok; ++t) {
             if (!v.any(t)) continue;
             ok = mbar_wait_inline(&bars->q_empty[t], (nq[t] & 1u) ^ 1u, abort_flag, p.st, kWhere | (7u << 16));
@@ -589,8 +630,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_x32(tO + t * 128 + ch * 32, o);
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
-            *part_o(smem, t * kBM + row, ch * 8 + j / 4) = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
-                                                                       __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+            *part_o(smem, t * kBM + row, ch * 8 + j / 4) =
+                make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]), __uint_as_float(o[j + 2]),
+                            __uint_as_float(o[j + 3]));
         }
       }
     } else {
@@ -680,15 +722,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos = p_first + row;
         const Seen v = {pos - p.w.window + 1 - kbase, min(pos, p.w.Sk - 1) - kbase, p.w.sinks - kbase};
         const int used = used_columns(p.w, own.ns, own.tile(i));
-        bool done = false;
-        if (!__any_sync(0xffffffffu, m == -INFINITY)) {
-          if (kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
-              (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks))
-            done = softmax_whole(tS, c, m, l);
-          else
-            done = softmax_cut(tS, c, m, l, v, used);
-        }
-        if (!done) softmax_two_pass(tS, c, m, l, v, used);
+        bool done, fine;
+        if (kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
+            (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks) &&
+            !__any_sync(0xffffffffu, m == -INFINITY))
+          done = softmax_whole(tS, c, m, l, fine);
+        else
+          done = softmax_cut(tS, c, m, l, v, used, fine);
+        if (!done) softmax_two_pass(tS, c, m, l, v, used, fine);
         tc_fence_before();
         mbar_arrive(&bars->p_full[t]);
       }
@@ -750,7 +791,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         if (n + u >= pairs) break;
-        if (!(f[u] < 0.f)) a = make_float4(a.x + f[u] * v[u].x, a.y + f[u] * v[u].y, a.z + f[u] * v[u].z, a.w + f[u] * v[u].w);
+        if (!(f[u] < 0.f))
+          a = make_float4(a.x + f[u] * v[u].x, a.y + f[u] * v[u].y, a.z + f[u] * v[u].z, a.w + f[u] * v[u].w);
         if (++ac == p.parts) {
           uint2 o;
           o.x = pack_bf16x2(a.x, a.y);
@@ -846,19 +888,26 @@ int launch_window_fwd(const WindowFwd& a, cudaStream_t stream) {
   p.o_bs = a.o_batch_stride;
   p.l_hs = a.lse_head_stride;
   p.l_bs = a.lse_batch_stride;
-  p.B = a.B;
   p.H = a.H;
-  p.G = a.H / a.Hkv;
+  p.by_g = Divisor(a.H / a.Hkv);
   p.w = a.w;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.st = a.st;
   const Plan plan = plan_of(a.w, a.B, a.H);
   if (plan.items > 0x7fffffffLL - kSms) return -1;
   p.items = static_cast<int>(plan.items);
+  p.nq = (a.w.Sq + 2 * kBM - 1) / (2 * kBM);
   p.parts = plan.parts;
   const long long window_rows = std::min<long long>(a.w.Sk, static_cast<long long>(a.w.window) + a.w.sinks + 2 * kBM);
   const long long kv_heads = std::max<long long>(1, kGroupBytes / (window_rows * 4 * kD));
-  p.head_group = static_cast<int>(std::min<long long>(static_cast<long long>(a.B) * a.H, kv_heads * p.G));
+  const int heads = static_cast<int>(plan.items / p.nq);
+  p.head_group = static_cast<int>(std::min<long long>(heads, kv_heads * (a.H / a.Hkv)));
+  p.last_group = (heads - 1) / p.head_group;
+  p.last_size = heads - p.last_group * p.head_group;
+  p.by_h = Divisor(a.H);
+  p.by_group_items = Divisor(p.nq * p.head_group);
+  p.by_group = Divisor(p.head_group);
+  p.by_last = Divisor(p.last_size);
   if (plan.parts > 1) {
     if ((rc = allow_parts()) != 0) return rc;
     cudaLaunchAttribute at;
@@ -866,8 +915,8 @@ int launch_window_fwd(const WindowFwd& a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, attn_window_fwd_kernel<true>, tq, tk, tv, p) == cudaSuccess ? 0 : -4;
   }
   static DeviceOnce smem_set;
-  if ((rc = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(attn_window_fwd_kernel<false>), kSmemBytes)) != 0)
-    return rc;
+  const void* fn = reinterpret_cast<const void*>(attn_window_fwd_kernel<false>);
+  if ((rc = set_smem_limit_once(smem_set, fn, kSmemBytes)) != 0) return rc;
   attn_window_fwd_kernel<false>
       <<<static_cast<unsigned>(std::min<long long>(plan.items, kSms)), kThreads, kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError() == cudaSuccess ? 0 : -4;

@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(32 * kWarps) window_split_kernel(const __grid_
           float mx = fmaxf(s[nt][e], s[nt][2 + e]);
 #pragma unroll
           for (int w = 4; w < 32; w *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          mx = mx > m[nt][e] + kRescaleThreshold ? mx : m[nt][e];  // each row for itself: no other row's keys change its bits
+          // each row for itself: no other row's keys change its bits
+          mx = mx > m[nt][e] + kRescaleThreshold ? mx : m[nt][e];
           const float a = weight(m[nt][e], mx);
           m[nt][e] = mx;
           l[nt][e] *= a;
