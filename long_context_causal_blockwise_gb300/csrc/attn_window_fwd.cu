@@ -637,12 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // O of a finished query tile out of TMEM while the softmax warps are on the next item.
-      uint32_t phase[2] = {0, 0};
+      uint32_t phases = 0;  // bit t
       bool ok = true;
       for (int k = static_cast<int>(kParts ? blockIdx.y : blockIdx.x); k < p.items && ok;
            k += kParts ? p.items : static_cast<int>(gridDim.x)) {
         const Item w = item_of(p, k);
-  #pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           if (!ok) continue;
           const int qi = w.q0 + t * kBM + row;
@@ -650,20 +650,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool any = key_tiles(p.w, w.q0 + t * kBM, kBM).count() > 0;  // else O was never formed
           float m = -INFINITY, l = 0.f;
           if (any) {
-            ok = mbar_wait_warp(&bars->row_full[t], phase[t], abort_flag, p.st, kWhere | (10u << 16));
+            ok = mbar_wait_warp(&bars->row_full[t], (phases >> t) & 1u, abort_flag, p.st, kWhere | (10u << 16));
             if (!ok) continue;
             const float2 r = reinterpret_cast<const float2*>(smem + kSmRow)[t * kBM + row];
             m = r.x;
             l = r.y;
             mbar_arrive(&bars->row_free[t]);
-            ok = mbar_wait_warp(&bars->o_full[t], phase[t], abort_flag, p.st, kWhere | (6u << 16));
+            ok = mbar_wait_warp(&bars->o_full[t], (phases >> t) & 1u, abort_flag, p.st, kWhere | (6u << 16));
             if (!ok) continue;
-            phase[t] ^= 1u;
+            phases ^= 1u << t;
             tc_fence_after();
           }
           const float inv_l = l == 0.f ? 0.f : 1.f / l;
           __nv_bfloat16* dst = p.o + w.b * p.o_bs + static_cast<long long>(qi) * p.o_rs + w.h * kD;
-  #pragma unroll
+#pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
             uint32_t o[32];
             if (any) {
@@ -673,11 +673,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars->o_free[t]);  // the next item's P V may write over O
               }
             } else {
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 32; ++j) o[j] = 0u;
             }
             if (valid) {
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 32; j += 8) {
                 uint4 u;
                 u.x = pack_bf16x2(__uint_as_float(o[j]) * inv_l, __uint_as_float(o[j + 1]) * inv_l);
