@@ -38,8 +38,10 @@
 // products, 165 / 192 with the warp issuing them together (the descriptors stay
 // in uniform registers), 140 / 193 with the epilogue in warps of its own and
 // cut tiles in small loops, 128 / 178 with the maximum looked for only where a
-// tile's sum says so, 124 / 177 with that for a row's first tile too and items
-// decoded without the compiler's divisions. Splitting a row's columns over two warps (16 softmax
+// tile's sum says so, 122 / 176 with that for a row's first tile too, items decoded
+// without the compiler's divisions and a shorter epilogue, 118 / 171 with tile 0
+// beginning its next item beside tile 1's last visit and O stored in whole lines.
+// Splitting a row's columns over two warps (16 softmax
 // warps) changed nothing.
 //
 //   warps 0-3   softmax of query tile 0 (thread = query row = TMEM lane)
@@ -83,7 +85,8 @@ constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kSmQ = 0;
 constexpr uint32_t kSmKV = 2 * kTileBytes;
 constexpr uint32_t kSmRow = kSmKV + kStages * kTileBytes;  // (m, l) of each query row
-constexpr uint32_t kSmBar = kSmRow + 2 * kBM * 8;
+constexpr uint32_t kSmOut = kSmRow + 2 * kBM * 8;  // O on its way out: 128 bytes of each row of a tile
+constexpr uint32_t kSmBar = kSmOut + kBM * 128;
 constexpr float kRescaleThreshold = 32.0f;  // log2 units
 constexpr long long kGroupBytes = 80LL << 20;  // K and V of the windows that a group of heads keeps in L2
 constexpr int kSms = 152;
@@ -461,16 +464,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Item w = item_of(p, k);
           const Visits<kParts> v = visits<kParts>(p, w.q0, part);
           const int xq = w.h * kD, xk = p.by_g.div(w.h) * kD;
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (!v.any(t)) continue;
+          // Q of tile 1 after the first K and V: its place is free last, and they must not wait for it.
+          auto load_q = [&](int t) {
+            if (!ok || !v.any(t)) return;
             ok = mbar_wait_inline(&bars->q_empty[t], (nq[t] & 1u) ^ 1u, abort_flag, p.st, kWhere | (7u << 16));
-            if (!ok) break;
+            if (!ok) return;
             mbar_arrive_expect_tx(&bars->q_full[t], kTileBytes);
             for (int half = 0; half < 2; ++half)
               tma_load_3d(smem + kSmQ + t * kTileBytes + half * kHalfBytes, &tm_q, &bars->q_full[t], xq + half * 64,
                           w.q0 + t * kBM, w.b);
             ++nq[t];
-          }
+          };
+          load_q(0);
           for (int i = v.first; i < v.end && ok; ++i) {
             for (int kv = 0; kv < 2; ++kv, ++it) {
               const int slot = it % kStages;
@@ -485,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d_hint(smem + kSmKV + slot * kTileBytes + half * kHalfBytes, map, &bars->kv_full[slot],
                                  xk + half * 64, v.all.tile(i) * kBN, w.b, pol);
             }
+            if (i == v.first) load_q(1);
           }
         }
         if (!ok) {
@@ -508,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v_desc = sdesc_sw128(sbase + kSmKV + kTileBytes, kHalfBytes, 1024);
       // Visit g of the CTA has K in ring slot 2 (g & 1) and V in the slot after it.
       auto issue_qk = [&](int t, uint32_t g) {
-        const uint64_t qa = sdesc_advance(q_desc, t * kTileBytes), kb = sdesc_advance(k_desc, (g & 1u) * 2 * kTileBytes);
+        const uint64_t qa = sdesc_advance(q_desc, t * kTileBytes);
+        const uint64_t kb = sdesc_advance(k_desc, (g & 1u) * 2 * kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
           const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
@@ -538,64 +545,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       uint32_t g = 0;  // visits of the items before, and of this one
       uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
+      uint32_t acc[2] = {0, 0};
       bool ok = true;
-      for (int k = static_cast<int>(kParts ? blockIdx.y : blockIdx.x); k < p.items && ok;
-           k += kParts ? p.items : static_cast<int>(gridDim.x)) {
-        const Item w = item_of(p, k);
-        const Visits<kParts> v = visits<kParts>(p, w.q0, part);
-        if (v.first == v.end) continue;
-        uint32_t acc[2] = {0, 0};
-        ok = wait_kv(g, 0);
-        // First products. S_t is free: the previous item's last P V of tile t was issued before.
+      auto wait_p = [&](int t) {
+        ok = mbar_wait_warp(&bars->p_full[t], p_phase[t], abort_flag, p.st, kWhere | (4u << 16));
+        p_phase[t] ^= 1u;
+        if (ok && acc[t] == 0) {  // the first P V of an item writes over O: the previous one's has been read
+          ok = mbar_wait_warp(&bars->o_free[t], o_phase[t] ^ 1u, abort_flag, p.st, kWhere | (8u << 16));
+          o_phase[t] ^= 1u;
+        }
+        tc_fence_after();
+        return ok;
+      };
+      int k = static_cast<int>(kParts ? blockIdx.y : blockIdx.x) - (kParts ? p.items : static_cast<int>(gridDim.x));
+      Visits<kParts> v;
+      v.first = v.end = 0;
+      for (bool more = true; more && ok;) {
+        if (v.first < v.end) {
+          for (int i = v.first; i + 1 < v.end && ok; ++i, ++g) {
+            ok = wait_kv(g, 1);
+            if (!ok) break;
+            bool k_ready = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!ok) continue;
+              if (v.active(t, i)) {
+                if (!wait_p(t)) continue;
+                issue_pv(t, g, acc[t], used_columns(p.w, v.own[t].ns, v.all.tile(i)));
+                acc[t] = 1;
+                if (i == v.last(t)) tc_commit_if(&bars->o_full[t], one);
+              }
+              if (v.active(t, i + 1)) {  // S over P once the product above has read it (issue order)
+                if (!k_ready) {
+                  ok = wait_kv(g + 1, 0);
+                  if (!ok) continue;
+                  k_ready = true;
+                }
+                issue_qk(t, g + 1);
+                if (i + 1 == v.last(t)) tc_commit_if(&bars->q_empty[t], one);
+              }
+            }
+            if (!ok) break;
+            tc_commit_if(&bars->kv_empty[2 * (g & 1u) + 1], one);
+            tc_commit_if(&bars->kv_empty[2 * ((g + 1) & 1u)], one);
+          }
+          if (!ok) break;
+        }
+        Visits<kParts> next;  // of the next item with a key, found while the softmax warps are at work
+        do {
+          k += kParts ? p.items : static_cast<int>(gridDim.x);
+          more = k < p.items;
+          if (more) next = visits<kParts>(p, item_of(p, k).q0, part);
+        } while (more && next.first == next.end);
+        if (v.first < v.end) ok = wait_kv(g, 1);
+        // The item's last visit and the next one's first products: tile 0's go before the wait for tile 1's last P.
+        const uint32_t g1 = v.first < v.end ? g + 1 : g;
+        bool k_ready = false;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok || !v.any(t)) continue;
+          if (!ok) continue;
+          if (v.first < v.end && v.active(t, v.end - 1)) {  // in a loop: this code runs once an item
+            if (!wait_p(t)) continue;
+            const int cols = used_columns(p.w, v.own[t].ns, v.all.tile(v.end - 1));
+            const uint64_t vb = sdesc_advance(v_desc, (g & 1u) * 2 * kTileBytes);
+#pragma unroll 1
+            for (int kk = 0; kk * 16 < cols; ++kk)
+              mma_ts_if(tm + 256 + t * 128, tm + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv,
+                        kk > 0 ? 1u : acc[t], one);
+            tc_commit_if(&bars->o_full[t], one);
+          }
+          acc[t] = 0;
+          if (!more || !next.any(t)) continue;
+          if (!k_ready) {
+            ok = wait_kv(g1, 0);
+            if (!ok) continue;
+            k_ready = true;
+          }
           ok = mbar_wait_warp(&bars->q_full[t], q_phase[t], abort_flag, p.st, kWhere | (2u << 16));
           if (!ok) continue;
           q_phase[t] ^= 1u;
           tc_fence_after();
-          if (v.active(t, v.first)) {
-            issue_qk(t, g);
-            if (v.last(t) == v.first) tc_commit_if(&bars->q_empty[t], one);
+          if (next.active(t, next.first)) {
+            issue_qk(t, g1);
+            if (next.last(t) == next.first) tc_commit_if(&bars->q_empty[t], one);
           }
         }
         if (!ok) break;
-        tc_commit_if(&bars->kv_empty[2 * (g & 1u)], one);
-        for (int i = v.first; i < v.end && ok; ++i, ++g) {
-          ok = wait_kv(g, 1);
-          if (!ok) break;
-          bool k_ready = false;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok) continue;
-            if (v.active(t, i)) {
-              ok = mbar_wait_warp(&bars->p_full[t], p_phase[t], abort_flag, p.st, kWhere | (4u << 16));
-              if (!ok) continue;
-              p_phase[t] ^= 1u;
-              if (acc[t] == 0) {  // the first P V of an item writes over O: the previous one's has been read
-                ok = mbar_wait_warp(&bars->o_free[t], o_phase[t] ^ 1u, abort_flag, p.st, kWhere | (8u << 16));
-                if (!ok) continue;
-                o_phase[t] ^= 1u;
-              }
-              tc_fence_after();
-              issue_pv(t, g, acc[t], used_columns(p.w, v.own[t].ns, v.all.tile(i)));
-              acc[t] = 1;
-              if (i == v.last(t)) tc_commit_if(&bars->o_full[t], one);
-            }
-            if (v.active(t, i + 1)) {  // S over P once the product above has read it (issue order)
-              if (!k_ready) {
-                ok = wait_kv(g + 1, 0);
-                if (!ok) continue;
-                k_ready = true;
-              }
-              issue_qk(t, g + 1);
-              if (i + 1 == v.last(t)) tc_commit_if(&bars->q_empty[t], one);
-            }
-          }
-          if (!ok) break;
-          tc_commit_if(&bars->kv_empty[2 * (g & 1u) + 1], one);
-          if (i + 1 < v.end) tc_commit_if(&bars->kv_empty[2 * ((g + 1) & 1u)], one);
-        }
+        if (v.first < v.end) tc_commit_if(&bars->kv_empty[2 * (g & 1u) + 1], one);
+        if (more) tc_commit_if(&bars->kv_empty[2 * (g1 & 1u)], one);
+        g = g1;
+        v = next;
       }
       // Every MMA issued must finish before TMEM is released.
       tc_commit_if(&bars->mma_done, one);
@@ -662,7 +701,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
           }
           const float inv_l = l == 0.f ? 0.f : 1.f / l;
-          __nv_bfloat16* dst = p.o + w.b * p.o_bs + static_cast<long long>(qi) * p.o_rs + w.h * kD;
+          // Half of the columns at a time through shared memory, so that a store covers four whole lines, not a piece
+          // of 32: the softmax warps' barrier arrivals wait behind them in the same queue.
+          const int row0 = w.q0 + t * kBM + 32 * (warp - kEpilogueWarp);  // the warp's first
+          __nv_bfloat16* dst = p.o + w.b * p.o_bs + static_cast<long long>(row0) * p.o_rs + w.h * kD;
+          uint8_t* stage = smem + kSmOut + (warp - kEpilogueWarp) * 32 * 128;
 #pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
             uint32_t o[32];
@@ -676,16 +719,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j) o[j] = 0u;
             }
-            if (valid) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                uint4 u;
-                u.x = pack_bf16x2(__uint_as_float(o[j]) * inv_l, __uint_as_float(o[j + 1]) * inv_l);
-                u.y = pack_bf16x2(__uint_as_float(o[j + 2]) * inv_l, __uint_as_float(o[j + 3]) * inv_l);
-                u.z = pack_bf16x2(__uint_as_float(o[j + 4]) * inv_l, __uint_as_float(o[j + 5]) * inv_l);
-                u.w = pack_bf16x2(__uint_as_float(o[j + 6]) * inv_l, __uint_as_float(o[j + 7]) * inv_l);
-                *reinterpret_cast<uint4*>(dst + ch * 32 + j) = u;
+            for (int j = 0; j < 32; j += 8) {
+              uint4 u;
+              u.x = pack_bf16x2(__uint_as_float(o[j]) * inv_l, __uint_as_float(o[j + 1]) * inv_l);
+              u.y = pack_bf16x2(__uint_as_float(o[j + 2]) * inv_l, __uint_as_float(o[j + 3]) * inv_l);
+              u.z = pack_bf16x2(__uint_as_float(o[j + 4]) * inv_l, __uint_as_float(o[j + 5]) * inv_l);
+              u.w = pack_bf16x2(__uint_as_float(o[j + 6]) * inv_l, __uint_as_float(o[j + 7]) * inv_l);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((((ch & 1) * 4 + j / 8) ^ (lane & 7)) << 4)) = u;
+            }
+            if (ch & 1) {
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = 4 * i + (lane >> 3);
+                const uint4 u = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                if (row0 + r < p.w.Sq)
+                  *reinterpret_cast<uint4*>(dst + r * p.o_rs + (ch >> 1) * 64 + (lane & 7) * 8) = u;
               }
+              __syncwarp();
             }
           }
           if (valid)
