@@ -38,11 +38,10 @@
 // products, 165 / 192 with the warp issuing them together (the descriptors stay
 // in uniform registers), 140 / 193 with the epilogue in warps of its own and
 // cut tiles in small loops, 128 / 178 with the maximum looked for only where a
-// tile's sum says so, 122 / 176 with that for a row's first tile too, items decoded
-// without the compiler's divisions and a shorter epilogue, 118 / 171 with tile 0
-// beginning its next item beside tile 1's last visit and O stored in whole lines.
-// Splitting a row's columns over two warps (16 softmax
-// warps) changed nothing.
+// tile's sum says so, 122 / 170 with items decoded without the compiler's
+// divisions, a shorter epilogue, tile 0 beginning its next item beside tile 1's
+// last visit and O stored in whole lines. Splitting a row's columns over two
+// warps (16 softmax warps) changed nothing.
 //
 //   warps 0-3   softmax of query tile 0 (thread = query row = TMEM lane)
 //   warps 4-7   softmax of query tile 1
@@ -277,7 +276,8 @@ __device__ __forceinline__ void load_seen(uint32_t (&s)[64], uint32_t tS, int ch
 // over S in TMEM, l brought up. The second product reads columns [0, used).
 // Columns go in halves of 64, read again for the second pass (P overwrites only
 // columns that were read before); a half that no row of the warp sees costs
-// only its zeros. Kept small: it runs where the one-pass forms below give up.
+// only its zeros. Kept small: it runs for the first tile of a row and where the
+// one-pass forms below give up.
 __device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m, float& l, const Seen v, int used,
                                                  bool keep_m) {
   float mx = -INFINITY;
@@ -318,27 +318,15 @@ __device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m,
 // The one-pass forms take P against the maximum as it stands, without looking
 // for a new one: the tile's row sum tells afterwards whether a score was too far
 // above it (some P over 2^32 makes a sum over 2^32; none makes one up to 2^39 at
-// most). Then, or at a NaN, S is still in place and the two passes run. A row
-// that has seen nothing yet takes 0 for its maximum: right if its sum, of the
-// keys that it sees here, comes out neither that large nor under 2^-30, beside
-// which weights lost under 2^-126 are nothing. False: nothing was done.
-constexpr float kMostSum = 549755813888.f;           // 2^39
-constexpr float kLeastSum = 9.313225746154785e-10f;  // 2^-30
+// most). Then, or at a NaN, S is still in place and the two passes run; they
+// keep the maximum of a row whose own sum is fine, so that no row's bits depend
+// on another row's scores. (A row's first tile takes two passes: weights against
+// its largest score, which is exactly 1, give a row that sees one key that key's
+// v to the bit. Against 0 they would be a little faster, and would not.)
+// False: nothing was done.
+constexpr float kMostSum = 549755813888.f;  // 2^39
 
-// Whether the weights that the warp's rows took against their m (0 if it was
-// -inf: it is set here) stand. `fine`: whether this row's do; if another's do
-// not, the two passes keep its m all the same, so that no row's bits depend on
-// another row's scores.
-__device__ __forceinline__ bool accept(float& m, float& l, float sum, bool sees, bool& fine) {
-  const bool fresh = m == -INFINITY && sees;
-  fine = sum <= kMostSum && (!fresh || sum >= kLeastSum);
-  if (fine && fresh) m = 0.f;
-  if (!__all_sync(0xffffffffu, fine)) return false;
-  l += sum;
-  return true;
-}
-
-// All 128 columns visible, every row of the warp with a maximum.
+// All 128 columns visible.
 __device__ __forceinline__ bool softmax_whole(uint32_t tS, float c, float m, float& l, bool& fine) {
   uint32_t s[128], pk[64];
   tmem_ld_x64(tS, *reinterpret_cast<uint32_t(*)[64]>(s));
@@ -362,31 +350,30 @@ __device__ __forceinline__ bool softmax_whole(uint32_t tS, float c, float m, flo
 }
 
 // A tile that the mask cuts.
-__device__ __forceinline__ bool softmax_cut(uint32_t tS, float c, float& m, float& l, const Seen v, int used,
+__device__ __forceinline__ bool softmax_cut(uint32_t tS, float c, float m, float& l, const Seen v, int used,
                                             bool& fine) {
   uint32_t pk[64];
-  const float neg_m = m == -INFINITY ? 0.f : -m;
-  bool sees = false;
   float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t* pks = pk + 32 * half;
-    const bool here = 64 * half < used && (v.word(64 * half) | v.word(64 * half + 32)) != 0;
-    sees |= here;
-    if (__any_sync(0xffffffffu, here)) {
+    if (64 * half < used && __any_sync(0xffffffffu, v.word(64 * half) | v.word(64 * half + 32))) {
       uint32_t s[64];
       load_seen(s, tS, 64 * half, v);
-      weights(s, pks, c, neg_m, sa0, sa1);
-      weights(s + 32, pks + 16, c, neg_m, sb0, sb1);
+      weights(s, pks, c, -m, sa0, sa1);
+      weights(s + 32, pks + 16, c, -m, sb0, sb1);
     } else {
 #pragma unroll
       for (int k = 0; k < 32; ++k) pks[k] = 0u;
     }
   }
-  if (!accept(m, l, (sa0 + sb0) + (sa1 + sb1), sees, fine)) return false;
+  const float sum = (sa0 + sb0) + (sa1 + sb1);
+  fine = sum <= kMostSum;
+  if (!__all_sync(0xffffffffu, fine)) return false;
   tmem_st_x32_nowait(tS, *reinterpret_cast<uint32_t(*)[32]>(pk));
   if (used > 64) tmem_st_x32_nowait(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
   tmem_wait_st();
+  l += sum;
   return true;
 }
 
@@ -774,13 +761,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos = p_first + row;
         const Seen v = {pos - p.w.window + 1 - kbase, min(pos, p.w.Sk - 1) - kbase, p.w.sinks - kbase};
         const int used = used_columns(p.w, own.ns, own.tile(i));
-        bool done, fine;
-        if (kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
-            (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks) &&
-            !__any_sync(0xffffffffu, m == -INFINITY))
-          done = softmax_whole(tS, c, m, l, fine);
-        else
-          done = softmax_cut(tS, c, m, l, v, used, fine);
+        bool done = false, fine = false;
+        if (!__any_sync(0xffffffffu, m == -INFINITY)) {
+          if (kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
+              (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks))
+            done = softmax_whole(tS, c, m, l, fine);
+          else
+            done = softmax_cut(tS, c, m, l, v, used, fine);
+        }
         if (!done) softmax_two_pass(tS, c, m, l, v, used, fine);
         tc_fence_before();
         mbar_arrive(&bars->p_full[t]);

@@ -123,6 +123,19 @@ def test_few_rows_forward(H, Hkv, Sq):
         _check(q, k, v, window, sinks, pos0, name=f"Sk {Sk} window {window}")
 
 
+@pytest.mark.parametrize("H,Hkv,S", [(2, 1, 300), (48, 24, 420), (8, 8, 3)])
+def test_row_of_one_key_gives_its_v(H, Hkv, S):
+    """Weight 1 of a single key: O is its v to the bit (so Delta cancels dP), in every form of the call."""
+    q, k, v = _rand(H, (2, S, H, D), (2, S, Hkv, D), (2, S, Hkv, D))
+    o, _ = lcb.attn_window_fwd(q, k, v, 1)
+    assert torch.equal(o, v.repeat_interleave(H // Hkv, dim=2))
+    o, _ = lcb.attn_window_fwd(q, k, v, S)
+    assert torch.equal(o[:, 0], v[:, 0].repeat_interleave(H // Hkv, dim=1))
+    lens = torch.tensor([S, 1], dtype=torch.int32, device="cuda")
+    o, _ = lcb.attn_window_decode(q[:, :1], k, v, lens, 1)
+    assert torch.equal(o[:, 0], torch.stack([v[0, S - 1], v[1, 0]]).repeat_interleave(H // Hkv, dim=1))
+
+
 @pytest.mark.parametrize("H", [2, 20])
 def test_large_scores_and_sharp_rows(H):
     """Scores of hundreds (the running maximum moves by more than 2^8 between tiles), and one key that takes all."""
