@@ -39,9 +39,10 @@
 // in uniform registers), 140 / 193 with the epilogue in warps of its own and
 // cut tiles in small loops, 128 / 178 with the maximum looked for only where a
 // tile's sum says so, 122 / 170 with items decoded without the compiler's
-// divisions, a shorter epilogue, tile 0 beginning its next item beside tile 1's
-// last visit and O stored in whole lines. Splitting a row's columns over two
-// warps (16 softmax warps) changed nothing.
+// divisions, tile 0 beginning its next item beside tile 1's last visit and O
+// stored in whole lines, 115 / 170 with loops for all code that runs a few times
+// an item (one instruction fetch in six had missed). Splitting a row's columns
+// over two warps (16 softmax warps) changed nothing.
 //
 //   warps 0-3   softmax of query tile 0 (thread = query row = TMEM lane)
 //   warps 4-7   softmax of query tile 1
@@ -165,9 +166,16 @@ template <bool kParts>
 struct Visits {
   KeyTiles all, own[2];
   int first, end, sinks[2], from[2], to[2];
-  __device__ __forceinline__ bool any(int t) const { return kParts ? last(t) >= first : own[t].count() > 0; }
-  __device__ __forceinline__ bool active(int t, int i) const { return i < sinks[t] || (i >= from[t] && i < to[t]); }
-  __device__ __forceinline__ int last(int t) const { return to[t] > from[t] ? to[t] - 1 : sinks[t] - 1; }
+  // (no index that the compiler does not know: the arrays stay in registers)
+  __device__ __forceinline__ bool any(int t) const {
+    return kParts ? last(t) >= first : (t ? own[1].count() : own[0].count()) > 0;
+  }
+  __device__ __forceinline__ bool active(int t, int i) const {
+    return t ? i < sinks[1] || (i >= from[1] && i < to[1]) : i < sinks[0] || (i >= from[0] && i < to[0]);
+  }
+  __device__ __forceinline__ int last(int t) const {
+    return t ? (to[1] > from[1] ? to[1] : sinks[1]) - 1 : (to[0] > from[0] ? to[0] : sinks[0]) - 1;
+  }
 };
 
 // Key tile kt in the stream `all`.
@@ -272,44 +280,54 @@ __device__ __forceinline__ void load_seen(uint32_t (&s)[64], uint32_t tS, int ch
     if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = __float_as_uint(-INFINITY);
 }
 
+// The same for 32.
+__device__ __forceinline__ void load_seen(uint32_t (&s)[32], uint32_t tS, int ch, const Seen& v) {
+  tmem_ld_x32(tS + ch, s);
+  const uint32_t see = v.word(ch);
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (!((see >> k) & 1u)) s[k] = __float_as_uint(-INFINITY);
+}
+
 // A score tile in two passes: the maximum first, raised if it has to be, then P
 // over S in TMEM, l brought up. The second product reads columns [0, used).
-// Columns go in halves of 64, read again for the second pass (P overwrites only
-// columns that were read before); a half that no row of the warp sees costs
+// Columns go in pieces of 32, read again for the second pass (P overwrites only
+// columns that were read before); a piece that no row of the warp sees costs
 // only its zeros. Kept small: it runs for the first tile of a row and where the
 // one-pass forms below give up.
 __device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m, float& l, const Seen v, int used,
                                                  bool keep_m) {
   float mx = -INFINITY;
 #pragma unroll 1
-  for (int ch = 0; ch < used; ch += 64) {
-    if (!__any_sync(0xffffffffu, v.word(ch) | v.word(ch + 32))) continue;
-    uint32_t s[64];
+  for (int ch = 0; ch < used; ch += 32) {
+    if (!__any_sync(0xffffffffu, v.word(ch))) continue;
+    uint32_t s[32];
     load_seen(s, tS, ch, v);
-    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    float m2[2] = {mx, -INFINITY};
 #pragma unroll
-    for (int e = 0; e < 64; e += 8)
+    for (int e = 0; e < 32; e += 4)
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        m4[u] = fmax3(m4[u], __uint_as_float(s[e + 2 * u]), __uint_as_float(s[e + 2 * u + 1]));
-    mx = fmaxf(mx, fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])));
+      for (int u = 0; u < 2; ++u)
+        m2[u] = fmax3(m2[u], __uint_as_float(s[e + 2 * u]), __uint_as_float(s[e + 2 * u + 1]));
+    mx = fmaxf(m2[0], m2[1]);
   }
   raise_max(tS, m, l, keep_m ? m : fmaxf(m, mx * c));
   const float neg_m = (m == -INFINITY) ? 0.f : -m;
-  float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
+  float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;  // sums of the even pieces, and of the odd
 #pragma unroll 1
-  for (int ch = 0; ch < used; ch += 64) {
-    uint32_t pk[32];
-    if (__any_sync(0xffffffffu, v.word(ch) | v.word(ch + 32))) {
-      uint32_t s[64];
+  for (int ch = 0; ch < used; ch += 32) {
+    uint32_t pk[16];
+    if (__any_sync(0xffffffffu, v.word(ch))) {
+      uint32_t s[32];
       load_seen(s, tS, ch, v);
       weights(s, pk, c, neg_m, sa0, sa1);
-      weights(s + 32, pk + 16, c, neg_m, sb0, sb1);
     } else {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) pk[k] = 0u;
+      for (int k = 0; k < 16; ++k) pk[k] = 0u;
     }
-    tmem_st_x32_nowait(tS + ch / 2, pk);
+    tmem_st_x16_nowait(tS + ch / 2, pk);
+    const float t0 = sa0, t1 = sa1;
+    sa0 = sb0, sa1 = sb1, sb0 = t0, sb1 = t1;
   }
   tmem_wait_st();
   l += (sa0 + sb0) + (sa1 + sb1);
@@ -349,29 +367,33 @@ __device__ __forceinline__ bool softmax_whole(uint32_t tS, float c, float m, flo
   return true;
 }
 
-// A tile that the mask cuts.
+// A tile that the mask cuts. The halves in a loop, not unrolled: this code runs
+// a few times an item, and is fetched again each time.
 __device__ __forceinline__ bool softmax_cut(uint32_t tS, float c, float m, float& l, const Seen v, int used,
                                             bool& fine) {
-  uint32_t pk[64];
+  uint32_t p0[32], p1[32];
   float sa0 = 0.f, sa1 = 0.f, sb0 = 0.f, sb1 = 0.f;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t* pks = pk + 32 * half;
-    if (64 * half < used && __any_sync(0xffffffffu, v.word(64 * half) | v.word(64 * half + 32))) {
+  for (int k = 0; k < 32; ++k) p1[k] = 0u;
+#pragma unroll 1
+  for (int ch = 0; ch < kBN; ch += 64) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) p0[k] = p1[k];
+    if (ch < used && __any_sync(0xffffffffu, v.word(ch) | v.word(ch + 32))) {
       uint32_t s[64];
-      load_seen(s, tS, 64 * half, v);
-      weights(s, pks, c, -m, sa0, sa1);
-      weights(s + 32, pks + 16, c, -m, sb0, sb1);
+      load_seen(s, tS, ch, v);
+      weights(s, p1, c, -m, sa0, sa1);
+      weights(s + 32, p1 + 16, c, -m, sb0, sb1);
     } else {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) pks[k] = 0u;
+      for (int k = 0; k < 32; ++k) p1[k] = 0u;
     }
   }
   const float sum = (sa0 + sb0) + (sa1 + sb1);
   fine = sum <= kMostSum;
   if (!__all_sync(0xffffffffu, fine)) return false;
-  tmem_st_x32_nowait(tS, *reinterpret_cast<uint32_t(*)[32]>(pk));
-  if (used > 64) tmem_st_x32_nowait(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+  tmem_st_x32_nowait(tS, p0);
+  if (used > 64) tmem_st_x32_nowait(tS + 32, p1);
   tmem_wait_st();
   l += sum;
   return true;
@@ -531,15 +553,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         return r;
       };
       uint32_t g = 0;  // visits of the items before, and of this one
-      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
-      uint32_t acc[2] = {0, 0};
+      uint32_t q_phase = 0, p_phase = 0, o_phase = 0, acc = 0;  // bit t
       bool ok = true;
       auto wait_p = [&](int t) {
-        ok = mbar_wait_warp(&bars->p_full[t], p_phase[t], abort_flag, p.st, kWhere | (4u << 16));
-        p_phase[t] ^= 1u;
-        if (ok && acc[t] == 0) {  // the first P V of an item writes over O: the previous one's has been read
-          ok = mbar_wait_warp(&bars->o_free[t], o_phase[t] ^ 1u, abort_flag, p.st, kWhere | (8u << 16));
-          o_phase[t] ^= 1u;
+        ok = mbar_wait_warp(&bars->p_full[t], (p_phase >> t) & 1u, abort_flag, p.st, kWhere | (4u << 16));
+        p_phase ^= 1u << t;
+        if (ok && ((acc >> t) & 1u) == 0) {  // the first P V of an item writes over O: the previous one's has been read
+          ok = mbar_wait_warp(&bars->o_free[t], ((o_phase >> t) & 1u) ^ 1u, abort_flag, p.st, kWhere | (8u << 16));
+          o_phase ^= 1u << t;
         }
         tc_fence_after();
         return ok;
@@ -558,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) continue;
               if (v.active(t, i)) {
                 if (!wait_p(t)) continue;
-                issue_pv(t, g, acc[t], used_columns(p.w, v.own[t].ns, v.all.tile(i)));
-                acc[t] = 1;
+                issue_pv(t, g, (acc >> t) & 1u, used_columns(p.w, (t ? v.own[1].ns : v.own[0].ns), v.all.tile(i)));
+                acc |= 1u << t;
                 if (i == v.last(t)) tc_commit_if(&bars->o_full[t], one);
               }
               if (v.active(t, i + 1)) {  // S over P once the product above has read it (issue order)
@@ -588,29 +609,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The item's last visit and the next one's first products: tile 0's go before the wait for tile 1's last P.
         const uint32_t g1 = v.first < v.end ? g + 1 : g;
         bool k_ready = false;
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           if (!ok) continue;
           if (v.first < v.end && v.active(t, v.end - 1)) {  // in a loop: this code runs once an item
             if (!wait_p(t)) continue;
-            const int cols = used_columns(p.w, v.own[t].ns, v.all.tile(v.end - 1));
+            const int cols = used_columns(p.w, (t ? v.own[1].ns : v.own[0].ns), v.all.tile(v.end - 1));
             const uint64_t vb = sdesc_advance(v_desc, (g & 1u) * 2 * kTileBytes);
 #pragma unroll 1
             for (int kk = 0; kk * 16 < cols; ++kk)
               mma_ts_if(tm + 256 + t * 128, tm + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv,
-                        kk > 0 ? 1u : acc[t], one);
+                        kk > 0 ? 1u : (acc >> t) & 1u, one);
             tc_commit_if(&bars->o_full[t], one);
           }
-          acc[t] = 0;
+          acc &= ~(1u << t);
           if (!more || !next.any(t)) continue;
           if (!k_ready) {
             ok = wait_kv(g1, 0);
             if (!ok) continue;
             k_ready = true;
           }
-          ok = mbar_wait_warp(&bars->q_full[t], q_phase[t], abort_flag, p.st, kWhere | (2u << 16));
+          ok = mbar_wait_warp(&bars->q_full[t], (q_phase >> t) & 1u, abort_flag, p.st, kWhere | (2u << 16));
           if (!ok) continue;
-          q_phase[t] ^= 1u;
+          q_phase ^= 1u << t;
           tc_fence_after();
           if (next.active(t, next.first)) {
             issue_qk(t, g1);
