@@ -30,10 +30,10 @@
 // after the pass every CTA joins its share of the rows from all of them through
 // distributed shared memory.
 //
-// What bounds it: the tensor core, fed from shared memory. With the softmax
-// taken out, 131 visits of the 1000-row chunk below take 163 us: 80 clocks a
-// 128 x 128 x 16 product where the pipe alone needs 64. Measured on the way
-// (us; 8K tokens x 32 heads, window 1024 / a 1000-row chunk of a 64K context,
+// What bounds it: the tensor core, fed from shared memory. Between an item's
+// ends a visit of both query tiles takes 2350 cycles, 73 for each of its 32
+// products of 128 x 128 x 16 where the pipe alone needs 64; with a window of
+// 1024 the ends are a sixth of an item. Measured on the way (us; 8K tokens x 32 heads, window 1024 / a 1000-row chunk of a 64K context,
 // window 16384): 192 / 237 with a CTA per item and one thread issuing the
 // products, 165 / 192 with the warp issuing them together (the descriptors stay
 // in uniform registers), 140 / 193 with the epilogue in warps of its own and
