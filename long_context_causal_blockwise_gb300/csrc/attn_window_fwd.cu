@@ -30,19 +30,19 @@
 // after the pass every CTA joins its share of the rows from all of them through
 // distributed shared memory.
 //
-// What bounds it: the tensor core, fed from shared memory. Between an item's
-// ends a visit of both query tiles takes 2350 cycles, 73 for each of its 32
-// products of 128 x 128 x 16 where the pipe alone needs 64; with a window of
-// 1024 the ends are a sixth of an item. Measured on the way (us; 8K tokens x 32 heads, window 1024 / a 1000-row chunk of a 64K context,
-// window 16384): 192 / 237 with a CTA per item and one thread issuing the
-// products, 165 / 192 with the warp issuing them together (the descriptors stay
-// in uniform registers), 140 / 193 with the epilogue in warps of its own and
-// cut tiles in small loops, 128 / 178 with the maximum looked for only where a
-// tile's sum says so, 122 / 170 with items decoded without the compiler's
-// divisions, tile 0 beginning its next item beside tile 1's last visit and O
-// stored in whole lines, 115 / 170 with loops for all code that runs a few times
-// an item (one instruction fetch in six had missed). Splitting a row's columns
-// over two warps (16 softmax warps) changed nothing.
+// What bounds it: the tensor core, fed from shared memory. Between an item's ends
+// a visit of both query tiles takes 2350 cycles, 73 for each of its 32 products
+// of 128 x 128 x 16 where the pipe alone needs 64; with a window of 1024 the ends
+// are a sixth of an item. Measured on the way (us; 8K tokens x 32 heads, window
+// 1024 / a 1000-row chunk of a 64K context, window 16384): 192 / 237 with a CTA
+// per item and one thread issuing the products, 165 / 192 with the warp issuing
+// them together (the descriptors stay in uniform registers), 140 / 193 with the
+// epilogue in warps of its own and cut tiles in small loops, 128 / 178 with the
+// maximum looked for only where a tile's sum says so, 122 / 170 with items
+// decoded without the compiler's divisions, tile 0 beginning its next item beside
+// tile 1's last visit and O stored in whole lines, 115 / 170 with loops for all
+// code that runs a few times an item (one instruction fetch in six had missed).
+// Splitting a row's columns over two warps (16 softmax warps) changed nothing.
 //
 //   warps 0-3   softmax of query tile 0 (thread = query row = TMEM lane)
 //   warps 4-7   softmax of query tile 1
