@@ -812,6 +812,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tbase, 512);
   }
   if constexpr (kParts) {
+    // What follows is every warp's: the warpgroups go back to the launch's 128 registers a thread (what two give up is
+    // what the other two take).
+    if (warp < kEpilogueWarp)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     // Join the parts: row r = part + parts * i of the item's 256 here, i in turn by warp i % 16, lane = four features.
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
