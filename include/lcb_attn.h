@@ -402,7 +402,9 @@ int lcb_rope_axes(const void* x, void* y, int B, int S, int H, int D, double the
  * In v (and in q, k, dO of the backward) a non-finite row spreads to rows that
  * do not see it but share a tile with it (128 x 128 at most; the sizes decide),
  * since 0 * NaN is NaN in the products. Keys at or past Sk or lens[b] are never
- * read.
+ * read. O is finite where the largest |v| stays below 2^120 / (the keys that a
+ * row sees + 512): it is summed before the division by the softmax's sum, with
+ * weights up to 2^8 (2^15 for a single key of a 128-key tile).
  *
  * attn_window_fwd — O (bf16 [B, Sq, H, D]) and LSE (fp32, natural log, scale
  * included). Deterministic.

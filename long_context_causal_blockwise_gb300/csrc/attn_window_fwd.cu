@@ -8,10 +8,13 @@
 // of a head as two 128-row tiles that ping-pong, so the tensor core works on
 // one while the softmax warps work on the other; K and V stream by TMA through
 // a four-slot ring; S and O live in TMEM, P goes back over S as the second
-// product's A operand; the running maximum m is raised lazily, only when a score
-// passes it by 32 to 39 in base 2. O / l is exact for any m; P stays below 2^39,
-// l below 2^60 and O below 2^60 max |v|, and what falls under 2^-126 is 2^-126
-// of a term that is there.
+// product's A operand. The weights are 2^(s - m) against a reference m that is
+// set to 2^16 above a row's largest score and raised lazily, only when a score
+// passes that largest one by 24 to 31 in base 2. O / l is exact for any m; a
+// tile's row sum of P stays below 2^15, so that l stays below 2^8 times the keys
+// of the tiles that a row visits and O below that times max |v|, as in the full
+// forward and the split kernel (a row that is finite in one form is finite in the
+// others). Weights under 2^-126 are lost: 2^-110 of one that is there.
 //
 // What the window adds: a CTA streams only the key tiles that one of its rows
 // can see (the sink tiles, then the window's), each query tile skips those of
@@ -87,7 +90,11 @@ constexpr uint32_t kSmKV = 2 * kTileBytes;
 constexpr uint32_t kSmRow = kSmKV + kStages * kTileBytes;  // (m, l) of each query row
 constexpr uint32_t kSmOut = kSmRow + 2 * kBM * 8;  // O on its way out: 128 bytes of each row of a tile
 constexpr uint32_t kSmBar = kSmOut + kBM * 128;
-constexpr float kRescaleThreshold = 32.0f;  // log2 units
+// log2 units: the reference m lies kLead above the largest score when it is set; a score may pass it by
+// kRescaleThreshold. Without the lead, raises are frequent for sharp scores (8K tokens, window 1024, scores of standard
+// deviation 4: 226 us for 117; at 1 no difference).
+constexpr float kLead = 16.0f;
+constexpr float kRescaleThreshold = 8.0f;
 constexpr long long kGroupBytes = 80LL << 20;  // K and V of the windows that a group of heads keeps in L2
 constexpr int kSms = 152;
 constexpr int kMaxCluster = 16;  // above 8 the size is not portable, but allowed on request
@@ -225,12 +232,14 @@ __device__ __forceinline__ int used_columns(const WindowShape& w, int own_ns, in
   return kt < own_ns ? min(kBN, w.sinks - kt * kBN) : kBN;
 }
 
-// Raises the running maximum m to m_new where that passes it by more than the
-// threshold, and rescales l and O (TMEM, 256 columns after S) with it. A row
-// that has seen nothing yet takes m_new as it is: its l and O are 0.
-__device__ __forceinline__ void raise_max(uint32_t tS, float& m, float& l, float m_new) {
+// Sets the reference m anew, kLead above the largest score `top`, where that
+// passes it by more than the threshold, and rescales l and O (TMEM, 256 columns
+// after S) with it. A row that has seen nothing yet takes its first: its l and O
+// are 0.
+__device__ __forceinline__ void raise_max(uint32_t tS, float& m, float& l, float top) {
   const bool fresh = m == -INFINITY;
-  const bool resc = !fresh && m_new > m + kRescaleThreshold;
+  const bool resc = !fresh && top > m + kRescaleThreshold;
+  const float m_new = top + kLead;
   if (__any_sync(0xffffffffu, resc)) {
     // O in pieces of 16 columns: beside the 128 scores, larger ones would not fit the registers
     const float alpha = resc ? ex2_approx(m - m_new) : 1.0f;
@@ -289,7 +298,7 @@ __device__ __forceinline__ void load_seen(uint32_t (&s)[32], uint32_t tS, int ch
     if (!((see >> k) & 1u)) s[k] = __float_as_uint(-INFINITY);
 }
 
-// A score tile in two passes: the maximum first, raised if it has to be, then P
+// A score tile in two passes: the maximum first, m raised if it has to be, then P
 // over S in TMEM, l brought up. The second product reads columns [0, used).
 // Columns go in pieces of 32, read again for the second pass (P overwrites only
 // columns that were read before); a piece that no row of the warp sees costs
@@ -333,16 +342,16 @@ __device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m,
   l += (sa0 + sb0) + (sa1 + sb1);
 }
 
-// The one-pass forms take P against the maximum as it stands, without looking
-// for a new one: the tile's row sum tells afterwards whether a score was too far
-// above it (some P over 2^32 makes a sum over 2^32; none makes one up to 2^39 at
+// The one-pass forms take P against the reference as it stands, without looking
+// for a maximum: the tile's row sum tells afterwards whether a score was too far
+// above it (some P over 2^15 makes a sum over 2^15; 128 P up to 2^8 make 2^15 at
 // most). Then, or at a NaN, S is still in place and the two passes run; they
-// keep the maximum of a row whose own sum is fine, so that no row's bits depend
-// on another row's scores. (A row's first tile takes two passes: weights against
-// its largest score, which is exactly 1, give a row that sees one key that key's
-// v to the bit. Against 0 they would be a little faster, and would not.)
+// keep the reference of a row whose own sum is fine, so that no row's bits depend
+// on another row's scores. (A row's first tile takes two passes: a weight of
+// 2^-16, exact in bf16, for its largest score gives a row that sees one key that
+// key's v to the bit. Against 0 they would be a little faster, and would not.)
 // False: nothing was done.
-constexpr float kMostSum = 549755813888.f;  // 2^39
+constexpr float kMostSum = 32768.f;  // 2^15
 
 // All 128 columns visible.
 __device__ __forceinline__ bool softmax_whole(uint32_t tS, float c, float m, float& l, bool& fine) {
