@@ -278,6 +278,8 @@ struct Seen {
   __device__ __forceinline__ uint32_t word(int ch) const {
     return low_bits(to + 1 - ch) & (~low_bits(from - ch) | low_bits(sink - ch));
   }
+  // Whether it sees any of the tile's.
+  __device__ __forceinline__ bool any() const { return to >= 0 && (from <= min(to, kBN - 1) || sink > 0); }
 };
 
 // 64 scores from column ch on, the hidden ones -inf.
@@ -346,10 +348,13 @@ __device__ __forceinline__ void softmax_two_pass(uint32_t tS, float c, float& m,
 // for a maximum: the tile's row sum tells afterwards whether a score was too far
 // above it (some P over 2^15 makes a sum over 2^15; 128 P up to 2^8 make 2^15 at
 // most). Then, or at a NaN, S is still in place and the two passes run; they
-// keep the reference of a row whose own sum is fine, so that no row's bits depend
-// on another row's scores. (A row's first tile takes two passes: a weight of
+// keep the reference of a row whose own sum is fine. They run at once where the
+// mask has shown some row of the warp nothing yet: a choice by position, so that
+// no row's bits depend on another row's scores. (Where all that a row was shown
+// had a score of -inf, its sum here is infinite or NaN, and it alone takes its
+// first reference.) A row's first tile takes two passes because a weight of
 // 2^-16, exact in bf16, for its largest score gives a row that sees one key that
-// key's v to the bit. Against 0 they would be a little faster, and would not.)
+// key's v to the bit; against 0 it would be a little faster, and would not.
 // False: nothing was done.
 constexpr float kMostSum = 32768.f;  // 2^15
 
@@ -782,6 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         to = visits_before(all, own, part_begin(all.count(), part + 1, p.parts));
       }
       float m = -INFINITY, l = 0.f;
+      bool shown = false;  // whether the mask has left this row a key so far
       for (int i = from; i < to; ++i, s_phase ^= 1u) {
         ok = mbar_wait_warp(&bars->s_full[t], s_phase, abort_flag, p.st, kWhere | (5u << 16));
         if (!ok) break;
@@ -792,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Seen v = {pos - p.w.window + 1 - kbase, min(pos, p.w.Sk - 1) - kbase, p.w.sinks - kbase};
         const int used = used_columns(p.w, own.ns, own.tile(i));
         bool done = false, fine = false;
-        if (!__any_sync(0xffffffffu, m == -INFINITY)) {
+        if (__all_sync(0xffffffffu, shown)) {
           if (kbase + kBN - 1 <= p_first && kbase + kBN <= p.w.Sk &&
               (p_first + kBM - 1 - kbase < p.w.window || kbase + kBN <= p.w.sinks))
             done = softmax_whole(tS, c, m, l, fine);
@@ -800,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             done = softmax_cut(tS, c, m, l, v, used, fine);
         }
         if (!done) softmax_two_pass(tS, c, m, l, v, used, fine);
+        shown |= v.any();
         tc_fence_before();
         mbar_arrive(&bars->p_full[t]);
       }

@@ -1,6 +1,6 @@
-"""GPU tests of rows of windowed attention at the ends of their range, in each
-form of the forward (keys split over a cluster, a block of rows shared by a
-cluster, 128-row tiles) and in the decode call."""
+"""GPU tests of rows of windowed attention at the ends of their range and beside
+one another, in each form of the forward (keys split over a cluster, a block of
+rows shared by a cluster, 128-row tiles) and in the decode call."""
 
 import pytest
 import torch
@@ -48,3 +48,23 @@ def test_large_values_stay_finite(H, Hkv, Sq, Sk, window):
     o, lse = lcb.attn_window_decode(q[:, :3], k, v, lens, window)
     torch.cuda.synchronize()
     check_attn(to64(q[:, :3]), to64(k), to64(v), window, 0, Sk - 3, SCALE, to64(o), to64(lse))
+
+
+@pytest.mark.parametrize("H,Hkv,Sq,Sk,window", FORMS)
+def test_rows_beside_one_that_has_seen_nothing_yet(H, Hkv, Sq, Sk, window):
+    """A row's bits are its own: they do not change when another row's scores of the first two thirds of the keys are
+    all -inf (a product past the fp32 range), so that it takes its maximum later."""
+    q, k, v = _climbing(Sk + 1, H, Hkv, Sq, Sk)
+    q[..., 0] = 0
+    k[..., 0] = 0
+    k[:, :2 * Sk // 3, :, 0] = -3e38
+    want = lcb.attn_window_fwd(q, k, v, Sk)
+    rows = torch.arange(1, Sq, 32, device="cuda")
+    q[:, rows, :, 0] = 3e38  # times -3e38: -inf
+    got = lcb.attn_window_fwd(q, k, v, Sk)
+    torch.cuda.synchronize()
+    others = torch.ones(Sq, dtype=torch.bool, device="cuda")
+    others[rows] = False
+    assert torch.equal(got[0][:, others], want[0][:, others])
+    assert torch.equal(got[1][:, :, others], want[1][:, :, others])
+    assert torch.isfinite(got[0]).all() and not torch.equal(got[1][:, :, rows], want[1][:, :, rows])
