@@ -2,12 +2,13 @@
 one another, in each form of the forward (keys split over a cluster, a block of
 rows shared by a cluster, 128-row tiles) and in the decode call."""
 
+import numpy as np
 import pytest
 import torch
 
 import long_context_causal_blockwise_gb300 as lcb
 from parity import to64
-from window_bounds import check_attn
+from window_bounds import U, check_attn
 
 pytestmark = pytest.mark.gpu
 D = 128
@@ -68,3 +69,31 @@ def test_rows_beside_one_that_has_seen_nothing_yet(H, Hkv, Sq, Sk, window):
     assert torch.equal(got[0][:, others], want[0][:, others])
     assert torch.equal(got[1][:, :, others], want[1][:, :, others])
     assert torch.isfinite(got[0]).all() and not torch.equal(got[1][:, :, rows], want[1][:, :, rows])
+
+
+@pytest.mark.parametrize("B,H,Hkv,Sq,Sk,window,sinks", [
+    (1, 48, 48, 1000, 9000, 8000, 4),  # 19 heads' windows fit the L2 share: groups of 19, 19 and 10
+    (1, 48, 24, 1000, 9000, 8000, 0),  # of 38 and 10
+    (2, 20, 20, 1100, 9001, 8000, 130),  # of 19, 19 and 2, a group over both sequences
+])
+def test_more_than_one_group_of_heads(B, H, Hkv, Sq, Sk, window, sinks):
+    """Heads whose windows' K and V exceed what a group of heads keeps in L2, a last group that is smaller: every row of
+    every head is written (outputs start as NaN) and right."""
+    q, k, v = _rand(Sq, (B, Sq, H, D), (B, Sk, Hkv, D), (B, Sk, Hkv, D))
+    o = torch.full_like(q, float("nan"))
+    lse = torch.full((B, H, Sq), float("nan"), device="cuda")
+    lcb.attn_window_fwd(q, k, v, window, sinks, o=o, lse=lse)
+    p = (Sk - Sq + torch.arange(Sq, device="cuda"))[:, None]
+    j = torch.arange(Sk, device="cuda")[None]
+    hidden = ~((j <= p) & ((p - j < window) | (j < sinks)))
+    for b in range(B):
+        for h in range(H):
+            qd, kd, vd = q[b, :, h].double(), k[b, :, h * Hkv // H].double(), v[b, :, h * Hkv // H].double()
+            s = (qd @ kd.T * SCALE).masked_fill(hidden, float("-inf"))
+            want = torch.logsumexp(s, dim=1)
+            pr = torch.exp(s - want[:, None])
+            # the bounds of window_bounds.py
+            E = (2 * 2 * 128 * 2.0 ** -24 * SCALE * (qd.abs() @ kd.abs().T)).amax(dim=1, keepdim=True) + 2.0 ** -20
+            err = (o[b, :, h].double() - pr @ vd).abs()
+            assert (err <= U * (pr @ vd).abs() + (U + E) * (pr @ vd.abs())).all(), (b, h)
+            assert ((lse[b, h].double() - want).abs() <= E[:, 0] + 2.0 ** -21 * (1 + want.abs())).all(), (b, h)
