@@ -397,7 +397,8 @@ int lcb_rope_axes(const void* x, void* y, int B, int S, int H, int D, double the
  * Sizes: Sq, Sk, |q_pos0| <= 2^28; window >= 1, sinks >= 0; D = 128.
  * Pointers 16-byte aligned, strides in elements, multiples of 8; k and v share
  * strides, o and dO share strides, dk and dv share strides; outputs must not
- * overlap themselves or other arguments.
+ * overlap other arguments, and strides that make their rows (lse's too) overlap
+ * one another are refused.
  * Infinities and NaN: a score hidden by the mask is dropped whatever its value.
  * In v (and in q, k, dO of the backward) a non-finite row spreads to rows that
  * do not see it but share a tile with it (128 x 128 at most; the sizes decide),

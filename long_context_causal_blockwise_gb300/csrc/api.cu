@@ -115,6 +115,10 @@ bool window_output(const void* p, long long rs, long long bs, int B, int rows, i
   return p && aligned16(p) && stride_ok(rs) && stride_ok(bs) &&
          rows_apart(B, rows, static_cast<long long>(heads) * kHeadDim, rs, bs);
 }
+// The fp32 [B, heads, rows] statistics as an output: no two words the same.
+bool window_lse_output(const float* p, long long hs, long long bs, int B, int heads, int rows) {
+  return p && rows_apart(B, heads, rows, hs, bs);
+}
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -880,7 +884,8 @@ int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float*
   int rc = prep_window(&w, B, H, Hkv, Sq, Sk, D, window, sinks, q_pos0, scale);
   if (rc != LCB_OK) return rc;
   if (Sq == 0) return LCB_OK;
-  if (!window_output(o, o_row_stride, o_batch_stride, B, Sq, H) || !lse || lse_head_stride < 0 || lse_batch_stride < 0)
+  if (!window_output(o, o_row_stride, o_batch_stride, B, Sq, H) ||
+      !window_lse_output(lse, lse_head_stride, lse_batch_stride, B, H, Sq))
     return LCB_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (Sk == 0)
@@ -924,7 +929,8 @@ int attn_window_decode(const void* q, const void* k, const void* v, const int* l
   int rc = prep_window(&w, B, H, Hkv, T, Smax, D, window, sinks, 0, scale);
   if (rc != LCB_OK) return rc;
   if (T == 0) return LCB_OK;
-  if (!window_output(o, o_row_stride, o_batch_stride, B, T, H) || !lse || lse_head_stride < 0 || lse_batch_stride < 0)
+  if (!window_output(o, o_row_stride, o_batch_stride, B, T, H) ||
+      !window_lse_output(lse, lse_head_stride, lse_batch_stride, B, H, T))
     return LCB_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (Smax == 0)
