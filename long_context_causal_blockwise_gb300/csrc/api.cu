@@ -189,6 +189,38 @@ int allow_clusters_once(DeviceOnce& once, const void* kernel, int bytes) {
       LCB_ERR_CUDA);
 }
 
+ContextKey current_context() {
+  ContextKey at = {-1, 0};
+  if (cudaGetDevice(&at.dev) != cudaSuccess)
+    at.dev = -1;
+  else
+    at.id = current_context_id();
+  return at;
+}
+
+int resident_clusters(ClusterCounts& known, const ContextKey& at, DeviceOnce& once, const void* kernel, int threads,
+                      int bytes, int cluster) {
+  return known.get(at.dev, at.id, cluster, [&] {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (allow_clusters_once(once, kernel, bytes) != LCB_OK ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // the call goes on without such clusters: not an error of its own
+      return -1;
+    }
+    return n;
+  });
+}
+
 }  // namespace lcb
 
 using namespace lcb;

@@ -59,7 +59,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "attn_window.cuh"
@@ -97,7 +96,6 @@ constexpr float kLead = 16.0f;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr long long kGroupBytes = 80LL << 20;  // K and V of the windows that a group of heads keeps in L2
 constexpr int kSms = 152;
-constexpr int kMaxCluster = 16;  // above 8 the size is not portable, but allowed on request
 
 struct Bars {
   uint64_t q_full[2], q_empty[2];
@@ -893,11 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 const void* parts_kernel() { return reinterpret_cast<const void*>(attn_window_fwd_kernel<true>); }
-
-int allow_parts() {
-  static DeviceOnce once;
-  return allow_clusters_once(once, parts_kernel(), kSmemBytes);
-}
+DeviceOnce g_parts_allowed;
+ClusterCounts g_parts_resident;
 
 cudaLaunchConfig_t parts_config(cudaLaunchAttribute* at, int parts, long long items, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -912,23 +907,6 @@ cudaLaunchConfig_t parts_config(cudaLaunchAttribute* at, int parts, long long it
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cfg;
-}
-
-// Clusters of this size that the GPU holds at once (a property of the device model, asked for once), or 0.
-int resident_clusters(int parts) {
-  static std::atomic<int> known[kMaxCluster + 1];  // 0: not asked yet; n + 1
-  int n = known[parts].load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchAttribute at;
-    const cudaLaunchConfig_t cfg = parts_config(&at, parts, 1, nullptr);
-    int got = 0;
-    if (allow_parts() != 0 || cudaOccupancyMaxActiveClusters(&got, parts_kernel(), &cfg) != cudaSuccess) {
-      cudaGetLastError();  // such clusters do not fit: not an error of the call
-      got = 0;
-    }
-    known[parts].store(n = got + 1, std::memory_order_relaxed);
-  }
-  return n - 1;
 }
 
 // Items, the parts that an item is dealt to, and an estimate of the time in us
@@ -949,9 +927,13 @@ Plan plan_of(const WindowShape& w, int B, int H) {
   const int visits = key_tiles(w, (w.Sq - 1) / (2 * kBM) * 2 * kBM, 2 * kBM).count();
   const double visit_us = w.Sq > kBM ? 1.3 : 1.18;
   d.us = 0.6 + std::ceil(static_cast<double>(d.items) / kSms) * (5.4 + (d.items > kSms ? 1.18 : visit_us) * visits);
+  if (2 * d.items > kSms) return d;
+  const ContextKey at = current_context();
   for (int c = 2; c <= kMaxCluster && c * d.items <= kSms; ++c) {
     const double us = (w.Sq > kBM ? 15. : 11.) + visit_us * ((visits + c - 1) / c);
-    if (us < d.us && resident_clusters(c) >= d.items) d.parts = c, d.us = us;
+    if (us < d.us &&
+        resident_clusters(g_parts_resident, at, g_parts_allowed, parts_kernel(), kThreads, kSmemBytes, c) >= d.items)
+      d.parts = c, d.us = us;
   }
   return d;
 }
@@ -992,7 +974,7 @@ int launch_window_fwd(const WindowFwd& a, cudaStream_t stream) {
   p.by_group = Divisor(p.head_group);
   p.by_last = Divisor(p.last_size);
   if (plan.parts > 1) {
-    if ((rc = allow_parts()) != 0) return rc;
+    if ((rc = allow_clusters_once(g_parts_allowed, parts_kernel(), kSmemBytes)) != 0) return rc;
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t cfg = parts_config(&at, plan.parts, plan.items, stream);
     return cudaLaunchKernelEx(&cfg, attn_window_fwd_kernel<true>, tq, tk, tv, p) == cudaSuccess ? 0 : -4;

@@ -29,7 +29,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "attn_window.cuh"
@@ -43,7 +42,6 @@ namespace {
 constexpr int kD = 128;
 constexpr int kSms = 152;
 constexpr int kKeys = 16;  // keys per warp step
-constexpr int kMaxCluster = 16;  // above 8 the size is not portable, but allowed on request
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum is raised lazily, P stays <= 256
 
@@ -349,37 +347,25 @@ struct Form {
     return cfg;
   }
 
-  static int allow() {
+  static DeviceOnce& allowed() {
     static DeviceOnce once;
-    return allow_clusters_once(once, fn(), kSmem);
+    return once;
   }
 
-  // Clusters of this size that the GPU holds at once (a property of the device model, asked for once), or 0.
-  static int resident(int cluster) {
-    static std::atomic<int> known[kMaxCluster + 1];  // 0: not asked yet; n + 1
-    int n = known[cluster].load(std::memory_order_relaxed);
-    if (n == 0) {
-      cudaLaunchAttribute at;
-      const cudaLaunchConfig_t cfg = config(&at, cluster, 1, nullptr);
-      int got = 0;
-      if (allow() != 0 || cudaOccupancyMaxActiveClusters(&got, fn(), &cfg) != cudaSuccess) {
-        cudaGetLastError();  // such clusters do not fit: not an error of the call
-        got = 0;
-      }
-      known[cluster].store(n = got + 1, std::memory_order_relaxed);
-    }
-    return n - 1;
+  static int resident(const ContextKey& at, int cluster) {
+    static ClusterCounts known;
+    return resident_clusters(known, at, allowed(), fn(), 32 * kWarps, kSmem, cluster);
   }
 
   // The largest cluster with which all tiles are resident at once, every warp having a step; 0 if none.
-  static int one_wave(long long tiles, long long steps) {
+  static int one_wave(const ContextKey& at, long long tiles, long long steps) {
     for (int c = static_cast<int>(std::min<long long>(kMaxCluster, std::max<long long>(1, steps / kWarps))); c > 0; --c)
-      if (resident(c) >= tiles) return c;
+      if (resident(at, c) >= tiles) return c;
     return 0;
   }
 
   static int launch(const WindowSplit& p, long long tiles, cudaStream_t stream) {
-    const int rc = allow();
+    const int rc = allow_clusters_once(allowed(), fn(), kSmem);
     if (rc != 0) return rc;
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t cfg = config(&at, p.cluster, tiles, stream);
@@ -396,8 +382,9 @@ struct Form {
 // warps x 12: 10.8, four x 16 (a second wave): 18.
 template <int NT>
 int launch_rows(WindowSplit& p, long long tiles, long long steps, cudaStream_t stream) {
-  const int c2 = Form<NT, 2>::one_wave(tiles, steps), c4 = Form<NT, 4>::one_wave(tiles, steps),
-            c8 = Form<NT, 8>::one_wave(tiles, steps);
+  const ContextKey at = current_context();
+  const int c2 = Form<NT, 2>::one_wave(at, tiles, steps), c4 = Form<NT, 4>::one_wave(at, tiles, steps),
+            c8 = Form<NT, 8>::one_wave(at, tiles, steps);
   if (2 * c2 >= 4 * c4 && 2 * c2 >= 8 * c8) {
     p.cluster = std::max(1, c2);
     if (c2 == 0) {
@@ -408,7 +395,7 @@ int launch_rows(WindowSplit& p, long long tiles, long long steps, cudaStream_t s
       // of 17 steps 55, 61, 66, 81, 126; 4096 of 5 steps 45, 63, 80, 100, 194.
       double best = 0;
       for (int c = 1; c <= 8 && (c == 1 || c * 32 <= steps); ++c) {
-        const double waves = static_cast<double>(tiles) / std::max(1, Form<NT, 2>::resident(c));
+        const double waves = static_cast<double>(tiles) / std::max(1, Form<NT, 2>::resident(at, c));
         const double full = waves / std::ceil(waves);
         if (full > best + 0.02) best = full, p.cluster = c;
       }

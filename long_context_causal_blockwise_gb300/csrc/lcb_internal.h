@@ -34,8 +34,23 @@ unsigned long long current_context_id();
 // attributes belong to a device context). Returns 0, or LCB_ERR_CUDA.
 int set_smem_limit_once(DeviceOnce& once, const void* kernel, int bytes);
 
-// The same for a kernel launched in clusters, which may have up to 16 CTAs (8 is the portable limit).
+constexpr int kMaxCluster = 16;  // CTAs of a cluster: above 8 the size is not portable, but allowed on request
+
+// The same for a kernel launched in clusters of up to kMaxCluster CTAs.
 int allow_clusters_once(DeviceOnce& once, const void* kernel, int bytes);
+
+// The current device and its context; a device of -1 if there is none.
+struct ContextKey {
+  int dev;
+  unsigned long long id;
+};
+ContextKey current_context();
+
+// Clusters of `cluster` CTAs (`threads` each, `bytes` of dynamic shared memory) of a kernel that the GPU holds at
+// once, or 0. Asked of the driver once in each context; `once` holds the kernel's attributes.
+typedef DeviceCounts<kMaxCluster + 1> ClusterCounts;
+int resident_clusters(ClusterCounts& known, const ContextKey& at, DeviceOnce& once, const void* kernel, int threads,
+                      int bytes, int cluster);
 
 // One block of a forward launch (rows relative to the shared tensors).
 struct FwdTask {
