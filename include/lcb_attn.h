@@ -416,6 +416,17 @@ int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float*
                     long long o_row_stride, long long o_batch_stride, long long lse_head_stride,
                     long long lse_batch_stride, void* stream);
 
+#define LCB_WINDOW_FORM_EMPTY 0   /* no query rows, or no keys */
+#define LCB_WINDOW_FORM_SPLIT 1   /* few query rows: their keys split over clusters */
+#define LCB_WINDOW_FORM_CLUSTER 2 /* few blocks of query rows: a cluster shares a block's keys */
+#define LCB_WINDOW_FORM_TILES 3   /* 128-row tiles, a CTA walking over blocks */
+
+/* Which of its kernels attn_window_fwd takes for these sizes on the current
+ * device (without one it knows of no clusters), or a negative LCB_ERR_* code.
+ * The result is the same in all, within their roundings; for tests and
+ * measurements that mean one of them. */
+int attn_window_fwd_form(int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks, long long q_pos0);
+
 /* Bytes of device workspace attn_window_bwd needs for these sizes: Delta, the
  * tiled fp32 dQ accumulator, and fp32 dK/dV partials of key tiles whose queries
  * are dealt to several CTAs; 0 for sizes that attn_window_bwd refuses, or with

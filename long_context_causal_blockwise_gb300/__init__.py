@@ -8,6 +8,7 @@ Public calls (all run in this library's CUDA kernels):
   attn_lse_merge, zigzag_schedule, ring_schedule, permute_rows, cast_f32_bf16,
   rope (rotary position embedding with a raised base, and its inverse),
   attn_window_fwd / attn_window_bwd (sliding window with sinks, shared K/V heads),
+  attn_window_fwd_form (which of its kernels that forward takes),
   attn_window_decode (its form for the newest tokens against a K/V cache),
   rope_axes (rotary positions with several axes, and the inverse),
   cross_entropy (the loss head with an in-place backward),
@@ -39,6 +40,7 @@ from ._lib import (  # noqa: F401
     attn_window_bwd_workspace_bytes,
     attn_window_decode,
     attn_window_fwd,
+    attn_window_fwd_form,
     cast_f32_bf16,
     cross_entropy,
     dq_tiles_zero_,

@@ -85,6 +85,7 @@ _SIGNATURES = {
                        _I, _LL, _LL, _P], _I),
     "attn_window_fwd": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _LL, _F, _LL, _LL, _LL, _LL, _LL, _LL, _LL,
                          _LL, _P], _I),
+    "attn_window_fwd_form": ([_I, _I, _I, _I, _I, _I, _I, _I, _LL], _I),
     "attn_window_bwd_workspace_bytes": ([_I, _I, _I, _I, _I, _I, _I, _I, _LL], _SZ),
     "attn_window_bwd": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _LL, _F, _LL, _LL, _LL, _LL,
                          _LL, _LL, _LL, _LL, _LL, _LL, _LL, _LL, _P, _SZ, _P], _I),
@@ -603,6 +604,16 @@ def attn_window_fwd(q, k, v, window, sinks=0, q_pos0=None, scale=None, o=None, l
     if rc:
         _check("attn_window_fwd", rc)
     return o, lse
+
+
+def attn_window_fwd_form(B, H, Hkv, Sq, Sk, window, sinks=0, q_pos0=None, D=128):
+    """Which of its kernels attn_window_fwd takes for these sizes on the current device: "split" (few query rows, their
+    keys split over clusters), "cluster" (few blocks of query rows, a cluster to each), "tiles", or "empty"."""
+    rc = load().attn_window_fwd_form(B, H, Hkv, Sq, Sk, D, _count(window), _count(sinks),
+                                     Sk - Sq if q_pos0 is None else int(q_pos0))
+    if rc < 0:
+        _check("attn_window_fwd_form", rc)
+    return ("empty", "split", "cluster", "tiles")[rc]
 
 
 def attn_window_bwd_workspace_bytes(B, H, Hkv, Sq, Sk, window, sinks=0, q_pos0=None, D=128):

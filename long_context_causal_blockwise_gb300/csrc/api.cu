@@ -952,6 +952,15 @@ int attn_window_fwd(const void* q, const void* k, const void* v, void* o, float*
   return finish(launch_window_fwd(a, st), st);
 }
 
+int attn_window_fwd_form(int B, int H, int Hkv, int Sq, int Sk, int D, int window, int sinks, long long q_pos0) {
+  WindowShape w;
+  const int rc = prep_window(&w, B, H, Hkv, Sq, Sk, D, window, sinks, q_pos0, 1.f);
+  if (rc != LCB_OK) return rc;
+  if (Sq == 0 || Sk == 0) return LCB_WINDOW_FORM_EMPTY;
+  if (window_split_pays(B, H, Hkv, w)) return LCB_WINDOW_FORM_SPLIT;
+  return window_tiles_parts(w, B, H) > 1 ? LCB_WINDOW_FORM_CLUSTER : LCB_WINDOW_FORM_TILES;
+}
+
 int attn_window_decode(const void* q, const void* k, const void* v, const int* lens, void* o, float* lse, int B, int H,
                        int Hkv, int T, int Smax, int D, int window, int sinks, float scale, long long q_row_stride,
                        long long q_batch_stride, long long kv_row_stride, long long kv_batch_stride,

@@ -988,5 +988,6 @@ int launch_window_fwd(const WindowFwd& a, cudaStream_t stream) {
 }
 
 double window_tiles_us(const WindowShape& w, int B, int H) { return plan_of(w, B, H).us; }
+int window_tiles_parts(const WindowShape& w, int B, int H) { return plan_of(w, B, H).parts; }
 
 }  // namespace lcb

@@ -167,6 +167,7 @@ struct WindowFwd {
 };
 int launch_window_fwd(const WindowFwd& a, cudaStream_t stream);  // Sq, Sk > 0
 double window_tiles_us(const WindowShape& w, int B, int H);      // estimate of its time
+int window_tiles_parts(const WindowShape& w, int B, int H);      // CTAs that it gives a block of query rows
 
 struct WindowBwd {
   RowView q, k, v, o, dO;
