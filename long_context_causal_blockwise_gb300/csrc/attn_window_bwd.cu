@@ -166,7 +166,8 @@ struct WinParams {
 
 // Before the pass: the row statistics, and zeros for the dQ accumulator. One
 // warp a token row (rows past the last fill their tile: LSE = -inf gives P = 0)
-// over all heads, half a warp a head's dO.O, eight heads' loads in flight.
+// over all heads, half a warp a head's dO.O (O as the forward rounded it, the
+// sum in fp32), eight heads' loads in flight.
 // Bound by HBM: 512 bytes read and 520 written per row and head.
 __global__ void __launch_bounds__(256) window_bwd_prep_kernel(const __grid_constant__ WinParams p) {
   const int rows = p.q_tiles * kT;
@@ -457,8 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scl = p.scale;
     for (int s = 0; s <= n && ok; ++s) {
       if (s > 0) {
-        // Phase 2: dS'^T = scale P^T (dP^T - Delta), rounded to bf16 (half a step, 2^-9 of each value, of either
-        // sign) into shared memory for dK and dQ, which come out of the products scaled.
+        // Phase 2: dS'^T = scale P^T (dP^T - Delta), rounded to bf16 (half a step, up to 2^-8 of each value, of
+        // either sign) into shared memory for dK and dQ, which come out of the products scaled.
         const int i = s - 1;
         const uint32_t ph = static_cast<uint32_t>(i) & 1u;
         ok = mbar_wait_warp(&bars->dp_full, ph, abort_flag, p.st, kWhere | (6u << 16));
@@ -527,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         {
+          // to bf16 for dV (half a step, up to 2^-8 of each weight, of either sign); dS takes the fp32 values
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) pk[e >> 1] = pack_bf16x2(pv[e], pv[e + 1]);

@@ -255,8 +255,8 @@ __device__ __forceinline__ void raise_max(uint32_t tS, float& m, float& l, float
 }
 
 // P of 16 pairs of scores (bf16 pairs into pk), their sum into (s0, s1). P is
-// rounded to bf16 for the second product (half a step, 2^-9 of each weight, of
-// either sign); the sum is fp32.
+// rounded to bf16 for the second product (half a step, up to 2^-8 of each weight,
+// of either sign); the sum is fp32.
 __device__ __forceinline__ void weights(const uint32_t* s, uint32_t* pk, float c, float neg_m, float& s0, float& s1) {
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
@@ -914,8 +914,9 @@ cudaLaunchConfig_t parts_config(cudaLaunchAttribute* at, int parts, long long it
 // rows, 1.3 where both do, an item's start and end 5.4, a cluster and its join 5
 // or 9 more (64 or 128 KB of O a CTA through distributed shared memory). The
 // cluster, all of them resident at once, that promises most. us by parts 1, 2,
-// 4, 8, 12, 4 heads x 256 rows: window 16384 181, 108, 62, 40, 33; 2048 34, 27,
-// 21, 19, 19; 512 18, 18, 16, 15, 17.
+// 4, 8, 12, 16, 4 heads x 256 rows: window 16384 165, 103, 59, 38, 32, 30 (31 with
+// the 15 that the estimate takes); 2048 32, 26, 20, 19, 19, 19; 512 17, 18, 16,
+// 15, 16, 17.
 struct Plan {
   long long items;
   int parts;

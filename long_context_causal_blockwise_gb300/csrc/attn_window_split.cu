@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_split_kernel(const __grid_
         const float e0 = ex2_approx(s[nt][2 * u] - m0), e1 = ex2_approx(s[nt][2 * u + 1] - m1);
         l[nt][0] += e0;
         l[nt][1] += e1;
-        // P goes to bf16 for the product (half a step, 2^-9 of each weight, of either sign); l keeps fp32
+        // P goes to bf16 for the product (half a step, up to 2^-8 of each weight, of either sign); l keeps fp32
         pb[nt][u] = transpose_8x8(pack_bf16x2(e0, e1));
       }
     }
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_split_kernel(const __grid_
     }
   __syncthreads();
   const int d4 = (threadIdx.x & 31) * 4;
-  for (int r = warp; r < kRows; r += kWarps) {  // a warp joins a row: its four partials into slot 0
+  for (int r = warp; r < kRows; r += kWarps) {  // a warp joins a row: its partials into slot 0
     float M = sM[0][r];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sM[w][r]);
@@ -413,17 +413,20 @@ int launch_rows(WindowSplit& p, long long tiles, long long steps, cudaStream_t s
 }  // namespace
 
 // Query rows of one 16-row tile per K/V head always come here. For more, two
-// estimates in us, fitted to 190 forwards (1 to 2500 query rows, 1 to 40 heads,
-// G from 1 to 8, windows of 16 to 16384; the slower form is picked in one of
-// ten of them, by 20% at most). This kernel: a start, each row tile's own, and
-// its tensor work, whose keys feed 16 rows from registers. The 128-row tiles of
-// attn_window_fwd: a CTA walks the visits of 256 query rows of one head. us,
-// this kernel / tiles:
-//   H 32, Hkv 8, window 16384:  8 tokens 38 / 158, 32 tokens 91 / 160, 64 tokens 173 / 160
-//   H 32, Hkv 32, window 1024: 32 tokens 13 / 19, 128 tokens 27 / 20
-//   H 4, Hkv 4, window 4096:  256 tokens 26 / 53
-// More row tiles than the GPU holds at once do not pay: 1024 of 256 keys take
-// 64, 512 take 19.
+// estimates in us decide, fitted to forwards of 1 to 2500 query rows, 1 to 40
+// heads, G from 1 to 8 and windows of 16 to 16384. This kernel: a start, each
+// row tile's own, and its tensor work, whose keys feed 16 rows from registers.
+// The 128-row tiles of attn_window_fwd: the visits of 256 query rows of one
+// head, by one CTA or shared by a cluster. us, this kernel / tiles by one CTA /
+// tiles with the cluster that the plan gives them:
+//   H 32, Hkv 8, window 16384:  8 tokens 38 / 157 / 49, 32 tokens 91 / 157 / 50, 64 tokens 169 / 158 / 51
+//   H 32, Hkv 32, window 1024: 32 tokens 13 / 18 / 14, 128 tokens 27 / 20 / 16
+//   H 4, Hkv 4, window 4096:  256 tokens 26 / 51 / 21
+//   H 4, Hkv 4, window 512:  256 tokens 10 / 17 / 15
+// Of 140 other random forwards, each timed in all forms, 15 took a form that was
+// more than 2% slower than the best, 4 by more than 10%, the worst by 18%. More
+// row tiles than the GPU holds at once do not pay: 1024 of 256 keys take 37 and
+// 512 take 20 where the tiles take 15.
 bool window_split_pays(int B, int H, int Hkv, const WindowShape& w) {
   const int G = H / Hkv;
   const long long rows = static_cast<long long>(w.Sq) * G;
