@@ -52,6 +52,18 @@ def test_large_values_stay_finite(H, Hkv, Sq, Sk, window):
 
 
 @pytest.mark.parametrize("H,Hkv,Sq,Sk,window", FORMS)
+def test_small_values_keep_their_precision(H, Hkv, Sq, Sk, window):
+    """v times 2^-100 gives O times 2^-100. The weights reach down to 2^-16 below a row's largest, so that O before the
+    division holds products of 2^-116 |v|, subnormal in fp32: off by 2^-149 each, 2^-149 * 2^16 * 2^100 = 2^-33 of v's
+    unit after it, for at most 2^12 of them. Each O is then rounded once more."""
+    q, k, v = _rand(Sk + 2, (1, Sq, H, D), (1, Sk, Hkv, D), (1, Sk, Hkv, D))
+    want = lcb.attn_window_fwd(q, k, v, window)[0].double()
+    got = lcb.attn_window_fwd(q, k, (v.float() * 2.0 ** -100).to(torch.bfloat16), window)[0].double() * 2.0 ** 100
+    torch.cuda.synchronize()
+    assert ((got - want).abs() <= 2 * U * want.abs() + 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("H,Hkv,Sq,Sk,window", FORMS)
 def test_rows_beside_one_that_has_seen_nothing_yet(H, Hkv, Sq, Sk, window):
     """A row's bits are its own: they do not change when another row's scores of the first two thirds of the keys are
     all -inf (a product past the fp32 range), so that it takes its maximum later."""
