@@ -91,7 +91,7 @@ constexpr uint32_t kSmOut = kSmRow + 2 * kBM * 8;  // O on its way out: 128 byte
 constexpr uint32_t kSmBar = kSmOut + kBM * 128;
 // log2 units: the reference m lies kLead above the largest score when it is set; a score may pass it by
 // kRescaleThreshold. Without the lead, raises are frequent for sharp scores (8K tokens, window 1024, scores of standard
-// deviation 4: 226 us for 117; at 1 no difference).
+// deviation 4: 226 us for 117; at 1.5 no difference).
 constexpr float kLead = 16.0f;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr long long kGroupBytes = 80LL << 20;  // K and V of the windows that a group of heads keeps in L2
