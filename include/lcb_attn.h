@@ -467,6 +467,78 @@ int attn_window_decode(const void* q, const void* k, const void* v, const int* l
                        long long lse_batch_stride, void* stream);
 
 /*
+ * The K/V cache in 4 or 8 bits: written from bf16 K and V, read back as bf16,
+ * and attended to as it lies (attn_cache_decode).
+ *
+ * A cached row of a K/V head holds a K and a V vector of D = 128 channels.
+ * Each group of 32 channels has a bf16 scale s = max |x| / m rounded to
+ * nearest, m = 7 (bits 4) or 127 (bits 8); channel c holds n_c * s with n_c =
+ * x_c / s rounded to the nearest whole number, ties away from zero: off by at
+ * most s / 2 (and the scale's rounding at the group's largest, 2^-8 of it).
+ * A group whose largest magnitude is below 2^-100 holds zeros; one with an
+ * infinity or a NaN holds NaN in all 32 channels.
+ * A row is one record of lcb_kv_cache_row_bytes(bits) bytes, 144 or 272; the
+ * order of the codes in it is the library's (csrc/kv_cache.cuh).
+ * cache: [B, Hkv, Smax, row bytes], the rows of a head one after another,
+ * batch and head strides in BYTES, multiples of 16; 16-byte aligned. A row of
+ * zero bytes holds zeros. Sizes: T, Smax <= 2^28.
+ *
+ * lcb_kv_cache_row_bytes — bytes of a row, or LCB_ERR_UNSUPPORTED.
+ */
+int lcb_kv_cache_row_bytes(int bits);
+
+/*
+ * lcb_kv_cache_write — the T newest tokens' K and V (bf16 [B, T, Hkv, D], 16-
+ * byte aligned, strides in elements, multiples of 8, shared by k and v) go into
+ * the cache. lens: DEVICE int32 [B], the rows of each sequence with the new ones
+ * among them, as in attn_window_decode: token t of sequence b goes to row
+ * lens[b] - T + t. A token whose row would lie before 0 or at or past Smax is
+ * dropped: a batch of prompts of unequal length, padded on the left, is one
+ * call. Other rows are left as they were.
+ */
+int lcb_kv_cache_write(void* cache, const void* k, const void* v, const int* lens, int B, int Hkv, int T, int Smax,
+                       int D, int bits, long long cache_batch_stride, long long cache_head_stride,
+                       long long row_stride, long long batch_stride, void* stream);
+
+/*
+ * lcb_kv_cache_read — rows [start, start + n) of every head as bf16 k and v
+ * [B, n, Hkv, D] (16-byte aligned, strides in elements, multiples of 8, shared):
+ * n_c * s rounded once. lens: DEVICE int32 [B], or NULL; rows at or past
+ * lens[b] read as zeros, and the cache is not read there. For the next chunk of
+ * a prompt, say, which attends in bf16 (attn_window_fwd).
+ */
+int lcb_kv_cache_read(const void* cache, void* k, void* v, const int* lens, int B, int Hkv, int n, int start, int Smax,
+                      int D, int bits, long long cache_batch_stride, long long cache_head_stride, long long row_stride,
+                      long long batch_stride, void* stream);
+
+/* Bytes of device workspace attn_cache_decode needs for these sizes on the
+ * current device (few heads and many keys: partial results of more CTAs than a
+ * cluster holds); 0 for none, and for sizes that the call refuses. */
+size_t attn_cache_decode_workspace_bytes(int B, int H, int Hkv, int T, int Smax, int D, int bits, int window,
+                                         int sinks);
+
+/*
+ * attn_cache_decode — attn_window_decode over the quantised cache: q, o
+ * [B, T, H, D] bf16; token t of sequence b stands at position lens[b] - T + t
+ * (lens: DEVICE int32 [B], clamped to [0, Smax]) and sees the keys j <= p with
+ * p - j < window, and the first `sinks`. Attention is that over the held values
+ * n_c * s, unrounded; LSE fp32 (natural log, scale included). Each visible row
+ * is read once for all query rows of its head up to 16 of them (T * H / Hkv).
+ * Deterministic. Any T; for the many tokens of a prompt's chunk,
+ * lcb_kv_cache_read and attn_window_fwd are faster.
+ * A row with NaN makes NaN of those query rows alone that see it. window, sinks, scale, heads, q, o, lse and their
+ * strides as attn_window_decode; the cache as above. workspace: device memory
+ * of at least attn_cache_decode_workspace_bytes(), 16-byte aligned, contents
+ * ignored (NULL where that is 0); calls that may overlap on the GPU need
+ * workspaces of their own.
+ */
+int attn_cache_decode(const void* q, const void* cache, const int* lens, void* o, float* lse, int B, int H, int Hkv,
+                      int T, int Smax, int D, int bits, int window, int sinks, float scale, long long q_row_stride,
+                      long long q_batch_stride, long long cache_batch_stride, long long cache_head_stride,
+                      long long o_row_stride, long long o_batch_stride, long long lse_head_stride,
+                      long long lse_batch_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * lcb_permute_rows — row gather/scatter on the device, used to move a
  * [B=1, S, H, D] tensor into zigzag order and back, [ZZ].
  * scatter == 0: dst[t] = src[perm[t]];  scatter == 1: dst[perm[t]] = src[t].

@@ -10,6 +10,8 @@ Public calls (all run in this library's CUDA kernels):
   attn_window_fwd / attn_window_bwd (sliding window with sinks, shared K/V heads),
   attn_window_fwd_form (which of its kernels that forward takes),
   attn_window_decode (its form for the newest tokens against a K/V cache),
+  kv_cache_empty / kv_cache_write / kv_cache_read (a K/V cache in 4 or 8 bits),
+  attn_cache_decode (the newest tokens against that cache),
   rope_axes (rotary positions with several axes, and the inverse),
   cross_entropy (the loss head with an in-place backward),
   zigzag_attention_fwd / zigzag_attention_bwd (the one-device zigzag ring),
@@ -32,6 +34,8 @@ from ._lib import (  # noqa: F401
     attn_bwd_noalloc_max_rows,
     attn_bwd_preprocess,
     attn_bwd_workspace_bytes,
+    attn_cache_decode,
+    attn_cache_decode_workspace_bytes,
     attn_fwd,
     attn_fwd_ex,
     attn_fwd_group,
@@ -46,6 +50,9 @@ from ._lib import (  # noqa: F401
     dq_tiles_zero_,
     dq_tiles_zeros,
     dq_untile,
+    kv_cache_empty,
+    kv_cache_read,
+    kv_cache_write,
     load,
     permute_rows,
     ring_schedule,

@@ -91,6 +91,12 @@ _SIGNATURES = {
                          _LL, _LL, _LL, _LL, _LL, _LL, _LL, _LL, _P, _SZ, _P], _I),
     "attn_window_decode": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _LL, _LL, _LL, _LL, _LL, _LL, _LL,
                             _LL, _P], _I),
+    "lcb_kv_cache_row_bytes": ([_I], _I),
+    "lcb_kv_cache_write": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _LL, _LL, _LL, _LL, _P], _I),
+    "lcb_kv_cache_read": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _LL, _LL, _LL, _LL, _P], _I),
+    "attn_cache_decode_workspace_bytes": ([_I, _I, _I, _I, _I, _I, _I, _I, _I], _SZ),
+    "attn_cache_decode": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _LL, _LL, _LL, _LL, _LL, _LL, _LL,
+                           _LL, _P, _SZ, _P], _I),
     "lcb_permute_rows": ([_P, _P, _P, _I, _LL, _P], _I),
     "lcb_scatter_rows": ([_P, _P, _P, _I, _LL, _P], _I),
     "lcb_cast_f32_bf16": ([_P, _P, _LL, _P], _I),
@@ -683,6 +689,140 @@ def attn_window_decode(q, k_cache, v_cache, lens, window, sinks=0, scale=None, o
         ob, lh, lb, stream)
     if rc:
         _check("attn_window_decode", rc)
+    return o, lse
+
+
+# ------------------------------------------------------------------ the cache in 4 or 8 bits
+
+_ROW_BYTES = {4: 144, 8: 272}  # lcb_kv_cache_row_bytes
+_ROW_BITS = {n: bits for bits, n in _ROW_BYTES.items()}
+
+
+def kv_cache_empty(B, Hkv, Smax, bits=4, device="cuda"):
+    """A K/V cache for B sequences of up to Smax tokens, in 4 or 8 bits: uint8 [B, Hkv, Smax, 144 or 272].
+
+    Slices of it along the first two dimensions are caches too."""
+    if bits not in _ROW_BYTES:
+        raise ValueError(f"kv_cache_empty: bits must be 4 or 8, got {bits}")
+    return torch.zeros((B, Hkv, Smax, _ROW_BYTES[bits]), dtype=torch.uint8, device=device)
+
+
+def _cache(t, name):
+    """(B, Hkv, Smax, bits, batch stride, head stride) of a quantised cache."""
+    shape = t.shape
+    if t.dtype is not torch.uint8 or len(shape) != 4 or shape[3] not in _ROW_BITS:
+        raise ValueError(f"{name}: the cache must be uint8 [B, Hkv, Smax, 144 or 272] (kv_cache_empty), "
+                         f"got {t.dtype} {tuple(shape)}")
+    B, Hkv, Smax, row = shape
+    if t.is_contiguous():
+        return B, Hkv, Smax, _ROW_BITS[row], Hkv * Smax * row, Smax * row
+    bs, hs, rs, es = t.stride()
+    if es != 1 or rs != row and Smax > 1:
+        raise ValueError(f"{name}: the rows of a head must follow one another")
+    hs = hs if Hkv > 1 else Smax * row
+    return B, Hkv, Smax, _ROW_BITS[row], bs if B > 1 else Hkv * hs, hs
+
+
+def _lens_of(lens, B):
+    if lens.dtype is not torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous int32 [B] tensor")
+
+
+def kv_cache_write(cache, k, v, lens):
+    """The T newest tokens' K and V (bf16 [B, T, Hkv, 128] views of the same strides) go into the cache; returns it.
+
+    lens (CUDA int32 [B]): rows of each sequence with the new ones among them;
+    token t goes to row lens[b] - T + t, and is dropped if that is before 0 or
+    past the cache (prompts of unequal length, padded on the left, are one
+    call). Per group of 32 channels: scale bf16(max |x| / 7) in 4 bits (/ 127
+    in 8), x / scale to the nearest whole number, ties away from zero. A group
+    with an infinity or NaN reads as NaN."""
+    B, Hkv, Smax, bits, cb, ch = _cache(cache, "kv_cache_write")
+    ks, kr, kb = _rows(k, "k")
+    vs, vr, vb = _rows(v, "v")
+    if vs != ks or ks[0] != B or ks[2] != Hkv or ks[3] != 128:
+        raise ValueError(f"kv_cache_write: k and v must be [{B}, T, {Hkv}, 128] as the cache, got {tuple(ks)}, {tuple(vs)}")
+    T = ks[1]
+    if (vr != kr or vb != kb) and T:
+        raise ValueError("k and v must share strides")
+    _lens_of(lens, B)
+    stream = _raw_stream("kv_cache_write", cache.get_device(), (k, v, lens))
+    rc = (_LIB or load()).lcb_kv_cache_write(cache.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(), B, Hkv, T,
+                                             Smax, 128, bits, cb, ch, kr, kb, stream)
+    if rc:
+        _check("kv_cache_write", rc)
+    return cache
+
+
+def kv_cache_read(cache, n, start=0, lens=None, k=None, v=None):
+    """Rows [start, start + n) of the cache as bf16 K and V; returns (k, v) [B, n, Hkv, 128].
+
+    lens (CUDA int32 [B], optional): rows at or past lens[b] read as zeros."""
+    B, Hkv, Smax, bits, cb, ch = _cache(cache, "kv_cache_read")
+    n, start = int(n), int(start)
+    if n < 0 or start < 0 or start + n > Smax:
+        raise ValueError(f"kv_cache_read: rows [{start}, {start + n}) of a cache of {Smax}")
+    shape = torch.Size((B, n, Hkv, 128))
+    if k is None:
+        k = torch.empty(shape, dtype=_BF16, device=cache.device)
+    if v is None:
+        v = torch.empty_like(k)
+    (ks, kr, kb), (vs, vr, vb) = _rows(k, "k"), _rows(v, "v")
+    if ks != shape or vs != shape:
+        raise ValueError(f"kv_cache_read: k and v must be {tuple(shape)}, got {tuple(ks)}, {tuple(vs)}")
+    if (vr != kr or vb != kb) and n:
+        raise ValueError("k and v must share strides")
+    if lens is not None:
+        _lens_of(lens, B)
+    stream = _raw_stream("kv_cache_read", cache.get_device(), (k, v) if lens is None else (k, v, lens))
+    rc = (_LIB or load()).lcb_kv_cache_read(cache.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                            None if lens is None else lens.data_ptr(), B, Hkv, n, start, Smax, 128,
+                                            bits, cb, ch, kr, kb, stream)
+    if rc:
+        _check("kv_cache_read", rc)
+    return k, v
+
+
+def attn_cache_decode_workspace_bytes(B, H, Hkv, T, Smax, bits=4, window=None, sinks=0, D=128):
+    return int(load().attn_cache_decode_workspace_bytes(B, H, Hkv, T, Smax, D, bits,
+                                                        _MOST if window is None else _count(window), _count(sinks)))
+
+
+def attn_cache_decode(q, cache, lens, window=None, sinks=0, scale=None, o=None, lse=None, workspace=None):
+    """attn_window_decode over a quantised cache (kv_cache_empty, kv_cache_write); returns (o, lse fp32 [B, H, T]).
+
+    q [B, T, H, 128] bf16, the T newest tokens, whose K and V are in the cache
+    already: token t stands at position lens[b] - T + t. window=None: every key
+    up to its own position. Attention is over the values that the cache holds.
+    workspace: uint8 of attn_cache_decode_workspace_bytes (None: allocated
+    here)."""
+    B, Hkv, Smax, bits, cb, ch = _cache(cache, "attn_cache_decode")
+    qs, qr, qb = _rows(q, "q")
+    H, D = qs[2], qs[3]
+    if qs[0] != B or D != 128 or Hkv < 1 or H % Hkv:
+        raise ValueError(f"attn_cache_decode: q must be [{B}, T, H, 128] with the cache's {Hkv} heads dividing H, "
+                         f"got {tuple(qs)}")
+    _lens_of(lens, B)
+    T = qs[1]
+    window = _MOST if window is None else _count(window)
+    sinks = _count(sinks)
+    o, lse, orr, ob, lh, lb = _window_out(q, qs, o, lse)
+    lib = _LIB or load()
+    if workspace is None:
+        n = lib.attn_cache_decode_workspace_bytes(B, H, Hkv, T, Smax, D, bits, window, sinks)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    stream = _raw_stream("attn_cache_decode", q.get_device(),
+                         (cache, lens, o, lse) if workspace is None else (cache, lens, o, lse, workspace))
+    rc = lib.attn_cache_decode(
+        q.data_ptr(), cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, Smax, D, bits,
+        window, sinks, D ** -0.5 if scale is None else float(scale), qr, qb, cb, ch, orr, ob, lh, lb,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+    if rc:
+        _check("attn_cache_decode", rc)
     return o, lse
 
 

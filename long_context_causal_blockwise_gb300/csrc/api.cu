@@ -12,6 +12,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "kv_cache.cuh"
 #include "lcb_attn.h"
 #include "lcb_internal.h"
 
@@ -103,6 +104,11 @@ bool rows_apart(int B, int rows, long long row, long long rs, long long bs) {
   if (rs < 0 || bs < 0 || rs >= (1LL << 38) || bs >= (1LL << 38)) return false;
   if (rows > 1 && rs < row) return false;
   return B == 1 || bs >= (rows - 1) * rs + row || (bs >= row && (rows == 1 || rs >= (B - 1) * bs + row));
+}
+// The same for the heads of a [B, heads] view of `head` bytes each.
+bool heads_apart(int B, int heads, long long head, long long hs, long long bs) {
+  if (heads > 1 && hs < head) return false;
+  return B == 1 || bs >= (heads - 1) * hs + head || (bs >= head && (heads == 1 || hs >= (B - 1) * bs + head));
 }
 bool stride_ok(long long s) { return s >= 0 && (s % 8) == 0 && s < (1LL << 38); }
 
@@ -987,6 +993,129 @@ int attn_window_decode(const void* q, const void* k, const void* v, const int* l
                                                o_batch_stride, lse_head_stride, lse_batch_stride),
                                     st),
                 st);
+}
+
+// A quantised cache [B, Hkv, Smax, row bytes]; as an output its heads also lie apart from one another.
+static bool cache_view(const void* p, long long bs, long long hs, int B, int Hkv, int Smax, int bits, bool output) {
+  if (!p || !aligned16(p) || bs < 0 || hs < 0 || bs % 16 || hs % 16 || bs >= (1LL << 40) || hs >= (1LL << 40))
+    return false;
+  return !output || heads_apart(B, Hkv, static_cast<long long>(Smax) * cache_row_bytes(bits), hs, bs);
+}
+
+int lcb_kv_cache_row_bytes(int bits) {
+  return bits == 4 || bits == 8 ? cache_row_bytes(bits) : LCB_ERR_UNSUPPORTED;
+}
+
+int lcb_kv_cache_write(void* cache, const void* k, const void* v, const int* lens, int B, int Hkv, int T, int Smax,
+                       int D, int bits, long long cache_batch_stride, long long cache_head_stride,
+                       long long row_stride, long long batch_stride, void* stream) {
+  if (B < 1 || Hkv < 1 || T < 0 || Smax < 0 || T > kWindowMaxRows || Smax > kWindowMaxRows) return LCB_ERR_ARG;
+  if (D != kHeadDim || (bits != 4 && bits != 8)) return LCB_ERR_UNSUPPORTED;
+  if (T == 0 || Smax == 0) return LCB_OK;
+  if (!lens || (reinterpret_cast<uintptr_t>(lens) & 3u)) return LCB_ERR_ARG;
+  if (!cache_view(cache, cache_batch_stride, cache_head_stride, B, Hkv, Smax, bits, true) ||
+      !window_input(k, row_stride, batch_stride, Hkv) || !window_input(v, row_stride, batch_stride, Hkv))
+    return LCB_ERR_ARG;
+  KvCacheWrite a = {};
+  a.cache = static_cast<uint8_t*>(cache);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.lens = lens;
+  a.cache_batch_stride = cache_batch_stride;
+  a.cache_head_stride = cache_head_stride;
+  a.row_stride = row_stride;
+  a.batch_stride = batch_stride;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.T = T;
+  a.Smax = Smax;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(launch_kv_cache_write(a, bits, st), st);
+}
+
+int lcb_kv_cache_read(const void* cache, void* k, void* v, const int* lens, int B, int Hkv, int n, int start, int Smax,
+                      int D, int bits, long long cache_batch_stride, long long cache_head_stride, long long row_stride,
+                      long long batch_stride, void* stream) {
+  if (B < 1 || Hkv < 1 || n < 0 || start < 0 || Smax < 0 || Smax > kWindowMaxRows || start > Smax || n > Smax - start)
+    return LCB_ERR_ARG;
+  if (D != kHeadDim || (bits != 4 && bits != 8)) return LCB_ERR_UNSUPPORTED;
+  if (n == 0) return LCB_OK;
+  if (reinterpret_cast<uintptr_t>(lens) & 3u) return LCB_ERR_ARG;
+  if (!cache_view(cache, cache_batch_stride, cache_head_stride, B, Hkv, Smax, bits, false) ||
+      !window_output(k, row_stride, batch_stride, B, n, Hkv) || !window_output(v, row_stride, batch_stride, B, n, Hkv))
+    return LCB_ERR_ARG;
+  KvCacheRead a = {};
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.k = static_cast<__nv_bfloat16*>(k);
+  a.v = static_cast<__nv_bfloat16*>(v);
+  a.lens = lens;
+  a.cache_batch_stride = cache_batch_stride;
+  a.cache_head_stride = cache_head_stride;
+  a.row_stride = row_stride;
+  a.batch_stride = batch_stride;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.n = n;
+  a.start = start;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(launch_kv_cache_read(a, bits, st), st);
+}
+
+size_t attn_cache_decode_workspace_bytes(int B, int H, int Hkv, int T, int Smax, int D, int bits, int window,
+                                         int sinks) {
+  WindowShape w;
+  if (prep_window(&w, B, H, Hkv, T, Smax, D, window, sinks, 0, 1.f) != LCB_OK || (bits != 4 && bits != 8)) return 0;
+  if (T == 0 || Smax == 0) return 0;
+  return cache_decode_workspace(B, H, Hkv, T, Smax, w.window, w.sinks, bits);
+}
+
+int attn_cache_decode(const void* q, const void* cache, const int* lens, void* o, float* lse, int B, int H, int Hkv,
+                      int T, int Smax, int D, int bits, int window, int sinks, float scale, long long q_row_stride,
+                      long long q_batch_stride, long long cache_batch_stride, long long cache_head_stride,
+                      long long o_row_stride, long long o_batch_stride, long long lse_head_stride,
+                      long long lse_batch_stride, void* workspace, size_t ws_bytes, void* stream) {
+  WindowShape w;
+  int rc = prep_window(&w, B, H, Hkv, T, Smax, D, window, sinks, 0, scale);
+  if (rc != LCB_OK) return rc;
+  if (bits != 4 && bits != 8) return LCB_ERR_UNSUPPORTED;
+  if (T == 0) return LCB_OK;
+  if (!window_output(o, o_row_stride, o_batch_stride, B, T, H) ||
+      !window_lse_output(lse, lse_head_stride, lse_batch_stride, B, H, T))
+    return LCB_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (Smax == 0)
+    return finish(launch_fill_empty(o, 0, o_row_stride, o_batch_stride, lse, lse_head_stride, lse_batch_stride, B, H,
+                                    T, st),
+                  st);
+  if (!lens || (reinterpret_cast<uintptr_t>(lens) & 3u)) return LCB_ERR_ARG;
+  if (!window_input(q, q_row_stride, q_batch_stride, H) ||
+      !cache_view(cache, cache_batch_stride, cache_head_stride, B, Hkv, Smax, bits, false))
+    return LCB_ERR_ARG;
+  CacheDecode a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.lens = lens;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.workspace = static_cast<float*>(workspace);
+  a.q_rs = q_row_stride;
+  a.q_bs = q_batch_stride;
+  a.c_bs = cache_batch_stride;
+  a.c_hs = cache_head_stride;
+  a.o_rs = o_row_stride;
+  a.o_bs = o_batch_stride;
+  a.l_hs = lse_head_stride;
+  a.l_bs = lse_batch_stride;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.T = T;
+  a.Smax = Smax;
+  a.window = w.window;
+  a.sinks = w.sinks;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if ((rc = dev_status(&a.st)) != LCB_OK) return rc;
+  return finish(launch_cache_decode(a, bits, aligned16(workspace) ? ws_bytes : 0, st), st);
 }
 
 // Workspace of attn_window_bwd: two row statistics and a 128 x 128 fp32 dQ tile

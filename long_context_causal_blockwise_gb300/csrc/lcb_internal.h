@@ -204,4 +204,46 @@ struct WindowSplit {
 int launch_window_split(WindowSplit p, cudaStream_t stream);
 bool window_split_pays(int B, int H, int Hkv, const WindowShape& w);  // for a forward without lens; Sq, Sk > 0
 
+// The quantised K/V cache (kv_cache.cuh). k and v share strides (elements); cache strides in bytes.
+struct KvCacheWrite {
+  uint8_t* cache;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const int* lens;  // token t of sequence b goes to row lens[b] - T + t
+  long long cache_batch_stride, cache_head_stride, row_stride, batch_stride;
+  int B, Hkv, T, Smax;
+  int blocks;  // set by the launch, as units
+  long long units;
+};
+int launch_kv_cache_write(KvCacheWrite p, int bits, cudaStream_t stream);
+
+struct KvCacheRead {
+  const uint8_t* cache;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  const int* lens;  // null: every row is filled
+  long long cache_batch_stride, cache_head_stride, row_stride, batch_stride;
+  int B, Hkv, n, start;
+  int blocks;
+  long long units;
+};
+int launch_kv_cache_read(KvCacheRead p, int bits, cudaStream_t stream);
+
+// Attention of T query rows per head over the cache: as WindowSplit with lens.
+struct CacheDecode {
+  const __nv_bfloat16* q;
+  const uint8_t* cache;
+  const int* lens;
+  __nv_bfloat16* o;
+  float* lse;
+  float* workspace;  // partials of parts > 1
+  long long q_rs, q_bs, c_bs, c_hs, o_rs, o_bs, l_hs, l_bs;
+  int B, H, Hkv, T, Smax, window, sinks;
+  float scale_log2;
+  int row_tiles, cluster, parts;  // set by the launch
+  DevStatus st;
+};
+size_t cache_decode_workspace(int B, int H, int Hkv, int T, int Smax, int window, int sinks, int bits);
+int launch_cache_decode(CacheDecode p, int bits, size_t ws_bytes, cudaStream_t stream);
+
 }  // namespace lcb

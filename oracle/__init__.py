@@ -45,6 +45,7 @@ from .attention import (  # noqa: F401
 )
 from .merge import lse_merge  # noqa: F401
 from .rope import rope  # noqa: F401
+from .kv_cache import cache_codes, cache_values, round_bf16  # noqa: F401
 from .cross_entropy import ce_fwd, ce_grad, ce_lse  # noqa: F401
 from .ulysses import seq_to_head as ulysses_seq_to_head, head_to_seq as ulysses_head_to_seq  # noqa: F401
 from .ulysses import ulysses_attn_fwd  # noqa: F401
