@@ -7,6 +7,7 @@ loaded, every call raises (there is no fallback).
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -784,8 +785,14 @@ def kv_cache_read(cache, n, start=0, lens=None, k=None, v=None):
 
 
 def attn_cache_decode_workspace_bytes(B, H, Hkv, T, Smax, bits=4, window=None, sinks=0, D=128):
-    return int(load().attn_cache_decode_workspace_bytes(B, H, Hkv, T, Smax, D, bits,
-                                                        _MOST if window is None else _count(window), _count(sinks)))
+    """Bytes of workspace that attn_cache_decode needs for these sizes on the current device."""
+    return _cache_decode_workspace(torch.cuda.current_device() if torch.cuda.is_available() else -1, B, H, Hkv, T, Smax,
+                                   D, bits, _MOST if window is None else _count(window), _count(sinks))
+
+
+@functools.lru_cache(maxsize=4096)  # a decoding loop asks for the same sizes over and over
+def _cache_decode_workspace(device, *sizes):
+    return int(load().attn_cache_decode_workspace_bytes(*sizes))
 
 
 def attn_cache_decode(q, cache, lens, window=None, sinks=0, scale=None, o=None, lse=None, workspace=None):
@@ -809,7 +816,7 @@ def attn_cache_decode(q, cache, lens, window=None, sinks=0, scale=None, o=None, 
     o, lse, orr, ob, lh, lb = _window_out(q, qs, o, lse)
     lib = _LIB or load()
     if workspace is None:
-        n = lib.attn_cache_decode_workspace_bytes(B, H, Hkv, T, Smax, D, bits, window, sinks)
+        n = _cache_decode_workspace(q.get_device(), B, H, Hkv, T, Smax, D, bits, window, sinks)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     elif not workspace.is_contiguous():

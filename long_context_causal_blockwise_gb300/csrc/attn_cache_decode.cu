@@ -5,32 +5,42 @@
 // A cached row holds, per group G of 32 channels, whole numbers and a scale:
 //   k_jc = s^K_jG n_jc,   x_ij = scale * sum_G s^K_jG sum_{c in G} q_ic n_jc
 //   v_jc = s^V_jG n_jc,   o_ic = sum_j (p_ij s^V_jG) n_jc / l_i
-// so the products take the whole numbers, which bf16 holds exactly, and the
-// scales go to the scores and to the weights: nothing of the cache is rounded.
-// (p s^V is rounded to bf16 for the second product, as P is in the other
-// forms: half a step, up to 2^-8 of each weight, of either sign.)
+// so the products take the whole numbers, which 8 or 16 bits hold exactly, and
+// the scales go to the scores and to the weights: nothing of the cache is
+// rounded. p s^V goes to bf16 for the second product, as P does in the other
+// forms: half a step, up to 2^-8 of each weight, of either sign. Q goes to fp16
+// for the first one, after a division by a power of two that puts a row's
+// largest element into [2^8, 2^9): exact but for elements below 2^-17 of that
+// largest, whose errors are under 2^-28 of it.
 //
 // Every visible record (144 or 272 bytes) is read once for all query rows that
 // share its head, up to 16 of them. HBM bounds it only if little is done per
-// byte: at 6.7 TB/s an SM gets a key every 6 clocks (4 bits), 24 issue slots
-// for its 256 numbers. Hence
+// byte: at 6.7 TB/s an SM gets a 4-bit key every 6 clocks, 24 issue slots for
+// its 256 numbers. Hence
 //   S^T[16 keys][8 rows] = K Q^T  and  O^T[128][8 rows] += V^T P^T  on warp
-//     mma.sync (m16n8k16) with operands in registers, as attn_window_split.cu:
-//     tcgen05 would want its operand unpacked into shared or tensor memory;
-//   codes stored in operand order, so that a shift, one bitwise operation and a
-//     packed add make two of them bf16 numbers;
-//   records brought to shared memory by bulk copies, one instruction for a
-//     unit of 4.5 KB, in a ring of each warp's own: no address arithmetic and
-//     no barrier among warps.
+//     mma.sync (m16n8k16) with operands in registers, as attn_window_split.cu.
+//     tcgen05 would want its operand unpacked into shared or tensor memory, and
+//     8-bit products (m16n8k32) are two 16-bit ones and conversions here;
+//   codes stored as parts of subnormal numbers in operand order, so that little
+//     more than an AND makes a register of them an operand (kv_cache.cuh). The
+//     smallness is made up for by Q's power of two and the scores' factor, and
+//     for V by weights times 2^96 (less while scales are so large that those
+//     would not fit), taken back when the parts are joined;
+//   records brought to shared memory by bulk copies, one instruction for
+//     several KB: no address arithmetic.
 //
-// The visible keys of a (sequence, K/V head, row tile) are split evenly over
-// the warps of a cluster of CTAs, whose partial (m, l, O) are joined in shared
-// memory, then through distributed shared memory. Where there are too few
-// tiles for clusters to fill the GPU, a tile gets several clusters, which leave
-// partials in a workspace for a second kernel. No atomics: the same result
-// every time.
+// Two forms share that loop. With few keys in all, a cluster of CTAs takes a
+// (sequence, K/V head, row tile), its keys dealt evenly to the cluster's warps,
+// whose partial (m, l, O) are joined in shared memory, then through distributed
+// shared memory: one launch, no workspace. With more, the units of all tiles
+// form one line that is cut into equal pieces, one for each CTA that the GPU
+// holds, whatever the lengths and however few the heads; a CTA walks over its
+// piece tile by tile, and pieces of a tile that several CTAs share go to a
+// workspace, which a second kernel joins. No atomics: the same result every
+// time.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cmath>
@@ -46,25 +56,44 @@ namespace lcb {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kStep = 16;   // keys of a product
-constexpr int kDepth = 3;   // units of a warp's ring
+constexpr int kSms = 152;
+constexpr int kStep = 16;  // keys of a product, and of a warp's turn
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum is raised lazily, P stays <= 256
 constexpr uint32_t kWhere = 9u << 24;
 
-template <int BITS>
-struct Unit {  // keys that one bulk copy brings
-  static constexpr int kKeys = BITS == 4 ? 32 : 16;
-  static constexpr int kBytes = kKeys * cache_row_bytes(BITS);
-};
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// mma_f16 with nothing to add to.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
@@ -84,355 +113,824 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // Weight of a partial with maximum m in a sum with maximum M >= m (both -inf: the partial is empty, or NaN).
 __device__ __forceinline__ float weight(float m, float M) { return m == M ? 1.f : ex2_approx(m - M); }
 
-// A CTA's shared memory. The ring's bytes become the warps' partials, joined into slot 0, once the keys are done.
-template <int NT, int BITS, int kWarps>
-struct Smem {
-  static constexpr int kRows = 8 * NT;
-  union {
-    uint8_t ring[kWarps][kDepth][Unit<BITS>::kBytes];
-    float O[kWarps][kRows][kD];
+// A row tile of a (sequence, K/V head), and the keys that a row of it sees:
+// [0, ns) and [lo, hi), in units of `keys` that do not cross from one to the
+// other; every key of the units [whole0, whole1) is seen by every row.
+struct Tile {
+  int b, hk, r0;         // rows r = (token r / G, query head hk * G + r % G), r0 <= r < r0 + rows
+  int p0, p_min, p_max;  // positions of token 0, of the tile's first row and of its last
+  int lo, hi, ns, sink_units, units, whole0, whole1;
+};
+
+__device__ __forceinline__ Tile make_tile(const CacheDecode& p, int b, int hk, int mt, int rows, int keys) {
+  Tile a;
+  a.b = b;
+  a.hk = hk;
+  a.r0 = mt * rows;
+  const int len = min(max(p.lens[b], 0), p.Smax);
+  a.p0 = len - p.T;
+  a.p_min = a.p0;
+  a.p_max = len - 1;
+  if (p.row_tiles > 1) {
+    a.p_min = a.p0 + a.r0 / p.G;
+    a.p_max = a.p0 + min(p.T * p.G - 1, a.r0 + rows - 1) / p.G;
+  }
+  a.lo = max(0, a.p_min - p.window + 1);
+  a.hi = max(a.lo, a.p_max + 1);
+  a.ns = max(0, min(min(p.sinks, a.lo), a.p_max + 1));
+  a.sink_units = (a.ns + keys - 1) / keys;
+  a.units = a.sink_units + (a.hi - a.lo + keys - 1) / keys;
+  a.whole0 = a.sink_units + (max(0, a.p_max - p.window + 1 - a.lo) + keys - 1) / keys;
+  a.whole1 = a.sink_units + max(0, min(a.p_min + 1, a.hi) - a.lo) / keys;
+  return a;
+}
+
+__device__ __forceinline__ int first_key(const Tile& a, int u, int keys) {
+  return u * keys + (u < a.sink_units ? 0 : a.lo - a.sink_units * keys);
+}
+// Keys of unit u, whose first is j0.
+__device__ __forceinline__ int keys_of(const Tile& a, int u, int j0, int keys) {
+  return min(keys, (u < a.sink_units ? a.ns : a.hi) - j0);
+}
+
+// n things dealt in order to `parts`, the first n % parts of which get one more.
+struct Share {
+  int each, more;
+  __device__ Share(int n, int parts) : each(n / parts), more(n - n / parts * parts) {}
+  __device__ int begin(int i) const { return i * each + min(i, more); }  // of part i
+  __device__ int part_of(int x) const {                                  // that has thing x
+    const int cut = more * (each + 1);
+    return x < cut ? x / (each + 1) : more + (x - cut) / each;
+  }
+};
+
+// How a tile of ROWS query rows lies in the eight columns of a product, and
+// what a lane (g, t) has of them.
+//   8, 16: a column is a row; lane t has the rows 2t and 2t + 1 of every eight.
+//     The scores come as four sums, one for each group of channels, and a
+//     weight goes into the second product four times, once with each scale.
+//   4: a column 2r + h is half h of row r: the groups 2h and 2h + 1, Q being zero
+//     in the other half. So two sums and two operands do where eight columns of
+//     whole rows take four, and lane t has row t alone: 310 instructions for
+//     sixteen keys instead of 345.
+template <int ROWS>
+struct Cols {
+  static constexpr bool kHalves = ROWS == 4;
+  static constexpr int kTiles = ROWS == 16 ? 2 : 1;          // eights of columns
+  static constexpr int kMine = kHalves ? 1 : 2 * kTiles;     // rows of a lane
+  static constexpr int kSums = kHalves ? 2 : 4;              // sums, and operands, per eight columns
+  static __device__ int row(int i, int t) { return kHalves ? t : 8 * (i >> 1) + 2 * t + (i & 1); }  // a lane's i-th
+};
+
+// 2^e, e from -126 to 127.
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+constexpr int kUp = 96;            // weights go into the second product times 2^96, which subnormal codes take back
+constexpr int kUpRange = 119 - kUp;  // while V's scales are below 2^23: a weight is 2^8 at most
+
+template <int ROWS, int BITS>
+struct State {
+  using C = Cols<ROWS>;
+  uint32_t q[C::kTiles][16];    // Q's fragments, in K's channel order
+  float c[C::kMine];            // a row's scores in base 2 are its products times this
+  int pr[C::kMine];             // its position; -1 past the last row
+  float o[8][C::kTiles][4];     // o[2 G + f]: channels 32 G + 4 g + 2 f + {0, 1}, each of columns 2t, 2t + 1
+  float m[C::kMine], l[C::kMine];
+  float neg_m[C::kMine], raise_at[C::kMine];  // -m (0 while nothing is seen); the product above which m is raised
+  float up;                     // what weights go into the second product with: 2^kUp, or less
+  uint32_t up_limit;            // bf16, twice: V's scales above it want a smaller one
+  // O of a lane's row i in channel 32 G + 4 g + k, times `up` and a subnormal's factor
+  __device__ float& out(int i, int G, int k) {
+    const int col = C::kHalves ? G >> 1 : i & 1;
+    return o[2 * G + (k >> 1)][C::kHalves ? 0 : i >> 1][2 * (k & 1) + col];
+  }
+  __device__ float true_out(int i, int G, int k, float down) {
+    return out(i, G, k) * (BITS == 4 && (k & 1) ? 0x1p61f : 0x1p65f) * down;
+  }
+  // 2^68 / up: an exponent of at most 85
+  __device__ float down() const { return exp2_int(68 - (static_cast<int>(__float_as_uint(up) >> 23) - 127)); }
+};
+
+// A lane's part of Q as it lies in memory.
+template <int ROWS>
+struct RawQ {
+  uint4 v[Cols<ROWS>::kTiles][Cols<ROWS>::kHalves ? 2 : 4];
+};
+
+template <int ROWS>
+__device__ __forceinline__ RawQ<ROWS> load_q(const CacheDecode& p, const Tile& a, int g, int t) {
+  using C = Cols<ROWS>;
+  RawQ<ROWS> x;
+#pragma unroll
+  for (int nt = 0; nt < C::kTiles; ++nt) {
+    const int r = a.r0 + (C::kHalves ? g >> 1 : 8 * nt + g);
+    const int tok = p.G == 1 ? r : r / p.G;
+    const __nv_bfloat16* src = p.q + a.b * p.q_bs + static_cast<long long>(tok) * p.q_rs +
+                               (a.hk * p.G + r - tok * p.G) * kD + 8 * t + (C::kHalves ? 64 * (g & 1) : 0);
+#pragma unroll
+    for (int c = 0; c < (C::kHalves ? 2 : 4); ++c)
+      x.v[nt][c] = r < p.T * p.G ? *reinterpret_cast<const uint4*>(src + 32 * c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  return x;
+}
+
+template <int ROWS, int BITS>
+__device__ __forceinline__ void begin(State<ROWS, BITS>& w, const RawQ<ROWS>& raw, const CacheDecode& p, const Tile& a,
+                                      int g, int t) {
+  using C = Cols<ROWS>;
+  constexpr int kLoaded = C::kHalves ? 2 : 4;  // groups that the lane has
+  constexpr int kTop = 8;
+#pragma unroll
+  for (int nt = 0; nt < C::kTiles; ++nt) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < kLoaded; ++c) {
+      const uint32_t x[4] = {raw.v[nt][c].x, raw.v[nt][c].y, raw.v[nt][c].z, raw.v[nt][c].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7fffu, x[i] >> 16 & 0x7fffu));
+    }
+#pragma unroll
+    for (int x = 1; x < (C::kHalves ? 8 : 4); x *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const int e = static_cast<int>(top >> 7);  // 127 more than the exponent; 255 with infinities or NaN
+    const int up = min(126, kTop + 127 - e);
+    const float f = e == 255 ? __int_as_float(0x7fc00000) : exp2_int(up);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 v = raw.v[nt][C::kHalves ? c & 1 : c];
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      const bool zero = C::kHalves && (c >> 1) != (g & 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float fi = BITS == 4 && (i & 1) ? f * 0.0625f : f;  // those codes are 2^4 as large
+        const __half2 y = __floats2half2_rn(bf16lo_to_f32(x[i]) * fi, bf16hi_to_f32(x[i]) * fi);
+        w.q[nt][4 * c + i] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&y);
+      }
+    }
+    // the power of two back, and the subnormal codes' 2^24
+    const float back = exp2_int(-up) * 0x1p24f * p.scale_log2;
+    if (C::kHalves) {
+      w.c[0] = __shfl_sync(0xffffffffu, back, 8 * t);
+    } else {
+      w.c[2 * nt] = __shfl_sync(0xffffffffu, back, 8 * t);
+      w.c[C::kMine > 1 ? 2 * nt + 1 : 0] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w.o[i][nt][k] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < C::kMine; ++i) {
+    const int r = a.r0 + C::row(i, t);
+    w.pr[i] = r < p.T * p.G ? a.p0 + (p.G == 1 ? r : r / p.G) : -1;
+    w.m[i] = w.raise_at[i] = -INFINITY;
+    w.l[i] = w.neg_m[i] = 0.f;
+  }
+  w.up = exp2_int(kUp);
+  w.up_limit = 0x10001u * ((kUpRange + 127) * 128 - 1);
+}
+
+// V's scales (of keys g and g + 8) are so large that weights times `up` would
+// not fit: the smaller `up` that the largest one needs. NaN is none of them.
+template <int ROWS, int BITS>
+__device__ __forceinline__ void lower_up(State<ROWS, BITS>& w, const uint4 (&sc)[2]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = i < 2 ? sc[h].z : sc[h].w, s = i & 1 ? x >> 16 : x & 0xffffu;
+      top = max(top, s < 0x7f80u ? s : 0u);
+    }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (top <= (w.up_limit & 0xffffu)) return;
+  const int e = static_cast<int>(top >> 7) - 126;  // scales below 2^e
+  const int range = min(e + 8, 128);               // room for some growth
+  const float up = exp2_int(119 - range), f = up / w.up;
+  w.up = up;
+  w.up_limit = range >= 128 ? 0x7f7f7f7fu : 0x10001u * ((range + 127) * 128 - 1);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int nt = 0; nt < Cols<ROWS>::kTiles; ++nt)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w.o[i][nt][k] *= f;
+}
+
+// Sixteen keys at `rec`, the first nk of which exist: key j0 + i of the
+// sequence at i. CUT: some of them may be hidden from some rows.
+template <int ROWS, int BITS, bool CUT>
+__device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p, const uint8_t* rec, int j0, int nk, int g,
+                                     int t) {
+  using C = Cols<ROWS>;
+  constexpr int kRec = cache_row_bytes(BITS), kWords = BITS / 4;  // of a group, for a lane
+  // scales of keys g and g + 8: four of K, four of V
+  uint4 sc[2] = {*reinterpret_cast<const uint4*>(rec + g * kRec + cache_scale_offset(BITS)),
+                 *reinterpret_cast<const uint4*>(rec + (g + 8) * kRec + cache_scale_offset(BITS))};
+  if (CUT) {
+    if (g >= nk) sc[0].z = sc[0].w = 0u;
+    if (g + 8 >= nk) sc[1].z = sc[1].w = 0u;
+  }
+  auto k_scale = [&](int h, int c) {
+    const uint32_t x = c < 2 ? sc[h].x : sc[h].y;
+    return c & 1 ? bf16hi_to_f32(x) : bf16lo_to_f32(x);
   };
-  float M[kWarps][kRows], L[kWarps][kRows];
-  float cM[kRows], cL[kRows];
-  uint64_t full[kWarps][kDepth];
+  auto v_scale = [&](int h, int c) {
+    const uint32_t x = c < 2 ? sc[h].z : sc[h].w;
+    return c & 1 ? bf16hi_to_f32(x) : bf16lo_to_f32(x);
+  };
+  // ---- S^T: s[h][i] is key 8h + g, the lane's row i
+  float s[2][C::kMine];
+  {
+    uint32_t kw[2][4 * kWords];  // a key's words: one, or two, of each group
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(rec + (g + 8 * h) * kRec + 64 * i + 16 * t);
+        kw[h][4 * i] = v.x;
+        kw[h][4 * i + 1] = v.y;
+        kw[h][4 * i + 2] = v.z;
+        kw[h][4 * i + 3] = v.w;
+      }
+    float acc[C::kSums][C::kTiles][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t x[2][4];  // pairs of channels of keys g and g + 8
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const Fields f = k4_fields(kw[h][c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[h][i] = BITS == 4 ? f.pair(i) : k8_f16x2(kw[h][(2 * c + (i >> 1)) % (4 * kWords)], i & 1);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < C::kTiles; ++nt) {
+          const uint32_t b0 = w.q[nt][4 * c + 2 * h], b1 = w.q[nt][4 * c + 2 * h + 1];
+          if (h == 0 && c < C::kSums)
+            mma_f16_first(acc[c][nt], x[0][2 * h], x[1][2 * h], x[0][2 * h + 1], x[1][2 * h + 1], b0, b1);
+          else
+            mma_f16(acc[c % C::kSums][nt], x[0][2 * h], x[1][2 * h], x[0][2 * h + 1], x[1][2 * h + 1], b0, b1);
+        }
+      if (!C::kHalves)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < C::kMine; ++i) {
+            const float x = acc[c % C::kSums][i >> 1][2 * h + (i & 1)];
+            s[h][i] = c == 0 ? k_scale(h, c) * x : fmaf(k_scale(h, c), x, s[h][i]);
+          }
+    }
+    if (C::kHalves)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        s[h][0] = fmaf(k_scale(h, 3), acc[1][0][2 * h + 1],
+                       fmaf(k_scale(h, 2), acc[0][0][2 * h + 1],
+                            fmaf(k_scale(h, 1), acc[1][0][2 * h], k_scale(h, 0) * acc[0][0][2 * h])));
+  }
+  bool seen[2][C::kMine];
+  if (CUT) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = 8 * h + g, j = j0 + i;
+#pragma unroll
+      for (int x = 0; x < C::kMine; ++x) {
+        const int pp = w.pr[x];
+        seen[h][x] = i < nk && j <= pp && (pp - j < p.window || j < p.sinks);
+        if (!seen[h][x]) s[h][x] = -INFINITY;
+      }
+    }
+  }
+  bool raise = false;
+#pragma unroll
+  for (int i = 0; i < C::kMine; ++i) raise |= s[0][i] > w.raise_at[i] || s[1][i] > w.raise_at[i];
+  const uint32_t v_top = max_u16x2(max_u16x2(sc[0].z, sc[0].w), max_u16x2(sc[1].z, sc[1].w));
+  raise |= max_u16x2(v_top, w.up_limit) != w.up_limit;
+  if (__any_sync(0xffffffffu, raise)) {
+    lower_up(w, sc);
+#pragma unroll
+    for (int i = 0; i < C::kMine; ++i) {
+      float mx = fmaxf(s[0][i], s[1][i]) * w.c[i];
+#pragma unroll
+      for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      // each row for itself: no other row's keys change its bits
+      mx = mx > w.m[i] + kRescaleThreshold ? mx : w.m[i];
+      const float a = weight(w.m[i], mx);
+      w.m[i] = mx;
+      w.neg_m[i] = mx == -INFINITY ? 0.f : -mx;
+      w.raise_at[i] = (mx + kRescaleThreshold) / w.c[i];
+      w.l[i] *= a;
+#pragma unroll
+      for (int G = 0; G < 4; ++G)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w.out(i, G, k) *= a;
+    }
+  }
+  // ---- P^T, times V's scales per group, as operands with the keys along t
+  uint32_t pb[C::kSums][C::kTiles][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float e[C::kMine];
+#pragma unroll
+    for (int i = 0; i < C::kMine; ++i) {
+      e[i] = ex2_approx(fmaf(s[h][i], w.c[i], w.neg_m[i]));
+      w.l[i] += e[i];
+      e[i] *= w.up;
+    }
+    // a weight times a scale; what belongs to a hidden row may be anything
+    auto product = [&](int i, int c) { return CUT && !seen[h][i] ? 0.f : e[i] * v_scale(h, c); };
+#pragma unroll
+    for (int c = 0; c < C::kSums; ++c)
+#pragma unroll
+      for (int nt = 0; nt < C::kTiles; ++nt)
+        pb[c][nt][h] = transpose_8x8(C::kHalves ? pack_bf16x2(product(0, c), product(0, c + 2))
+                                                : pack_bf16x2(product(2 * nt, c), product(C::kMine > 1 ? 2 * nt + 1 : 0, c)));
+  }
+  // ---- O^T += V^T P^T
+  uint32_t vw[4][2 * kWords];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint8_t* at = rec + (2 * t + (i & 1) + 8 * (i >> 1)) * kRec + cache_v_offset(BITS) + 2 * BITS * g;
+    if (BITS == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(at);
+      vw[i][0] = v.x;
+      vw[i][1] = v.y;
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(at);
+      vw[i][0] = v.x;
+      vw[i][1] = v.y;
+      vw[i][(2 * kWords) - 2] = v.z;
+      vw[i][(2 * kWords) - 1] = v.w;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t a[4][2];  // the group's four channels: keys 2t, 2t + 1 and 2t + 8, 2t + 9
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (BITS == 4) {
+        const Fields v = v4_fields(vw[2 * h][c >> 1], vw[2 * h + 1][c >> 1], c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i][h] = v.pair(i);
+      } else {
+        const V8 v = {vw[2 * h][c % (2 * kWords)], vw[2 * h + 1][c % (2 * kWords)]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i][h] = v.pair(i);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int nt = 0; nt < C::kTiles; ++nt)
+        mma_bf16(w.o[2 * c + f][nt], a[2 * f][0], a[2 * f + 1][0], a[2 * f][1], a[2 * f + 1][1],
+                 pb[c % C::kSums][nt][0], pb[c % C::kSums][nt][1]);
+  }
+}
+
+// The warps' parts of a tile.
+template <int ROWS, int kWarps>
+struct Parts {
+  float O[kWarps][ROWS][kD];
+  float M[kWarps][ROWS], L[kWarps][ROWS];
+};
+
+// Joins them; emit(r, M, L, a) gets row r, four channels a lane, from the warp that joined it.
+template <int ROWS, int BITS, int kWarps, class Emit>
+__device__ __forceinline__ void join_warps(Parts<ROWS, kWarps>& sm, State<ROWS, BITS>& w, int warp, int lane,
+                                           Emit&& emit) {
+  using C = Cols<ROWS>;
+  const int g = lane >> 2, t = lane & 3;
+  const float down = w.down();
+#pragma unroll
+  for (int i = 0; i < C::kMine; ++i) {
+    const int r = C::row(i, t);
+#pragma unroll
+    for (int x = 4; x < 32; x *= 2) w.l[i] += __shfl_xor_sync(0xffffffffu, w.l[i], x);
+    if (g == 0) {
+      sm.M[warp][r] = w.m[i];
+      sm.L[warp][r] = w.l[i];
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<float4*>(&sm.O[warp][r][32 * c + 4 * g]) =
+          make_float4(w.true_out(i, c, 0, down), w.true_out(i, c, 1, down), w.true_out(i, c, 2, down),
+                      w.true_out(i, c, 3, down));
+  }
+  __syncthreads();
+  for (int r = warp; r < ROWS; r += kWarps) {
+    // lane x has part x's maximum and sum
+    const float m = lane < kWarps ? sm.M[lane < kWarps ? lane : 0][r] : -INFINITY;
+    float M = m;
+#pragma unroll
+    for (int x = 1; x < kWarps; x *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    M = __shfl_sync(0xffffffffu, M, 0);
+    const float f = lane < kWarps ? weight(m, M) : 0.f;
+    float L = lane < kWarps ? f * sm.L[lane < kWarps ? lane : 0][r] : 0.f;
+#pragma unroll
+    for (int x = 1; x < 32; x *= 2) L += __shfl_xor_sync(0xffffffffu, L, x);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+      const float fx = __shfl_sync(0xffffffffu, f, x);
+      const float4 v = *reinterpret_cast<const float4*>(&sm.O[x][r][lane * 4]);
+      a = make_float4(a.x + fx * v.x, a.y + fx * v.y, a.z + fx * v.z, a.w + fx * v.w);
+    }
+    emit(r, M, L, a);
+  }
+}
+
+// Row r of a tile, four channels a lane.
+__device__ __forceinline__ void store_row(const CacheDecode& p, const Tile& a, int r, float M, float L, float4 v,
+                                          int lane) {
+  r += a.r0;
+  if (r >= p.T * p.G) return;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int tok = p.G == 1 ? r : r / p.G, h = a.hk * p.G + r - tok * p.G;
+  uint2 x;
+  x.x = pack_bf16x2(v.x * inv, v.y * inv);
+  x.y = pack_bf16x2(v.z * inv, v.w * inv);
+  *reinterpret_cast<uint2*>(p.o + a.b * p.o_bs + static_cast<long long>(tok) * p.o_rs + h * kD + 4 * lane) = x;
+  if (lane == 0) p.lse[a.b * p.l_bs + h * p.l_hs + tok] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+}
+
+// ------------------------------------------------------------------ a cluster for each tile
+
+// Few keys a warp: a ring of two units, 4.5 KB each, of each warp's own.
+template <int BITS>
+constexpr int unit_keys() { return BITS == 4 ? 32 : 16; }
+constexpr int kUnits = 2;
+
+template <int ROWS, int BITS, int kWarps>
+struct ClusterSmem {
+  uint8_t ring[kWarps][kUnits][unit_keys<BITS>() * cache_row_bytes(BITS)];
+  Parts<ROWS, kWarps> parts;
+  float cM[ROWS], cL[ROWS];
+  uint64_t full[kWarps][kUnits];
   int abort;
 };
 
-// NT: 8-row tiles of query rows (1 or 2); kWarps: warps of a CTA.
-template <int NT, int BITS, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 12) / kWarps) cache_decode_kernel(const __grid_constant__ CacheDecode p) {
-  constexpr int kRows = 8 * NT;
-  constexpr int kRec = cache_row_bytes(BITS), kPlanes = cache_planes(BITS);
-  constexpr int kKeys = Unit<BITS>::kKeys;
+constexpr int warps_per_sm(int ROWS) { return ROWS == 16 ? 12 : 16; }  // 168 and 128 registers a thread
+
+template <int ROWS, int BITS, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, warps_per_sm(ROWS) / kWarps)
+    cache_decode_kernel(const __grid_constant__ CacheDecode p) {
+  constexpr int kKeys = unit_keys<BITS>(), kRec = cache_row_bytes(BITS);
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  auto& sm = *reinterpret_cast<Smem<NT, BITS, kWarps>*>(smem_raw);
+  auto& sm = *reinterpret_cast<ClusterSmem<ROWS, BITS, kWarps>*>(smem_raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % p.cluster;
   int tile = static_cast<int>(blockIdx.x) / p.cluster;
-  const int part = tile % p.parts;
-  tile /= p.parts;
   const int mt = tile % p.row_tiles;
   tile /= p.row_tiles;
-  const int hk = tile % p.Hkv, b = tile / p.Hkv;
-  const int G = p.H / p.Hkv, R = p.T * G;
-  const int r0 = mt * kRows;  // rows r = (token r / G, query head hk * G + r % G)
-
   uint64_t* full = sm.full[warp];
   if (lane == 0) {
-    for (int i = 0; i < kDepth; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < kUnits; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
   if (threadIdx.x == 0) sm.abort = 0;
   __syncthreads();
-
-  const int len = min(max(p.lens[b], 0), p.Smax);
-  const int p0 = len - p.T;  // position of token 0
-  const int p_min = p0 + r0 / G, p_max = p0 + min(R - 1, r0 + kRows - 1) / G;
-  // keys that a row of this tile sees: [0, ns) and [lo, hi), in units that do not cross from one to the other
-  const int lo = max(0, p_min - p.window + 1), hi = min(len, p_max + 1);
-  const int ns = max(0, min(min(p.sinks, lo), hi));
-  const int sink_units = (ns + kKeys - 1) / kKeys;
-  const int units = sink_units + (max(0, hi - lo) + kKeys - 1) / kKeys;
-  auto first_key = [&](int u) { return u < sink_units ? u * kKeys : lo + (u - sink_units) * kKeys; };
-  auto keys_of = [&](int u) { return min(kKeys, (u < sink_units ? ns : hi) - first_key(u)); };
-
-  // this warp's units
-  const long long workers = static_cast<long long>(p.parts) * p.cluster * kWarps;
-  const long long me = (static_cast<long long>(part) * p.cluster + rank) * kWarps + warp;
-  const int u0 = static_cast<int>(me * units / workers), u1 = static_cast<int>((me + 1) * units / workers);
-
-  const uint8_t* head = p.cache + b * p.c_bs + hk * p.c_hs;
-  uint8_t(*ring)[Unit<BITS>::kBytes] = sm.ring[warp];
-  auto fetch = [&](int u, int at) {  // lane 0
-    const uint32_t bytes = static_cast<uint32_t>(keys_of(u)) * kRec;
+  const Tile a = make_tile(p, tile / p.Hkv, tile % p.Hkv, mt, ROWS, kKeys);
+  const Share share(a.units, p.cluster * kWarps);
+  const int me = rank * kWarps + warp;
+  int u = share.begin(me);
+  const int u1 = share.begin(me + 1);
+  const uint8_t* head = p.cache + a.b * p.c_bs + a.hk * p.c_hs;
+  auto fetch = [&](int x, int at) {  // by one lane
+    const int j0 = first_key(a, x, kKeys);
+    const uint32_t bytes = static_cast<uint32_t>(keys_of(a, x, j0, kKeys)) * kRec;
     mbar_arrive_expect_tx(&full[at], bytes);
-    bulk_load(ring[at], head + static_cast<long long>(first_key(u)) * kRec, bytes, &full[at]);
+    bulk_load(sm.ring[warp][at], head + static_cast<long long>(j0) * kRec, bytes, &full[at]);
   };
+  const RawQ<ROWS> raw = load_q<ROWS>(p, a, g, t);
   if (lane == 0)
-    for (int i = 0; i < kDepth && u0 + i < u1; ++i) fetch(u0 + i, i);
-
-  // Q fragments, in K's channel order
-  uint32_t qf[NT][8][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = r0 + 8 * nt + g;
-    const __nv_bfloat16* src =
-        p.q + b * p.q_bs + static_cast<long long>(r / G) * p.q_rs + (hk * G + r % G) * kD + 8 * t;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint4 v = r < R ? *reinterpret_cast<const uint4*>(src + 32 * c) : make_uint4(0u, 0u, 0u, 0u);
-      qf[nt][2 * c][0] = v.x;
-      qf[nt][2 * c][1] = v.y;
-      qf[nt][2 * c + 1][0] = v.z;
-      qf[nt][2 * c + 1][1] = v.w;
-    }
-  }
-  int pr[NT][2];  // positions of this lane's score columns (rows past the last see nothing)
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = r0 + 8 * nt + 2 * t + e;
-      pr[nt][e] = r < R ? p0 + r / G : -1;
-    }
-
-  float o[8][NT][4];  // o[2 c + f]: channels 32 c + 4 g + 2 f + {0, 1} of rows 2t, 2t + 1
-  float m[NT][2], l[NT][2];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      m[nt][e] = -INFINITY;
-      l[nt][e] = 0.f;
-    }
-
+    for (int i = 0; i < kUnits && u + i < u1; ++i) fetch(u + i, i);
+  State<ROWS, BITS> w;
+  begin(w, raw, p, a, g, t);
   int at = 0;
   uint32_t phase = 0;
   bool ok = true;
-  int u = u0;
   for (; u < u1; ++u) {
     ok = mbar_wait_warp(&full[at], phase, &sm.abort, p.st, kWhere);
     if (!ok) break;
-    const int j0 = first_key(u), nk = keys_of(u);
-    // every key of the unit is seen by every row of the tile
-    const bool whole = nk == kKeys && j0 + kKeys - 1 <= p_min && (p_max - j0 < p.window || j0 + kKeys <= p.sinks);
+    const uint8_t* rec = sm.ring[warp][at];
+    const int j0 = first_key(a, u, kKeys), nk = keys_of(a, u, j0, kKeys);
+    if (u >= a.whole0 && u < a.whole1) {
 #pragma unroll
-    for (int sub = 0; sub < kKeys / kStep; ++sub) {
-      if (sub * kStep >= nk) break;
-      const uint8_t* rec = ring[at] + sub * kStep * kRec;
-      // scales of keys g and g + 8: four of K, four of V
-      const uint4 sc[2] = {*reinterpret_cast<const uint4*>(rec + g * kRec + cache_scale_offset(BITS)),
-                           *reinterpret_cast<const uint4*>(rec + (g + 8) * kRec + cache_scale_offset(BITS))};
-      // ---- S^T: s[nt][2u + e] is key 8u + g, row 8 nt + 2t + e
-      float s[NT][4];
-      {
-        uint4 kw[kPlanes][2];
-#pragma unroll
-        for (int pl = 0; pl < kPlanes; ++pl)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            kw[pl][h] = *reinterpret_cast<const uint4*>(rec + (g + 8 * h) * kRec + pl * kPlaneBytes + 16 * t);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float acc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-          uint32_t w[kPlanes][2];
-#pragma unroll
-          for (int pl = 0; pl < kPlanes; ++pl)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              w[pl][h] = c == 0 ? kw[pl][h].x : c == 1 ? kw[pl][h].y : c == 2 ? kw[pl][h].z : kw[pl][h].w;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a0 = codes_bf16x2<BITS>(w[0][0], w[kPlanes - 1][0], 2 * h);
-            const uint32_t a1 = codes_bf16x2<BITS>(w[0][1], w[kPlanes - 1][1], 2 * h);
-            const uint32_t a2 = codes_bf16x2<BITS>(w[0][0], w[kPlanes - 1][0], 2 * h + 1);
-            const uint32_t a3 = codes_bf16x2<BITS>(w[0][1], w[kPlanes - 1][1], 2 * h + 1);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16816(acc[nt], a0, a1, a2, a3, qf[nt][2 * c + h][0], qf[nt][2 * c + h][1]);
-          }
-          const uint32_t k0 = c < 2 ? sc[0].x : sc[0].y, k1 = c < 2 ? sc[1].x : sc[1].y;
-          const float s0 = c & 1 ? bf16hi_to_f32(k0) : bf16lo_to_f32(k0);
-          const float s1 = c & 1 ? bf16hi_to_f32(k1) : bf16lo_to_f32(k1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float f = e < 2 ? s0 : s1;
-              s[nt][e] = c == 0 ? f * acc[nt][e] : fmaf(f, acc[nt][e], s[nt][e]);
-            }
-        }
-      }
-      bool seen[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] *= p.scale_log2;
-      if (!whole) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = sub * kStep + 8 * h + g, j = j0 + i;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int pp = pr[nt][e];
-              seen[nt][2 * h + e] = i < nk && j <= pp && (pp - j < p.window || j < p.sinks);
-              if (!seen[nt][2 * h + e]) s[nt][2 * h + e] = -INFINITY;
-            }
-        }
-      }
-      bool raise = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) raise |= s[nt][e] > m[nt][e & 1] + kRescaleThreshold;
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(s[nt][e], s[nt][2 + e]);
-#pragma unroll
-            for (int w = 4; w < 32; w *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-            // each row for itself: no other row's keys change its bits
-            mx = mx > m[nt][e] + kRescaleThreshold ? mx : m[nt][e];
-            const float a = weight(m[nt][e], mx);
-            m[nt][e] = mx;
-            l[nt][e] *= a;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              o[i][nt][e] *= a;
-              o[i][nt][2 + e] *= a;
-            }
-          }
-      }
-      // ---- P^T, times V's scales per group, as operands with the keys along t
-      uint32_t pb[NT][4][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float e0 = ex2_approx(s[nt][2 * h] - m0), e1 = ex2_approx(s[nt][2 * h + 1] - m1);
-          l[nt][0] += e0;
-          l[nt][1] += e1;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t w = c < 2 ? sc[h].z : sc[h].w;
-            const float f = c & 1 ? bf16hi_to_f32(w) : bf16lo_to_f32(w);
-            float x0 = e0 * f, x1 = e1 * f;
-            if (!whole) {  // a hidden row's scale may be anything
-              x0 = seen[nt][2 * h] ? x0 : 0.f;
-              x1 = seen[nt][2 * h + 1] ? x1 : 0.f;
-            }
-            pb[nt][c][h] = transpose_8x8(pack_bf16x2(x0, x1));
-          }
-        }
-      }
-      // ---- O^T += V^T P^T
-      uint2 vw[kPlanes][4];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-      for (int pl = 0; pl < kPlanes; ++pl)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          vw[pl][i] = *reinterpret_cast<const uint2*>(rec + (2 * t + (i & 1) + 8 * (i >> 1)) * kRec +
-                                                      cache_v_offset(BITS) + pl * kPlaneBytes + 8 * g);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t sel = c & 1 ? 0x7632 : 0x5410;
-        uint32_t x[kPlanes][2];  // a channel's codes of two keys, 16 bits apart
-#pragma unroll
-        for (int pl = 0; pl < kPlanes; ++pl)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            x[pl][h] = c < 2 ? __byte_perm(vw[pl][2 * h].x, vw[pl][2 * h + 1].x, sel)
-                             : __byte_perm(vw[pl][2 * h].y, vw[pl][2 * h + 1].y, sel);
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const uint32_t a0 = codes_bf16x2<BITS>(x[0][0], x[kPlanes - 1][0], 2 * f);
-          const uint32_t a1 = codes_bf16x2<BITS>(x[0][0], x[kPlanes - 1][0], 2 * f + 1);
-          const uint32_t a2 = codes_bf16x2<BITS>(x[0][1], x[kPlanes - 1][1], 2 * f);
-          const uint32_t a3 = codes_bf16x2<BITS>(x[0][1], x[kPlanes - 1][1], 2 * f + 1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816(o[2 * c + f][nt], a0, a1, a2, a3, pb[nt][c][0], pb[nt][c][1]);
-        }
-      }
+      for (int i = 0; i < kKeys; i += kStep) step<ROWS, BITS, false>(w, p, rec + i * kRec, j0 + i, kStep, g, t);
+    } else {
+      for (int i = 0; i < nk; i += kStep) step<ROWS, BITS, true>(w, p, rec + i * kRec, j0 + i, nk - i, g, t);
     }
     __syncwarp();  // the unit has been read: its place is free
-    if (lane == 0 && u + kDepth < u1) fetch(u + kDepth, at);
-    if (++at == kDepth) {
-      at = 0;
-      phase ^= 1u;
-    }
+    if (lane == 0 && u + kUnits < u1) fetch(u + kUnits, at);
+    at ^= 1;
+    phase ^= static_cast<uint32_t>(at == 0);
   }
-  if (!ok && lane == 0)  // copies in flight land before the ring is used for anything else
-    for (int i = u; i < min(u + kDepth, u1); ++i) {
-      const int a = (i - u0) % kDepth;
-      drain_wait(&full[a], static_cast<uint32_t>((i - u0) / kDepth) & 1u, p.st.limit);
+  if (!ok && lane == 0)  // copies in flight land before the CTA can end
+    for (const int end = min(u + kUnits, u1); u < end; ++u) {
+      drain_wait(&full[at], phase, p.st.limit);
+      at ^= 1;
+      phase ^= static_cast<uint32_t>(at == 0);
     }
-  __syncthreads();
-
-  // ---- join the warps
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 8 * nt + 2 * t + e;
-#pragma unroll
-      for (int w = 4; w < 32; w *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], w);
-      if (g == 0) {
-        sm.M[warp][r] = m[nt][e];
-        sm.L[warp][r] = l[nt][e];
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<float4*>(&sm.O[warp][r][32 * c + 4 * g]) =
-            make_float4(o[2 * c][nt][e], o[2 * c][nt][2 + e], o[2 * c + 1][nt][e], o[2 * c + 1][nt][2 + e]);
-    }
-  __syncthreads();
-  const int d4 = lane * 4;
-  for (int r = warp; r < kRows; r += kWarps) {  // a warp joins a row: its partials into slot 0
-    float M = sm.M[0][r];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm.M[w][r]);
-    float L = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = weight(sm.M[w][r], M);
-      const float4 v = *reinterpret_cast<const float4*>(&sm.O[w][r][d4]);
-      L += f * sm.L[w][r];
-      a = make_float4(a.x + f * v.x, a.y + f * v.y, a.z + f * v.z, a.w + f * v.w);
-    }
-    *reinterpret_cast<float4*>(&sm.O[0][r][d4]) = a;
+  __syncwarp();
+  join_warps(sm.parts, w, warp, lane, [&](int r, float M, float L, float4 v) {  // into slot 0
+    *reinterpret_cast<float4*>(&sm.parts.O[0][r][4 * lane]) = v;
     if (lane == 0) {
       sm.cM[r] = M;
       sm.cL[r] = L;
     }
-  }
-  // ---- join the cluster: row r by rank r % cluster
+  });
+  // ---- row r by rank r % cluster
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
-  for (int r = rank + p.cluster * warp; r < kRows; r += p.cluster * kWarps) {
-    if (r0 + r >= R) break;
+  for (int r = rank + p.cluster * warp; r < ROWS; r += p.cluster * kWarps) {
     float M = -INFINITY;
     for (int c = 0; c < p.cluster; ++c) M = fmaxf(M, *cluster.map_shared_rank(&sm.cM[r], c));
     float L = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = 0; c < p.cluster; ++c) {
       const float f = weight(*cluster.map_shared_rank(&sm.cM[r], c), M);
-      const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sm.O[0][r][d4], c));
+      const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sm.parts.O[0][r][4 * lane], c));
       L += f * *cluster.map_shared_rank(&sm.cL[r], c);
-      a = make_float4(a.x + f * v.x, a.y + f * v.y, a.z + f * v.z, a.w + f * v.w);
+      v = make_float4(v.x + f * x.x, v.y + f * x.y, v.z + f * x.z, v.w + f * x.w);
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int tok = (r0 + r) / G, h = hk * G + (r0 + r) % G;
-    uint2 w;
-    w.x = pack_bf16x2(a.x * inv, a.y * inv);
-    w.y = pack_bf16x2(a.z * inv, a.w * inv);
-    *reinterpret_cast<uint2*>(p.o + b * p.o_bs + static_cast<long long>(tok) * p.o_rs + h * kD + d4) = w;
-    if (lane == 0)
-      p.lse[b * p.l_bs + h * p.l_hs + tok] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+    store_row(p, a, r, M, L, v, lane);
   }
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-template <int NT, int BITS, int kWarps>
-struct Form {
-  static constexpr int kSmem = sizeof(Smem<NT, BITS, kWarps>);
-  static const void* fn() { return reinterpret_cast<const void*>(cache_decode_kernel<NT, BITS, kWarps>); }
+// ------------------------------------------------------------------ the units of all tiles as one line
+//
+// A CTA to an SM, whose warps take the sixteens of a unit: one bulk copy brings
+// 16 keys for each, and the warp that is the last to have read it refills its
+// place, so that the warps stay within a ring's length of one another (with a
+// ring for each warp, or two CTAs to an SM, the scheduler lets some warps finish
+// long before the others, which then run alone).
+//
+// Tiles stand in the order (sequence, K/V head, row tile); their N units (fewer
+// than 2^31) are dealt in order to C CTAs, C at most N so that each has some.
+// What a CTA has of a tile that it does not have whole goes to slot 2 i (the
+// first tile that it meets) or 2 i + 1 (the last): ROWS x 128 sums, then the
+// rows' maxima, then their sums of weights.
+
+template <int ROWS, int BITS>
+struct Line {
+  static constexpr int kWarps = warps_per_sm(ROWS);
+  static constexpr int kKeys = kWarps * kStep;                  // of a unit
+  static constexpr int kBytes = kKeys * cache_row_bytes(BITS);
+  static constexpr int kDepth = BITS == 4 ? 4 : 2;              // units of the ring
+  static constexpr int kSlot = ROWS * (kD + 2);                 // floats
+  struct Smem {
+    uint8_t ring[kDepth][kBytes];
+    Parts<ROWS, kWarps> parts;
+    uint64_t full[kDepth];
+    int done[kDepth];  // warps that have read the unit in this place
+    int abort;
+  };
+};
+
+__device__ __forceinline__ int head_units(const CacheDecode& p, int b, int rows, int keys) {  // of a K/V head's row tiles
+  int n = 0;
+  for (int mt = 0; mt < p.row_tiles; ++mt) n += make_tile(p, b, 0, mt, rows, keys).units;
+  return n;
+}
+
+// The units of all sequences, and of those before `b`, by a whole warp.
+__device__ __forceinline__ int all_units(const CacheDecode& p, int b, int rows, int keys, int lane, int* before) {
+  int n = 0, m = 0;
+  for (int i = lane; i < p.B; i += 32) {
+    const int x = p.Hkv * head_units(p, i, rows, keys);
+    n += x;
+    if (i < b) m += x;
+  }
+  *before = __reduce_add_sync(0xffffffffu, m);
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// The sequence of unit x, and the units before it.
+__device__ __forceinline__ int sequence_of(const CacheDecode& p, int x, int rows, int keys, int lane, int* before) {
+  int sum = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int mine = b0 + lane < p.B ? p.Hkv * head_units(p, b0 + lane, rows, keys) : 0;
+    int upto = mine;  // inclusive prefix
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, sum + upto > x);
+    if (past || b0 + 32 >= p.B) {
+      const int i = past ? __ffs(past) - 1 : 31;
+      *before = sum + __shfl_sync(0xffffffffu, upto - mine, i);
+      return min(b0 + i, p.B - 1);
+    }
+    sum += __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+
+__device__ __forceinline__ int add_acq_rel(int* at, int x) {
+  int old;
+  asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], %2;" : "=r"(old) : "r"(smem_u32(at)), "r"(x) : "memory");
+  return old;
+}
+
+template <int ROWS, int BITS>
+__global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
+    cache_decode_line_kernel(const __grid_constant__ CacheDecode p) {
+  using F = Line<ROWS, BITS>;
+  constexpr int kWarps = F::kWarps, kKeys = F::kKeys, kDepth = F::kDepth, kRec = cache_row_bytes(BITS);
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  auto& sm = *reinterpret_cast<typename F::Smem*>(smem_raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int cta = static_cast<int>(blockIdx.x);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel waits for this one's end
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kDepth; ++i) {
+      mbar_init(&sm.full[i], 1);
+      sm.done[i] = 0;
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  int before;
+  const int N = all_units(p, 0, ROWS, kKeys, lane, &before);
+  const int C = min(N, static_cast<int>(gridDim.x));
+  if (cta >= C) return;
+  const Share share(N, C);
+  const int x0 = share.begin(cta);
+  int left = share.begin(cta + 1) - x0;
+  int b = sequence_of(p, x0, ROWS, kKeys, lane, &before);
+  const int per_head = head_units(p, b, ROWS, kKeys);
+  int hk = (x0 - before) / per_head, mt = 0;
+  int off = x0 - before - hk * per_head;  // in the tile
+  Tile a = make_tile(p, b, hk, mt, ROWS, kKeys);
+  // To the tile that has unit `off` of the present one and those behind it. None has if the lengths change meanwhile.
+  auto next_tile = [&] {
+    while (off >= a.units && left > 0) {
+      off -= a.units;
+      if (++mt == p.row_tiles) {
+        mt = 0;
+        if (++hk == p.Hkv) {
+          hk = 0;
+          if (++b == p.B) left = b = 0;
+        }
+      }
+      a = make_tile(p, b, hk, mt, ROWS, kKeys);
+    }
+  };
+  auto fetch = [&](int u, int at) {  // by one lane
+    const uint8_t* head = p.cache + a.b * p.c_bs + a.hk * p.c_hs;
+    const int j0 = first_key(a, u, kKeys);
+    const uint32_t bytes = static_cast<uint32_t>(keys_of(a, u, j0, kKeys)) * kRec;
+    mbar_arrive_expect_tx(&sm.full[at], bytes);
+    bulk_load(sm.ring[at], head + static_cast<long long>(j0) * kRec, bytes, &sm.full[at]);
+  };
+  next_tile();
+  int n = max(0, min(left, a.units - off));
+  RawQ<ROWS> raw = load_q<ROWS>(p, a, g, t);
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kDepth && i < n; ++i) fetch(off + i, i);
+  __syncthreads();  // the barriers are set up
+  int at = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  float* slot = p.workspace + 2LL * cta * F::kSlot;
+  for (;;) {
+    State<ROWS, BITS> w;
+    begin(w, raw, p, a, g, t);
+    const int end = off + n;
+    for (int u = off; u < end; ++u) {
+      ok = mbar_wait_warp(&sm.full[at], phase, &sm.abort, p.st, kWhere);
+      if (!ok) break;
+      const uint8_t* rec = sm.ring[at] + warp * kStep * kRec;
+      if (u >= a.whole0 && u < a.whole1) {
+        step<ROWS, BITS, false>(w, p, rec, 0, kStep, g, t);
+      } else {
+        const int j0 = first_key(a, u, kKeys), nk = keys_of(a, u, j0, kKeys) - warp * kStep;
+        if (nk > 0) step<ROWS, BITS, true>(w, p, rec, j0 + warp * kStep, nk, g, t);
+      }
+      __syncwarp();
+      if (lane == 0 && add_acq_rel(&sm.done[at], 1) == kWarps - 1) {  // every warp has read the unit
+        sm.done[at] = 0;
+        if (u + kDepth < end) fetch(u + kDepth, at);
+      }
+      if (++at == kDepth) {
+        at = 0;
+        phase ^= 1u;
+      }
+    }
+    const Tile now = a;
+    const bool whole = n == a.units;
+    left -= n;
+    off += n;
+    next_tile();
+    __syncthreads();  // the ring is empty, or a wait ran out
+    if (sm.abort) break;
+    if (left > 0) {  // the next tile's copies are on their way while this one's parts are joined
+      n = min(left, a.units - off);
+      raw = load_q<ROWS>(p, a, g, t);
+      if (threadIdx.x == 0)
+        for (int i = 0, x = at; i < kDepth && i < n; ++i, x = x + 1 == kDepth ? 0 : x + 1) fetch(off + i, x);
+    }
+    join_warps(sm.parts, w, warp, lane, [&](int r, float M, float L, float4 v) {
+      if (whole) {
+        store_row(p, now, r, M, L, v, lane);
+      } else {
+        *reinterpret_cast<float4*>(slot + r * kD + 4 * lane) = v;
+        if (lane == 0) {
+          slot[ROWS * kD + r] = M;
+          slot[ROWS * (kD + 1) + r] = L;
+        }
+      }
+    });
+    if (left <= 0) break;
+    slot = p.workspace + (2LL * cta + 1) * F::kSlot;
+  }
+  if (!ok && threadIdx.x == 0)  // copies in flight land before the CTA ends
+    for (int i = 0; i < kDepth; ++i) {
+      drain_wait(&sm.full[at], phase, p.st.limit);
+      if (++at == kDepth) {
+        at = 0;
+        phase ^= 1u;
+      }
+    }
+}
+// kSplit warps join a row of a tile that several CTAs share; rows of tiles
+// without a key get their zeros here.
+template <int ROWS, int BITS, int kSplit>
+__global__ void __launch_bounds__(256) cache_decode_join_kernel(const __grid_constant__ CacheDecode p, int ctas) {
+  constexpr int kKeys = Line<ROWS, BITS>::kKeys, kSlot = Line<ROWS, BITS>::kSlot;
+  constexpr int kRowsHere = 8 / kSplit;
+  __shared__ float4 sO[8][32];
+  __shared__ float sM[8], sL[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = static_cast<int>(blockIdx.x) % (ROWS / kRowsHere);
+  int tile = static_cast<int>(blockIdx.x) / (ROWS / kRowsHere);
+  const int mt = tile % p.row_tiles;
+  tile /= p.row_tiles;
+  const int b = tile / p.Hkv, hk = tile % p.Hkv;
+  const Tile a = make_tile(p, b, hk, mt, ROWS, kKeys);
+  int start;
+  const int N = all_units(p, b, ROWS, kKeys, lane, &start);
+  start += hk * head_units(p, b, ROWS, kKeys);
+  for (int i = 0; i < mt; ++i) start += make_tile(p, b, hk, i, ROWS, kKeys).units;
+  const int r = sub * kRowsHere + warp / kSplit, part = warp % kSplit;
+  const Share share(max(N, 1), max(1, min(N, ctas)));
+  const int i0 = share.part_of(start), i1 = share.part_of(start + max(a.units, 1) - 1);
+  const bool at_start = share.begin(i0) == start;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.units == 0) {
+    if (part == 0) store_row(p, a, r, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f), lane);
+    return;
+  }
+  if (i0 == i1) return;  // stored by the one CTA that has it
+  float M = -INFINITY, L = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = i0 + part; i <= i1; i += kSplit) {
+    const float* slot = p.workspace + (2LL * i + (i > i0 || at_start ? 0 : 1)) * kSlot;
+    const float4 x = *reinterpret_cast<const float4*>(slot + r * kD + 4 * lane);
+    const float m = slot[ROWS * kD + r], l = slot[ROWS * (kD + 1) + r];
+    const float top = fmaxf(M, m), f = weight(M, top), g = weight(m, top);
+    M = top;
+    L = f * L + g * l;
+    v = make_float4(f * v.x + g * x.x, f * v.y + g * x.y, f * v.z + g * x.z, f * v.w + g * x.w);
+  }
+  if (kSplit > 1) {
+    sO[warp][lane] = v;
+    if (lane == 0) {
+      sM[warp] = M;
+      sL[warp] = L;
+    }
+    __syncthreads();
+    if (part != 0) return;
+    float top = M;
+#pragma unroll
+    for (int i = 1; i < kSplit; ++i) top = fmaxf(top, sM[warp + i]);
+    const float f = weight(M, top);
+    M = top;
+    L *= f;
+    v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
+#pragma unroll
+    for (int i = 1; i < kSplit; ++i) {
+      const float4 x = sO[warp + i][lane];
+      const float g = weight(sM[warp + i], top);
+      L += g * sL[warp + i];
+      v = make_float4(v.x + g * x.x, v.y + g * x.y, v.z + g * x.z, v.w + g * x.w);
+    }
+  }
+  store_row(p, a, r, M, L, v, lane);
+}
+
+// ------------------------------------------------------------------ launches
+
+template <int ROWS, int BITS, int kWarps>
+struct ClusterForm {
+  static constexpr int kSmem = sizeof(ClusterSmem<ROWS, BITS, kWarps>);
+  static const void* fn() { return reinterpret_cast<const void*>(cache_decode_kernel<ROWS, BITS, kWarps>); }
 
   static DeviceOnce& allowed() {
     static DeviceOnce once;
@@ -459,47 +957,169 @@ struct Form {
     at.val.clusterDim.x = static_cast<unsigned>(p.cluster);
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.parts * p.cluster));
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.cluster));
     cfg.blockDim = dim3(32 * kWarps);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_decode_kernel<NT, BITS, kWarps>, p) == cudaSuccess ? 0 : -4;
+    return cudaLaunchKernelEx(&cfg, cache_decode_kernel<ROWS, BITS, kWarps>, p) == cudaSuccess ? 0 : -4;
   }
 };
 
-template <int NT, int BITS>
-int launch_rows(CacheDecode& p, long long tiles, long long units, cudaStream_t stream) {
-  const ContextKey at = current_context();
-  const int c4 = Form<NT, BITS, 4>::one_wave(at, tiles, units), c8 = Form<NT, BITS, 8>::one_wave(at, tiles, units);
-  if (4 * c4 >= 8 * c8) {
-    p.cluster = std::max(1, c4);
-    return Form<NT, BITS, 4>::launch(p, tiles, stream);
+template <int ROWS, int BITS>
+struct LineForm {
+  static constexpr int kSmem = sizeof(typename Line<ROWS, BITS>::Smem), kThreads = 32 * Line<ROWS, BITS>::kWarps;
+  static const void* fn() { return reinterpret_cast<const void*>(cache_decode_line_kernel<ROWS, BITS>); }
+
+  static DeviceOnce& allowed() {
+    static DeviceOnce once;
+    return once;
   }
-  p.cluster = c8;
-  return Form<NT, BITS, 8>::launch(p, tiles, stream);
+
+  static int ctas(const ContextKey& at) {  // that the GPU holds at once
+    static ClusterCounts known;
+    return resident_clusters(known, at, allowed(), fn(), kThreads, kSmem, 1);
+  }
+
+  static size_t workspace(int n) { return 2 * sizeof(float) * Line<ROWS, BITS>::kSlot * static_cast<size_t>(n); }
+
+  static int launch(const CacheDecode& p, long long tiles, int n, cudaStream_t stream) {
+    const int rc = allow_clusters_once(allowed(), fn(), kSmem);
+    if (rc != 0) return rc;
+    cache_decode_line_kernel<ROWS, BITS><<<n, kThreads, kSmem, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return -4;
+    // A warp or two a row where a tile has few parts, eight where it has many.
+    constexpr int kNarrow = ROWS == 4 ? 2 : 1;
+    const bool wide = n > 8 * tiles;
+    cudaLaunchAttribute at;  // it starts beside the end of the kernel before it
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * (wide ? ROWS : ROWS * kNarrow / 8)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, BITS, 8>, p, n)
+                               : cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, BITS, kNarrow>, p, n);
+    return e == cudaSuccess ? 0 : -4;
+  }
+};
+
+// Sizes of a call as its launch sees them: the host knows no lengths.
+struct Plan {
+  int rows;
+  long long row_tiles, tiles, keys;  // keys: the most that a tile can see
+};
+
+Plan plan_of(int B, int H, int Hkv, int T, int Smax, int window, int sinks) {
+  Plan a;
+  const long long R = static_cast<long long>(T) * (H / Hkv);
+  a.rows = R <= 4 ? 4 : R <= 8 ? 8 : 16;
+  a.row_tiles = (R + a.rows - 1) / a.rows;
+  a.tiles = static_cast<long long>(B) * Hkv * a.row_tiles;
+  a.keys = std::min<long long>(Smax, static_cast<long long>(window) + T - 1 + sinks);
+  return a;
 }
+
+// The cluster form of a call: 4 or 8 warps a CTA, whichever puts more warps on
+// the GPU in one wave, and the cluster (1 where not even that fits).
+template <int ROWS, int BITS>
+struct ClusterChoice {
+  int warps, cluster;
+  long long in_flight;  // warps of the tiles that the GPU holds at once
+  ClusterChoice(const Plan& a, const ContextKey& at) {
+    const long long units = (a.keys + unit_keys<BITS>() - 1) / unit_keys<BITS>();
+    const int c4 = ClusterForm<ROWS, BITS, 4>::one_wave(at, a.tiles, units);
+    const int c8 = ROWS == 16 ? 0 : ClusterForm<ROWS, BITS, 8>::one_wave(at, a.tiles, units);
+    warps = 4 * c4 >= 8 * c8 ? 4 : 8;
+    cluster = std::max(1, warps == 4 ? c4 : c8);
+    in_flight = std::min<long long>(a.tiles * cluster * warps, kSms * warps_per_sm(ROWS));
+  }
+};
+
+// CTAs of the line form, or 0 for the cluster form: two estimates in us, by the
+// most keys that the sizes allow, fitted to both forms at fourteen sizes. A
+// cluster form is done when its warps' share of the bytes is; the line form has a
+// longer start, a second kernel, and some 3 us for each tile that a CTA begins
+// after its first. us, cluster / line, 4 bits unless said: 32 heads x 777 keys 6 /
+// 8, x 2052 8 / 12; 8 x 8 heads x 20001, eight rows, 37 / 42; 160 x 32772 127 / 122;
+// 8 x 131072 in 8 bits 69 / 51; 8 x 524288 204 / 106; 1 x 524288 123 / 25; 4 x
+// 100000 33 / 26; 512 x 2000 25 / 39; 80 x 5000 in 8 bits 20 / 24; 40 x 32768 39 / 42.
+template <int ROWS, int BITS>
+int line_ctas(const Plan& a, const ClusterChoice<ROWS, BITS>& c, const ContextKey& at) {
+  const int n = LineForm<ROWS, BITS>::ctas(at);
+  const long long units = a.tiles * ((a.keys + Line<ROWS, BITS>::kKeys - 1) / Line<ROWS, BITS>::kKeys + 1);
+  if (n <= 0 || a.row_tiles > 8 || units >= 1LL << 31) return 0;
+  const double hbm_us = static_cast<double>(a.tiles) * a.keys * cache_row_bytes(BITS) / 6.7e6;
+  const double busy = static_cast<double>(c.in_flight) / (kSms * warps_per_sm(ROWS));
+  const double cluster_us = 5 + 1.15 * hbm_us / std::min(1.0, (BITS == 4 ? 1.0 : 1.5) * busy);
+  const double line_us = 9.5 + 1.08 * hbm_us + 3.5 * std::max(0.0, static_cast<double>(a.tiles) / n - 1);
+  return line_us < cluster_us ? n : 0;
+}
+
+template <int ROWS, int BITS>
+int launch_rows(CacheDecode& p, const Plan& a, size_t ws_bytes, cudaStream_t stream) {
+  const ContextKey at = current_context();
+  const ClusterChoice<ROWS, BITS> c(a, at);
+  const int n = line_ctas<ROWS, BITS>(a, c, at);
+  if (n > 0) {
+    if (!p.workspace || ws_bytes < LineForm<ROWS, BITS>::workspace(n)) return -1;
+    return LineForm<ROWS, BITS>::launch(p, a.tiles, n, stream);
+  }
+  p.cluster = c.cluster;
+  return c.warps == 4 ? ClusterForm<ROWS, BITS, 4>::launch(p, a.tiles, stream)
+                      : ClusterForm<ROWS, BITS, 8>::launch(p, a.tiles, stream);
+}
+
+// f with the row count and the bits as types.
+template <class F>
+auto with_form(int rows, int bits, F&& f) {
+  if (bits == 4)
+    return rows == 4   ? f.template operator()<4, 4>()
+           : rows == 8 ? f.template operator()<8, 4>()
+                       : f.template operator()<16, 4>();
+  return rows == 4   ? f.template operator()<4, 8>()
+         : rows == 8 ? f.template operator()<8, 8>()
+                     : f.template operator()<16, 8>();
+}
+
+struct WorkspaceOf {
+  const Plan& a;
+  template <int ROWS, int BITS>
+  size_t operator()() const {
+    const ContextKey at = current_context();
+    return LineForm<ROWS, BITS>::workspace(line_ctas<ROWS, BITS>(a, ClusterChoice<ROWS, BITS>(a, at), at));
+  }
+};
+
+struct Launch {
+  CacheDecode& p;
+  const Plan& a;
+  size_t ws_bytes;
+  cudaStream_t stream;
+  template <int ROWS, int BITS>
+  int operator()() const {
+    return launch_rows<ROWS, BITS>(p, a, ws_bytes, stream);
+  }
+};
 
 }  // namespace
 
-size_t cache_decode_workspace(int, int, int, int, int, int, int, int) { return 0; }
+size_t cache_decode_workspace(int B, int H, int Hkv, int T, int Smax, int window, int sinks, int bits) {
+  const Plan a = plan_of(B, H, Hkv, T, Smax, window, sinks);
+  return with_form(a.rows, bits, WorkspaceOf{a});
+}
 
-int launch_cache_decode(CacheDecode p, int bits, size_t, cudaStream_t stream) {
-  const long long R = static_cast<long long>(p.T) * (p.H / p.Hkv);
-  if (R > kWindowMaxRows) return -1;
-  const int rows = R <= 8 ? 8 : 16;
-  p.row_tiles = static_cast<int>((R + rows - 1) / rows);
-  p.parts = 1;
-  const long long tiles = static_cast<long long>(p.B) * p.Hkv * p.row_tiles;
-  if (tiles > 0x7fffffffLL / kMaxCluster) return -1;
-  if (tiles == 0) return 0;
-  // Most keys that a row tile can see, from the host's side of the sizes.
-  const long long seen = std::min<long long>(p.Smax, static_cast<long long>(p.window) + p.T - 1 + p.sinks);
-  const int keys = bits == 4 ? Unit<4>::kKeys : Unit<8>::kKeys;
-  const long long units = (seen + keys - 1) / keys;
-  if (bits == 4) return rows == 8 ? launch_rows<1, 4>(p, tiles, units, stream) : launch_rows<2, 4>(p, tiles, units, stream);
-  return rows == 8 ? launch_rows<1, 8>(p, tiles, units, stream) : launch_rows<2, 8>(p, tiles, units, stream);
+int launch_cache_decode(CacheDecode p, int bits, size_t ws_bytes, cudaStream_t stream) {
+  p.G = p.H / p.Hkv;
+  if (static_cast<long long>(p.T) * p.G > kWindowMaxRows) return -1;
+  const Plan a = plan_of(p.B, p.H, p.Hkv, p.T, p.Smax, p.window, p.sinks);
+  if (a.tiles > 0x7fffffffLL / kMaxCluster) return -1;
+  p.row_tiles = static_cast<int>(a.row_tiles);
+  p.cluster = 1;
+  return with_form(a.rows, bits, Launch{p, a, ws_bytes, stream});
 }
 
 }  // namespace lcb

@@ -30,13 +30,14 @@ constexpr int kRows = 8;  // rows of a warp
 // of the others, and their reciprocals, are then normal numbers.
 constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100
 
-// n of eight channels, from x / s by one multiplication. bf16 values and scales
+// n of a channel, from x / s by one multiplication. bf16 values and scales
 // have 8 significant bits, so x / s is a tie (a whole number and a half) or away
 // from one by more than 2^-11 of itself; a reciprocal that is larger by 2^-20
 // moves ties past the half, and nothing else across one. Adding 1.5 * 2^23
 // leaves the rounded number in the low bits.
+// As sign (bit 7) and magnitude.
 __device__ __forceinline__ uint32_t quant_code(float x, float inv) {
-  return __float_as_uint(fmaf(x, inv, 12582912.f));
+  return (__float_as_uint(fmaf(fabsf(x), inv, 12582912.f)) & 0x7fu) | (__float_as_uint(x) >> 24 & 0x80u);
 }
 
 template <int BITS>
@@ -92,23 +93,29 @@ __global__ void __launch_bounds__(32 * kWarps) kv_cache_write_kernel(const __gri
     uint8_t* rec = rec0 + r * kRec;
     if ((j & 3) == 0)
       reinterpret_cast<__nv_bfloat16*>(rec + cache_scale_offset(BITS))[(is_v ? 4 : 0) + G] = s;
-#pragma unroll
-    for (int plane = 0; plane < cache_planes(BITS); ++plane) {
-      uint32_t u[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        u[i] = BITS == 4 ? (n[i] + 8u) & 15u : plane == 0 ? ((n[i] + 128u) >> 4) & 15u : n[i] & 15u;
-      if (!is_v) {
-        uint32_t word = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) word |= u[2 * e] << (4 * e) | u[2 * e + 1] << (4 * e + 16);
-        reinterpret_cast<uint32_t*>(rec + plane * kPlaneBytes)[4 * (j & 3) + G] = word;
+    auto sign = [&](int i) { return n[i] >> 7; };
+    auto mag = [&](int i) { return n[i] & 0x7fu; };
+    if (!is_v) {
+      uint32_t* words = reinterpret_cast<uint32_t*>(rec);
+      if (BITS == 4) {
+        words[4 * (j & 3) + G] = pack_fields(n[0], n[2], n[4], n[6]) | pack_fields(n[1], n[3], n[5], n[7]) << 16;
       } else {
-        uint16_t* half = reinterpret_cast<uint16_t*>(rec + cache_v_offset(BITS) + plane * kPlaneBytes);
 #pragma unroll
         for (int f = 0; f < 2; ++f)
-          half[4 * (2 * (j & 3) + f) + G] =
-              static_cast<uint16_t>(u[4 * f] | u[4 * f + 1] << 4 | u[4 * f + 2] << 8 | u[4 * f + 3] << 12);
+          words[16 * (G >> 1) + 4 * (j & 3) + 2 * (G & 1) + f] =
+              mag(4 * f) | sign(4 * f) << 15 | mag(4 * f + 1) << 16 | sign(4 * f + 1) << 31 | mag(4 * f + 2) << 8 |
+              sign(4 * f + 2) << 23 | mag(4 * f + 3) << 24 | sign(4 * f + 3) << 7;
+      }
+    } else {
+      uint8_t* at = rec + cache_v_offset(BITS);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int g = 2 * (j & 3) + f, i = 4 * f;
+        if (BITS == 4)
+          reinterpret_cast<uint16_t*>(at)[4 * g + G] =
+              static_cast<uint16_t>(pack_fields(n[i], n[i + 1], n[i + 2], n[i + 3]));
+        else
+          reinterpret_cast<uint32_t*>(at)[4 * g + G] = n[i] | n[i + 1] << 8 | n[i + 2] << 16 | n[i + 3] << 24;
       }
     }
   }
@@ -159,21 +166,34 @@ __global__ void __launch_bounds__(32 * kWarps) kv_cache_read_kernel(const __grid
       const uint8_t* rec = recs[warp] + r * kRec;
       const uint32_t s1 = reinterpret_cast<const uint16_t*>(rec + cache_scale_offset(BITS))[(is_v ? 4 : 0) + G];
       const uint32_t s = s1 | s1 << 16;
-      uint32_t word[2];  // a plane's, pair e of the channels in nibbles e and e + 4
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(rec);
+      if (!is_v && BITS == 4) {
+        const Fields x = k4_fields(words[4 * (j & 3) + G]);
 #pragma unroll
-      for (int plane = 0; plane < cache_planes(BITS); ++plane) {
-        if (!is_v) {
-          word[plane] = reinterpret_cast<const uint32_t*>(rec + plane * kPlaneBytes)[4 * (j & 3) + G];
-        } else {
-          const uint16_t* half = reinterpret_cast<const uint16_t*>(rec + cache_v_offset(BITS) + plane * kPlaneBytes);
-          const uint32_t a = half[8 * (j & 3) + G], c = half[8 * (j & 3) + 4 + G];
-          // nibbles 0, 2 of both half-words, then 1, 3 of both
-          word[plane] = (a & 0xfu) | (a >> 4 & 0xf0u) | (c & 0xfu) << 8 | (c >> 8 & 0xfu) << 12 |
-                        (a >> 4 & 0xfu) << 16 | (a >> 12) << 20 | (c >> 4 & 0xfu) << 24 | (c >> 12) << 28;
+        for (int f = 0; f < 4; ++f) w[f] = f & 1 ? (x.pair(f) & 0x80008000u) | (x.pair(f) >> 4 & 0x00070007u) : x.pair(f);
+      } else if (!is_v) {
+        const uint32_t* two = words + 16 * (G >> 1) + 4 * (j & 3) + 2 * (G & 1);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) w[f] = k8_f16x2(two[f >> 1], f & 1);
+      } else if (BITS == 4) {
+        const uint16_t* half = reinterpret_cast<const uint16_t*>(rec + cache_v_offset(BITS));
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const uint32_t a = half[4 * (2 * (j & 3) + f) + G];
+          // fields 0, 1 and 2, 3 as pairs
+          w[2 * f] = (a & 0x8007u) | (a << 13 & 0x70000u) | (a << 17 & 0x80000000u);
+          w[2 * f + 1] = (a >> 8 & 7u) | (a << 8 & 0x8000u) | (a << 5 & 0x70000u) | (a << 25 & 0x80000000u);
+        }
+      } else {
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const uint32_t x = words[cache_v_offset(BITS) / 4 + 4 * (2 * (j & 3) + f) + G];
+          w[2 * f] = permute_bytes(x, 0, 0x9180);
+          w[2 * f + 1] = permute_bytes(x, 0, 0xb3a2);
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = codes_bf16x2<BITS>(word[0], word[cache_planes(BITS) - 1], e);
+      for (int e = 0; e < 4; ++e) w[e] = signed_bf16x2(w[e]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = hmul2_bf16(w[e], s);  // the one rounding: n and s have 8 bits each
     }

@@ -2,23 +2,35 @@
 //
 // A row holds a K and a V vector of 128 channels. Each group of 32 channels
 // has a bf16 scale s; channel c holds s * n with a whole number n: -7 .. 7 in a
-// 4-bit cache, -127 .. 127 in an 8-bit one. The row is one record of
-//   planes * 64 bytes   K codes
-//   planes * 64 bytes   V codes
-//   8 + 8 bytes         K's and V's four scales
+// 4-bit cache, -127 .. 127 in an 8-bit one, kept as a sign and a magnitude. The
+// row is one record of
+//   16 * bits bytes   K codes
+//   16 * bits bytes   V codes
+//   8 + 8 bytes       K's and V's four scales
 // (144 bytes in 4 bits, 272 in 8), so that one contiguous stream carries all
-// that attention reads of a head. Codes are kept off zero: u = n + 8 in one
-// plane of 4-bit numbers, or u = n + 128 as two, its high and its low half.
+// that attention reads of a head.
 //
-// Within a plane the codes lie in the order in which a lane (g, t) of a warp
-// takes them as operands of m16n8k16 products (the sum over channels and the
-// order of O's channels are free to permute):
-//   K: lane t takes channels 32 G + 8 t .. + 7 of the groups G = 0 .. 3, one
-//      32-bit word each: word 4 t + G. Pair e of a word's channels (2e, 2e + 1)
-//      is its nibbles e and e + 4, 16 bits apart, so one shift and one bitwise
-//      operation make it a pair of bf16 numbers (below).
-//   V: lane g takes channels 32 G + 4 g .. + 3 of each group, 16 bits each:
-//      half-word 4 g + G, channel i in nibble i.
+// The codes lie as a lane (g, t) of a warp takes them for operands of tensor
+// products (the sum over channels and the order of O's channels are free to
+// permute). A magnitude in the low bits of a floating-point number whose
+// exponent is zero is a subnormal number, a power of two times the magnitude,
+// and tensor cores multiply those exactly; so one bitwise AND, after at most a
+// rotation, a byte permute and a shift, takes a pair of codes:
+//   4 bits: four codes in 16 bits, as fields 0 .. 3. ANDed with 0x8007 they
+//     leave field 0; shifted left by 1 and ANDed with 0x8070 field 1, 2^4 as
+//     large; with the two bytes exchanged before, fields 2 and 3.
+//   K, 4 bits: lane t takes channels 32 G + 8 t .. + 7 of the groups G = 0 .. 3,
+//     word 4 t + G, as pairs of fp16: field i of its halves has channels 2 i and
+//     2 i + 1 (n * 2^-24 or n * 2^-20).
+//   K, 8 bits: the same channels, words 16 (G / 2) + 4 t + 2 (G % 2) + {0, 1}, as
+//     fp16 (n * 2^-24). A word ANDed with 0x807f807f has the first two of its four
+//     channels, rotated right by 8 bits before that the others.
+//   V, 4 bits: lane g takes channels 32 G + 4 g .. + 3 of each group, half-word
+//     4 g + G, its fields. Those of two keys side by side in a register are pairs
+//     of bf16 (n * 2^-133 or n * 2^-129).
+//   V, 8 bits: the same channels, bytes 16 g + 4 G + {0 .. 3}, sign and magnitude:
+//     a byte permute that repeats the sign, ANDed with 0x807f807f, makes those of
+//     two keys a bf16 pair (n * 2^-133).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -27,43 +39,65 @@
 namespace lcb {
 
 constexpr int kCacheGroup = 32;  // channels of a scale
-constexpr int kPlaneBytes = 64;
 
-constexpr int cache_planes(int bits) { return bits / 4; }
-constexpr int cache_v_offset(int bits) { return cache_planes(bits) * kPlaneBytes; }
-constexpr int cache_scale_offset(int bits) { return 2 * cache_planes(bits) * kPlaneBytes; }
-constexpr int cache_row_bytes(int bits) { return cache_scale_offset(bits) + 16; }
+constexpr int cache_v_offset(int bits) { return 16 * bits; }
+constexpr int cache_scale_offset(int bits) { return 32 * bits; }
+constexpr int cache_row_bytes(int bits) { return 32 * bits + 16; }
 
-__device__ __forceinline__ uint32_t hadd2_bf16(uint32_t a, uint32_t b) {
+// Four codes in 16 bits, from signs (bit 7) and magnitudes.
+__device__ __forceinline__ uint32_t pack_fields(uint32_t n0, uint32_t n1, uint32_t n2, uint32_t n3) {
+  return (n0 & 7u) | (n0 & 0x80u) << 8 | (n1 & 7u) << 3 | (n1 & 0x80u) << 7 | (n2 & 7u) << 8 | (n2 & 0x80u) |
+         (n3 & 7u) << 11 | (n3 & 0x80u) >> 1;
+}
+
+// Bytes of (a, b) by the nibbles of `sel`, the highest bit of a nibble giving eight copies of that byte's sign.
+__device__ __forceinline__ uint32_t permute_bytes(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
+}
+
+__device__ __forceinline__ uint32_t rotate_right(uint32_t x, int n) { return __funnelshift_r(x, x, n); }
+
+// Fields of both halves of a word.
+struct Fields {
+  uint32_t x, y;  // the word, and with the bytes of its halves exchanged
+  __device__ __forceinline__ uint32_t pair(int i) const {
+    const uint32_t v = i < 2 ? x : y;
+    return i & 1 ? (v << 1) & 0x80708070u : v & 0x80078007u;
+  }
+};
+
+// K of a lane's word in 4 bits, as pairs of fp16.
+__device__ __forceinline__ Fields k4_fields(uint32_t w) { return {w, permute_bytes(w, w, 0x2301)}; }
+
+// V of one channel group of two keys in 4 bits, from the words that have it (G odd: in the high half), as pairs of bf16.
+__device__ __forceinline__ Fields v4_fields(uint32_t key0, uint32_t key1, int G) {
+  return {permute_bytes(key0, key1, G & 1 ? 0x7632 : 0x5410), permute_bytes(key0, key1, G & 1 ? 0x6723 : 0x4501)};
+}
+
+// K of a word in 8 bits: channels 2 f and 2 f + 1 of its four, as fp16.
+__device__ __forceinline__ uint32_t k8_f16x2(uint32_t w, int f) { return (f ? rotate_right(w, 8) : w) & 0x807f807fu; }
+
+// V of one channel group of two keys in 8 bits.
+struct V8 {
+  uint32_t key0, key1;
+  __device__ __forceinline__ uint32_t pair(int i) const {
+    return permute_bytes(key0, key1, 0xc480u + 0x1111u * static_cast<uint32_t>(i)) & 0x807f807fu;
+  }
+};
+
+// A word of signs and magnitudes, sign and 7 bits at each end of 16, as whole numbers in bf16. Exact.
+__device__ __forceinline__ uint32_t signed_bf16x2(uint32_t x) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x007f007fu) | 0x43004300u), "r"(0xc300c300u));  // 128 + u - 128
+  return r | (x & 0x80008000u);
 }
 
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-
-__device__ __forceinline__ uint32_t hfma2_bf16(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
-// Nibbles 0 and 4 of x as bf16 numbers 128 + u: they become the low mantissa bits of 128.
-__device__ __forceinline__ uint32_t nibbles_bf16x2(uint32_t x) { return (x & 0x000f000fu) | 0x43004300u; }
-
-// The numbers n of nibbles i and i + 4 of a plane's word (4 bits), or of the
-// high and the low plane's (8 bits), as a pair of bf16. Exact at every step:
-// all are whole numbers of at most 8 significant bits.
-template <int BITS>
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w0, uint32_t w1, int i) {
-  const uint32_t h = nibbles_bf16x2(w0 >> (4 * i));
-  if (BITS == 4) return hadd2_bf16(h, 0xc308c308u);                 // 128 + u - 136
-  const uint32_t x = hfma2_bf16(h, 0x41804180u, 0xc510c510u);       // 16 (128 + hi) - 2304 = 16 hi - 256
-  return hadd2_bf16(x, nibbles_bf16x2(w1 >> (4 * i)));              // + 128 + lo: n = 16 hi + lo - 128
 }
 
 }  // namespace lcb

@@ -236,11 +236,11 @@ struct CacheDecode {
   const int* lens;
   __nv_bfloat16* o;
   float* lse;
-  float* workspace;  // partials of parts > 1
+  float* workspace;  // of the form that needs one
   long long q_rs, q_bs, c_bs, c_hs, o_rs, o_bs, l_hs, l_bs;
   int B, H, Hkv, T, Smax, window, sinks;
   float scale_log2;
-  int row_tiles, cluster, parts;  // set by the launch
+  int G, row_tiles, cluster;  // set by the launch
   DevStatus st;
 };
 size_t cache_decode_workspace(int B, int H, int Hkv, int T, int Smax, int window, int sinks, int bits);
