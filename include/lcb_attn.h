@@ -517,16 +517,29 @@ int lcb_kv_cache_read(const void* cache, void* k, void* v, const int* lens, int 
 size_t attn_cache_decode_workspace_bytes(int B, int H, int Hkv, int T, int Smax, int D, int bits, int window,
                                          int sinks);
 
+#define LCB_CACHE_FORM_EMPTY 0   /* no tokens, or no rows of the cache */
+#define LCB_CACHE_FORM_CLUSTER 1 /* a cluster of CTAs for each sequence, K/V head and 16 query rows at most */
+#define LCB_CACHE_FORM_LINE 2    /* the keys of all of those dealt evenly to the GPU's CTAs; a second kernel joins */
+#define LCB_CACHE_FORM_TILES 3   /* the same with 128 query rows and the cache unpacked to shared memory */
+
+/* Which of its kernels attn_cache_decode takes for these sizes on the current
+ * device, or a negative LCB_ERR_* code. The result is the same in all, within
+ * their roundings; for tests and measurements that mean one of them. */
+int attn_cache_decode_form(int B, int H, int Hkv, int T, int Smax, int D, int bits, int window, int sinks);
+
 /*
  * attn_cache_decode — attn_window_decode over the quantised cache: q, o
  * [B, T, H, D] bf16; token t of sequence b stands at position lens[b] - T + t
  * (lens: DEVICE int32 [B], clamped to [0, Smax]) and sees the keys j <= p with
  * p - j < window, and the first `sinks`. Attention is that over the held values
- * n_c * s, unrounded; LSE fp32 (natural log, scale included). Each visible row
- * is read once for all query rows of its head up to 16 of them (T * H / Hkv).
- * Deterministic. Any T; for the many tokens of a prompt's chunk,
- * lcb_kv_cache_read and attn_window_fwd are faster.
- * A row with NaN makes NaN of those query rows alone that see it. window, sinks, scale, heads, q, o, lse and their
+ * n_c * s; LSE fp32 (natural log, scale included). Each visible row is read once
+ * for all query rows of its head up to 16 of them (T * H / Hkv), or 128 in the
+ * form for many rows. Deterministic. Any T; for the hundreds of tokens of a
+ * prompt's chunk, lcb_kv_cache_read and attn_window_fwd are faster.
+ * What is rounded: weights (and O) to bf16, as in the windowed attention; in the
+ * form for many rows also V, to bf16 as lcb_kv_cache_read gives it.
+ * A row with NaN makes NaN of those query rows alone that see it; in the form for
+ * many rows V's NaN also of others of their tile. window, sinks, scale, heads, q, o, lse and their
  * strides as attn_window_decode; the cache as above. workspace: device memory
  * of at least attn_cache_decode_workspace_bytes(), 16-byte aligned, contents
  * ignored (NULL where that is 0); calls that may overlap on the GPU need

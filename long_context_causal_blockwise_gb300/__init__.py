@@ -12,6 +12,7 @@ Public calls (all run in this library's CUDA kernels):
   attn_window_decode (its form for the newest tokens against a K/V cache),
   kv_cache_empty / kv_cache_write / kv_cache_read (a K/V cache in 4 or 8 bits),
   attn_cache_decode (the newest tokens against that cache),
+  attn_cache_decode_form (which of its kernels that call takes),
   rope_axes (rotary positions with several axes, and the inverse),
   cross_entropy (the loss head with an in-place backward),
   zigzag_attention_fwd / zigzag_attention_bwd (the one-device zigzag ring),
@@ -35,6 +36,7 @@ from ._lib import (  # noqa: F401
     attn_bwd_preprocess,
     attn_bwd_workspace_bytes,
     attn_cache_decode,
+    attn_cache_decode_form,
     attn_cache_decode_workspace_bytes,
     attn_fwd,
     attn_fwd_ex,

@@ -96,6 +96,7 @@ _SIGNATURES = {
     "lcb_kv_cache_write": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _LL, _LL, _LL, _LL, _P], _I),
     "lcb_kv_cache_read": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _LL, _LL, _LL, _LL, _P], _I),
     "attn_cache_decode_workspace_bytes": ([_I, _I, _I, _I, _I, _I, _I, _I, _I], _SZ),
+    "attn_cache_decode_form": ([_I, _I, _I, _I, _I, _I, _I, _I, _I], _I),
     "attn_cache_decode": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _LL, _LL, _LL, _LL, _LL, _LL, _LL,
                            _LL, _P, _SZ, _P], _I),
     "lcb_permute_rows": ([_P, _P, _P, _I, _LL, _P], _I),
@@ -795,6 +796,17 @@ def _cache_decode_workspace(device, *sizes):
     return int(load().attn_cache_decode_workspace_bytes(*sizes))
 
 
+def attn_cache_decode_form(B, H, Hkv, T, Smax, bits=4, window=None, sinks=0, D=128):
+    """Which of its kernels attn_cache_decode takes for these sizes on the current device: "cluster" (few keys: a cluster
+    of CTAs for each sequence and K/V head), "line" (the keys of all dealt evenly over the GPU, a second kernel joins),
+    "tiles" (the same for many query rows a K/V head), or "empty"."""
+    rc = load().attn_cache_decode_form(B, H, Hkv, T, Smax, D, bits, _MOST if window is None else _count(window),
+                                       _count(sinks))
+    if rc < 0:
+        _check("attn_cache_decode_form", rc)
+    return ("empty", "cluster", "line", "tiles")[rc]
+
+
 def attn_cache_decode(q, cache, lens, window=None, sinks=0, scale=None, o=None, lse=None, workspace=None):
     """attn_window_decode over a quantised cache (kv_cache_empty, kv_cache_write); returns (o, lse fp32 [B, H, T]).
 
@@ -814,16 +826,16 @@ def attn_cache_decode(q, cache, lens, window=None, sinks=0, scale=None, o=None, 
     window = _MOST if window is None else _count(window)
     sinks = _count(sinks)
     o, lse, orr, ob, lh, lb = _window_out(q, qs, o, lse)
-    lib = _LIB or load()
+    dev = q.get_device()
+    stream = _raw_stream("attn_cache_decode", dev, (cache, lens, o, lse) if workspace is None else (cache, lens, o, lse,
+                                                                                                  workspace))
     if workspace is None:
-        n = _cache_decode_workspace(q.get_device(), B, H, Hkv, T, Smax, D, bits, window, sinks)
+        n = _cache_decode_workspace(dev, B, H, Hkv, T, Smax, D, bits, window, sinks)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    stream = _raw_stream("attn_cache_decode", q.get_device(),
-                         (cache, lens, o, lse) if workspace is None else (cache, lens, o, lse, workspace))
-    rc = lib.attn_cache_decode(
+    rc = (_LIB or load()).attn_cache_decode(
         q.data_ptr(), cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, Smax, D, bits,
         window, sinks, D ** -0.5 if scale is None else float(scale), qr, qb, cb, ch, orr, ob, lh, lb,
         None if workspace is None else workspace.data_ptr(),

@@ -1069,6 +1069,15 @@ size_t attn_cache_decode_workspace_bytes(int B, int H, int Hkv, int T, int Smax,
   return cache_decode_workspace(B, H, Hkv, T, Smax, w.window, w.sinks, bits);
 }
 
+int attn_cache_decode_form(int B, int H, int Hkv, int T, int Smax, int D, int bits, int window, int sinks) {
+  WindowShape w;
+  const int rc = prep_window(&w, B, H, Hkv, T, Smax, D, window, sinks, 0, 1.f);
+  if (rc != LCB_OK) return rc;
+  if (bits != 4 && bits != 8) return LCB_ERR_UNSUPPORTED;
+  if (T == 0 || Smax == 0) return LCB_CACHE_FORM_EMPTY;
+  return cache_decode_form(B, H, Hkv, T, Smax, w.window, w.sinks, bits);
+}
+
 int attn_cache_decode(const void* q, const void* cache, const int* lens, void* o, float* lse, int B, int H, int Hkv,
                       int T, int Smax, int D, int bits, int window, int sinks, float scale, long long q_row_stride,
                       long long q_batch_stride, long long cache_batch_stride, long long cache_head_stride,

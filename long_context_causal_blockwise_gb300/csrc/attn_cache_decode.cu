@@ -45,10 +45,8 @@
 #include <algorithm>
 #include <cmath>
 
-#include "attn_window.cuh"
-#include "kv_cache.cuh"
-#include "lcb_internal.h"
-#include "mma_warp.cuh"
+#include "cache_line.cuh"
+#include "lcb_attn.h"
 
 namespace cg = cooperative_groups;
 
@@ -101,68 +99,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-
-// Contiguous bytes (a multiple of 16, both ends aligned to 16) into shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// Weight of a partial with maximum m in a sum with maximum M >= m (both -inf: the partial is empty, or NaN).
-__device__ __forceinline__ float weight(float m, float M) { return m == M ? 1.f : ex2_approx(m - M); }
-
-// A row tile of a (sequence, K/V head), and the keys that a row of it sees:
-// [0, ns) and [lo, hi), in units of `keys` that do not cross from one to the
-// other; every key of the units [whole0, whole1) is seen by every row.
-struct Tile {
-  int b, hk, r0;         // rows r = (token r / G, query head hk * G + r % G), r0 <= r < r0 + rows
-  int p0, p_min, p_max;  // positions of token 0, of the tile's first row and of its last
-  int lo, hi, ns, sink_units, units, whole0, whole1;
-};
-
-__device__ __forceinline__ Tile make_tile(const CacheDecode& p, int b, int hk, int mt, int rows, int keys) {
-  Tile a;
-  a.b = b;
-  a.hk = hk;
-  a.r0 = mt * rows;
-  const int len = min(max(p.lens[b], 0), p.Smax);
-  a.p0 = len - p.T;
-  a.p_min = a.p0;
-  a.p_max = len - 1;
-  if (p.row_tiles > 1) {
-    a.p_min = a.p0 + a.r0 / p.G;
-    a.p_max = a.p0 + min(p.T * p.G - 1, a.r0 + rows - 1) / p.G;
-  }
-  a.lo = max(0, a.p_min - p.window + 1);
-  a.hi = max(a.lo, a.p_max + 1);
-  a.ns = max(0, min(min(p.sinks, a.lo), a.p_max + 1));
-  a.sink_units = (a.ns + keys - 1) / keys;
-  a.units = a.sink_units + (a.hi - a.lo + keys - 1) / keys;
-  a.whole0 = a.sink_units + (max(0, a.p_max - p.window + 1 - a.lo) + keys - 1) / keys;
-  a.whole1 = a.sink_units + max(0, min(a.p_min + 1, a.hi) - a.lo) / keys;
-  return a;
-}
-
-__device__ __forceinline__ int first_key(const Tile& a, int u, int keys) {
-  return u * keys + (u < a.sink_units ? 0 : a.lo - a.sink_units * keys);
-}
-// Keys of unit u, whose first is j0.
-__device__ __forceinline__ int keys_of(const Tile& a, int u, int j0, int keys) {
-  return min(keys, (u < a.sink_units ? a.ns : a.hi) - j0);
-}
-
-// n things dealt in order to `parts`, the first n % parts of which get one more.
-struct Share {
-  int each, more;
-  __device__ Share(int n, int parts) : each(n / parts), more(n - n / parts * parts) {}
-  __device__ int begin(int i) const { return i * each + min(i, more); }  // of part i
-  __device__ int part_of(int x) const {                                  // that has thing x
-    const int cut = more * (each + 1);
-    return x < cut ? x / (each + 1) : more + (x - cut) / each;
-  }
-};
 
 // How a tile of ROWS query rows lies in the eight columns of a product, and
 // what a lane (g, t) has of them.
@@ -541,20 +477,6 @@ __device__ __forceinline__ void join_warps(Parts<ROWS, kWarps>& sm, State<ROWS, 
   }
 }
 
-// Row r of a tile, four channels a lane.
-__device__ __forceinline__ void store_row(const CacheDecode& p, const Tile& a, int r, float M, float L, float4 v,
-                                          int lane) {
-  r += a.r0;
-  if (r >= p.T * p.G) return;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int tok = p.G == 1 ? r : r / p.G, h = a.hk * p.G + r - tok * p.G;
-  uint2 x;
-  x.x = pack_bf16x2(v.x * inv, v.y * inv);
-  x.y = pack_bf16x2(v.z * inv, v.w * inv);
-  *reinterpret_cast<uint2*>(p.o + a.b * p.o_bs + static_cast<long long>(tok) * p.o_rs + h * kD + 4 * lane) = x;
-  if (lane == 0) p.lse[a.b * p.l_bs + h * p.l_hs + tok] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
-}
-
 // ------------------------------------------------------------------ a cluster for each tile
 
 // Few keys a warp: a ring of two units, 4.5 KB each, of each warp's own.
@@ -592,7 +514,8 @@ __global__ void __launch_bounds__(32 * kWarps, warps_per_sm(ROWS) / kWarps)
   }
   if (threadIdx.x == 0) sm.abort = 0;
   __syncthreads();
-  const Tile a = make_tile(p, tile / p.Hkv, tile % p.Hkv, mt, ROWS, kKeys);
+  const int b = tile / p.Hkv;
+  const Tile a = make_tile(p, length(p, p.lens[b]), b, tile % p.Hkv, mt, ROWS, kKeys);
   const Share share(a.units, p.cluster * kWarps);
   const int me = rank * kWarps + warp;
   int u = share.begin(me);
@@ -663,17 +586,11 @@ __global__ void __launch_bounds__(32 * kWarps, warps_per_sm(ROWS) / kWarps)
 
 // ------------------------------------------------------------------ the units of all tiles as one line
 //
-// A CTA to an SM, whose warps take the sixteens of a unit: one bulk copy brings
-// 16 keys for each, and the warp that is the last to have read it refills its
-// place, so that the warps stay within a ring's length of one another (with a
-// ring for each warp, or two CTAs to an SM, the scheduler lets some warps finish
-// long before the others, which then run alone).
-//
-// Tiles stand in the order (sequence, K/V head, row tile); their N units (fewer
-// than 2^31) are dealt in order to C CTAs, C at most N so that each has some.
-// What a CTA has of a tile that it does not have whole goes to slot 2 i (the
-// first tile that it meets) or 2 i + 1 (the last): ROWS x 128 sums, then the
-// rows' maxima, then their sums of weights.
+// (cache_line.cuh.) A CTA to an SM, whose warps take the sixteens of a unit: one
+// bulk copy brings 16 keys for each, and the warp that is the last to have read
+// it refills its place, so that the warps stay within a ring's length of one
+// another (with a ring for each warp, or two CTAs to an SM, the scheduler lets
+// some warps finish long before the others, which then run alone).
 
 template <int ROWS, int BITS>
 struct Line {
@@ -681,54 +598,15 @@ struct Line {
   static constexpr int kKeys = kWarps * kStep;                  // of a unit
   static constexpr int kBytes = kKeys * cache_row_bytes(BITS);
   static constexpr int kDepth = BITS == 4 ? 4 : 2;              // units of the ring
-  static constexpr int kSlot = ROWS * (kD + 2);                 // floats
   struct Smem {
     uint8_t ring[kDepth][kBytes];
     Parts<ROWS, kWarps> parts;
     uint64_t full[kDepth];
     int done[kDepth];  // warps that have read the unit in this place
     int abort;
+    int lens[kLineSequences];
   };
 };
-
-__device__ __forceinline__ int head_units(const CacheDecode& p, int b, int rows, int keys) {  // of a K/V head's row tiles
-  int n = 0;
-  for (int mt = 0; mt < p.row_tiles; ++mt) n += make_tile(p, b, 0, mt, rows, keys).units;
-  return n;
-}
-
-// The units of all sequences, and of those before `b`, by a whole warp.
-__device__ __forceinline__ int all_units(const CacheDecode& p, int b, int rows, int keys, int lane, int* before) {
-  int n = 0, m = 0;
-  for (int i = lane; i < p.B; i += 32) {
-    const int x = p.Hkv * head_units(p, i, rows, keys);
-    n += x;
-    if (i < b) m += x;
-  }
-  *before = __reduce_add_sync(0xffffffffu, m);
-  return __reduce_add_sync(0xffffffffu, n);
-}
-
-// The sequence of unit x, and the units before it.
-__device__ __forceinline__ int sequence_of(const CacheDecode& p, int x, int rows, int keys, int lane, int* before) {
-  int sum = 0;
-  for (int b0 = 0;; b0 += 32) {
-    const int mine = b0 + lane < p.B ? p.Hkv * head_units(p, b0 + lane, rows, keys) : 0;
-    int upto = mine;  // inclusive prefix
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += y;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, sum + upto > x);
-    if (past || b0 + 32 >= p.B) {
-      const int i = past ? __ffs(past) - 1 : 31;
-      *before = sum + __shfl_sync(0xffffffffu, upto - mine, i);
-      return min(b0 + i, p.B - 1);
-    }
-    sum += __shfl_sync(0xffffffffu, upto, 31);
-  }
-}
 
 __device__ __forceinline__ int add_acq_rel(int* at, int x) {
   int old;
@@ -755,32 +633,11 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
     sm.abort = 0;
     fence_mbar_init();
   }
-  int before;
-  const int N = all_units(p, 0, ROWS, kKeys, lane, &before);
-  const int C = min(N, static_cast<int>(gridDim.x));
-  if (cta >= C) return;
-  const Share share(N, C);
-  const int x0 = share.begin(cta);
-  int left = share.begin(cta + 1) - x0;
-  int b = sequence_of(p, x0, ROWS, kKeys, lane, &before);
-  const int per_head = head_units(p, b, ROWS, kKeys);
-  int hk = (x0 - before) / per_head, mt = 0;
-  int off = x0 - before - hk * per_head;  // in the tile
-  Tile a = make_tile(p, b, hk, mt, ROWS, kKeys);
-  // To the tile that has unit `off` of the present one and those behind it. None has if the lengths change meanwhile.
-  auto next_tile = [&] {
-    while (off >= a.units && left > 0) {
-      off -= a.units;
-      if (++mt == p.row_tiles) {
-        mt = 0;
-        if (++hk == p.Hkv) {
-          hk = 0;
-          if (++b == p.B) left = b = 0;
-        }
-      }
-      a = make_tile(p, b, hk, mt, ROWS, kKeys);
-    }
-  };
+  copy_lengths(p, sm.lens);
+  __syncthreads();
+  Walk<ROWS, kKeys> walk;
+  if (!walk.start(p, sm.lens, cta, static_cast<int>(gridDim.x), lane)) return;
+  const Tile& a = walk.a;
   auto fetch = [&](int u, int at) {  // by one lane
     const uint8_t* head = p.cache + a.b * p.c_bs + a.hk * p.c_hs;
     const int j0 = first_key(a, u, kKeys);
@@ -788,21 +645,19 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
     mbar_arrive_expect_tx(&sm.full[at], bytes);
     bulk_load(sm.ring[at], head + static_cast<long long>(j0) * kRec, bytes, &sm.full[at]);
   };
-  next_tile();
-  int n = max(0, min(left, a.units - off));
+  int n = walk.here();
   RawQ<ROWS> raw = load_q<ROWS>(p, a, g, t);
   if (threadIdx.x == 0)
-    for (int i = 0; i < kDepth && i < n; ++i) fetch(off + i, i);
-  __syncthreads();  // the barriers are set up
+    for (int i = 0; i < kDepth && i < n; ++i) fetch(walk.off + i, i);
   int at = 0;
   uint32_t phase = 0;
   bool ok = true;
-  float* slot = p.workspace + 2LL * cta * F::kSlot;
+  float* slot = p.workspace + 2LL * cta * slot_floats(ROWS);
   for (;;) {
     State<ROWS, BITS> w;
     begin(w, raw, p, a, g, t);
-    const int end = off + n;
-    for (int u = off; u < end; ++u) {
+    const int end = walk.off + n;
+    for (int u = walk.off; u < end; ++u) {
       ok = mbar_wait_warp(&sm.full[at], phase, &sm.abort, p.st, kWhere);
       if (!ok) break;
       const uint8_t* rec = sm.ring[at] + warp * kStep * kRec;
@@ -824,16 +679,14 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
     }
     const Tile now = a;
     const bool whole = n == a.units;
-    left -= n;
-    off += n;
-    next_tile();
+    walk.advance(p, sm.lens, n);
     __syncthreads();  // the ring is empty, or a wait ran out
     if (sm.abort) break;
-    if (left > 0) {  // the next tile's copies are on their way while this one's parts are joined
-      n = min(left, a.units - off);
+    if (walk.left > 0) {  // the next tile's copies are on their way while this one's parts are joined
+      n = walk.here();
       raw = load_q<ROWS>(p, a, g, t);
       if (threadIdx.x == 0)
-        for (int i = 0, x = at; i < kDepth && i < n; ++i, x = x + 1 == kDepth ? 0 : x + 1) fetch(off + i, x);
+        for (int i = 0, x = at; i < kDepth && i < n; ++i, x = x + 1 == kDepth ? 0 : x + 1) fetch(walk.off + i, x);
     }
     join_warps(sm.parts, w, warp, lane, [&](int r, float M, float L, float4 v) {
       if (whole) {
@@ -846,8 +699,8 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
         }
       }
     });
-    if (left <= 0) break;
-    slot = p.workspace + (2LL * cta + 1) * F::kSlot;
+    if (walk.left <= 0) break;
+    slot = p.workspace + (2LL * cta + 1) * slot_floats(ROWS);
   }
   if (!ok && threadIdx.x == 0)  // copies in flight land before the CTA ends
     for (int i = 0; i < kDepth; ++i) {
@@ -858,73 +711,6 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
       }
     }
 }
-// kSplit warps join a row of a tile that several CTAs share; rows of tiles
-// without a key get their zeros here.
-template <int ROWS, int BITS, int kSplit>
-__global__ void __launch_bounds__(256) cache_decode_join_kernel(const __grid_constant__ CacheDecode p, int ctas) {
-  constexpr int kKeys = Line<ROWS, BITS>::kKeys, kSlot = Line<ROWS, BITS>::kSlot;
-  constexpr int kRowsHere = 8 / kSplit;
-  __shared__ float4 sO[8][32];
-  __shared__ float sM[8], sL[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = static_cast<int>(blockIdx.x) % (ROWS / kRowsHere);
-  int tile = static_cast<int>(blockIdx.x) / (ROWS / kRowsHere);
-  const int mt = tile % p.row_tiles;
-  tile /= p.row_tiles;
-  const int b = tile / p.Hkv, hk = tile % p.Hkv;
-  const Tile a = make_tile(p, b, hk, mt, ROWS, kKeys);
-  int start;
-  const int N = all_units(p, b, ROWS, kKeys, lane, &start);
-  start += hk * head_units(p, b, ROWS, kKeys);
-  for (int i = 0; i < mt; ++i) start += make_tile(p, b, hk, i, ROWS, kKeys).units;
-  const int r = sub * kRowsHere + warp / kSplit, part = warp % kSplit;
-  const Share share(max(N, 1), max(1, min(N, ctas)));
-  const int i0 = share.part_of(start), i1 = share.part_of(start + max(a.units, 1) - 1);
-  const bool at_start = share.begin(i0) == start;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (a.units == 0) {
-    if (part == 0) store_row(p, a, r, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f), lane);
-    return;
-  }
-  if (i0 == i1) return;  // stored by the one CTA that has it
-  float M = -INFINITY, L = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = i0 + part; i <= i1; i += kSplit) {
-    const float* slot = p.workspace + (2LL * i + (i > i0 || at_start ? 0 : 1)) * kSlot;
-    const float4 x = *reinterpret_cast<const float4*>(slot + r * kD + 4 * lane);
-    const float m = slot[ROWS * kD + r], l = slot[ROWS * (kD + 1) + r];
-    const float top = fmaxf(M, m), f = weight(M, top), g = weight(m, top);
-    M = top;
-    L = f * L + g * l;
-    v = make_float4(f * v.x + g * x.x, f * v.y + g * x.y, f * v.z + g * x.z, f * v.w + g * x.w);
-  }
-  if (kSplit > 1) {
-    sO[warp][lane] = v;
-    if (lane == 0) {
-      sM[warp] = M;
-      sL[warp] = L;
-    }
-    __syncthreads();
-    if (part != 0) return;
-    float top = M;
-#pragma unroll
-    for (int i = 1; i < kSplit; ++i) top = fmaxf(top, sM[warp + i]);
-    const float f = weight(M, top);
-    M = top;
-    L *= f;
-    v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
-#pragma unroll
-    for (int i = 1; i < kSplit; ++i) {
-      const float4 x = sO[warp + i][lane];
-      const float g = weight(sM[warp + i], top);
-      L += g * sL[warp + i];
-      v = make_float4(v.x + g * x.x, v.y + g * x.y, v.z + g * x.z, v.w + g * x.w);
-    }
-  }
-  store_row(p, a, r, M, L, v, lane);
-}
-
 // ------------------------------------------------------------------ launches
 
 template <int ROWS, int BITS, int kWarps>
@@ -982,39 +768,26 @@ struct LineForm {
     return resident_clusters(known, at, allowed(), fn(), kThreads, kSmem, 1);
   }
 
-  static size_t workspace(int n) { return 2 * sizeof(float) * Line<ROWS, BITS>::kSlot * static_cast<size_t>(n); }
+  static size_t workspace(int n) { return 2 * sizeof(float) * slot_floats(ROWS) * static_cast<size_t>(n); }
 
   static int launch(const CacheDecode& p, long long tiles, int n, cudaStream_t stream) {
     const int rc = allow_clusters_once(allowed(), fn(), kSmem);
     if (rc != 0) return rc;
     cache_decode_line_kernel<ROWS, BITS><<<n, kThreads, kSmem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return -4;
-    // A warp or two a row where a tile has few parts, eight where it has many.
-    constexpr int kNarrow = ROWS == 4 ? 2 : 1;
-    const bool wide = n > 8 * tiles;
-    cudaLaunchAttribute at;  // it starts beside the end of the kernel before it
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * (wide ? ROWS : ROWS * kNarrow / 8)));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, BITS, 8>, p, n)
-                               : cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, BITS, kNarrow>, p, n);
-    return e == cudaSuccess ? 0 : -4;
+    return launch_cache_join<ROWS, Line<ROWS, BITS>::kKeys>(p, tiles, n, stream);
   }
 };
 
 // Sizes of a call as its launch sees them: the host knows no lengths.
 struct Plan {
-  int rows;
+  int B, rows;
   long long row_tiles, tiles, keys;  // keys: the most that a tile can see
 };
 
 Plan plan_of(int B, int H, int Hkv, int T, int Smax, int window, int sinks) {
   Plan a;
+  a.B = B;
   const long long R = static_cast<long long>(T) * (H / Hkv);
   a.rows = R <= 4 ? 4 : R <= 8 ? 8 : 16;
   a.row_tiles = (R + a.rows - 1) / a.rows;
@@ -1051,11 +824,11 @@ template <int ROWS, int BITS>
 int line_ctas(const Plan& a, const ClusterChoice<ROWS, BITS>& c, const ContextKey& at) {
   const int n = LineForm<ROWS, BITS>::ctas(at);
   const long long units = a.tiles * ((a.keys + Line<ROWS, BITS>::kKeys - 1) / Line<ROWS, BITS>::kKeys + 1);
-  if (n <= 0 || a.row_tiles > 8 || units >= 1LL << 31) return 0;
+  if (n <= 0 || a.B > kLineSequences || a.row_tiles > 8 || units >= 1LL << 31) return 0;
   const double hbm_us = static_cast<double>(a.tiles) * a.keys * cache_row_bytes(BITS) / 6.7e6;
   const double busy = static_cast<double>(c.in_flight) / (kSms * warps_per_sm(ROWS));
   const double cluster_us = 5 + 1.15 * hbm_us / std::min(1.0, (BITS == 4 ? 1.0 : 1.5) * busy);
-  const double line_us = 9.5 + 1.08 * hbm_us + 3.5 * std::max(0.0, static_cast<double>(a.tiles) / n - 1);
+  const double line_us = 12 + 1.08 * hbm_us + 3.5 * std::max(0.0, static_cast<double>(a.tiles) / n - 1);
   return line_us < cluster_us ? n : 0;
 }
 
@@ -1107,9 +880,34 @@ struct Launch {
 
 }  // namespace
 
+// CTAs of the form with 128-row tiles (attn_cache_tiles.cu), or 0 for one of the
+// forms here, which unpack the keys once for every sixteen rows: two estimates in
+// us. us, those here / 128-row tiles: 8 heads x 65536 keys, 32 rows 65 / 50, 64 rows
+// 109 / 51, in 8 bits 139 / 63; 32 x 20000, 128 rows 208 / 58; 8 x 65536, window 16384,
+// 4000 rows 1222 / 431; 8 x 2000, 56 rows 13 / 17; 8 x 500, 20 rows 9 / 14.
+static int tiles_ctas(const Plan& a, int T, int G, int bits, const ContextKey& at) {
+  const long long R = static_cast<long long>(T) * G;
+  if (R <= 16 || a.B > kLineSequences) return 0;
+  const long long units = a.tiles / a.row_tiles * ((R + 127) / 128) * (a.keys / 128 + 2);
+  if (units >= 1LL << 31) return 0;
+  const int n = cache_tiles_ctas(bits, at);
+  if (n <= 0) return 0;
+  const double tiles_us = 13 + (bits == 4 ? 1.5 : 1.9) * static_cast<double>(units) / n;
+  const double here_us = 9 + 0.75e-3 * static_cast<double>(a.tiles) * ((a.keys + 15) / 16);
+  return tiles_us < here_us ? n : 0;
+}
+
 size_t cache_decode_workspace(int B, int H, int Hkv, int T, int Smax, int window, int sinks, int bits) {
   const Plan a = plan_of(B, H, Hkv, T, Smax, window, sinks);
+  const int n = tiles_ctas(a, T, H / Hkv, bits, current_context());
+  if (n > 0) return cache_tiles_workspace(n);
   return with_form(a.rows, bits, WorkspaceOf{a});
+}
+
+int cache_decode_form(int B, int H, int Hkv, int T, int Smax, int window, int sinks, int bits) {
+  const Plan a = plan_of(B, H, Hkv, T, Smax, window, sinks);
+  if (tiles_ctas(a, T, H / Hkv, bits, current_context()) > 0) return LCB_CACHE_FORM_TILES;
+  return cache_decode_workspace(B, H, Hkv, T, Smax, window, sinks, bits) ? LCB_CACHE_FORM_LINE : LCB_CACHE_FORM_CLUSTER;
 }
 
 int launch_cache_decode(CacheDecode p, int bits, size_t ws_bytes, cudaStream_t stream) {
@@ -1117,6 +915,9 @@ int launch_cache_decode(CacheDecode p, int bits, size_t ws_bytes, cudaStream_t s
   if (static_cast<long long>(p.T) * p.G > kWindowMaxRows) return -1;
   const Plan a = plan_of(p.B, p.H, p.Hkv, p.T, p.Smax, p.window, p.sinks);
   if (a.tiles > 0x7fffffffLL / kMaxCluster) return -1;
+  const int n = tiles_ctas(a, p.T, p.G, bits, current_context());
+  if (n > 0)
+    return p.workspace && ws_bytes >= cache_tiles_workspace(n) ? launch_cache_tiles(p, bits, n, stream) : -1;
   p.row_tiles = static_cast<int>(a.row_tiles);
   p.cluster = 1;
   return with_form(a.rows, bits, Launch{p, a, ws_bytes, stream});

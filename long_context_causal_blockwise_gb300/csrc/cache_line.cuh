@@ -1,0 +1,291 @@
+// Attention over the quantised cache (attn_cache_decode.cu, attn_cache_tiles.cu):
+// the keys that a tile of query rows sees, and their deal over the GPU.
+#pragma once
+
+#include "attn_window.cuh"
+#include "kv_cache.cuh"
+#include "lcb_internal.h"
+#include "mma_warp.cuh"
+
+namespace lcb {
+
+constexpr int kCacheD = 128;
+constexpr int kLineSequences = 1024;  // whose lengths a CTA keeps in shared memory
+
+// Contiguous bytes (a multiple of 16, both ends aligned to 16) into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Weight of a partial with maximum m in a sum with maximum M >= m (both -inf: the partial is empty, or NaN).
+__device__ __forceinline__ float weight(float m, float M) { return m == M ? 1.f : ex2_approx(m - M); }
+
+// Rows of a sequence in the cache.
+__device__ __forceinline__ int length(const CacheDecode& p, int len) { return min(max(len, 0), p.Smax); }
+
+// A row tile of a (sequence, K/V head), and the keys that a row of it sees:
+// [0, ns) and [lo, hi), in units of `keys` that do not cross from one to the
+// other; every key of the units [whole0, whole1) is seen by every row.
+struct Tile {
+  int b, hk, r0;         // rows r = (token r / G, query head hk * G + r % G), r0 <= r < r0 + rows
+  int p0, p_min, p_max;  // positions of token 0, of the tile's first row and of its last
+  int lo, hi, ns, sink_units, units, whole0, whole1;
+};
+
+__device__ __forceinline__ Tile make_tile(const CacheDecode& p, int len, int b, int hk, int mt, int rows,
+                                          int keys) {
+  Tile a;
+  a.b = b;
+  a.hk = hk;
+  a.r0 = mt * rows;
+  a.p0 = len - p.T;
+  a.p_min = a.p0;
+  a.p_max = len - 1;
+  if (p.row_tiles > 1) {
+    a.p_min = a.p0 + a.r0 / p.G;
+    a.p_max = a.p0 + min(p.T * p.G - 1, a.r0 + rows - 1) / p.G;
+  }
+  a.lo = max(0, a.p_min - p.window + 1);
+  a.hi = max(a.lo, a.p_max + 1);
+  a.ns = max(0, min(min(p.sinks, a.lo), a.p_max + 1));
+  a.sink_units = (a.ns + keys - 1) / keys;
+  a.units = a.sink_units + (a.hi - a.lo + keys - 1) / keys;
+  a.whole0 = a.sink_units + (max(0, a.p_max - p.window + 1 - a.lo) + keys - 1) / keys;
+  a.whole1 = a.sink_units + max(0, min(a.p_min + 1, a.hi) - a.lo) / keys;
+  return a;
+}
+
+__device__ __forceinline__ int first_key(const Tile& a, int u, int keys) {
+  return u * keys + (u < a.sink_units ? 0 : a.lo - a.sink_units * keys);
+}
+// Keys of unit u, whose first is j0.
+__device__ __forceinline__ int keys_of(const Tile& a, int u, int j0, int keys) {
+  return min(keys, (u < a.sink_units ? a.ns : a.hi) - j0);
+}
+
+// n things dealt in order to `parts`, the first n % parts of which get one more.
+struct Share {
+  int each, more;
+  __device__ Share(int n, int parts) : each(n / parts), more(n - n / parts * parts) {}
+  __device__ int begin(int i) const { return i * each + min(i, more); }  // of part i
+  __device__ int part_of(int x) const {                                  // that has thing x
+    const int cut = more * (each + 1);
+    return x < cut ? x / (each + 1) : more + (x - cut) / each;
+  }
+};
+
+// Row r of a tile, four channels a lane.
+__device__ __forceinline__ void store_row(const CacheDecode& p, const Tile& a, int r, float M, float L, float4 v,
+                                          int lane) {
+  r += a.r0;
+  if (r >= p.T * p.G) return;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int tok = p.G == 1 ? r : r / p.G, h = a.hk * p.G + r - tok * p.G;
+  uint2 x;
+  x.x = pack_bf16x2(v.x * inv, v.y * inv);
+  x.y = pack_bf16x2(v.z * inv, v.w * inv);
+  *reinterpret_cast<uint2*>(p.o + a.b * p.o_bs + static_cast<long long>(tok) * p.o_rs + h * kCacheD + 4 * lane) = x;
+  if (lane == 0) p.lse[a.b * p.l_bs + h * p.l_hs + tok] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ the units of all tiles as one line
+//
+// Tiles stand in the order (sequence, K/V head, row tile); their N units (fewer
+// than 2^31) are dealt in order to C CTAs, C at most N so that each has some.
+// What a CTA has of a tile that it does not have whole goes to slot 2 i (the
+// first tile that it meets) or 2 i + 1 (the last): ROWS x 128 sums, then the
+// rows' maxima, then their sums of weights.
+
+constexpr int slot_floats(int rows) { return rows * (kCacheD + 2); }
+
+__device__ __forceinline__ int head_units(const CacheDecode& p, int len, int rows, int keys) {  // of a K/V head's row tiles
+  int n = 0;
+  for (int mt = 0; mt < p.row_tiles; ++mt) n += make_tile(p, len, 0, 0, mt, rows, keys).units;
+  return n;
+}
+
+// The units of all sequences, and of those before `b`, by a whole warp.
+__device__ __forceinline__ int all_units(const CacheDecode& p, const int* lens, int b, int rows, int keys, int lane,
+                                         int* before) {
+  int n = 0, m = 0;
+  for (int i = lane; i < p.B; i += 32) {
+    const int x = p.Hkv * head_units(p, lens[i], rows, keys);
+    n += x;
+    if (i < b) m += x;
+  }
+  *before = __reduce_add_sync(0xffffffffu, m);
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// The sequence of unit x, and the units before it.
+__device__ __forceinline__ int sequence_of(const CacheDecode& p, const int* lens, int x, int rows, int keys, int lane,
+                                           int* before) {
+  int sum = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int mine = b0 + lane < p.B ? p.Hkv * head_units(p, lens[b0 + lane], rows, keys) : 0;
+    int upto = mine;  // inclusive prefix
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, sum + upto > x);
+    if (past || b0 + 32 >= p.B) {
+      const int i = past ? __ffs(past) - 1 : 31;
+      *before = sum + __shfl_sync(0xffffffffu, upto - mine, i);
+      return min(b0 + i, p.B - 1);
+    }
+    sum += __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+
+// A CTA's way along the line. The lengths are a copy that the CTA made (one for
+// all its warps, which otherwise might disagree about it if somebody changes
+// them meanwhile, and wait for one another for ever).
+template <int ROWS, int KEYS>
+struct Walk {
+  Tile a;
+  int off, left;  // the CTA's next unit in the tile; units that it still has
+  int b, hk, mt;
+
+  // False for a CTA without units.
+  __device__ __forceinline__ bool start(const CacheDecode& p, const int* lens, int cta, int ctas, int lane) {
+    int before;
+    const int N = all_units(p, lens, 0, ROWS, KEYS, lane, &before);
+    const int C = min(N, ctas);
+    if (cta >= C) return false;
+    const Share share(N, C);
+    const int x0 = share.begin(cta);
+    left = share.begin(cta + 1) - x0;
+    b = sequence_of(p, lens, x0, ROWS, KEYS, lane, &before);
+    const int per_head = head_units(p, lens[b], ROWS, KEYS);
+    hk = (x0 - before) / per_head;
+    mt = 0;
+    off = x0 - before - hk * per_head;
+    a = make_tile(p, lens[b], b, hk, mt, ROWS, KEYS);
+    settle(p, lens);
+    return true;
+  }
+  // Units of the present tile that are the CTA's.
+  __device__ __forceinline__ int here() const { return min(left, a.units - off); }
+  __device__ __forceinline__ void advance(const CacheDecode& p, const int* lens, int n) {
+    left -= n;
+    off += n;
+    settle(p, lens);
+  }
+  __device__ __forceinline__ void settle(const CacheDecode& p, const int* lens) {
+    while (off >= a.units && left > 0) {
+      off -= a.units;
+      if (++mt == p.row_tiles) {
+        mt = 0;
+        if (++hk == p.Hkv) {
+          hk = 0;
+          if (++b == p.B) left = b = 0;
+        }
+      }
+      a = make_tile(p, lens[b], b, hk, mt, ROWS, KEYS);
+    }
+  }
+};
+
+// A CTA's copy of the lengths.
+__device__ __forceinline__ void copy_lengths(const CacheDecode& p, int* lens) {
+  for (int i = threadIdx.x; i < p.B; i += blockDim.x) lens[i] = length(p, p.lens[i]);
+}
+
+// kSplit warps join a row of a tile that several CTAs share; rows of tiles
+// without a key get their zeros here.
+template <int ROWS, int KEYS, int kSplit>
+__global__ void __launch_bounds__(256) cache_decode_join_kernel(const __grid_constant__ CacheDecode p, int ctas) {
+  constexpr int kSlot = slot_floats(ROWS);
+  constexpr int kRowsHere = 8 / kSplit;
+  __shared__ float4 sO[8][32];
+  __shared__ float sM[8], sL[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = static_cast<int>(blockIdx.x) % (ROWS / kRowsHere);
+  int tile = static_cast<int>(blockIdx.x) / (ROWS / kRowsHere);
+  const int mt = tile % p.row_tiles;
+  tile /= p.row_tiles;
+  const int b = tile / p.Hkv, hk = tile % p.Hkv;
+  const int len = length(p, p.lens[b]);
+  const Tile a = make_tile(p, len, b, hk, mt, ROWS, KEYS);
+  int start;
+  const int N = all_units(p, p.lens, b, ROWS, KEYS, lane, &start);
+  start += hk * head_units(p, len, ROWS, KEYS);
+  for (int i = 0; i < mt; ++i) start += make_tile(p, len, b, hk, i, ROWS, KEYS).units;
+  const int r = sub * kRowsHere + warp / kSplit, part = warp % kSplit;
+  const Share share(max(N, 1), max(1, min(N, ctas)));
+  const int i0 = share.part_of(start), i1 = share.part_of(start + max(a.units, 1) - 1);
+  const bool at_start = share.begin(i0) == start;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.r0 + r >= p.T * p.G) {  // the last tile has fewer rows
+    if (kSplit > 1 && kRowsHere > 1) __syncthreads();
+    return;
+  }
+  if (a.units == 0) {
+    if (part == 0) store_row(p, a, r, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f), lane);
+    return;
+  }
+  if (i0 == i1) return;  // stored by the one CTA that has it
+  float M = -INFINITY, L = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = i0 + part; i <= i1; i += kSplit) {
+    const float* slot = p.workspace + (2LL * i + (i > i0 || at_start ? 0 : 1)) * kSlot;
+    const float4 y = *reinterpret_cast<const float4*>(slot + r * kCacheD + 4 * lane);
+    const float m = slot[ROWS * kCacheD + r], l = slot[ROWS * (kCacheD + 1) + r];
+    const float top = fmaxf(M, m), f = weight(M, top), g = weight(m, top);
+    M = top;
+    L = f * L + g * l;
+    v = make_float4(f * v.x + g * y.x, f * v.y + g * y.y, f * v.z + g * y.z, f * v.w + g * y.w);
+  }
+  if (kSplit > 1) {
+    sO[warp][lane] = v;
+    if (lane == 0) {
+      sM[warp] = M;
+      sL[warp] = L;
+    }
+    __syncthreads();
+    if (part != 0) return;
+    float top = M;
+#pragma unroll
+    for (int i = 1; i < kSplit; ++i) top = fmaxf(top, sM[warp + i]);
+    const float f = weight(M, top);
+    M = top;
+    L *= f;
+    v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
+#pragma unroll
+    for (int i = 1; i < kSplit; ++i) {
+      const float4 x = sO[warp + i][lane];
+      const float g = weight(sM[warp + i], top);
+      L += g * sL[warp + i];
+      v = make_float4(v.x + g * x.x, v.y + g * x.y, v.z + g * x.z, v.w + g * x.w);
+    }
+  }
+  store_row(p, a, r, M, L, v, lane);
+}
+
+// The join after a line kernel of n CTAs, which may start beside its end.
+template <int ROWS, int KEYS>
+int launch_cache_join(const CacheDecode& p, long long tiles, int n, cudaStream_t stream) {
+  // A warp or two a row where a tile has few parts, eight where it has many.
+  constexpr int kNarrow = ROWS == 4 ? 2 : 1;
+  const bool wide = n > 8 * tiles;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * (wide ? ROWS : ROWS * kNarrow / 8)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, KEYS, 8>, p, n)
+                             : cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, KEYS, kNarrow>, p, n);
+  return e == cudaSuccess ? 0 : -4;
+}
+
+}  // namespace lcb

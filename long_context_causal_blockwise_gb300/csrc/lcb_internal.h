@@ -243,7 +243,13 @@ struct CacheDecode {
   int G, row_tiles, cluster;  // set by the launch
   DevStatus st;
 };
+// Its form for more than sixteen query rows a K/V head: CTAs that the GPU holds at once (0: none), the workspace that so
+// many need, and the launch.
+int cache_tiles_ctas(int bits, const ContextKey& at);
+size_t cache_tiles_workspace(int ctas);
+int launch_cache_tiles(CacheDecode p, int bits, int ctas, cudaStream_t stream);
 size_t cache_decode_workspace(int B, int H, int Hkv, int T, int Smax, int window, int sinks, int bits);
+int cache_decode_form(int B, int H, int Hkv, int T, int Smax, int window, int sinks, int bits);  // LCB_CACHE_FORM_*
 int launch_cache_decode(CacheDecode p, int bits, size_t ws_bytes, cudaStream_t stream);
 
 }  // namespace lcb

@@ -3,7 +3,16 @@ equals the fp64 oracle's values to the bit; attention over it is checked
 element by element against the fp64 oracle on the held values, within the
 bounds of window_bounds.py: the kernel's products take the held whole numbers
 exactly, its scores are fp32 sums of 128 terms, and it rounds the weights
-(times V's scale) and O to bf16, as the other windowed kernels do."""
+(times V's scale) and O to bf16, as the other windowed kernels do.
+
+The form for many query rows ("tiles") also rounds what it multiplies:
+  V to bf16, by U |v| at most: U (P |V|) more in O, whose bound so becomes
+    U |O| + (2 U + E) (P |V|);
+  K in 8 bits, of which the magnitude's lower 4 bits times the scale go to fp16:
+    by 2^-12 * 15 s <= 2^-12 * 15 / 127 * (the group's largest |k|) (1 + 2^-8) a
+    value, so a score by scale * sum_G (sum |q|) top_G 2^-12 * 15 / 127 (1 + 2^-8),
+    which is added to E twice, as the score's other error is.
+"""
 
 import numpy as np
 import pytest
@@ -50,12 +59,43 @@ def _filled(seed, B, Hkv, Smax, bits, scale=1.0):
     return cache, _held(k, bits), _held(v, bits)
 
 
+def _check_tiles(q, kd, vd, window, sinks, pos0, o, lse, bits, name):
+    """window_bounds.check_attn's comparison with the roundings of the form for many rows; one sequence."""
+    r = oracle.window_attn(q, kd, vd, window, sinks, pos0, SCALE)
+    G = q.shape[2] // kd.shape[2]
+    assert np.isfinite(o).all(), name
+    seen = np.isfinite(r["lse"])
+    assert np.array_equal(np.isfinite(lse), seen) and (lse[~seen] == -np.inf).all(), name
+    for h in range(q.shape[2]):
+        kh, vh, qh = np.abs(kd[0, :, h // G]), np.abs(vd[0, :, h // G]), np.abs(q[0, :, h])
+        p = r["p"][0, h]
+        err = 2 * 128 * 2.0 ** -24 * SCALE * (qh @ kh.T)
+        if bits == 8:
+            top = kh.reshape(-1, 4, 32).max(axis=2)
+            err = err + SCALE * (qh.reshape(-1, 4, 32).sum(axis=2) @ top.T) * 2.0 ** -12 * 15 / 127 * (1 + 2.0 ** -8)
+        E = (err * (p > 0)).max(axis=1, initial=0.0)[:, None] * 2 + 2.0 ** -20
+        rows = seen[0, h]
+        ltol = E[rows, 0] + 2.0 ** -21 * (1 + np.abs(r["lse"][0, h][rows]))
+        assert (np.abs(lse[0, h][rows] - r["lse"][0, h][rows]) <= ltol).all(), f"{name} LSE"
+        want = r["o"][0, :, h]
+        bound = 2.0 ** -8 * np.abs(want) + (2 * 2.0 ** -8 + E) * (p @ vh) + 1e-30
+        ratio = np.abs(o[0, :, h] - want) / bound
+        assert (ratio <= 1).all(), f"{name} O: off by {ratio.max():.2f} bounds"
+
+
 def _check(q, cache, kd, vd, lens, window, sinks, name="", **kw):
     o, lse = lcb.attn_cache_decode(q, cache, _lens(*lens), window, sinks, **kw)
     torch.cuda.synchronize()
     W = 1 << 30 if window is None else window
+    B, T, H, _ = q.shape
+    bits = 4 if cache.shape[3] == 144 else 8
+    form = lcb.attn_cache_decode_form(B, H, cache.shape[1], T, cache.shape[2], bits, window, sinks)
     for b, n in enumerate(lens):
         n = min(max(n, 0), kd.shape[1])
+        if form == "tiles":
+            _check_tiles(to64(q[b:b + 1]), kd[b:b + 1, :n], vd[b:b + 1, :n], W, sinks, n - T, to64(o[b:b + 1]),
+                         to64(lse[b:b + 1]), bits, f"{name} sequence {b}")
+            continue
         check_attn(to64(q[b:b + 1]), kd[b:b + 1, :n], vd[b:b + 1, :n], W, sinks, n - q.shape[1], SCALE,
                    to64(o[b:b + 1]), to64(lse[b:b + 1]), name=f"{name} sequence {b}")
     return o, lse
@@ -200,6 +240,46 @@ def test_attention_vs_oracle(bits, B, H, Hkv, T, Smax, lens, window, sinks):
     q, = _rand(H, (B, T, H, D))
     _check(q, cache, kd, vd, lens, window, sinks)
     _check(4 * q, cache, kd, vd, lens, window, sinks, "sharp")
+
+
+# Sizes that take each form on a GB300: B, H, Hkv, T, Smax, lens, window, sinks
+FORMS = [
+    ("cluster", 1, 32, 32, 1, 777, (777,), None, 0),
+    ("cluster", 3, 12, 4, 5, 700, (700, 650, 3), 333, 40),      # 15 rows
+    ("line", 1, 1, 1, 1, 60000, (59999,), None, 0),             # one head: 152 CTAs share it
+    ("line", 2, 8, 2, 1, 30000, (30000, 1), None, 0),
+    ("line", 2, 12, 2, 1, 30011, (30011, 17000), 29000, 300),   # six rows; sinks over several units
+    ("line", 1, 16, 1, 1, 80000, (80000,), None, 0),            # sixteen rows
+    ("line", 3, 4, 1, 2, 30000, (12345, 0, 30000), None, 0),    # eight rows; a sequence without keys
+    ("line", 5, 2, 1, 2, 30000, (30000, 100, 7, 9000, 1), 25000, 3),
+    ("tiles", 1, 8, 2, 32, 12000, (11999,), None, 0),           # 128 rows
+    ("tiles", 2, 8, 1, 9, 20000, (20000, 1501), None, 0),       # 72
+    ("tiles", 2, 4, 2, 200, 3000, (3000, 150), 2000, 129),      # four row tiles, tokens before the first row
+    ("tiles", 3, 3, 3, 130, 3500, (3500, 0, 129), None, 5),     # two, the second with two rows; a sequence without keys
+    ("tiles", 1, 24, 1, 2, 150000, (149999,), None, 0),         # 48 rows, many keys
+]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("form,B,H,Hkv,T,Smax,lens,window,sinks", FORMS)
+def test_each_form_vs_oracle(form, bits, B, H, Hkv, T, Smax, lens, window, sinks):
+    assert lcb.attn_cache_decode_form(B, H, Hkv, T, Smax, bits, window, sinks) == form
+    cache, kd, vd = _filled(Smax + T, B, Hkv, Smax, bits)
+    q, = _rand(H, (B, T, H, D))
+    a = _check(q, cache, kd, vd, lens, window, sinks)
+    for _ in range(3):
+        b = lcb.attn_cache_decode(q, cache, _lens(*lens), window, sinks)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    _check(6 * q, cache, kd, vd, lens, window, sinks, "sharp")
+    # a given workspace, of any contents
+    n = lcb.attn_cache_decode_workspace_bytes(B, H, Hkv, T, Smax, bits, window, sinks)
+    assert (n > 0) == (form != "cluster")
+    ws = torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    b = lcb.attn_cache_decode(q, cache, _lens(*lens), window, sinks, workspace=ws)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    if n:
+        with pytest.raises(lcb.AttnError):
+            lcb.attn_cache_decode(q, cache, _lens(*lens), window, sinks, workspace=ws[:n - 16])
 
 
 @pytest.mark.parametrize("bits", [4, 8])
