@@ -587,10 +587,14 @@ __global__ void __launch_bounds__(32 * kWarps, warps_per_sm(ROWS) / kWarps)
 // ------------------------------------------------------------------ the units of all tiles as one line
 //
 // (cache_line.cuh.) A CTA to an SM, whose warps take the sixteens of a unit: one
-// bulk copy brings 16 keys for each, and the warp that is the last to have read
-// it refills its place, so that the warps stay within a ring's length of one
-// another (with a ring for each warp, or two CTAs to an SM, the scheduler lets
-// some warps finish long before the others, which then run alone).
+// bulk copy brings 16 keys for each, and its place is refilled once all have read
+// it, so that the warps stay within a ring's length of one another (with a ring
+// for each warp, or two CTAs to an SM, the scheduler lets some warps finish long
+// before the others, which then run alone). Who refills: with a ring of four or
+// more, a warp in turn, a unit later, by when the others mostly have read theirs
+// too; with two there is no time to lose, and the last one to have read does it,
+// as a counter tells (us, in turn / the last: 8 heads x 524288 keys in 4 bits 105 /
+// 110; 8 x 131072 in 8 bits 66 / 51).
 
 template <int ROWS, int BITS>
 struct Line {
@@ -598,10 +602,11 @@ struct Line {
   static constexpr int kKeys = kWarps * kStep;                  // of a unit
   static constexpr int kBytes = kKeys * cache_row_bytes(BITS);
   static constexpr int kDepth = BITS == 4 ? 4 : 2;              // units of the ring
+  static constexpr bool kInTurn = kDepth > 2;
   struct Smem {
     uint8_t ring[kDepth][kBytes];
     Parts<ROWS, kWarps> parts;
-    uint64_t full[kDepth];
+    uint64_t full[kDepth], empty[kDepth];
     int done[kDepth];  // warps that have read the unit in this place
     int abort;
     int lens[kLineSequences];
@@ -628,6 +633,7 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDepth; ++i) {
       mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kWarps);
       sm.done[i] = 0;
     }
     sm.abort = 0;
@@ -668,7 +674,15 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
         if (nk > 0) step<ROWS, BITS, true>(w, p, rec, j0 + warp * kStep, nk, g, t);
       }
       __syncwarp();
-      if (lane == 0 && add_acq_rel(&sm.done[at], 1) == kWarps - 1) {  // every warp has read the unit
+      if (F::kInTurn) {
+        if (lane == 0) {
+          mbar_arrive(&sm.empty[at]);
+          const int x = u - 1 + kDepth, back = at == 0 ? kDepth - 1 : at - 1;  // in the place of the unit before this one
+          if (u > walk.off && x < end && x % kWarps == warp &&
+              mbar_wait_inline(&sm.empty[back], phase ^ static_cast<uint32_t>(at == 0), &sm.abort, p.st, kWhere + 0x10000u))
+            fetch(x, back);
+        }
+      } else if (lane == 0 && add_acq_rel(&sm.done[at], 1) == kWarps - 1) {
         sm.done[at] = 0;
         if (u + kDepth < end) fetch(u + kDepth, at);
       }
@@ -816,9 +830,9 @@ struct ClusterChoice {
 // most keys that the sizes allow, fitted to both forms at fourteen sizes. A
 // cluster form is done when its warps' share of the bytes is; the line form has a
 // longer start, a second kernel, and some 3 us for each tile that a CTA begins
-// after its first. us, cluster / line, 4 bits unless said: 32 heads x 777 keys 6 /
-// 8, x 2052 8 / 12; 8 x 8 heads x 20001, eight rows, 37 / 42; 160 x 32772 127 / 122;
-// 8 x 131072 in 8 bits 69 / 51; 8 x 524288 204 / 106; 1 x 524288 123 / 25; 4 x
+// after its first; with more than four rows it is bound by its instructions. us, cluster / line, 4 bits unless said: 32 heads x 777 keys 6 /
+// 8, x 2052 8 / 12; 8 x 8 heads x 20001, eight rows, 37 / 42; 160 x 32772 127 / 120;
+// 8 x 131072 in 8 bits 69 / 51; 8 x 524288 204 / 105; 1 x 524288 123 / 25; 4 x
 // 100000 33 / 26; 512 x 2000 25 / 39; 80 x 5000 in 8 bits 20 / 24; 40 x 32768 39 / 42.
 template <int ROWS, int BITS>
 int line_ctas(const Plan& a, const ClusterChoice<ROWS, BITS>& c, const ContextKey& at) {
@@ -828,7 +842,7 @@ int line_ctas(const Plan& a, const ClusterChoice<ROWS, BITS>& c, const ContextKe
   const double hbm_us = static_cast<double>(a.tiles) * a.keys * cache_row_bytes(BITS) / 6.7e6;
   const double busy = static_cast<double>(c.in_flight) / (kSms * warps_per_sm(ROWS));
   const double cluster_us = 5 + 1.15 * hbm_us / std::min(1.0, (BITS == 4 ? 1.0 : 1.5) * busy);
-  const double line_us = 12 + 1.08 * hbm_us + 3.5 * std::max(0.0, static_cast<double>(a.tiles) / n - 1);
+  const double line_us = 12 + (BITS == 4 && ROWS > 4 ? 1.25 : 1.08) * hbm_us + 3.5 * std::max(0.0, static_cast<double>(a.tiles) / n - 1);
   return line_us < cluster_us ? n : 0;
 }
 
