@@ -28,16 +28,35 @@ constexpr int kRows = 8;  // rows of a warp
 
 // A group whose largest magnitude is below this is held as zeros: the scales
 // of the others, and their reciprocals, are then normal numbers.
-constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100
+constexpr float kTiny = 0x1p-100f;
 
-// n of a channel, from x / s by one multiplication. bf16 values and scales
+// |n| of a channel, from |x| / s by one multiplication. bf16 values and scales
 // have 8 significant bits, so x / s is a tie (a whole number and a half) or away
 // from one by more than 2^-11 of itself; a reciprocal that is larger by 2^-20
-// moves ties past the half, and nothing else across one. Adding 1.5 * 2^23
-// leaves the rounded number in the low bits.
-// As sign (bit 7) and magnitude.
-__device__ __forceinline__ uint32_t quant_code(float x, float inv) {
-  return (__float_as_uint(fmaf(fabsf(x), inv, 12582912.f)) & 0x7fu) | (__float_as_uint(x) >> 24 & 0x80u);
+// moves ties past the half, and nothing else across one, its own error included.
+// Adding 1.5 * 2^23 leaves the rounded number in the low bits of the result.
+__device__ __forceinline__ uint32_t magnitude(float x, float inv) {
+  return __float_as_uint(fmaf(fabsf(x), inv, 12582912.f));
+}
+constexpr uint32_t kMagic = 0x4b400000u;  // the bits around it
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Four codes in 16 bits (kv_cache.cuh): magnitudes m0 .. m3 with kMagic around them; the signs are those of bytes a1, b1
+// (fields 0, 2) and, by `sel`, of c and d (fields 1, 3).
+__device__ __forceinline__ uint32_t pack_fields(uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3, uint32_t a, uint32_t b,
+                                                uint32_t sel_ab, uint32_t c, uint32_t d, uint32_t sel_cd) {
+  const uint32_t even = permute_bytes(b, a, sel_ab) & 0x8080u, odd = permute_bytes(d, c, sel_cd) & 0x8080u;
+  return (m0 + 8u * m1 + 256u * m2 + 2048u * m3) & 0x3f3fu | even | odd >> 1;
 }
 
 template <int BITS>
@@ -64,58 +83,62 @@ __global__ void __launch_bounds__(32 * kWarps) kv_cache_write_kernel(const __gri
   for (int r = 0; r < kRows; ++r)
     if (r >= lo && r < hi) x[r] = __ldcs(reinterpret_cast<const uint4*>(src + r * p.row_stride));
   uint8_t* rec0 = recs[warp];
+  // where in a record the lane's scale and its two pieces of codes go: K's side by side, V's those of two lanes' operands
+  const int t = j & 3;
+  const int scale_at = cache_scale_offset(BITS) + 2 * ((is_v ? 4 : 0) + G);
+  const int code_at = BITS == 4 ? (is_v ? 64 + 16 * t + 2 * G : 16 * t + 4 * G)
+                                : (is_v ? 128 + 32 * t + 4 * G : 64 * (G >> 1) + 16 * t + 8 * (G & 1));
+  const int code_step = BITS == 4 ? (is_v ? 8 : 2) : (is_v ? 16 : 4);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     if (r < lo || r >= hi) continue;  // the same for the whole warp
-    const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+    uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
     // The largest magnitude, as bit patterns: those of infinities and NaN are the largest.
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const float amax = __uint_as_float(top);
-    __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(amax, BITS == 4 ? 7.f : 127.f));
-    const float sf = __bfloat162float(s);
-    float inv = __frcp_rn(sf) * (1.f + 9.5367431640625e-7f);
-    if (!(amax >= kTiny)) {
+    uint32_t top = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                             max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    top = max(top & 0xffffu, top >> 16);
+    // The scale. max / m times 1 / m as a number: no quotient lies so near a midpoint that it would round another way.
+    const float amax = __uint_as_float(top << 16);
+    __nv_bfloat16 s = __float2bfloat16_rn(amax * (BITS == 4 ? 1.f / 7.f : 1.f / 127.f));
+    float inv = rcp_approx(__bfloat162float(s)) * (1.f + 9.5367431640625e-7f);
+    const bool bad = top >= 0x7f80u;  // an infinity or NaN in the group: the whole group reads as NaN
+    if (bad || amax < kTiny) {
+      s = __ushort_as_bfloat16(bad ? 0x7fc0 : 0);
       inv = 0.f;
-      s = __ushort_as_bfloat16(0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] &= 0x80008000u;  // (0 times an infinity is none)
     }
-    const bool bad = top >= 0x7f800000u;  // an infinity or NaN in the group: the whole group reads as NaN
-    if (bad) s = __ushort_as_bfloat16(0x7fc0);
     uint32_t n[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      n[2 * e] = bad ? 0u : quant_code(bf16lo_to_f32(w[e]), inv);
-      n[2 * e + 1] = bad ? 0u : quant_code(bf16hi_to_f32(w[e]), inv);
+      n[2 * e] = magnitude(bf16lo_to_f32(w[e]), inv);
+      n[2 * e + 1] = magnitude(bf16hi_to_f32(w[e]), inv);
     }
     uint8_t* rec = rec0 + r * kRec;
-    if ((j & 3) == 0)
-      reinterpret_cast<__nv_bfloat16*>(rec + cache_scale_offset(BITS))[(is_v ? 4 : 0) + G] = s;
-    auto sign = [&](int i) { return n[i] >> 7; };
-    auto mag = [&](int i) { return n[i] & 0x7fu; };
-    if (!is_v) {
-      uint32_t* words = reinterpret_cast<uint32_t*>(rec);
-      if (BITS == 4) {
-        words[4 * (j & 3) + G] = pack_fields(n[0], n[2], n[4], n[6]) | pack_fields(n[1], n[3], n[5], n[7]) << 16;
-      } else {
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          words[16 * (G >> 1) + 4 * (j & 3) + 2 * (G & 1) + f] =
-              mag(4 * f) | sign(4 * f) << 15 | mag(4 * f + 1) << 16 | sign(4 * f + 1) << 31 | mag(4 * f + 2) << 8 |
-              sign(4 * f + 2) << 23 | mag(4 * f + 3) << 24 | sign(4 * f + 3) << 7;
-      }
+    if ((j & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(rec + scale_at) = s;
+    // K and V differ in the order of their codes: operands are chosen, so that all lanes do the same.
+    if (BITS == 4) {
+      // K: channels 0, 2, 4, 6 and 1, 3, 5, 7; V: 0 .. 3 and 4 .. 7
+      const uint32_t n1 = is_v ? n[1] : n[2], n2 = is_v ? n[2] : n[4], n3 = is_v ? n[3] : n[6];
+      const uint32_t n4 = is_v ? n[4] : n[1], n5 = is_v ? n[5] : n[3], n6 = is_v ? n[6] : n[5];
+      const uint32_t lo = pack_fields(n[0], n1, n2, n3, w[0], is_v ? w[1] : w[2], 0x51, is_v ? w[0] : w[1],
+                                      is_v ? w[1] : w[3], is_v ? 0x73 : 0x51);
+      const uint32_t hi = pack_fields(n4, n5, n6, n[7], is_v ? w[2] : w[0], is_v ? w[3] : w[2], is_v ? 0x51 : 0x73,
+                                      is_v ? w[2] : w[1], w[3], 0x73);
+      *reinterpret_cast<uint16_t*>(rec + code_at) = static_cast<uint16_t>(lo);
+      *reinterpret_cast<uint16_t*>(rec + code_at + code_step) = static_cast<uint16_t>(hi);
     } else {
-      uint8_t* at = rec + cache_v_offset(BITS);
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const int g = 2 * (j & 3) + f, i = 4 * f;
-        if (BITS == 4)
-          reinterpret_cast<uint16_t*>(at)[4 * g + G] =
-              static_cast<uint16_t>(pack_fields(n[i], n[i + 1], n[i + 2], n[i + 3]));
-        else
-          reinterpret_cast<uint32_t*>(at)[4 * g + G] = n[i] | n[i + 1] << 8 | n[i + 2] << 16 | n[i + 3] << 24;
+        const uint32_t a = w[2 * f], c = w[2 * f + 1];
+        const uint32_t n1 = is_v ? n[4 * f + 2] : n[4 * f + 1], n2 = is_v ? n[4 * f + 1] : n[4 * f + 2];
+        // magnitudes of channels 0, n2, n1, 3 in bytes 0 .. 3, what is around them taken off
+        const uint32_t mags = n[4 * f] + (n2 << 8) + (n1 << 16) + (n[4 * f + 3] << 24) - (kMagic + (kMagic << 8));
+        const uint32_t sa = a & 0x80008000u, sc = c & 0x80008000u;
+        const uint32_t signs = is_v ? permute_bytes(sa, sc, 0x7531) : sa | rotate_right(sc, 24);
+        *reinterpret_cast<uint32_t*>(rec + code_at + f * code_step) = mags | signs;
       }
     }
   }

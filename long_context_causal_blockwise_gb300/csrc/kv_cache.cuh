@@ -44,12 +44,6 @@ constexpr int cache_v_offset(int bits) { return 16 * bits; }
 constexpr int cache_scale_offset(int bits) { return 32 * bits; }
 constexpr int cache_row_bytes(int bits) { return 32 * bits + 16; }
 
-// Four codes in 16 bits, from signs (bit 7) and magnitudes.
-__device__ __forceinline__ uint32_t pack_fields(uint32_t n0, uint32_t n1, uint32_t n2, uint32_t n3) {
-  return (n0 & 7u) | (n0 & 0x80u) << 8 | (n1 & 7u) << 3 | (n1 & 0x80u) << 7 | (n2 & 7u) << 8 | (n2 & 0x80u) |
-         (n3 & 7u) << 11 | (n3 & 0x80u) >> 1;
-}
-
 // Bytes of (a, b) by the nibbles of `sel`, the highest bit of a nibble giving eight copies of that byte's sign.
 __device__ __forceinline__ uint32_t permute_bytes(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;

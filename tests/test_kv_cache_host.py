@@ -47,26 +47,28 @@ def test_oracle_error_bound(bits):
 
 @pytest.mark.parametrize("m", [7, 127])
 def test_one_multiplication_rounds_as_the_division(m):
-    """x * inv with inv = fp32(fp32(1 / s) * (1 + 2^-20)), rounded to the nearest whole number, is x / s rounded with
-    ties away from zero, for every pair of bf16 significands at every distance that a group has."""
+    """x * inv with inv = fp32(r * (1 + 2^-20)), rounded to the nearest whole number, is x / s rounded with ties away from
+    zero, for every pair of bf16 significands at every distance that a group has, and r = 1 / s to two steps either way."""
     S = np.arange(128, 256, dtype=np.float64)[:, None]
-    inv = (np.float32(1) / S.astype(np.float32)).astype(np.float32)
-    inv = (inv * np.float32(1 + 2.0 ** -20)).astype(np.float64)
-    for e in range(-3, 9):
-        x = np.arange(128, 256, dtype=np.float64)[None, :] * 2.0 ** e
-        q = x / S
-        want = np.floor(q + 0.5)
-        got = np.rint(x * inv)  # 8 by 24 bits: the product is exact in fp64, as inside the fused multiply-add
-        use = q <= m * (1 + 2.0 ** -8)
-        assert np.array_equal(got[use], want[use])
-        assert (want[use] <= m).all()
+    for off in (-2, -1, 0, 1, 2):
+        r = (np.float32(1) / S.astype(np.float32)).astype(np.float32)
+        r = (r.view(np.int32) + off).view(np.float32)
+        inv = (r * np.float32(1 + 2.0 ** -20)).astype(np.float64)
+        for e in range(-3, 9):
+            x = np.arange(128, 256, dtype=np.float64)[None, :] * 2.0 ** e
+            q = x / S
+            want = np.floor(q + 0.5)
+            got = np.rint(x * inv)  # 8 by 24 bits: the product is exact in fp64, as inside the fused multiply-add
+            use = q <= m * (1 + 2.0 ** -8)
+            assert np.array_equal(got[use], want[use])
+            assert (want[use] <= m).all()
 
 
 def test_scales_are_one_rounding():
-    """fp32(max / m) rounded to bf16 is max / m rounded to bf16: no quotient lies next to a midpoint."""
+    """fp32(max * fp32(1 / m)) rounded to bf16 is max / m rounded to bf16: no quotient lies next to a midpoint."""
     X = np.arange(128, 256, dtype=np.float32)
     for m in (7, 127):
-        q32 = (X / np.float32(m)).astype(np.float64)
+        q32 = (X * (np.float32(1) / np.float32(m))).astype(np.float64)
         assert np.array_equal(oracle.round_bf16(q32), oracle.round_bf16(X.astype(np.float64) / m))
 
 
