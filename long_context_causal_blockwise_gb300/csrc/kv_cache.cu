@@ -45,18 +45,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+// The larger magnitudes of two pairs of bf16 (with some sign); NaN where there is one.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-
-// Four codes in 16 bits (kv_cache.cuh): magnitudes m0 .. m3 with kMagic around them; the signs are those of bytes a1, b1
-// (fields 0, 2) and, by `sel`, of c and d (fields 1, 3).
-__device__ __forceinline__ uint32_t pack_fields(uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3, uint32_t a, uint32_t b,
-                                                uint32_t sel_ab, uint32_t c, uint32_t d, uint32_t sel_cd) {
-  const uint32_t even = permute_bytes(b, a, sel_ab) & 0x8080u, odd = permute_bytes(d, c, sel_cd) & 0x8080u;
-  return (m0 + 8u * m1 + 256u * m2 + 2048u * m3) & 0x3f3fu | even | odd >> 1;
 }
 
 template <int BITS>
@@ -64,11 +57,12 @@ __global__ void __launch_bounds__(32 * kWarps) kv_cache_write_kernel(const __gri
   constexpr int kRec = cache_row_bytes(BITS);
   __shared__ __align__(16) uint8_t recs[kWarps][kRows * kRec];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const uint32_t unit = blockIdx.x * kWarps + warp;
   if (unit >= p.units) return;
-  const int h = static_cast<int>(unit % p.Hkv);
-  const long long bt = unit / p.Hkv;
-  const int t0 = static_cast<int>(bt % p.blocks) * kRows, b = static_cast<int>(bt / p.blocks);
+  const uint32_t bt = unit / static_cast<uint32_t>(p.Hkv);
+  const int h = static_cast<int>(unit - bt * p.Hkv);
+  const int b = static_cast<int>(bt / static_cast<uint32_t>(p.blocks));
+  const int t0 = static_cast<int>(bt - static_cast<uint32_t>(b) * p.blocks) * kRows;
   // token t goes to row first + t
   const long long first = static_cast<long long>(p.lens[b]) - p.T;
   const int lo = static_cast<int>(max(0LL, min(static_cast<long long>(kRows), -first - t0)));
@@ -83,62 +77,75 @@ __global__ void __launch_bounds__(32 * kWarps) kv_cache_write_kernel(const __gri
   for (int r = 0; r < kRows; ++r)
     if (r >= lo && r < hi) x[r] = __ldcs(reinterpret_cast<const uint4*>(src + r * p.row_stride));
   uint8_t* rec0 = recs[warp];
-  // where in a record the lane's scale and its two pieces of codes go: K's side by side, V's those of two lanes' operands
+  // Where in a record the lane's scale and its two pieces of codes go: K's side by side, V's those of two lanes' operands.
   const int t = j & 3;
   const int scale_at = cache_scale_offset(BITS) + 2 * ((is_v ? 4 : 0) + G);
   const int code_at = BITS == 4 ? (is_v ? 64 + 16 * t + 2 * G : 16 * t + 4 * G)
                                 : (is_v ? 128 + 32 * t + 4 * G : 64 * (G >> 1) + 16 * t + 8 * (G & 1));
   const int code_step = BITS == 4 ? (is_v ? 8 : 2) : (is_v ? 16 : 4);
+  // K and V differ in the order of their codes. So that all lanes do the same, a word's magnitudes are summed with the
+  // lane's own powers of two (mod 2^32, where kMagic's share is taken off at the start), and its signs gathered by the
+  // lane's own byte selectors. 4 bits: channel e's field is e / 2 of half e % 2 (K) or e % 4 of half e / 4 (V).
+  uint32_t mul[8], base = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (BITS == 4) {
+      const int i = is_v ? e & 3 : e >> 1;
+      mul[e] = 1u << (16 * (is_v ? e >> 2 : e & 1) + 8 * (i >> 1) + 3 * (i & 1));
+      base -= kMagic * mul[e];
+    } else {
+      const int i = e & 3;  // both words alike: bytes 0 2 1 3 (K), 0 1 2 3 (V)
+      mul[e] = 1u << 8 * (is_v || i == 0 || i == 3 ? i : 3 - i);
+      if (e < 4) base -= kMagic * mul[e];
+    }
+  }
+  const uint32_t sel_a = is_v ? 0x7531 : 0x3715;  // 4 bits; the sign bytes of words 0, 2 and of words 1, 3
+  const uint32_t sel_c = is_v ? 0x2604 : 0x3210, sel_d = is_v ? 0x3715 : 0x7654;
+  const uint32_t sel_8 = is_v ? 0x7531 : 0x3517;
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     if (r < lo || r >= hi) continue;  // the same for the whole warp
-    uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-    // The largest magnitude, as bit patterns: those of infinities and NaN are the largest.
-    uint32_t top = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                             max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-    top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    top = max(top & 0xffffu, top >> 16);
+    const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+    // The largest magnitude of the group.
+    uint32_t top = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
+    top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t amax_bits = max(top << 16 & 0x7fff0000u, top & 0x7fff0000u);
     // The scale. max / m times 1 / m as a number: no quotient lies so near a midpoint that it would round another way.
-    const float amax = __uint_as_float(top << 16);
-    __nv_bfloat16 s = __float2bfloat16_rn(amax * (BITS == 4 ? 1.f / 7.f : 1.f / 127.f));
-    float inv = rcp_approx(__bfloat162float(s)) * (1.f + 9.5367431640625e-7f);
-    const bool bad = top >= 0x7f80u;  // an infinity or NaN in the group: the whole group reads as NaN
-    if (bad || amax < kTiny) {
-      s = __ushort_as_bfloat16(bad ? 0x7fc0 : 0);
-      inv = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] &= 0x80008000u;  // (0 times an infinity is none)
-    }
+    const float amax = __uint_as_float(amax_bits);
+    uint32_t s = __bfloat16_as_ushort(__float2bfloat16_rn(amax * (BITS == 4 ? 1.f / 7.f : 1.f / 127.f)));
+    float inv = rcp_approx(__uint_as_float(s << 16)) * (1.f + 9.5367431640625e-7f);
+    const bool bad = amax_bits >= 0x7f800000u;  // an infinity or NaN in the group: the whole group reads as NaN
+    const bool none = !(amax >= kTiny);         // (NaN too)
+    if (none) s = 0, inv = 0.f;
+    if (bad) s = 0x7fc0;
+    uint8_t* rec = rec0 + r * kRec;
+    if ((j & 3) == 0) *reinterpret_cast<uint16_t*>(rec + scale_at) = static_cast<uint16_t>(s);
     uint32_t n[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       n[2 * e] = magnitude(bf16lo_to_f32(w[e]), inv);
       n[2 * e + 1] = magnitude(bf16hi_to_f32(w[e]), inv);
     }
-    uint8_t* rec = rec0 + r * kRec;
-    if ((j & 3) == 0) *reinterpret_cast<__nv_bfloat16*>(rec + scale_at) = s;
-    // K and V differ in the order of their codes: operands are chosen, so that all lanes do the same.
     if (BITS == 4) {
-      // K: channels 0, 2, 4, 6 and 1, 3, 5, 7; V: 0 .. 3 and 4 .. 7
-      const uint32_t n1 = is_v ? n[1] : n[2], n2 = is_v ? n[2] : n[4], n3 = is_v ? n[3] : n[6];
-      const uint32_t n4 = is_v ? n[4] : n[1], n5 = is_v ? n[5] : n[3], n6 = is_v ? n[6] : n[5];
-      const uint32_t lo = pack_fields(n[0], n1, n2, n3, w[0], is_v ? w[1] : w[2], 0x51, is_v ? w[0] : w[1],
-                                      is_v ? w[1] : w[3], is_v ? 0x73 : 0x51);
-      const uint32_t hi = pack_fields(n4, n5, n6, n[7], is_v ? w[2] : w[0], is_v ? w[3] : w[2], is_v ? 0x51 : 0x73,
-                                      is_v ? w[2] : w[1], w[3], 0x73);
-      *reinterpret_cast<uint16_t*>(rec + code_at) = static_cast<uint16_t>(lo);
-      *reinterpret_cast<uint16_t*>(rec + code_at + code_step) = static_cast<uint16_t>(hi);
+      uint32_t sum = base;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += n[e] * mul[e];
+      if (bad) sum = 0;
+      const uint32_t a = permute_bytes(w[0], w[2], sel_a), c = permute_bytes(w[1], w[3], sel_a);
+      const uint32_t even = permute_bytes(a, c, sel_c), odd = permute_bytes(a, c, sel_d);
+      const uint32_t word = sum | ((even & 0x80808080u) | (odd >> 1 & 0x40404040u));
+      *reinterpret_cast<uint16_t*>(rec + code_at) = static_cast<uint16_t>(word);
+      *reinterpret_cast<uint16_t*>(rec + code_at + code_step) = static_cast<uint16_t>(word >> 16);
     } else {
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const uint32_t a = w[2 * f], c = w[2 * f + 1];
-        const uint32_t n1 = is_v ? n[4 * f + 2] : n[4 * f + 1], n2 = is_v ? n[4 * f + 1] : n[4 * f + 2];
-        // magnitudes of channels 0, n2, n1, 3 in bytes 0 .. 3, what is around them taken off
-        const uint32_t mags = n[4 * f] + (n2 << 8) + (n1 << 16) + (n[4 * f + 3] << 24) - (kMagic + (kMagic << 8));
-        const uint32_t sa = a & 0x80008000u, sc = c & 0x80008000u;
-        const uint32_t signs = is_v ? permute_bytes(sa, sc, 0x7531) : sa | rotate_right(sc, 24);
-        *reinterpret_cast<uint32_t*>(rec + code_at + f * code_step) = mags | signs;
+        uint32_t sum = base;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += n[4 * f + e] * mul[e];
+        if (bad) sum = 0;
+        *reinterpret_cast<uint32_t*>(rec + code_at + f * code_step) =
+            sum | (permute_bytes(w[2 * f], w[2 * f + 1], sel_8) & 0x80808080u);
       }
     }
   }
@@ -155,11 +162,12 @@ __global__ void __launch_bounds__(32 * kWarps) kv_cache_read_kernel(const __grid
   constexpr int kVecs = kRows * kRec / 16;  // 16-byte vectors of a warp's rows
   __shared__ __align__(16) uint8_t recs[kWarps][kRows * kRec];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const uint32_t unit = blockIdx.x * kWarps + warp;
   if (unit >= p.units) return;
-  const int h = static_cast<int>(unit % p.Hkv);
-  const long long bt = unit / p.Hkv;
-  const int t0 = static_cast<int>(bt % p.blocks) * kRows, b = static_cast<int>(bt / p.blocks);
+  const uint32_t bt = unit / static_cast<uint32_t>(p.Hkv);
+  const int h = static_cast<int>(unit - bt * p.Hkv);
+  const int b = static_cast<int>(bt / static_cast<uint32_t>(p.blocks));
+  const int t0 = static_cast<int>(bt - static_cast<uint32_t>(b) * p.blocks) * kRows;
   const int rows = min(kRows, p.n - t0);
   // rows of the cache that are filled; the others read as zeros
   const int have = p.lens ? max(0, min(rows, max(p.lens[b], 0) - (p.start + t0))) : rows;
@@ -224,31 +232,39 @@ __global__ void __launch_bounds__(32 * kWarps) kv_cache_read_kernel(const __grid
   }
 }
 
+// Warps' units of B sequences of n rows and Hkv heads; below zero where there are more than 32 bits number (2^35 rows).
+long long units_of(int B, int n, int Hkv, int& blocks) {
+  blocks = n / kRows + (n % kRows != 0);
+  const long long rows = static_cast<long long>(B) * blocks;
+  if (rows == 0) return 0;
+  return rows > 0xffffffffLL / Hkv ? -1 : rows * Hkv;
+}
+
 }  // namespace
 
 int launch_kv_cache_write(KvCacheWrite p, int bits, cudaStream_t stream) {
-  p.blocks = (p.T + kRows - 1) / kRows;
-  p.units = static_cast<long long>(p.B) * p.blocks * p.Hkv;
-  const long long grid = (p.units + kWarps - 1) / kWarps;
-  if (grid > 0x7fffffffLL) return -1;
-  if (grid == 0) return 0;
+  const long long units = units_of(p.B, p.T, p.Hkv, p.blocks);
+  if (units < 0) return -1;
+  if (units == 0) return 0;
+  p.units = static_cast<unsigned>(units);
+  const unsigned grid = p.units / kWarps + (p.units % kWarps != 0);
   if (bits == 4)
-    kv_cache_write_kernel<4><<<static_cast<unsigned>(grid), 32 * kWarps, 0, stream>>>(p);
+    kv_cache_write_kernel<4><<<grid, 32 * kWarps, 0, stream>>>(p);
   else
-    kv_cache_write_kernel<8><<<static_cast<unsigned>(grid), 32 * kWarps, 0, stream>>>(p);
+    kv_cache_write_kernel<8><<<grid, 32 * kWarps, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 
 int launch_kv_cache_read(KvCacheRead p, int bits, cudaStream_t stream) {
-  p.blocks = (p.n + kRows - 1) / kRows;
-  p.units = static_cast<long long>(p.B) * p.blocks * p.Hkv;
-  const long long grid = (p.units + kWarps - 1) / kWarps;
-  if (grid > 0x7fffffffLL) return -1;
-  if (grid == 0) return 0;
+  const long long units = units_of(p.B, p.n, p.Hkv, p.blocks);
+  if (units < 0) return -1;
+  if (units == 0) return 0;
+  p.units = static_cast<unsigned>(units);
+  const unsigned grid = p.units / kWarps + (p.units % kWarps != 0);
   if (bits == 4)
-    kv_cache_read_kernel<4><<<static_cast<unsigned>(grid), 32 * kWarps, 0, stream>>>(p);
+    kv_cache_read_kernel<4><<<grid, 32 * kWarps, 0, stream>>>(p);
   else
-    kv_cache_read_kernel<8><<<static_cast<unsigned>(grid), 32 * kWarps, 0, stream>>>(p);
+    kv_cache_read_kernel<8><<<grid, 32 * kWarps, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 

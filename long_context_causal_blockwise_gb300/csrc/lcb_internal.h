@@ -213,7 +213,7 @@ struct KvCacheWrite {
   long long cache_batch_stride, cache_head_stride, row_stride, batch_stride;
   int B, Hkv, T, Smax;
   int blocks;  // set by the launch, as units
-  long long units;
+  unsigned units;
 };
 int launch_kv_cache_write(KvCacheWrite p, int bits, cudaStream_t stream);
 
@@ -225,7 +225,7 @@ struct KvCacheRead {
   long long cache_batch_stride, cache_head_stride, row_stride, batch_stride;
   int B, Hkv, n, start;
   int blocks;
-  long long units;
+  unsigned units;
 };
 int launch_kv_cache_read(KvCacheRead p, int bits, cudaStream_t stream);
 
