@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(32 * kWarps) kv_cache_write_kernel(const __grid_constant__ KvCacheWrite p) {
+__global__ void __launch_bounds__(32 * kWarps, 8) kv_cache_write_kernel(const __grid_constant__ KvCacheWrite p) {
   constexpr int kRec = cache_row_bytes(BITS);
   __shared__ __align__(16) uint8_t recs[kWarps][kRows * kRec];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
