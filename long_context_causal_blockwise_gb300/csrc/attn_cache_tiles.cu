@@ -24,8 +24,16 @@
 // above 2^-8 of the largest of the sixteen keys, off by 2^-19 of that key's largest
 // value at most where not. In 8 bits it is two numbers, the magnitude's upper 3
 // bits (so exact) and its lower 4 (off by half a step, 2^-12 of them, 2^-15 of the
-// largest magnitude), and two products. Q as in attn_cache_decode.cu. V goes to bf16 as 2^-16 s n: off by
-// half a step, 2^-8 of each value at most, as kv_cache_read rounds it; P as ever.
+// largest magnitude), and two products. Q as in attn_cache_decode.cu.
+//
+// V and the weights P are of one type, for each sixteen keys (a product's step) on
+// its own. Where the sixteen keys' scales of V are ordinary (2^-7, in 8 bits 2^-11,
+// up to 16, or zero) they are fp16: 2^-12 s n, off by 2^-13 of the group's largest
+// value at best, 2^-9 of it at the smallest scales, and 2^7 P, off by 2^-12 down to
+// weights of 2^-21 of the largest. Otherwise, and where fewer than sixteen keys
+// exist, bf16 with the same powers of two: off by half a step, 2^-9 to 2^-8 of each
+// value. (bf16 for all of them: errors 2.8e-3 of the outputs instead of 1.7e-3, which
+// is what rounding these to bf16 costs.)
 //
 // The units of all tiles are dealt evenly to the CTAs, one to an SM, and joined
 // by a second kernel (cache_line.cuh). Streams are joined first, in tensor memory:
@@ -72,15 +80,16 @@ template <int BITS>
 struct Smem {  // 1024-byte aligned
   uint8_t K[2][kTileBytes], V[2][kTileBytes], Q[kTileBytes];
   uint8_t raw[Raw<BITS>::kStages][Raw<BITS>::kBytes];
-  float k_factor[4][8];  // by unit modulo 4: the power of two taken from K, for each sixteen keys
+  // by unit modulo 4: the power of two taken from K, for each sixteen keys; below zero where their V and P are bf16
+  float k_factor[4][8];
   float M[2][kRows], L[2][kRows];
   Bars bars;
   int lens[kLineSequences];
 };
 
 // Instruction descriptor, kind::f16, fp32 sums: fp16 operands (format 0).
-constexpr uint32_t idesc_f16(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+constexpr uint32_t idesc_f16(int M, int N, bool transposed_b = false) {
+  return (1u << 4) | (transposed_b ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
@@ -108,8 +117,8 @@ __device__ __forceinline__ uint32_t hfma2_bf16(uint32_t a, uint32_t b, uint32_t 
   return r;
 }
 
-constexpr int kVDown = 16;               // V's tiles hold V times 2^-16
-constexpr uint32_t kVUp = 0x7a007a00u;   // 2^(133 - 16), twice in bf16: a scale times it is what a code is multiplied by
+constexpr int kVDown = 12;      // V's tiles hold V times 2^-12,
+constexpr float kWeightUp = 7;  // the weights are times 2^7: 2^15 at most, as a maximum may lag by kRescaleThreshold
 
 // A lane (key, t) of eight keys takes its key's channels 32 G + 8 t .. + 7 of all four groups, odd keys the two of a pair
 // of groups in reverse: eight lanes, of two neighbouring rows, then store into different banks.
@@ -124,9 +133,20 @@ __device__ __forceinline__ uint8_t* chunk_of(uint8_t* tile, uint32_t first, int 
   return tile + ((first ^ (j & 1 ? 64u : 0u)) + round * 1024 + (j >> 1) * kHalfBytes);
 }
 
+// Whether a scale of V among the sixteen keys is not one for fp16.
+template <int BITS>
+__device__ __forceinline__ bool wide_v(const uint8_t* rec, int lane) {
+  const uint32_t x = *reinterpret_cast<const uint32_t*>(rec + (lane >> 1) * cache_row_bytes(BITS) +
+                                                        cache_scale_offset(BITS) + 8 + 4 * (lane & 1));
+  constexpr uint32_t kLow = (BITS == 4 ? 120u : 116u) << 7, kHigh = 131u << 7;  // 2^-7 or 2^-11, 2^4
+  auto out = [](uint32_t a) { return a != 0 && (a < kLow || a >= kHigh); };
+  return __any_sync(0xffffffffu, out(x & 0xffffu) || out(x >> 16));
+}
+
 // Sixteen keys of K by a warp: rows row0 .. + 15 of the tile; the first nk of the records exist.
 template <int BITS>
-__device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int row0, int nk, float* factor, int lane) {
+__device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int row0, int nk, float* factor, int lane,
+                                         bool& is_wide) {
   constexpr int kRec = cache_row_bytes(BITS);
   // the largest finite scale of the sixteen keys, as bits
   uint32_t top = 0;
@@ -137,10 +157,11 @@ __device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int 
     top = max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u);
   }
   top = __reduce_max_sync(0xffffffffu, top);
+  const bool wide = is_wide = nk < 16 || wide_v<BITS>(rec, lane);
   // scales are below 2^(e + 1): times 2^(14 - e) they are fp16, and with the codes' 2^-24 they make s n 2^(-10 - e)
   const int e = max(static_cast<int>(top >> 7) - 127, -100);
   const float up = exp2_int(14 - e);
-  if (lane == 0) *factor = exp2_int(min(10 + e, 127));
+  if (lane == 0) *factor = exp2_int(min(10 + e, 127)) * (wide ? -1.f : 1.f);
   const Lane at(lane);
   const uint8_t* r0 = rec + at.key * kRec;
   const uint32_t first = at.first_chunk(row0), order = at.odd ? 0x1032 : 0x3210;
@@ -189,18 +210,23 @@ __device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int 
   }
 }
 
-// s n 2^-16 of a pair of V's codes: by one multiplication with s 2^117 (up), where that fits; otherwise s n from the
-// magnitude's 128 + m first. sh: bits that the magnitude is to the left.
-template <bool LARGE>
-__device__ __forceinline__ uint32_t v_value(uint32_t code, uint32_t s, uint32_t up, int sh) {
-  if (!LARGE) return hmul2_bf16(code, up);
+// 2^-12 s n of a pair of V's codes, as they lie (magnitudes sh bits to the left). fp16: by one multiplication, by 2^12 s
+// over that shift. bf16, for any scale: from the magnitude's 128 + m, by 2^-12 s.
+template <bool WIDE>
+__device__ __forceinline__ uint32_t v_value(uint32_t code, uint32_t s, int sh) {
+  if (!WIDE) return hmul2_f16(code, s);
   const uint32_t m = ((code & 0x7fff7fffu) >> sh) | 0x43004300u;
-  const uint32_t x = hfma2_bf16(m, s, hmul2_bf16(s, 0xc300c300u));  // (128 + m) s - 128 s
-  return hmul2_bf16(x, 0x37803780u) | (code & 0x80008000u);         // 2^-16
+  return hfma2_bf16(m, s, hmul2_bf16(s, 0xc300c300u)) | (code & 0x80008000u);  // (128 + m) s - 128 s
+}
+template <bool WIDE>
+__device__ __forceinline__ uint32_t v_scales(uint32_t s) {
+  if (WIDE) return hmul2_bf16(s, 0x39803980u);
+  const __half2 h = __floats2half2_rn(bf16lo_to_f32(s) * 4096.f, bf16hi_to_f32(s) * 4096.f);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Sixteen keys of V, by a warp; keys past the last become zeros.
-template <int BITS, bool LARGE, bool FULL>
+// Sixteen keys of V, by a warp; keys past the last (of wide ones) become zeros.
+template <int BITS, bool WIDE>
 __device__ __forceinline__ void unpack_v(const uint8_t* rec, uint8_t* tile, int row0, int nk, int lane) {
   constexpr int kRec = cache_row_bytes(BITS);
   const Lane at(lane);
@@ -210,21 +236,21 @@ __device__ __forceinline__ void unpack_v(const uint8_t* rec, uint8_t* tile, int 
 #pragma unroll
   for (int round = 0; round < 2; ++round) {
     const uint8_t* r = r0 + round * 8 * kRec;
-    const uint32_t keep = FULL || 8 * round + at.key < nk ? ~0u : 0u;
+    const uint32_t keep = !WIDE || 8 * round + at.key < nk ? ~0u : 0u;
     const uint2 sc = *reinterpret_cast<const uint2*>(r + cache_scale_offset(BITS) + 8);
     if (BITS == 4) {
       // half-words of lanes 2 t and 2 t + 1: words with groups 0, 1 and 2, 3 of each
       const uint4 v = *reinterpret_cast<const uint4*>(r + cache_v_offset(BITS) + 16 * at.t);
 #pragma unroll
       for (int gp = 0; gp < 2; ++gp) {
-        const uint32_t s = gp ? sc.y : sc.x;
-        const uint32_t up = hmul2_bf16(s, kVUp), up16 = hmul2_bf16(up, 0x3d803d80u);
+        const uint32_t s = v_scales<WIDE>(gp ? sc.y : sc.x);
+        const uint32_t s16 = WIDE ? s : hmul2_f16(s, 0x2c002c00u);  // odd fields are 2^4 as large
         uint32_t c[2][4];  // channels 4 f + i of both groups
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           const Fields x = k4_fields(gp ? (f ? v.w : v.y) : (f ? v.z : v.x));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[f][i] = v_value<LARGE>(x.pair(i), s, i & 1 ? up16 : up, i & 1 ? 4 : 0);
+          for (int i = 0; i < 4; ++i) c[f][i] = v_value<WIDE>(x.pair(i), i & 1 ? s16 : s, i & 1 ? 4 : 0);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -235,6 +261,7 @@ __device__ __forceinline__ void unpack_v(const uint8_t* rec, uint8_t* tile, int 
         }
       }
     } else {
+      const uint32_t s01 = v_scales<WIDE>(sc.x), s23 = v_scales<WIDE>(sc.y);
       uint32_t w[2][4];  // of groups in the lane's order
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
@@ -246,27 +273,18 @@ __device__ __forceinline__ void unpack_v(const uint8_t* rec, uint8_t* tile, int 
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t s2 = j < 2 ? sc.x : sc.y;
+        const uint32_t s2 = j < 2 ? s01 : s23;
         const uint32_t s = permute_bytes(s2, s2, j & 1 ? sel1 : sel0);
-        const uint32_t up = hmul2_bf16(s, kVUp);
         uint32_t o[4];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          o[2 * f] = v_value<LARGE>(permute_bytes(w[f][j], 0, 0x9180) & 0x807f807fu, s, up, 0) & keep;
-          o[2 * f + 1] = v_value<LARGE>(permute_bytes(w[f][j], 0, 0xb3a2) & 0x807f807fu, s, up, 0) & keep;
+          o[2 * f] = v_value<WIDE>(permute_bytes(w[f][j], 0, 0x9180) & 0x807f807fu, s, 0) & keep;
+          o[2 * f + 1] = v_value<WIDE>(permute_bytes(w[f][j], 0, 0xb3a2) & 0x807f807fu, s, 0) & keep;
         }
         st_shared16(chunk_of(tile, first, round, j), o[0], o[1], o[2], o[3]);
       }
     }
   }
-}
-
-// Whether a scale of V among the sixteen keys is too large for one multiplication: 2^10, or NaN.
-template <int BITS>
-__device__ __forceinline__ bool large_v(const uint8_t* rec, int lane) {
-  const uint32_t x = *reinterpret_cast<const uint32_t*>(rec + (lane >> 1) * cache_row_bytes(BITS) +
-                                                        cache_scale_offset(BITS) + 8 + 4 * (lane & 1));
-  return __any_sync(0xffffffffu, (x & 0xffffu) >= 0x4480u || (x >> 16) >= 0x4480u);
 }
 
 template <int BITS>
@@ -364,19 +382,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           ok = mbar_wait_warp(&bars.k_empty[kt], (BITS == 4 ? ph : static_cast<uint32_t>(i) & 1u) ^ 1u, abort_flag, p.st,
                               kWhere | (3u << 16));
         if (!ok) break;
+        bool wide = true;
         if (mine > 0)
-          unpack_k<BITS>(rec, sm.K[kt], row0, mine, &sm.k_factor[i & 3][w], lane);
+          unpack_k<BITS>(rec, sm.K[kt], row0, mine, &sm.k_factor[i & 3][w], lane, wide);
         else if (lane == 0)
-          sm.k_factor[i & 3][w] = 1.f;
+          sm.k_factor[i & 3][w] = -1.f;
         fence_to_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.k_full[kt]);
         ok = mbar_wait_warp(&bars.v_empty[t], ph ^ 1u, abort_flag, p.st, kWhere | (4u << 16));
         if (!ok) break;
-        if (mine < 16 || large_v<BITS>(rec, lane))
-          unpack_v<BITS, true, false>(rec, sm.V[t], row0, mine, lane);
+        if (wide)
+          unpack_v<BITS, true>(rec, sm.V[t], row0, mine, lane);
         else
-          unpack_v<BITS, false, true>(rec, sm.V[t], row0, mine, lane);
+          unpack_v<BITS, false>(rec, sm.V[t], row0, mine, lane);
         fence_to_async();
         __syncwarp();
         if (lane == 0) {
@@ -390,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
   } else if (any && warp == kProducts) {
     // ------------------------------------------------------------ products
     const uint32_t elected = elect_one();
-    const uint32_t idesc_qk = idesc_f16(kRows, kKeys), idesc_pv = idesc_bf16(kRows, kD, false, true);
+    const uint32_t idesc_qk = idesc_f16(kRows, kKeys), idesc_pv = idesc_f16(kRows, kD, true),
+                   idesc_pv_wide = idesc_bf16(kRows, kD, false, true);
     const uint32_t sQ = uniform(smem_u32(sm.Q)), sK = uniform(smem_u32(sm.K)), sV = uniform(smem_u32(sm.V));
     const uint32_t tb = uniform(tbase);
     int seg = 0;
@@ -429,10 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           if (!ok) break;
           tc_fence_after();
           const uint64_t vb = sdesc_sw128(sV + t * kTileBytes, kHalfBytes, 1024);
+          const uint32_t wide = __ballot_sync(0xffffffffu, lane < 8 && sm.k_factor[i & 3][lane & 7] < 0.f);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts_if(tb + 256 + t * 128, tb + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048), idesc_pv, x > 2 || kk > 0,
-                      elected);
+            mma_ts_if(tb + 256 + t * 128, tb + t * 128 + kk * 8, sdesc_advance(vb, kk * 2048),
+                      wide >> kk & 1u ? idesc_pv_wide : idesc_pv, x > 2 || kk > 0, elected);
           tc_commit_if(&bars.v_empty[t], elected);
           if (x + 2 > n) tc_commit_if(&bars.o_full[t], elected);  // the stream's last in this tile
         }
@@ -528,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
                 y = fmax3(y, __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]));
                 z = fmax3(z, __uint_as_float(s[16 * h + k + 2]), __uint_as_float(s[16 * h + k + 3]));
               }
-              mx = fmaxf(mx, fmaxf(y, z) * (c * (h ? kf.y : kf.x)));
+              mx = fmaxf(mx, fmaxf(y, z) * (c * fabsf(h ? kf.y : kf.x)));
             }
           }
           const float m_new = fmaxf(m, mx);
@@ -550,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
               m = m_new;
             }
           }
-          const float neg_m = m == -INFINITY ? 0.f : -m;
+          const float neg_m = m == -INFINITY ? 0.f : kWeightUp - m;
 #pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
             uint32_t s[32], pk[16];
@@ -562,13 +583,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
                 if (hidden(32 * ch + k)) s[k] = __float_as_uint(-INFINITY);
             float la = 0.f, lb = 0.f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float f = c * (k < 8 ? kf.x : kf.y);
-              float x0, x1;
-              ffma2(x0, x1, __uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]), f, f, neg_m, neg_m);
-              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              fadd2(la, lb, la, lb, p0, p1);
-              pk[k] = pack_bf16x2(p0, p1);
+            for (int h = 0; h < 2; ++h) {
+              const float f = c * fabsf(h ? kf.y : kf.x);
+              float w[16];
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                ffma2(w[k], w[k + 1], __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]), f, f, neg_m, neg_m);
+                w[k] = ex2_approx(w[k]), w[k + 1] = ex2_approx(w[k + 1]);
+                fadd2(la, lb, la, lb, w[k], w[k + 1]);
+              }
+              if ((h ? kf.y : kf.x) < 0.f) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) pk[8 * h + k] = pack_bf16x2(w[2 * k], w[2 * k + 1]);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const __half2 x = __floats2half2_rn(w[2 * k], w[2 * k + 1]);
+                  pk[8 * h + k] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+              }
             }
             l += la + lb;
             tmem_st_x16(tS + ch * 16, pk);  // over scores that have been read
@@ -582,6 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
         ok = mbar_wait_warp(&bars.o_full[t], o_phase, abort_flag, p.st, kWhere | (10u << 16));
         o_phase ^= 1u;
       }
+      m -= kWeightUp;  // what the weights and sums are relative to
       sm.M[t][row] = m;
       sm.L[t][row] = l;
       asm volatile("bar.sync 1, 256;" ::: "memory");
