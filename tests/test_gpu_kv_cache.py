@@ -6,8 +6,12 @@ exactly, its scores are fp32 sums of 128 terms, and it rounds the weights
 (times V's scale) and O to bf16, as the other windowed kernels do.
 
 The form for many query rows ("tiles") also rounds what it multiplies:
-  V to bf16, by U |v| at most: U (P |V|) more in O, whose bound so becomes
-    U |O| + (2 U + E) (P |V|);
+  V, where sixteen keys' scales allow it, to fp16 over 2^12: by 2^-12 |v|, or below fp16's normal numbers by 2^-25 times
+    2^12. There the scales are 2^-7 or more in 4 bits, 2^-11 in 8, so a group's largest value `top` is 7 * 2^-7 or
+    127 * 2^-11 at least, but for the half a step by which bf16 may have rounded its scale up, and 2^-13 is at most
+    top / 400. Otherwise to bf16, by U |v|. Either way by dv = max(U |v|, min(2^-13, top / 400)) at most.
+  the weights to fp16 with them: 2^-12 of each, or 2^-25 over the 2^7 by which they are raised, of a sum that is 1 at
+    least: 2^-32 of each key's |v| more. So O is within U |O| + (U + E) (P |V|) + P dV + 2^-32 sum |v|.
   K in 8 bits, of which the magnitude's lower 4 bits times the scale go to fp16:
     by 2^-12 * 15 s <= 2^-12 * 15 / 127 * (the group's largest |k|) (1 + 2^-8) a
     value, so a score by scale * sum_G (sum |q|) top_G 2^-12 * 15 / 127 (1 + 2^-8),
@@ -78,7 +82,9 @@ def _check_tiles(q, kd, vd, window, sinks, pos0, o, lse, bits, name):
         ltol = E[rows, 0] + 2.0 ** -21 * (1 + np.abs(r["lse"][0, h][rows]))
         assert (np.abs(lse[0, h][rows] - r["lse"][0, h][rows]) <= ltol).all(), f"{name} LSE"
         want = r["o"][0, :, h]
-        bound = 2.0 ** -8 * np.abs(want) + (2 * 2.0 ** -8 + E) * (p @ vh) + 1e-30
+        top = np.repeat(vh.reshape(-1, 4, 32).max(axis=2), 32, axis=1)
+        dv = np.maximum(2.0 ** -8 * vh, np.minimum(2.0 ** -13, top / 400))
+        bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + E) * (p @ vh) + p @ dv + 2.0 ** -32 * vh.sum(axis=0) + 1e-30
         ratio = np.abs(o[0, :, h] - want) / bound
         assert (ratio <= 1).all(), f"{name} O: off by {ratio.max():.2f} bounds"
 
@@ -323,6 +329,83 @@ def test_attention_over_the_range_of_values(bits, kscale, vscale):
     _check(q, cache, _held(k, bits), _held(v, bits), (Smax,), 700, 4)
 
 
+SOME = [("line", 2, 12, 2, 1, 30011), ("line", 1, 2, 1, 1, 40000), ("tiles", 1, 8, 2, 32, 12000), ("tiles", 2, 8, 1, 9, 20000)]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("which", ["small V", "large V", "small K", "large K", "V of all sizes", "V grows", "small groups"])
+@pytest.mark.parametrize("form,B,H,Hkv,T,Smax", SOME)
+def test_each_form_over_the_range_of_values(form, B, H, Hkv, T, Smax, which, bits):
+    """As above in the other forms, and V whose sizes change from key to key, along the keys, and among channels."""
+    assert lcb.attn_cache_decode_form(B, H, Hkv, T, Smax, bits) == form
+    k, v, q = _rand(10, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))
+    g = torch.Generator(device="cuda").manual_seed(11)
+    if which == "small V":
+        v = v * 2.0 ** -90
+    elif which == "large V":
+        v = v * 2.0 ** 95
+    elif which in ("small K", "large K"):
+        f = 2.0 ** (-60 if which == "small K" else 60)
+        k, q = k * f, q / f
+    elif which == "V of all sizes":
+        v = v * torch.exp2(torch.randint(-30, 30, (B, Smax, Hkv, 1), generator=g, device="cuda").float()).to(BF16)
+    elif which == "V grows":
+        v = v * torch.exp2((torch.arange(Smax, device="cuda") * 80 // Smax - 40).float()).to(BF16)[None, :, None, None]
+    else:
+        v = v * torch.exp2(-torch.arange(D, device="cuda") // 32 * 5.0).to(BF16)
+    cache = lcb.kv_cache_write(lcb.kv_cache_empty(B, Hkv, Smax, bits=bits), k, v, _lens(*[Smax] * B))
+    _check(q, cache, _held(k, bits), _held(v, bits), [Smax] * B, None, 0, which)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("form,B,H,Hkv,T,Smax,lens,window,sinks", [
+    ("line", 2, 12, 2, 2, 30011, (29000, 17001), 20000, 300),
+    ("line", 1, 16, 1, 1, 80000, (79990,), 70001, 5),
+    ("tiles", 1, 8, 2, 32, 12000, (11500,), 9001, 3),
+    ("tiles", 2, 8, 1, 9, 20000, (19999, 19001), 18000, 129),
+    ("tiles", 2, 4, 2, 200, 4000, (3900, 2500), 2000, 0),
+])
+def test_each_form_reads_nothing_hidden(form, bits, B, H, Hkv, T, Smax, lens, window, sinks):
+    """Rows that no token sees hold NaN; then the newest row does, which the last token alone sees."""
+    assert lcb.attn_cache_decode_form(B, H, Hkv, T, Smax, bits, window, sinks) == form
+    cache, kd, vd = _filled(7, B, Hkv, Smax, bits)
+    q, = _rand(8, (B, T, H, D))
+    want = _check(q, cache, kd, vd, lens, window, sinks)
+    for b, n in enumerate(lens):
+        cache[b, :, n:] = 0xFF
+        cache[b, :, sinks:max(sinks, n - T - window + 1)] = 0xFF
+    got = lcb.attn_cache_decode(q, cache, _lens(*lens), window, sinks)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for b, n in enumerate(lens):
+        cache[b, 0, n - 1, -16:-8] = 0xFF  # K's scales
+    o, lse = lcb.attn_cache_decode(q, cache, _lens(*lens), window, sinks)
+    G = H // Hkv
+    assert torch.isnan(o[:, -1, :G]).all() and torch.isnan(lse[:, :G, -1]).all()
+    assert torch.equal(o[:, :-1], want[0][:, :-1]) and torch.equal(o[:, -1, G:], want[0][:, -1, G:])
+    assert torch.equal(lse[:, :, :-1], want[1][:, :, :-1]) and torch.equal(lse[:, G:], want[1][:, G:])
+    for b, n in enumerate(lens):
+        cache[b, 0, n - 1] = 0xFF
+    o, lse = lcb.attn_cache_decode(q, cache, _lens(*lens), window, sinks)
+    assert torch.isnan(o[:, -1, :G]).all() and torch.isnan(lse[:, :G, -1]).all()
+    assert torch.equal(o[:, :, G:], want[0][:, :, G:]) and torch.equal(lse[:, :, :-1], want[1][:, :, :-1])
+    if form != "tiles":  # there V's NaN reach the tile's other rows
+        assert torch.equal(o[:, :-1], want[0][:, :-1])
+
+
+def test_more_sequences_than_the_line_holds():
+    """Above 1024 sequences of any length: checked against the same sequences in calls of their own."""
+    B, H, Hkv, T, Smax = 1300, 4, 2, 2, 260
+    cache, kd, vd = _filled(23, B, Hkv, Smax, 4)
+    q, = _rand(24, (B, T, H, D))
+    lens = [(37 * b) % (Smax + 20) for b in range(B)]
+    o, lse = lcb.attn_cache_decode(q, cache, _lens(*lens), 200, 3)
+    for b in (0, 1, 511, 1024, 1299):
+        _check(q[b:b + 1], cache[b:b + 1], kd[b:b + 1], vd[b:b + 1], [lens[b]], 200, 3)
+    for s in range(0, B, 1000):
+        a = lcb.attn_cache_decode(q[s:s + 1000], cache[s:s + 1000], _lens(*lens[s:s + 1000]), 200, 3)
+        torch.testing.assert_close(o[s:s + 1000].float(), a[0].float(), rtol=2 ** -6, atol=2 ** -6)
+
+
 def test_infinite_and_nan_queries_stay_in_their_rows():
     cache, kd, vd = _filled(11, 1, 2, 200, 4)
     q, = _rand(12, (1, 3, 8, D))
@@ -406,7 +489,7 @@ def test_chunked_prompt_through_the_cache():
         _check(q[:, s:e].contiguous(), cache, _held(k, 8), _held(v, 8), (e,), 300, 4)
 
 
-@pytest.mark.parametrize("B,H,Hkv,Smax", [(2, 8, 2, 900), (1, 1, 1, 60000), (1, 8, 8, 20000)])
+@pytest.mark.parametrize("B,H,Hkv,Smax", [(2, 8, 2, 900), (1, 1, 1, 60000), (1, 8, 8, 20000), (1, 64, 2, 20000)])
 def test_repeated_captured_and_on_another_stream(B, H, Hkv, Smax):
     """The same bits every time; a captured step replays with the lengths and tokens of the moment."""
     cache, kd, vd = _filled(21, B, Hkv, Smax, 4)
@@ -444,19 +527,46 @@ def test_repeated_captured_and_on_another_stream(B, H, Hkv, Smax):
     assert lens.tolist() == [Smax // 2 + 4] * B
 
 
-def test_two_calls_at_once():
-    """Calls that overlap on two streams, each with buffers of its own."""
+@pytest.mark.parametrize("H", [4, 64])
+def test_two_calls_at_once(H):
+    """Calls that overlap on two streams, each with buffers of its own; then two captured ones, replayed together."""
     sets = []
     for i in range(2):
         cache, kd, vd = _filled(50 + i, 1, 2, 40000, 4)
-        q, = _rand(60 + i, (1, 2, 4, D))
+        q, = _rand(60 + i, (1, 2, H, D))
         sets.append((cache, kd, vd, q, torch.cuda.Stream(), []))
+    assert lcb.attn_cache_decode_form(1, H, 2, 2, 40000) == ("line" if H == 4 else "tiles")
+    lens = _lens(40000)
     torch.cuda.synchronize()
     for _ in range(10):
         for cache, _, _, q, stream, out in sets:
             with torch.cuda.stream(stream):
-                out.append(lcb.attn_cache_decode(q, cache, _lens(40000)))
+                out.append(lcb.attn_cache_decode(q, cache, lens))
+    torch.cuda.synchronize()
+    graphs = []
+    for cache, _, _, q, stream, out in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out.append(lcb.attn_cache_decode(q, cache, lens))
+        graphs.append(graph)
+    for _ in range(10):
+        for graph, (_, _, _, _, stream, _) in zip(graphs, sets):
+            with torch.cuda.stream(stream):
+                graph.replay()
     torch.cuda.synchronize()
     for cache, kd, vd, q, _, out in sets:
         want = _check(q, cache, kd, vd, (40000,), None, 0)
         assert all(torch.equal(o, want[0]) and torch.equal(lse, want[1]) for o, lse in out)
+
+
+def test_wrong_devices():
+    cache, _, _ = _filled(70, 1, 2, 64, 4)
+    k, v, q = _rand(71, (1, 3, 2, D), (1, 3, 2, D), (1, 3, 4, D))
+    lens = _lens(64)
+    for call in (lambda: lcb.kv_cache_write(cache, k.cpu(), v, lens), lambda: lcb.kv_cache_write(cache, k, v, lens.cpu()),
+                 lambda: lcb.kv_cache_write(cache.cpu(), k, v, lens), lambda: lcb.kv_cache_read(cache.cpu(), 3),
+                 lambda: lcb.kv_cache_read(cache, 3, lens=lens.cpu()), lambda: lcb.attn_cache_decode(q.cpu(), cache, lens),
+                 lambda: lcb.attn_cache_decode(q, cache, lens.cpu()), lambda: lcb.attn_cache_decode(q, cache.cpu(), lens),
+                 lambda: lcb.attn_cache_decode(q, cache, lens, o=q.cpu())):
+        with pytest.raises((ValueError, lcb.AttnError)):
+            call()
