@@ -880,6 +880,57 @@ def run_window(args):
     return 0
 
 
+def run_cache(args):
+    """Times the K/V cache in 4 bits: a prompt of 32768 tokens x 32 heads written and read back, and the newest token of
+    a batch of four against 32K windows of 40 heads (the shape of --window's decode); prints one JSON line (not the
+    headline bench line)."""
+    import torch
+
+    import long_context_causal_blockwise_gb300 as lcb
+
+    Sc, Hc, Bd, Hd, Wd, Smax, sinks, bits = 32768, 32, 4, 40, 32768, 40000, 4, 4
+    dev = torch.device("cuda", 0)
+    lcb.load()
+    g = torch.Generator(device=dev).manual_seed(0)
+
+    def timed(fn, steps):
+        for _ in range(max(3, args.warmup)):
+            fn()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(steps):
+            fn()
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / steps
+
+    steps = max(3, min(args.steps, 20))
+    k, v = (torch.randn(1, Sc, Hc, D, generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+    cache = lcb.kv_cache_empty(1, Hc, Sc, bits=bits, device=dev)
+    row = cache.shape[3]
+    lens = torch.full((1,), Sc, dtype=torch.int32, device=dev)
+    t_write = timed(lambda: lcb.kv_cache_write(cache, k, v, lens), steps)
+    t_read = timed(lambda: lcb.kv_cache_read(cache, Sc, k=k, v=v), steps)
+    nb_rows = Sc * Hc * (row + 4 * D)
+    kd, vd = (torch.randn(Bd, Smax, Hd, D, generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+    cache = lcb.kv_cache_empty(Bd, Hd, Smax, bits=bits, device=dev)
+    lens = torch.full((Bd,), Smax, dtype=torch.int32, device=dev)
+    lcb.kv_cache_write(cache, kd, vd, lens)
+    del kd, vd
+    q = torch.randn(Bd, 1, Hd, D, generator=g, device=dev).to(torch.bfloat16)
+    t_dec = timed(lambda: lcb.attn_cache_decode(q, cache, lens, Wd, sinks), steps)
+    nb_dec = Bd * Hd * (Wd + sinks) * row + Bd * Hd * (4 * D + 4)
+    pk = load_peaks()
+    print(json.dumps({
+        "metric": f"K/V cache in {bits} bits, {row} bytes a row: S{Sc} H{Hc} written and read back; decode B{Bd} H{Hd}, "
+                  f"window {Wd}",
+        "write_ms": t_write, **hbm_fields("write_", nb_rows, t_write, pk), "read_ms": t_read,
+        **hbm_fields("read_", nb_rows, t_read, pk), "decode_ms": t_dec, **hbm_fields("decode_", nb_dec, t_dec, pk),
+        "inputs": "larger than L2; no flush"}), flush=True)
+    return 0
+
+
 def run_merge(args):
     """Times the stand-alone LSE merge (attn_lse_merge) of one bf16 block into
     the fp32 accumulator, 16384 rows x 32 heads x 128 (the ring step's merge at
@@ -990,6 +1041,8 @@ def main():
                     help="time the RoPE kernel on a [1, 524288, 32, 128] tensor")
     ap.add_argument("--window", action="store_true",
                     help="time windowed attention with sinks (forward, backward, decode)")
+    ap.add_argument("--cache", action="store_true",
+                    help="time the K/V cache in 4 bits (write, read, decode)")
     ap.add_argument("--zigzag", action="store_true",
                     help="time the one-device zigzag ring (S=131072, P=8) against monolithic attention")
     ap.add_argument("--ulysses", action="store_true",
@@ -1003,6 +1056,8 @@ def main():
         return run_rope(args)
     if args.window:
         return run_window(args)
+    if args.cache:
+        return run_cache(args)
     if args.merge:
         return run_merge(args)
     if args.ulysses:

@@ -39,9 +39,15 @@
 // by a second kernel (cache_line.cuh). Streams are joined first, in tensor memory:
 // the warps of both see the same lanes, and take half of the channels each.
 //
-// Bound, for 64 rows: 128 keys' two products take the tensor core 1024 clocks
-// (a tile has 128 rows whether it uses them or not), their weights the
-// exponential unit as many, HBM 770.
+// Bound: 128 keys (a unit) take 2440 clocks. Their two products take the tensor
+// core 1024 of them (a tile has 128 rows whether it uses them or not), 128 rows'
+// weights the exponential unit 1024, HBM 770 in 4 bits. Shared memory has the most
+// to do: 96 KB that the products read, 82 KB that unpacking reads and writes, 18 KB
+// that arrive, 1540 clocks at 128 bytes each; and an unpacking warp's turn (its
+// sixteen keys of K 960 clocks, of V 700, two fences 330, and its waits) leaves no
+// room. 8 heads x 65536 keys, 64 rows: 53 us in 4 bits, 64 in 8; 32 heads x 20000,
+// 128 rows: 60. More warps only share this out: 16 softmax warps of 64 keys each
+// 56 us, 16 unpacking warps 69, 12 in turn 60.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

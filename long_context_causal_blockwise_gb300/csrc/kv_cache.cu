@@ -12,6 +12,14 @@
 // heads, whose rows lie side by side in K and V. Records go through shared
 // memory, where a lane's codes are scattered over the row, and leave or arrive
 // as contiguous 16-byte accesses: the rows of a head follow one another.
+//
+// 32768 tokens x 32 heads, at 6.7 TB/s 103 us in 4 bits and 123 in 8: read back in
+// 103 and 120, written in 120 and 122. At the memory's rate an SM has 116 issue slots
+// for a written row's 256 numbers, and in 4 bits they are what is short: with K's and
+// V's lanes in branches of their own, a division a group and signs moved one by one
+// it took 203 us, with operands selected instead 143, and with the sums of products
+// below 120. 1777 tokens x 3 x 8 heads in 8 bits: written in 8.5 us, read in 6.6 (of
+// 5.0 by bytes); one token: 2.3 and 1.7.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -38,8 +38,6 @@
 
 namespace lcb {
 
-constexpr int kCacheGroup = 32;  // channels of a scale
-
 constexpr int cache_v_offset(int bits) { return 16 * bits; }
 constexpr int cache_scale_offset(int bits) { return 32 * bits; }
 constexpr int cache_row_bytes(int bits) { return 32 * bits + 16; }
