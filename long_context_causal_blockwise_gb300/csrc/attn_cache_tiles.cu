@@ -126,17 +126,17 @@ __device__ __forceinline__ uint32_t hfma2_bf16(uint32_t a, uint32_t b, uint32_t 
 constexpr int kVDown = 12;      // V's tiles hold V times 2^-12,
 constexpr float kWeightUp = 7;  // the weights are times 2^7: 2^15 at most, as a maximum may lag by kRescaleThreshold
 
-// A lane (key, t) of eight keys takes its key's channels 32 G + 8 t .. + 7 of all four groups, odd keys the two of a pair
-// of groups in reverse: eight lanes, of two neighbouring rows, then store into different banks.
+// A lane (key, t) of eight keys takes its key's channels 32 G + 8 t .. + 7 of all four groups. Eight neighbouring lanes
+// have keys four apart: their records' quarters, 144 or 272 bytes a key, and their chunks of the tile's rows lie in
+// different banks.
 struct Lane {
   int key, t;
-  bool odd;
-  __device__ __forceinline__ explicit Lane(int lane) : key(lane >> 2), t(lane & 3), odd(lane & 4) {}
-  // of the j-th group's chunk in a tile, for rows 8 keys apart
-  __device__ __forceinline__ uint32_t first_chunk(int row0) const { return chunk_at(row0 + key, t + (odd ? 4 : 0)); }
+  __device__ __forceinline__ explicit Lane(int lane) : key((lane >> 3) | (lane & 4)), t(lane & 3) {}
+  // of the first group's chunk in a tile, for rows 8 keys apart
+  __device__ __forceinline__ uint32_t first_chunk(int row0) const { return chunk_at(row0 + key, t); }
 };
-__device__ __forceinline__ uint8_t* chunk_of(uint8_t* tile, uint32_t first, int round, int j) {
-  return tile + ((first ^ (j & 1 ? 64u : 0u)) + round * 1024 + (j >> 1) * kHalfBytes);
+__device__ __forceinline__ uint8_t* chunk_of(uint8_t* tile, uint32_t first, int round, int G) {
+  return tile + ((first ^ (G & 1 ? 64u : 0u)) + round * 1024 + (G >> 1) * kHalfBytes);
 }
 
 // Whether a scale of V among the sixteen keys is not one for fp16.
@@ -170,30 +170,20 @@ __device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int 
   if (lane == 0) *factor = exp2_int(min(10 + e, 127)) * (wide ? -1.f : 1.f);
   const Lane at(lane);
   const uint8_t* r0 = rec + at.key * kRec;
-  const uint32_t first = at.first_chunk(row0), order = at.odd ? 0x1032 : 0x3210;
+  const uint32_t first = at.first_chunk(row0);
 #pragma unroll
   for (int round = 0; round < 2; ++round) {
     const uint8_t* r = r0 + round * 8 * kRec;
     const uint2 sc = *reinterpret_cast<const uint2*>(r + cache_scale_offset(BITS));
-    uint32_t w[4 * (BITS / 4)];  // the lane's words, of groups in its order
+    uint32_t w[BITS];  // the lane's words
 #pragma unroll
     for (int i = 0; i < BITS / 4; ++i) {
       const uint4 v = *reinterpret_cast<const uint4*>(r + 64 * i + 16 * at.t);
-      if (BITS == 4) {
-        w[0] = at.odd ? v.y : v.x;
-        w[1] = at.odd ? v.x : v.y;
-        w[2] = at.odd ? v.w : v.z;
-        w[3] = at.odd ? v.z : v.w;
-      } else {
-        w[4 * i] = at.odd ? v.z : v.x;
-        w[4 * i + 1] = at.odd ? v.w : v.y;
-        w[4 * i + 2] = at.odd ? v.x : v.z;
-        w[4 * i + 3] = at.odd ? v.y : v.w;
-      }
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t x = permute_bytes(j < 2 ? sc.x : sc.y, 0, order);
+      const uint32_t x = j < 2 ? sc.x : sc.y;
       const float f = (j & 1 ? bf16hi_to_f32(x) : bf16lo_to_f32(x)) * up;
       const __half2 d = __floats2half2_rn(f, f);
       const uint32_t s = *reinterpret_cast<const uint32_t*>(&d);
@@ -238,7 +228,7 @@ __device__ __forceinline__ void unpack_v(const uint8_t* rec, uint8_t* tile, int 
   const Lane at(lane);
   const uint8_t* r0 = rec + at.key * kRec;
   const uint32_t first = at.first_chunk(row0);
-  const uint32_t sel0 = at.odd ? 0x7632 : 0x5410, sel1 = at.odd ? 0x5410 : 0x7632;  // of pairs of groups: the first, the second
+  constexpr uint32_t kSel[2] = {0x5410, 0x7632};  // of pairs of groups: the first, the second
 #pragma unroll
   for (int round = 0; round < 2; ++round) {
     const uint8_t* r = r0 + round * 8 * kRec;
@@ -260,7 +250,7 @@ __device__ __forceinline__ void unpack_v(const uint8_t* rec, uint8_t* tile, int 
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t sel = j ? sel1 : sel0;
+          const uint32_t sel = kSel[j];
           st_shared16(chunk_of(tile, first, round, 2 * gp + j), permute_bytes(c[0][0], c[0][1], sel) & keep,
                       permute_bytes(c[0][2], c[0][3], sel) & keep, permute_bytes(c[1][0], c[1][1], sel) & keep,
                       permute_bytes(c[1][2], c[1][3], sel) & keep);
@@ -268,19 +258,16 @@ __device__ __forceinline__ void unpack_v(const uint8_t* rec, uint8_t* tile, int 
       }
     } else {
       const uint32_t s01 = v_scales<WIDE>(sc.x), s23 = v_scales<WIDE>(sc.y);
-      uint32_t w[2][4];  // of groups in the lane's order
+      uint32_t w[2][4];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         const uint4 v = *reinterpret_cast<const uint4*>(r + cache_v_offset(BITS) + 32 * at.t + 16 * f);
-        w[f][0] = at.odd ? v.y : v.x;
-        w[f][1] = at.odd ? v.x : v.y;
-        w[f][2] = at.odd ? v.w : v.z;
-        w[f][3] = at.odd ? v.z : v.w;
+        w[f][0] = v.x, w[f][1] = v.y, w[f][2] = v.z, w[f][3] = v.w;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t s2 = j < 2 ? s01 : s23;
-        const uint32_t s = permute_bytes(s2, s2, j & 1 ? sel1 : sel0);
+        const uint32_t s = permute_bytes(s2, s2, j & 1 ? 0x3232 : 0x1010);
         uint32_t o[4];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
