@@ -536,13 +536,14 @@ int attn_cache_decode_form(int B, int H, int Hkv, int T, int Smax, int D, int bi
  * for all query rows of its head up to 16 of them (T * H / Hkv), or 128 in the
  * form for many rows. Deterministic. Any T; for the hundreds of tokens of a
  * prompt's chunk, lcb_kv_cache_read and attn_window_fwd are faster.
- * What is rounded: weights (and O) to bf16, as in the windowed attention; in the
- * form for many rows also V, to bf16 as lcb_kv_cache_read gives it.
- * A row with NaN makes NaN of those query rows alone that see it; in the form for
- * many rows V's NaN also of others of their tile. window, sinks, scale, heads, q, o, lse and their
- * strides as attn_window_decode; the cache as above. workspace: device memory
- * of at least attn_cache_decode_workspace_bytes(), 16-byte aligned, contents
- * ignored (NULL where that is 0); calls that may overlap on the GPU need
+ * What is rounded: weights times V's scales (and O) to bf16; in the form for many
+ * rows weights and V, to fp16 where V's scales for sixteen keys on end are
+ * ordinary (2^-7 to 16, in 8 bits 2^-11 to 16, or zero), otherwise to bf16.
+ * A cached NaN makes NaN of those query rows alone that see it (V's in its
+ * channels). O is finite where |v| < 2^113 / keys. window, sinks, scale, heads, q,
+ * o, lse and their strides as attn_window_decode; the cache as above. workspace:
+ * device memory of at least attn_cache_decode_workspace_bytes(), 16-byte aligned,
+ * contents ignored (NULL where that is 0); calls that may overlap on the GPU need
  * workspaces of their own.
  */
 int attn_cache_decode(const void* q, const void* cache, const int* lens, void* o, float* lse, int B, int H, int Hkv,

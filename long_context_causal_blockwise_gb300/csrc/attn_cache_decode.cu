@@ -56,7 +56,6 @@ namespace {
 constexpr int kD = 128;
 constexpr int kSms = 152;
 constexpr int kStep = 16;  // keys of a product, and of a warp's turn
-constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum is raised lazily, P stays <= 256
 constexpr uint32_t kWhere = 9u << 24;
 
@@ -107,8 +106,8 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
 //     weight goes into the second product four times, once with each scale.
 //   4: a column 2r + h is half h of row r: the groups 2h and 2h + 1, Q being zero
 //     in the other half. So two sums and two operands do where eight columns of
-//     whole rows take four, and lane t has row t alone: 310 instructions for
-//     sixteen keys instead of 345.
+//     whole rows take four, and lane t has row t alone: 283 instructions for
+//     sixteen keys in 4 bits, a fifth fewer.
 template <int ROWS>
 struct Cols {
   static constexpr bool kHalves = ROWS == 4;
@@ -830,10 +829,11 @@ struct ClusterChoice {
 // most keys that the sizes allow, fitted to both forms at fourteen sizes. A
 // cluster form is done when its warps' share of the bytes is; the line form has a
 // longer start, a second kernel, and some 3 us for each tile that a CTA begins
-// after its first; with more than four rows it is bound by its instructions. us, cluster / line, 4 bits unless said: 32 heads x 777 keys 6 /
-// 8, x 2052 8 / 12; 8 x 8 heads x 20001, eight rows, 37 / 42; 160 x 32772 127 / 120;
-// 8 x 131072 in 8 bits 69 / 51; 8 x 524288 204 / 105; 1 x 524288 123 / 25; 4 x
-// 100000 33 / 26; 512 x 2000 25 / 39; 80 x 5000 in 8 bits 20 / 24; 40 x 32768 39 / 42.
+// after its first; with more than four rows it is bound by its instructions. us,
+// cluster / line, 4 bits unless said: 32 heads x 777 keys 6 / 8, x 2052 8 / 12; 8 x 8
+// heads x 20001, eight rows, 37 / 42; 160 x 32772 127 / 120; 8 x 131072 in 8 bits
+// 69 / 51; 8 x 524288 204 / 105; 1 x 524288 123 / 25; 4 x 100000 33 / 26; 512 x 2000
+// 25 / 39; 80 x 5000 in 8 bits 20 / 24; 40 x 32768 39 / 42.
 template <int ROWS, int BITS>
 int line_ctas(const Plan& a, const ClusterChoice<ROWS, BITS>& c, const ContextKey& at) {
   const int n = LineForm<ROWS, BITS>::ctas(at);
@@ -842,7 +842,8 @@ int line_ctas(const Plan& a, const ClusterChoice<ROWS, BITS>& c, const ContextKe
   const double hbm_us = static_cast<double>(a.tiles) * a.keys * cache_row_bytes(BITS) / 6.7e6;
   const double busy = static_cast<double>(c.in_flight) / (kSms * warps_per_sm(ROWS));
   const double cluster_us = 5 + 1.15 * hbm_us / std::min(1.0, (BITS == 4 ? 1.0 : 1.5) * busy);
-  const double line_us = 12 + (BITS == 4 && ROWS > 4 ? 1.25 : 1.08) * hbm_us + 3.5 * std::max(0.0, static_cast<double>(a.tiles) / n - 1);
+  const double more = std::max(0.0, static_cast<double>(a.tiles) / n - 1);
+  const double line_us = 12 + (BITS == 4 && ROWS > 4 ? 1.25 : 1.08) * hbm_us + 3.5 * more;
   return line_us < cluster_us ? n : 0;
 }
 
@@ -896,9 +897,9 @@ struct Launch {
 
 // CTAs of the form with 128-row tiles (attn_cache_tiles.cu), or 0 for one of the
 // forms here, which unpack the keys once for every sixteen rows: two estimates in
-// us. us, those here / 128-row tiles: 8 heads x 65536 keys, 32 rows 65 / 50, 64 rows
-// 109 / 51, in 8 bits 139 / 63; 32 x 20000, 128 rows 208 / 58; 8 x 65536, window 16384,
-// 4000 rows 1222 / 431; 8 x 2000, 56 rows 13 / 17; 8 x 500, 20 rows 9 / 14.
+// us. us, those here / 128-row tiles: 8 heads x 65536 keys, 32 rows 65 / 51, 64 rows
+// 109 / 54, in 8 bits 139 / 64; 32 x 20000, 128 rows 208 / 61; 8 x 65536, window 16384,
+// 4000 rows 1222 / 455; 8 x 2000, 56 rows 13 / 17; 8 x 500, 20 rows 9 / 14.
 static int tiles_ctas(const Plan& a, int T, int G, int bits, const ContextKey& at) {
   const long long R = static_cast<long long>(T) * G;
   if (R <= 16 || a.B > kLineSequences) return 0;

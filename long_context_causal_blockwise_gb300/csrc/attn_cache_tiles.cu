@@ -33,7 +33,9 @@
 // weights of 2^-21 of the largest. Otherwise, and where fewer than sixteen keys
 // exist, bf16 with the same powers of two: off by half a step, 2^-9 to 2^-8 of each
 // value. (bf16 for all of them: errors 2.8e-3 of the outputs instead of 1.7e-3, which
-// is what rounding these to bf16 costs.)
+// is what rounding these to bf16 costs, and 2 us of 53 less.) NaN of V are zeros in
+// the tile, so that a weight of zero leaves nothing of them; the rows that see one
+// are told by bits, 1 us of 53.
 //
 // The units of all tiles are dealt evenly to the CTAs, one to an SM, and joined
 // by a second kernel (cache_line.cuh). Streams are joined first, in tensor memory:
@@ -45,8 +47,8 @@
 // to do: 96 KB that the products read, 82 KB that unpacking reads and writes, 18 KB
 // that arrive, 1540 clocks at 128 bytes each; and an unpacking warp's turn (its
 // sixteen keys of K 960 clocks, of V 700, two fences 330, and its waits) leaves no
-// room. 8 heads x 65536 keys, 64 rows: 53 us in 4 bits, 64 in 8; 32 heads x 20000,
-// 128 rows: 60. More warps only share this out: 16 softmax warps of 64 keys each
+// room. 8 heads x 65536 keys, 64 rows: 54 us in 4 bits, 64 in 8; 32 heads x 20000,
+// 128 rows: 61. More warps only share this out: 16 softmax warps of 64 keys each
 // 56 us, 16 unpacking warps 69, 12 in turn 60.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -88,7 +90,9 @@ struct Smem {  // 1024-byte aligned
   uint8_t raw[Raw<BITS>::kStages][Raw<BITS>::kBytes];
   // by unit modulo 4: the power of two taken from K, for each sixteen keys; below zero where their V and P are bf16
   float k_factor[4][8];
+  uint2 v_nan[4][8];  // and then, of which scales of V are NaN: bits 2 key + G / 2, G even and odd
   float M[2][kRows], L[2][kRows];
+  uint32_t nan[2][kRows];
   Bars bars;
   int lens[kLineSequences];
 };
@@ -139,20 +143,27 @@ __device__ __forceinline__ uint8_t* chunk_of(uint8_t* tile, uint32_t first, int 
   return tile + ((first ^ (G & 1 ? 64u : 0u)) + round * 1024 + (G >> 1) * kHalfBytes);
 }
 
-// Whether a scale of V among the sixteen keys is not one for fp16.
+// Whether a scale of V among the sixteen keys is not one for fp16; if so, which ones are NaN (v_nan; an infinity, which
+// kv_cache_write never leaves, counts as one).
 template <int BITS>
-__device__ __forceinline__ bool wide_v(const uint8_t* rec, int lane) {
+__device__ __forceinline__ bool wide_v(const uint8_t* rec, uint2* nan, int lane) {
   const uint32_t x = *reinterpret_cast<const uint32_t*>(rec + (lane >> 1) * cache_row_bytes(BITS) +
                                                         cache_scale_offset(BITS) + 8 + 4 * (lane & 1));
   constexpr uint32_t kLow = (BITS == 4 ? 120u : 116u) << 7, kHigh = 131u << 7;  // 2^-7 or 2^-11, 2^4
   auto out = [](uint32_t a) { return a != 0 && (a < kLow || a >= kHigh); };
-  return __any_sync(0xffffffffu, out(x & 0xffffu) || out(x >> 16));
+  const bool wide = __any_sync(0xffffffffu, out(x & 0xffffu) || out(x >> 16));
+  if (wide) {
+    const uint32_t even = __ballot_sync(0xffffffffu, (x & 0x7f80u) == 0x7f80u);
+    const uint32_t odd = __ballot_sync(0xffffffffu, (x & 0x7f800000u) == 0x7f800000u);
+    if (lane == 0) *nan = make_uint2(even, odd);
+  }
+  return wide;
 }
 
 // Sixteen keys of K by a warp: rows row0 .. + 15 of the tile; the first nk of the records exist.
 template <int BITS>
-__device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int row0, int nk, float* factor, int lane,
-                                         bool& is_wide) {
+__device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int row0, int nk, float* factor, uint2* nan,
+                                         int lane, bool& is_wide) {
   constexpr int kRec = cache_row_bytes(BITS);
   // the largest finite scale of the sixteen keys, as bits
   uint32_t top = 0;
@@ -163,7 +174,12 @@ __device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int 
     top = max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u);
   }
   top = __reduce_max_sync(0xffffffffu, top);
-  const bool wide = is_wide = nk < 16 || wide_v<BITS>(rec, lane);
+  bool wide = wide_v<BITS>(rec, nan, lane);
+  if (!wide && nk < 16) {
+    if (lane == 0) *nan = make_uint2(0, 0);
+    wide = true;
+  }
+  is_wide = wide;
   // scales are below 2^(e + 1): times 2^(14 - e) they are fp16, and with the codes' 2^-24 they make s n 2^(-10 - e)
   const int e = max(static_cast<int>(top >> 7) - 127, -100);
   const float up = exp2_int(14 - e);
@@ -216,7 +232,12 @@ __device__ __forceinline__ uint32_t v_value(uint32_t code, uint32_t s, int sh) {
 }
 template <bool WIDE>
 __device__ __forceinline__ uint32_t v_scales(uint32_t s) {
-  if (WIDE) return hmul2_bf16(s, 0x39803980u);
+  if (WIDE) {
+    // a NaN's values are zeros here; the rows that see them get theirs at the end (v_nan)
+    if ((s & 0x7f80u) == 0x7f80u) s &= 0xffff0000u;
+    if ((s & 0x7f800000u) == 0x7f800000u) s &= 0xffffu;
+    return hmul2_bf16(s, 0x39803980u);
+  }
   const __half2 h = __floats2half2_rn(bf16lo_to_f32(s) * 4096.f, bf16hi_to_f32(s) * 4096.f);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
@@ -377,9 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
         if (!ok) break;
         bool wide = true;
         if (mine > 0)
-          unpack_k<BITS>(rec, sm.K[kt], row0, mine, &sm.k_factor[i & 3][w], lane, wide);
+          unpack_k<BITS>(rec, sm.K[kt], row0, mine, &sm.k_factor[i & 3][w], &sm.v_nan[i & 3][w], lane, wide);
         else if (lane == 0)
-          sm.k_factor[i & 3][w] = -1.f;
+          sm.k_factor[i & 3][w] = -1.f, sm.v_nan[i & 3][w] = make_uint2(0, 0);
         fence_to_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.k_full[kt]);
@@ -508,6 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.q_full);
       float m = -INFINITY, l = 0.f;
+      uint32_t row_nan = 0;  // channel groups in which the row sees a NaN of V
+      auto spread = [](uint32_t two) { return (two & 1u) | (two & 2u) << 1; };  // groups 0, 2
       const int first = (i0 & 1) == t ? 0 : 1;  // the stream's first unit of the tile
       for (int x = first; x < n && ok; x += 2) {
         const int i = i0 + x;
@@ -586,6 +609,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
                 fadd2(la, lb, la, lb, w[k], w[k + 1]);
               }
               if ((h ? kf.y : kf.x) < 0.f) {
+                const uint2 nan = sm.v_nan[i & 3][2 * ch + h];
+                if ((nan.x | nan.y) != 0)  // V's NaN, as far as the row sees their keys
+#pragma unroll 1
+                  for (int k = 0; k < 16; ++k)
+                    if (!hidden(32 * ch + 16 * h + k))
+                      row_nan |= spread(nan.x >> 2 * k) | spread(nan.y >> 2 * k) << 1;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) pk[8 * h + k] = pack_bf16x2(w[2 * k], w[2 * k + 1]);
               } else {
@@ -611,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       m -= kWeightUp;  // what the weights and sums are relative to
       sm.M[t][row] = m;
       sm.L[t][row] = l;
+      sm.nan[t][row] = row_nan;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       tc_fence_after();
       // ---- both streams' parts of the row, channels 64 t .. + 63
@@ -632,6 +662,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             v[k] = (have_0 ? g0 * __uint_as_float(x[k]) : 0.f) + (have_1 ? g1 * __uint_as_float(y[k]) : 0.f);
+          if ((sm.nan[0][row] | sm.nan[1][row]) >> (2 * t + (ch >> 1)) & 1u)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __int_as_float(0x7fc00000);
           if (r < R_all) {
             if (whole_tile) {
               __nv_bfloat16* dst = p.o + a.b * p.o_bs + static_cast<long long>(tok) * p.o_rs +

@@ -388,8 +388,32 @@ def test_each_form_reads_nothing_hidden(form, bits, B, H, Hkv, T, Smax, lens, wi
     o, lse = lcb.attn_cache_decode(q, cache, _lens(*lens), window, sinks)
     assert torch.isnan(o[:, -1, :G]).all() and torch.isnan(lse[:, :G, -1]).all()
     assert torch.equal(o[:, :, G:], want[0][:, :, G:]) and torch.equal(lse[:, :, :-1], want[1][:, :, :-1])
-    if form != "tiles":  # there V's NaN reach the tile's other rows
-        assert torch.equal(o[:, :-1], want[0][:, :-1])
+    assert torch.equal(o[:, :-1], want[0][:, :-1])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("form,B,H,Hkv,T,Smax", [("cluster", 1, 16, 2, 2, 600), ("line", 1, 8, 2, 2, 40000),
+                                                 ("tiles", 1, 8, 2, 32, 12000), ("tiles", 2, 8, 1, 9, 20000)])
+def test_nan_in_v_stays_in_its_channels_and_rows(form, B, H, Hkv, T, Smax, bits):
+    """A NaN among one key's V makes NaN of its group of channels, for the tokens that see the key."""
+    assert lcb.attn_cache_decode_form(B, H, Hkv, T, Smax, bits) == form
+    k, v = _rand(80, (B, Smax, Hkv, D), (B, Smax, Hkv, D))
+    q, = _rand(81, (B, T, H, D))
+    lens = _lens(*[Smax] * B)
+    cache = lcb.kv_cache_write(lcb.kv_cache_empty(B, Hkv, Smax, bits=bits), k, v, lens)
+    want = lcb.attn_cache_decode(q, cache, lens)
+    G = H // Hkv
+    for key, channel, first in ((Smax - T + 1, 70, 1), (Smax - 1, 0, T - 1), (Smax // 2 + 3, 127, 0)):
+        bad = v.clone()
+        bad[0, key, -1, channel] = float("inf") if channel else float("nan")
+        lcb.kv_cache_write(cache, k, bad, lens)
+        o, lse = lcb.attn_cache_decode(q, cache, lens)
+        nan = torch.zeros_like(o, dtype=torch.bool)
+        nan[0, first:, -G:, channel // 32 * 32:channel // 32 * 32 + 32] = True
+        assert torch.equal(torch.isnan(o), nan) and not torch.isnan(lse).any()
+        # (the step's other V are rounded to bf16 then, in the form for many rows)
+        torch.testing.assert_close(o[~nan].float(), want[0][~nan].float(), rtol=2.0 ** -6, atol=2.0 ** -8)
+        torch.testing.assert_close(lse, want[1], rtol=0, atol=2.0 ** -20)
 
 
 def test_more_sequences_than_the_line_holds():
