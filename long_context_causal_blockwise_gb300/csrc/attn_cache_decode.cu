@@ -107,7 +107,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
 //   4: a column 2r + h is half h of row r: the groups 2h and 2h + 1, Q being zero
 //     in the other half. So two sums and two operands do where eight columns of
 //     whole rows take four, and lane t has row t alone: 283 instructions for
-//     sixteen keys in 4 bits, a fifth fewer.
+//     sixteen keys in 4 bits (eight rows: some 305).
 template <int ROWS>
 struct Cols {
   static constexpr bool kHalves = ROWS == 4;
