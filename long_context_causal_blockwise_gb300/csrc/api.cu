@@ -108,7 +108,9 @@ bool rows_apart(int B, int rows, long long row, long long rs, long long bs) {
 // The same for the heads of a [B, heads] view of `head` bytes each.
 bool heads_apart(int B, int heads, long long head, long long hs, long long bs) {
   if (heads > 1 && hs < head) return false;
-  return B == 1 || bs >= (heads - 1) * hs + head || (bs >= head && (heads == 1 || hs >= (B - 1) * bs + head));
+  const __int128 all_heads = static_cast<__int128>(heads - 1) * hs + head;  // (any int times a stride)
+  const __int128 all_batches = static_cast<__int128>(B - 1) * bs + head;
+  return B == 1 || bs >= all_heads || (bs >= head && (heads == 1 || hs >= all_batches));
 }
 bool stride_ok(long long s) { return s >= 0 && (s % 8) == 0 && s < (1LL << 38); }
 

@@ -107,14 +107,22 @@ __device__ __forceinline__ int head_units(const CacheDecode& p, int len, int row
   return n;
 }
 
-// The units of all sequences, and of those before `b`, by a whole warp.
+// The units of all sequences, and of those before `b`, by a whole warp, which shares out the row tiles of every sequence.
+// (lens may be the caller's own: lengths past the cache, or below zero, count as they do everywhere.)
 __device__ __forceinline__ int all_units(const CacheDecode& p, const int* lens, int b, int rows, int keys, int lane,
                                          int* before) {
   int n = 0, m = 0;
-  for (int i = lane; i < p.B; i += 32) {
-    const int x = p.Hkv * head_units(p, lens[i], rows, keys);
+  for (int i = 0, mt = lane; i < p.B;) {
+    if (mt >= p.row_tiles) {
+      const int more = mt / p.row_tiles;
+      mt -= more * p.row_tiles;
+      i += more;
+      continue;
+    }
+    const int x = p.Hkv * make_tile(p, length(p, lens[i]), 0, 0, mt, rows, keys).units;
     n += x;
     if (i < b) m += x;
+    mt += 32;
   }
   *before = __reduce_add_sync(0xffffffffu, m);
   return __reduce_add_sync(0xffffffffu, n);
@@ -214,11 +222,16 @@ __global__ void __launch_bounds__(256) cache_decode_join_kernel(const __grid_con
   const Tile a = make_tile(p, len, b, hk, mt, ROWS, KEYS);
   int start;
   const int N = all_units(p, p.lens, b, ROWS, KEYS, lane, &start);
-  start += hk * head_units(p, len, ROWS, KEYS);
-  for (int i = 0; i < mt; ++i) start += make_tile(p, len, b, hk, i, ROWS, KEYS).units;
+  {
+    int x = 0;  // units of the sequence's tiles before this one
+    for (int i = lane; i < p.row_tiles; i += 32)
+      x += (hk + (i < mt)) * make_tile(p, len, b, hk, i, ROWS, KEYS).units;
+    start += __reduce_add_sync(0xffffffffu, x);
+  }
   const int r = sub * kRowsHere + warp / kSplit, part = warp % kSplit;
   const Share share(max(N, 1), max(1, min(N, ctas)));
-  const int i0 = share.part_of(start), i1 = share.part_of(start + max(a.units, 1) - 1);
+  // (never past the slots that there are, even if somebody changes the lengths meanwhile)
+  const int i0 = min(share.part_of(start), ctas - 1), i1 = min(share.part_of(start + max(a.units, 1) - 1), ctas - 1);
   const bool at_start = share.begin(i0) == start;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (a.r0 + r >= p.T * p.G) {  // the last tile has fewer rows

@@ -263,6 +263,10 @@ FORMS = [
     ("tiles", 2, 4, 2, 200, 3000, (3000, 150), 2000, 129),      # four row tiles, tokens before the first row
     ("tiles", 3, 3, 3, 130, 3500, (3500, 0, 129), None, 5),     # two, the second with two rows; a sequence without keys
     ("tiles", 1, 24, 1, 2, 150000, (149999,), None, 0),         # 48 rows, many keys
+    ("line", 3, 8, 2, 1, 30000, (40000, -7, 29000), None, 0),   # lengths past the cache and below zero
+    ("line", 2, 8, 2, 1, 30000, (2 ** 31 - 1, 30000), None, 0),
+    ("tiles", 3, 8, 1, 9, 20000, (30000, -2 ** 31, 19000), None, 0),
+    ("tiles", 1, 2, 1, 3500, 3600, (5000,), 300, 7),            # more row tiles than a warp has lanes
 ]
 
 

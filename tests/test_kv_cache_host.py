@@ -102,6 +102,8 @@ def test_write_and_read_refusals_need_no_gpu():
             assert call(**bad) == ERR_ARG, bad
     assert write(lens=NUL) == ERR_ARG and write(T=-1) == ERR_ARG
     assert write(ch=1424) == ERR_ARG and write(cb=1440) == ERR_ARG  # heads, or sequences, of the output overlap
+    for B, Hkv in ((2 ** 31 - 1, 2), (2, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1)):  # strides times counts past 64 bits
+        assert write(B=B, Hkv=Hkv, ch=2 ** 39, cb=2 ** 39, rs=2 ** 38 - 8, bs=2 ** 38 - 8) == ERR_ARG
     assert write(T=0, cache=NUL) == OK and write(Smax=0, cache=NUL) == OK
     assert read(start=7) == ERR_ARG and read(start=-1) == ERR_ARG and read(n=11) == ERR_ARG and read(n=-1) == ERR_ARG
     assert read(bs=512) == ERR_ARG  # sequences of the output overlap
@@ -124,6 +126,12 @@ def test_attention_refusals_need_no_gpu():
         assert call(**bad) == ERR_ARG, bad
     assert call(T=0, q=NUL) == OK
     assert lib.attn_cache_decode_workspace_bytes(1, 3, 2, 1, 10, 128, 4, 5, 0) == 0  # a refused size
+    assert lib.attn_cache_decode_form(1, 3, 2, 1, 10, 128, 4, 5, 0) == ERR_ARG
+    assert lib.attn_cache_decode_form(1, 4, 2, 1, 10, 64, 4, 5, 0) == ERR_UNSUPPORTED
+    assert lib.attn_cache_decode_form(1, 4, 2, 1, 10, 128, 5, 5, 0) == ERR_UNSUPPORTED
+    assert lib.attn_cache_decode_form(1, 4, 2, 0, 10, 128, 4, 5, 0) == 0
+    with pytest.raises(lcb.AttnError):
+        lcb.attn_cache_decode_form(1, 4, 2, 1, 10, 4, window=-3)
     assert lib.attn_cache_decode_workspace_bytes(1, 4, 2, 1, 0, 128, 4, 5, 0) == 0
 
 
