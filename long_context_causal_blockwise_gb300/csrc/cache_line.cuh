@@ -101,28 +101,38 @@ __device__ __forceinline__ void store_row(const CacheDecode& p, const Tile& a, i
 
 constexpr int slot_floats(int rows) { return rows * (kCacheD + 2); }
 
-__device__ __forceinline__ int head_units(const CacheDecode& p, int len, int rows, int keys) {  // of a K/V head's row tiles
-  int n = 0;
-  for (int mt = 0; mt < p.row_tiles; ++mt) n += make_tile(p, len, 0, 0, mt, rows, keys).units;
-  return n;
+// Units of the first n row tiles of a K/V head.
+__device__ __forceinline__ int head_units(const CacheDecode& p, int len, int n, int rows, int keys) {
+  int x = 0;
+  for (int mt = 0; mt < n; ++mt) x += make_tile(p, len, 0, 0, mt, rows, keys).units;
+  return x;
 }
+// The same by a whole warp.
+__device__ __forceinline__ int head_units_warp(const CacheDecode& p, int len, int n, int rows, int keys, int lane) {
+  int x = 0;
+  for (int mt = lane; mt < n; mt += 32) x += make_tile(p, len, 0, 0, mt, rows, keys).units;
+  return __reduce_add_sync(0xffffffffu, x);
+}
+// Whether a warp takes the sequences one by one, its lanes the row tiles, or a lane a sequence.
+__device__ __forceinline__ bool lanes_take_tiles(const CacheDecode& p) { return p.row_tiles >= 32; }
 
-// The units of all sequences, and of those before `b`, by a whole warp, which shares out the row tiles of every sequence.
-// (lens may be the caller's own: lengths past the cache, or below zero, count as they do everywhere.)
+// The units of all sequences, and of those before `b`, by a whole warp. (lens may be the caller's own: lengths past the
+// cache, or below zero, count as they do everywhere.)
 __device__ __forceinline__ int all_units(const CacheDecode& p, const int* lens, int b, int rows, int keys, int lane,
                                          int* before) {
   int n = 0, m = 0;
-  for (int i = 0, mt = lane; i < p.B;) {
-    if (mt >= p.row_tiles) {
-      const int more = mt / p.row_tiles;
-      mt -= more * p.row_tiles;
-      i += more;
-      continue;
+  if (lanes_take_tiles(p)) {
+    for (int i = 0; i < p.B; ++i) {
+      if (i == b) m = n;
+      n += p.Hkv * head_units_warp(p, length(p, lens[i]), p.row_tiles, rows, keys, lane);
     }
-    const int x = p.Hkv * make_tile(p, length(p, lens[i]), 0, 0, mt, rows, keys).units;
+    *before = m;
+    return n;
+  }
+  for (int i = lane; i < p.B; i += 32) {
+    const int x = p.Hkv * head_units(p, length(p, lens[i]), p.row_tiles, rows, keys);
     n += x;
     if (i < b) m += x;
-    mt += 32;
   }
   *before = __reduce_add_sync(0xffffffffu, m);
   return __reduce_add_sync(0xffffffffu, n);
@@ -132,8 +142,18 @@ __device__ __forceinline__ int all_units(const CacheDecode& p, const int* lens, 
 __device__ __forceinline__ int sequence_of(const CacheDecode& p, const int* lens, int x, int rows, int keys, int lane,
                                            int* before) {
   int sum = 0;
+  if (lanes_take_tiles(p)) {
+    for (int b = 0;; ++b) {
+      const int next = sum + p.Hkv * head_units_warp(p, lens[b], p.row_tiles, rows, keys, lane);
+      if (next > x || b == p.B - 1) {
+        *before = sum;
+        return b;
+      }
+      sum = next;
+    }
+  }
   for (int b0 = 0;; b0 += 32) {
-    const int mine = b0 + lane < p.B ? p.Hkv * head_units(p, lens[b0 + lane], rows, keys) : 0;
+    const int mine = b0 + lane < p.B ? p.Hkv * head_units(p, lens[b0 + lane], p.row_tiles, rows, keys) : 0;
     int upto = mine;  // inclusive prefix
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -169,7 +189,7 @@ struct Walk {
     const int x0 = share.begin(cta);
     left = share.begin(cta + 1) - x0;
     b = sequence_of(p, lens, x0, ROWS, KEYS, lane, &before);
-    const int per_head = head_units(p, lens[b], ROWS, KEYS);
+    const int per_head = head_units_warp(p, lens[b], p.row_tiles, ROWS, KEYS, lane);
     hk = (x0 - before) / per_head;
     mt = 0;
     off = x0 - before - hk * per_head;
@@ -222,12 +242,7 @@ __global__ void __launch_bounds__(256) cache_decode_join_kernel(const __grid_con
   const Tile a = make_tile(p, len, b, hk, mt, ROWS, KEYS);
   int start;
   const int N = all_units(p, p.lens, b, ROWS, KEYS, lane, &start);
-  {
-    int x = 0;  // units of the sequence's tiles before this one
-    for (int i = lane; i < p.row_tiles; i += 32)
-      x += (hk + (i < mt)) * make_tile(p, len, b, hk, i, ROWS, KEYS).units;
-    start += __reduce_add_sync(0xffffffffu, x);
-  }
+  start += hk * head_units_warp(p, len, p.row_tiles, ROWS, KEYS, lane) + head_units_warp(p, len, mt, ROWS, KEYS, lane);
   const int r = sub * kRowsHere + warp / kSplit, part = warp % kSplit;
   const Share share(max(N, 1), max(1, min(N, ctas)));
   // (never past the slots that there are, even if somebody changes the lengths meanwhile)
