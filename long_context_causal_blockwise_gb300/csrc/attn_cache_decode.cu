@@ -899,7 +899,7 @@ struct Launch {
 // forms here, which unpack the keys once for every sixteen rows: two estimates in
 // us. us, those here / 128-row tiles: 8 heads x 65536 keys, 32 rows 65 / 51, 64 rows
 // 109 / 54, in 8 bits 139 / 64; 32 x 20000, 128 rows 208 / 61; 8 x 65536, window 16384,
-// 4000 rows 1222 / 455; 8 x 2000, 56 rows 13 / 17; 8 x 500, 20 rows 9 / 14.
+// 4000 rows 1222 / 337; 8 x 2000, 56 rows 13 / 17; 8 x 500, 20 rows 9 / 14.
 static int tiles_ctas(const Plan& a, int T, int G, int bits, const ContextKey& at) {
   const long long R = static_cast<long long>(T) * G;
   if (R <= 16 || a.B > kLineSequences) return 0;
