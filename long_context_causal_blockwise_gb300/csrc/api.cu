@@ -112,6 +112,12 @@ bool heads_apart(int B, int heads, long long head, long long hs, long long bs) {
   const __int128 all_batches = static_cast<__int128>(B - 1) * bs + head;
   return B == 1 || bs >= all_heads || (bs >= head && (heads == 1 || hs >= all_batches));
 }
+// A quantised cache [B, Hkv, Smax, row bytes]; as an output its heads also lie apart from one another.
+bool cache_view(const void* p, long long bs, long long hs, int B, int Hkv, int Smax, int bits, bool output) {
+  if (!p || !aligned16(p) || bs < 0 || hs < 0 || bs % 16 || hs % 16 || bs >= (1LL << 40) || hs >= (1LL << 40))
+    return false;
+  return !output || heads_apart(B, Hkv, static_cast<long long>(Smax) * cache_row_bytes(bits), hs, bs);
+}
 bool stride_ok(long long s) { return s >= 0 && (s % 8) == 0 && s < (1LL << 38); }
 
 // A bf16 input [B, rows, heads, 128] for TMA or 16-byte loads.
@@ -995,13 +1001,6 @@ int attn_window_decode(const void* q, const void* k, const void* v, const int* l
                                                o_batch_stride, lse_head_stride, lse_batch_stride),
                                     st),
                 st);
-}
-
-// A quantised cache [B, Hkv, Smax, row bytes]; as an output its heads also lie apart from one another.
-static bool cache_view(const void* p, long long bs, long long hs, int B, int Hkv, int Smax, int bits, bool output) {
-  if (!p || !aligned16(p) || bs < 0 || hs < 0 || bs % 16 || hs % 16 || bs >= (1LL << 40) || hs >= (1LL << 40))
-    return false;
-  return !output || heads_apart(B, Hkv, static_cast<long long>(Smax) * cache_row_bytes(bits), hs, bs);
 }
 
 int lcb_kv_cache_row_bytes(int bits) {
