@@ -225,7 +225,7 @@ __device__ __forceinline__ void begin(State<ROWS, BITS>& w, const RawQ<ROWS>& ra
   w.up_limit = 0x10001u * ((kUpRange + 127) * 128 - 1);
 }
 
-// V's scales (of keys g and g + 8) are so large that weights times `up` would
+// V's scales (of the lane's two keys) are so large that weights times `up` would
 // not fit: the smaller `up` that the largest one needs. NaN is none of them.
 template <int ROWS, int BITS>
 __device__ __forceinline__ void lower_up(State<ROWS, BITS>& w, const uint4 (&sc)[2]) {
@@ -252,6 +252,11 @@ __device__ __forceinline__ void lower_up(State<ROWS, BITS>& w, const uint4 (&sc)
       for (int k = 0; k < 4; ++k) w.o[i][nt][k] *= f;
 }
 
+// Which of a step's sixteen keys is row x + 8 h of the first product, and so the second one's x + 8 h along the sum: rows
+// 2 m and 2 m + 1 are four keys apart modulo eight, rows 0, 2, 4, 6 two and 1, 3, 5, 7 two. A record is four banks past
+// a multiple of 32, so that neither product's loads have two lanes in one bank.
+__device__ __forceinline__ int key_of(int x, int h) { return (x & 1 ? 8 + ((x + 3) & 7) : x) + h; }
+
 // Sixteen keys at `rec`, the first nk of which exist: key j0 + i of the
 // sequence at i. CUT: some of them may be hidden from some rows.
 template <int ROWS, int BITS, bool CUT>
@@ -259,12 +264,14 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
                                      int t) {
   using C = Cols<ROWS>;
   constexpr int kRec = cache_row_bytes(BITS), kWords = BITS / 4;  // of a group, for a lane
-  // scales of keys g and g + 8: four of K, four of V
-  uint4 sc[2] = {*reinterpret_cast<const uint4*>(rec + g * kRec + cache_scale_offset(BITS)),
-                 *reinterpret_cast<const uint4*>(rec + (g + 8) * kRec + cache_scale_offset(BITS))};
+  // the lane's keys of the first product, and their scales: four of K, four of V
+  const int key0 = key_of(g, 0);
+  const uint8_t* mine = rec + key0 * kRec;
+  uint4 sc[2] = {*reinterpret_cast<const uint4*>(mine + cache_scale_offset(BITS)),
+                 *reinterpret_cast<const uint4*>(mine + kRec + cache_scale_offset(BITS))};
   if (CUT) {
-    if (g >= nk) sc[0].z = sc[0].w = 0u;
-    if (g + 8 >= nk) sc[1].z = sc[1].w = 0u;
+    if (key0 >= nk) sc[0].z = sc[0].w = 0u;
+    if (key0 + 1 >= nk) sc[1].z = sc[1].w = 0u;
   }
   auto k_scale = [&](int h, int c) {
     const uint32_t x = c < 2 ? sc[h].x : sc[h].y;
@@ -274,7 +281,7 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
     const uint32_t x = c < 2 ? sc[h].z : sc[h].w;
     return c & 1 ? bf16hi_to_f32(x) : bf16lo_to_f32(x);
   };
-  // ---- S^T: s[h][i] is key 8h + g, the lane's row i
+  // ---- S^T: s[h][i] is key_of(g, h), the lane's row i
   float s[2][C::kMine];
   {
     uint32_t kw[2][4 * kWords];  // a key's words: one, or two, of each group
@@ -282,7 +289,7 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
-        const uint4 v = *reinterpret_cast<const uint4*>(rec + (g + 8 * h) * kRec + 64 * i + 16 * t);
+        const uint4 v = *reinterpret_cast<const uint4*>(mine + h * kRec + 64 * i + 16 * t);
         kw[h][4 * i] = v.x;
         kw[h][4 * i + 1] = v.y;
         kw[h][4 * i + 2] = v.z;
@@ -291,7 +298,7 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
     float acc[C::kSums][C::kTiles][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      uint32_t x[2][4];  // pairs of channels of keys g and g + 8
+      uint32_t x[2][4];  // pairs of channels of the lane's two keys
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const Fields f = k4_fields(kw[h][c]);
@@ -329,7 +336,7 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
   if (CUT) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int i = 8 * h + g, j = j0 + i;
+      const int i = key0 + h, j = j0 + i;
 #pragma unroll
       for (int x = 0; x < C::kMine; ++x) {
         const int pp = w.pr[x];
@@ -384,10 +391,10 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
                                                 : pack_bf16x2(product(2 * nt, c), product(C::kMine > 1 ? 2 * nt + 1 : 0, c)));
   }
   // ---- O^T += V^T P^T
-  uint32_t vw[4][2 * kWords];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+  uint32_t vw[4][2 * kWords];  // of rows 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint8_t* at = rec + (2 * t + (i & 1) + 8 * (i >> 1)) * kRec + cache_v_offset(BITS) + 2 * BITS * g;
+    const uint8_t* at = rec + key_of(2 * t + (i & 1), i >> 1) * kRec + cache_v_offset(BITS) + 2 * BITS * g;
     if (BITS == 4) {
       const uint2 v = *reinterpret_cast<const uint2*>(at);
       vw[i][0] = v.x;
@@ -402,7 +409,7 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    uint32_t a[4][2];  // the group's four channels: keys 2t, 2t + 1 and 2t + 8, 2t + 9
+    uint32_t a[4][2];  // the group's four channels: rows 2t, 2t + 1 and 2t + 8, 2t + 9
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (BITS == 4) {
