@@ -837,15 +837,16 @@ struct ClusterChoice {
 // cluster form is done when its warps' share of the bytes is; the line form has a
 // longer start, a second kernel, and some 3 us for each tile that a CTA begins
 // after its first; with more than four rows it is bound by its instructions. us,
-// cluster / line, 4 bits unless said: 32 heads x 777 keys 6 / 8, x 2052 8 / 12; 8 x 8
-// heads x 20001, eight rows, 37 / 42; 160 x 32772 127 / 120; 8 x 131072 in 8 bits
-// 69 / 51; 8 x 524288 204 / 105; 1 x 524288 123 / 25; 4 x 100000 33 / 26; 512 x 2000
-// 25 / 39; 80 x 5000 in 8 bits 20 / 24; 40 x 32768 39 / 42.
+// cluster / line, 4 bits unless said: 32 heads x 2052 keys 8 / 10; 8 x 8 heads x
+// 20001, eight rows, 38 / 42; 160 x 32772 127 / 119; 8 x 131072 in 8 bits 69 / 50; 8 x
+// 524288 204 / 103; 1 x 524288 123 / 26; 4 x 100000 33 / 23; 512 x 2000 26 / 36; 80 x
+// 5000 in 8 bits 20 / 24; 40 x 32768 40 / 40; 8 x 65536, eight rows 37 / 26, sixteen
+// 56 / 37. Of 33 sizes four take the slower form, by 3, 4, 12 and 15%.
 template <int ROWS, int BITS>
 int line_ctas(const Plan& a, const ClusterChoice<ROWS, BITS>& c, const ContextKey& at) {
   const int n = LineForm<ROWS, BITS>::ctas(at);
   const long long units = a.tiles * ((a.keys + Line<ROWS, BITS>::kKeys - 1) / Line<ROWS, BITS>::kKeys + 1);
-  if (n <= 0 || a.B > kLineSequences || a.row_tiles > 8 || units >= 1LL << 31) return 0;
+  if (n <= 0 || a.B > kLineSequences || a.row_tiles > 8 || units + a.tiles * kTileCost<ROWS> >= 1LL << 31) return 0;
   const double hbm_us = static_cast<double>(a.tiles) * a.keys * cache_row_bytes(BITS) / 6.7e6;
   const double busy = static_cast<double>(c.in_flight) / (kSms * warps_per_sm(ROWS));
   const double cluster_us = 5 + 1.15 * hbm_us / std::min(1.0, (BITS == 4 ? 1.0 : 1.5) * busy);
@@ -904,17 +905,17 @@ struct Launch {
 
 // CTAs of the form with 128-row tiles (attn_cache_tiles.cu), or 0 for one of the
 // forms here, which unpack the keys once for every sixteen rows: two estimates in
-// us. us, those here / 128-row tiles: 8 heads x 65536 keys, 32 rows 65 / 51, 64 rows
-// 109 / 54, in 8 bits 139 / 64; 32 x 20000, 128 rows 208 / 61; 8 x 65536, window 16384,
-// 4000 rows 1222 / 337; 8 x 2000, 56 rows 13 / 17; 8 x 500, 20 rows 9 / 14.
+// us. us, those here / 128-row tiles: 8 heads x 65536 keys, 32 rows 61 / 47, 64 rows
+// 104 / 48, in 8 bits 131 / 60; 32 x 20000, 128 rows 201 / 55; 8 x 65536, window 16384,
+// 4000 rows 1237 / 334; 8 x 2000, 56 rows 13 / 17; 8 x 500, 20 rows 9 / 14.
 static int tiles_ctas(const Plan& a, int T, int G, int bits, const ContextKey& at) {
   const long long R = static_cast<long long>(T) * G;
   if (R <= 16 || a.B > kLineSequences) return 0;
   const long long units = a.tiles / a.row_tiles * ((R + 127) / 128) * (a.keys / 128 + 2);
-  if (units >= 1LL << 31) return 0;
+  if (units + a.tiles * kTileCost<128> >= 1LL << 31) return 0;
   const int n = cache_tiles_ctas(bits, at);
   if (n <= 0) return 0;
-  const double tiles_us = 13 + (bits == 4 ? 1.5 : 1.9) * static_cast<double>(units) / n;
+  const double tiles_us = 12 + (bits == 4 ? 1.3 : 1.7) * static_cast<double>(units) / n;
   const double here_us = 9 + 0.75e-3 * static_cast<double>(a.tiles) * ((a.keys + 15) / 16);
   return tiles_us < here_us ? n : 0;
 }

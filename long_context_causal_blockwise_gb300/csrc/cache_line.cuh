@@ -93,44 +93,57 @@ __device__ __forceinline__ void store_row(const CacheDecode& p, const Tile& a, i
 
 // ------------------------------------------------------------------ the units of all tiles as one line
 //
-// Tiles stand in the order (sequence, K/V head, row tile); their N units (fewer
-// than 2^31) are dealt in order to C CTAs, C at most N so that each has some.
-// What a CTA has of a tile that it does not have whole goes to slot 2 i (the
-// first tile that it meets) or 2 i + 1 (the last): ROWS x 128 sums, then the
-// rows' maxima, then their sums of weights.
+// Tiles stand in the order (sequence, K/V head, row tile), each with as many
+// places as it has units, and kTileCost more in front of those where it has any:
+// what a CTA spends on coming to another tile (its last one's sums stored, Q, an
+// empty pipeline), in units. The N places (fewer than 2^31) are dealt in order to
+// C CTAs, C at most N. What a CTA has of a tile that it does not have whole goes
+// to slot 2 i (the first tile of which it has a unit) or 2 i + 1 (the last): ROWS
+// x 128 sums, then the rows' maxima, then their sums of weights.
+// (us, without the cost / with it: 8 tiles of 512 units with 128 rows, of which 7
+// of 152 CTAs see two, 55 / 48; 8 heads x 65536 keys, eight rows 30 / 26; 4 x 100000,
+// six rows, 26.5 / 23.4; 8 x 524288, four rows, 104 / 103. Half or one
+// and a half times the cost: within 2% for four and eight rows, 5% for the others.)
+
+template <int ROWS>
+constexpr int kTileCost = ROWS == 128 ? 7 : ROWS == 16 ? 9 : ROWS == 8 ? 5 : 4;
+template <int ROWS>
+__device__ __forceinline__ int places(int units) { return units > 0 ? units + kTileCost<ROWS> : 0; }
 
 constexpr int slot_floats(int rows) { return rows * (kCacheD + 2); }
 
-// Units of the first n row tiles of a K/V head.
-__device__ __forceinline__ int head_units(const CacheDecode& p, int len, int n, int rows, int keys) {
+// Places of the first n row tiles of a K/V head.
+template <int ROWS>
+__device__ __forceinline__ int head_places(const CacheDecode& p, int len, int n, int keys) {
   int x = 0;
-  for (int mt = 0; mt < n; ++mt) x += make_tile(p, len, 0, 0, mt, rows, keys).units;
+  for (int mt = 0; mt < n; ++mt) x += places<ROWS>(make_tile(p, len, 0, 0, mt, ROWS, keys).units);
   return x;
 }
 // The same by a whole warp.
-__device__ __forceinline__ int head_units_warp(const CacheDecode& p, int len, int n, int rows, int keys, int lane) {
+template <int ROWS>
+__device__ __forceinline__ int head_places_warp(const CacheDecode& p, int len, int n, int keys, int lane) {
   int x = 0;
-  for (int mt = lane; mt < n; mt += 32) x += make_tile(p, len, 0, 0, mt, rows, keys).units;
+  for (int mt = lane; mt < n; mt += 32) x += places<ROWS>(make_tile(p, len, 0, 0, mt, ROWS, keys).units);
   return __reduce_add_sync(0xffffffffu, x);
 }
 // Whether a warp takes the sequences one by one, its lanes the row tiles, or a lane a sequence.
 __device__ __forceinline__ bool lanes_take_tiles(const CacheDecode& p) { return p.row_tiles >= 32; }
 
-// The units of all sequences, and of those before `b`, by a whole warp. (lens may be the caller's own: lengths past the
+// The places of all sequences, and of those before `b`, by a whole warp. (lens may be the caller's own: lengths past the
 // cache, or below zero, count as they do everywhere.)
-__device__ __forceinline__ int all_units(const CacheDecode& p, const int* lens, int b, int rows, int keys, int lane,
-                                         int* before) {
+template <int ROWS>
+__device__ __forceinline__ int all_places(const CacheDecode& p, const int* lens, int b, int keys, int lane, int* before) {
   int n = 0, m = 0;
   if (lanes_take_tiles(p)) {
     for (int i = 0; i < p.B; ++i) {
       if (i == b) m = n;
-      n += p.Hkv * head_units_warp(p, length(p, lens[i]), p.row_tiles, rows, keys, lane);
+      n += p.Hkv * head_places_warp<ROWS>(p, length(p, lens[i]), p.row_tiles, keys, lane);
     }
     *before = m;
     return n;
   }
   for (int i = lane; i < p.B; i += 32) {
-    const int x = p.Hkv * head_units(p, length(p, lens[i]), p.row_tiles, rows, keys);
+    const int x = p.Hkv * head_places<ROWS>(p, length(p, lens[i]), p.row_tiles, keys);
     n += x;
     if (i < b) m += x;
   }
@@ -138,13 +151,13 @@ __device__ __forceinline__ int all_units(const CacheDecode& p, const int* lens, 
   return __reduce_add_sync(0xffffffffu, n);
 }
 
-// The sequence of unit x, and the units before it.
-__device__ __forceinline__ int sequence_of(const CacheDecode& p, const int* lens, int x, int rows, int keys, int lane,
-                                           int* before) {
+// The sequence of place x, and the places before it.
+template <int ROWS>
+__device__ __forceinline__ int sequence_of(const CacheDecode& p, const int* lens, int x, int keys, int lane, int* before) {
   int sum = 0;
   if (lanes_take_tiles(p)) {
     for (int b = 0;; ++b) {
-      const int next = sum + p.Hkv * head_units_warp(p, lens[b], p.row_tiles, rows, keys, lane);
+      const int next = sum + p.Hkv * head_places_warp<ROWS>(p, lens[b], p.row_tiles, keys, lane);
       if (next > x || b == p.B - 1) {
         *before = sum;
         return b;
@@ -153,7 +166,7 @@ __device__ __forceinline__ int sequence_of(const CacheDecode& p, const int* lens
     }
   }
   for (int b0 = 0;; b0 += 32) {
-    const int mine = b0 + lane < p.B ? p.Hkv * head_units(p, lens[b0 + lane], p.row_tiles, rows, keys) : 0;
+    const int mine = b0 + lane < p.B ? p.Hkv * head_places<ROWS>(p, lens[b0 + lane], p.row_tiles, keys) : 0;
     int upto = mine;  // inclusive prefix
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -176,37 +189,39 @@ __device__ __forceinline__ int sequence_of(const CacheDecode& p, const int* lens
 template <int ROWS, int KEYS>
 struct Walk {
   Tile a;
-  int off, left;  // the CTA's next unit in the tile; units that it still has
+  int off, left;  // the CTA's next unit in the tile; places that it still has
   int b, hk, mt;
 
   // False for a CTA without units.
   __device__ __forceinline__ bool start(const CacheDecode& p, const int* lens, int cta, int ctas, int lane) {
     int before;
-    const int N = all_units(p, lens, 0, ROWS, KEYS, lane, &before);
+    const int N = all_places<ROWS>(p, lens, 0, KEYS, lane, &before);
     const int C = min(N, ctas);
     if (cta >= C) return false;
     const Share share(N, C);
-    const int x0 = share.begin(cta);
-    left = share.begin(cta + 1) - x0;
-    b = sequence_of(p, lens, x0, ROWS, KEYS, lane, &before);
-    const int per_head = head_units_warp(p, lens[b], p.row_tiles, ROWS, KEYS, lane);
-    hk = (x0 - before) / per_head;
-    mt = 0;
-    off = x0 - before - hk * per_head;
-    a = make_tile(p, lens[b], b, hk, mt, ROWS, KEYS);
-    settle(p, lens);
-    return true;
+    int x = share.begin(cta);
+    left = share.begin(cta + 1) - x;
+    b = sequence_of<ROWS>(p, lens, x, KEYS, lane, &before);
+    const int per_head = head_places_warp<ROWS>(p, lens[b], p.row_tiles, KEYS, lane);
+    x -= before;
+    hk = x / per_head;
+    x -= hk * per_head;
+    for (mt = 0;; ++mt) {
+      a = make_tile(p, lens[b], b, hk, mt, ROWS, KEYS);
+      if (x < places<ROWS>(a.units) || mt == p.row_tiles - 1) break;
+      x -= places<ROWS>(a.units);
+    }
+    off = max(0, x - kTileCost<ROWS>);
+    left -= max(0, kTileCost<ROWS> - x);
+    return left > 0;
   }
   // Units of the present tile that are the CTA's.
   __device__ __forceinline__ int here() const { return min(left, a.units - off); }
   __device__ __forceinline__ void advance(const CacheDecode& p, const int* lens, int n) {
     left -= n;
     off += n;
-    settle(p, lens);
-  }
-  __device__ __forceinline__ void settle(const CacheDecode& p, const int* lens) {
     while (off >= a.units && left > 0) {
-      off -= a.units;
+      off = 0;
       if (++mt == p.row_tiles) {
         mt = 0;
         if (++hk == p.Hkv) {
@@ -215,6 +230,7 @@ struct Walk {
         }
       }
       a = make_tile(p, lens[b], b, hk, mt, ROWS, KEYS);
+      if (a.units > 0) left -= kTileCost<ROWS>;
     }
   }
 };
@@ -240,14 +256,16 @@ __global__ void __launch_bounds__(256) cache_decode_join_kernel(const __grid_con
   const int b = tile / p.Hkv, hk = tile % p.Hkv;
   const int len = length(p, p.lens[b]);
   const Tile a = make_tile(p, len, b, hk, mt, ROWS, KEYS);
-  int start;
-  const int N = all_units(p, p.lens, b, ROWS, KEYS, lane, &start);
-  start += hk * head_units_warp(p, len, p.row_tiles, ROWS, KEYS, lane) + head_units_warp(p, len, mt, ROWS, KEYS, lane);
+  int start;  // the tile's first place
+  const int N = all_places<ROWS>(p, p.lens, b, KEYS, lane, &start);
+  start += hk * head_places_warp<ROWS>(p, len, p.row_tiles, KEYS, lane) + head_places_warp<ROWS>(p, len, mt, KEYS, lane);
   const int r = sub * kRowsHere + warp / kSplit, part = warp % kSplit;
   const Share share(max(N, 1), max(1, min(N, ctas)));
-  // (never past the slots that there are, even if somebody changes the lengths meanwhile)
-  const int i0 = min(share.part_of(start), ctas - 1), i1 = min(share.part_of(start + max(a.units, 1) - 1), ctas - 1);
-  const bool at_start = share.begin(i0) == start;
+  // the CTAs of its first and last units (never past the slots that there are, even if somebody changes the lengths
+  // meanwhile), and whether the first one has none of the tile before
+  const int unit0 = start + kTileCost<ROWS>;
+  const int i0 = min(share.part_of(unit0), ctas - 1), i1 = min(share.part_of(unit0 + max(a.units, 1) - 1), ctas - 1);
+  const bool at_start = share.begin(i0) >= start;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (a.r0 + r >= p.T * p.G) {  // the last tile has fewer rows
     if (kSplit > 1 && kRowsHere > 1) __syncthreads();
