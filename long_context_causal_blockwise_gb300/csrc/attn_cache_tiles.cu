@@ -47,8 +47,8 @@
 // to do: 96 KB that the products read, 82 KB that unpacking reads and writes, 18 KB
 // that arrive, 1540 clocks at 128 bytes each; and an unpacking warp's turn (its
 // sixteen keys of K 960 clocks, of V 700, two fences 330, and its waits) leaves no
-// room. 8 heads x 65536 keys, 64 rows: 48 us in 4 bits, 60 in 8; 32 heads x 20000,
-// 128 rows: 55. More warps only share this out (us, when that first was 53): 16
+// room. 8 heads x 65536 keys, 64 rows: 47 us in 4 bits, 58 in 8; 32 heads x 20000,
+// 128 rows: 56. More warps only share this out (us, when that first was 53): 16
 // softmax warps of 64 keys each 56, 16 unpacking warps 69, 12 in turn 60.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -243,14 +243,15 @@ __device__ __forceinline__ void copy_lengths(const CacheDecode& p, int* lens) {
 // kSplit warps join a row of a tile that several CTAs share; rows of tiles
 // without a key get their zeros here.
 template <int ROWS, int KEYS, int kSplit>
-__global__ void __launch_bounds__(256) cache_decode_join_kernel(const __grid_constant__ CacheDecode p, int ctas) {
+__global__ void __launch_bounds__(256) cache_decode_join_kernel(const __grid_constant__ CacheDecode p, int ctas,
+                                                                int blocks) {
   constexpr int kSlot = slot_floats(ROWS);
   constexpr int kRowsHere = 8 / kSplit;
   __shared__ float4 sO[8][32];
   __shared__ float sM[8], sL[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = static_cast<int>(blockIdx.x) % (ROWS / kRowsHere);
-  int tile = static_cast<int>(blockIdx.x) / (ROWS / kRowsHere);
+  int tile = static_cast<int>(blockIdx.x) / blocks;  // of which a tile has so many
+  const int sub = static_cast<int>(blockIdx.x) - tile * blocks;
   const int mt = tile % p.row_tiles;
   tile /= p.row_tiles;
   const int b = tile / p.Hkv, hk = tile % p.Hkv;
@@ -324,13 +325,16 @@ int launch_cache_join(const CacheDecode& p, long long tiles, int n, cudaStream_t
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * (wide ? ROWS : ROWS * kNarrow / 8)));
+  const int rows = p.row_tiles > 1 ? ROWS : p.T * p.G;  // of a tile
+  const int blocks = wide ? rows : (rows * kNarrow + 7) / 8;
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * blocks));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, KEYS, 8>, p, n)
-                             : cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, KEYS, kNarrow>, p, n);
+  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, KEYS, 8>, p, n, blocks)
+                             : cudaLaunchKernelEx(&cfg, cache_decode_join_kernel<ROWS, KEYS, kNarrow>, p, n,
+                                                  blocks);
   return e == cudaSuccess ? 0 : -4;
 }
 
