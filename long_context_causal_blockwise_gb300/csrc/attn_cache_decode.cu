@@ -669,6 +669,7 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
     State<ROWS, BITS> w;
     begin(w, raw, p, a, g, t);
     const int end = walk.off + n;
+    int turn = walk.off + (warp + kWarps - (walk.off - 1 + kDepth) % kWarps) % kWarps;  // the unit after which this warp refills
     for (int u = walk.off; u < end; ++u) {
       ok = mbar_wait_warp(&sm.full[at], phase, &sm.abort, p.st, kWhere);
       if (!ok) break;
@@ -681,10 +682,11 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
       }
       __syncwarp();
       if (F::kInTurn) {
-        if (lane == 0) {
-          mbar_arrive(&sm.empty[at]);
+        if (lane == 0) mbar_arrive(&sm.empty[at]);
+        if (u == turn) {
+          turn += kWarps;
           const int x = u - 1 + kDepth, back = at == 0 ? kDepth - 1 : at - 1;  // in the place of the unit before this one
-          if (u > walk.off && x < end && x % kWarps == warp &&
+          if (lane == 0 && u > walk.off && x < end &&
               mbar_wait_inline(&sm.empty[back], phase ^ static_cast<uint32_t>(at == 0), &sm.abort, p.st, kWhere + 0x10000u))
             fetch(x, back);
         }
