@@ -106,8 +106,8 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
 //     weight goes into the second product four times, once with each scale.
 //   4: a column 2r + h is half h of row r: the groups 2h and 2h + 1, Q being zero
 //     in the other half. So two sums and two operands do where eight columns of
-//     whole rows take four, and lane t has row t alone: 283 instructions for
-//     sixteen keys in 4 bits (eight rows: some 305).
+//     whole rows take four, and lane t has row t alone: 260 instructions for
+//     sixteen keys in 4 bits in the line form (eight rows: 325).
 template <int ROWS>
 struct Cols {
   static constexpr bool kHalves = ROWS == 4;
@@ -840,9 +840,9 @@ struct ClusterChoice {
 // longer start, a second kernel, and some 3 us for each tile that a CTA begins
 // after its first; with more than four rows it is bound by its instructions. us,
 // cluster / line, 4 bits unless said: 32 heads x 2052 keys 8 / 10; 8 x 8 heads x
-// 20001, eight rows, 38 / 42; 160 x 32772 127 / 119; 8 x 131072 in 8 bits 69 / 50; 8 x
-// 524288 204 / 103; 1 x 524288 123 / 26; 4 x 100000 33 / 23; 512 x 2000 26 / 36; 80 x
-// 5000 in 8 bits 20 / 24; 40 x 32768 40 / 40; 8 x 65536, eight rows 37 / 26, sixteen
+// 20001, eight rows, 38 / 42; 160 x 32772 127 / 114; 8 x 131072 in 8 bits 69 / 50; 8 x
+// 524288 204 / 99; 1 x 524288 123 / 25; 4 x 100000 33 / 23; 512 x 2000 26 / 36; 80 x
+// 5000 in 8 bits 20 / 24; 40 x 32768 40 / 38; 8 x 65536, eight rows 37 / 26, sixteen
 // 56 / 37. Of 33 sizes four take the slower form, by 3, 4, 12 and 15%.
 template <int ROWS, int BITS>
 int line_ctas(const Plan& a, const ClusterChoice<ROWS, BITS>& c, const ContextKey& at) {
