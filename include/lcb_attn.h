@@ -538,7 +538,8 @@ int attn_cache_decode_form(int B, int H, int Hkv, int T, int Smax, int D, int bi
  * prompt's chunk, lcb_kv_cache_read and attn_window_fwd are faster.
  * What is rounded: weights times V's scales (and O) to bf16; in the form for many
  * rows weights and V, to fp16 where V's scales for sixteen keys on end are
- * ordinary (2^-7 to 16, in 8 bits 2^-11 to 16, or zero), otherwise to bf16.
+ * ordinary (2^-7 to 16, in 8 bits 2^-11 to 16, or zero), otherwise to bf16;
+ * weights in fp16 are also off by up to 2^-32 of a row's largest.
  * A cached NaN makes NaN of those query rows alone that see it (V's in its
  * channels). O is finite where |v| < 2^113 / keys. window, sinks, scale, heads, q,
  * o, lse and their strides as attn_window_decode; the cache as above. workspace:
