@@ -14,12 +14,13 @@
 // as contiguous 16-byte accesses: the rows of a head follow one another.
 //
 // 32768 tokens x 32 heads, at 6.7 TB/s 103 us in 4 bits and 123 in 8: read back in
-// 103 and 120, written in 120 and 122. At the memory's rate an SM has 116 issue slots
+// 103 and 119, written in 107 and 120. At the memory's rate an SM has 116 issue slots
 // for a written row's 256 numbers, and in 4 bits they are what is short: with K's and
 // V's lanes in branches of their own, a division a group and signs moved one by one
-// it took 203 us, with operands selected instead 143, and with the sums of products
-// below 120. 1777 tokens x 3 x 8 heads in 8 bits: written in 8.5 us, read in 6.6 (of
-// 5.0 by bytes); one token: 2.3 and 1.7.
+// it took 203 us, with operands selected instead 143, with the sums of products below
+// 120, and with all eight rows of a warp in one piece of code where they all exist
+// 107 (92 instructions a row). 1777 tokens x 3 x 8 heads in 8 bits: written in 7.8 us,
+// read in 6.7 (of 5.0 by bytes); one token: 2.1 and 1.6.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -81,9 +82,15 @@ __global__ void __launch_bounds__(32 * kWarps, 8) kv_cache_write_kernel(const __
   const int G = j >> 2;
   const __nv_bfloat16* src = (is_v ? p.v : p.k) + b * p.batch_stride + t0 * p.row_stride + h * kD + 8 * j;
   uint4 x[kRows];
+  const bool full = lo == 0 && hi == kRows;
+  if (full) {
 #pragma unroll
-  for (int r = 0; r < kRows; ++r)
-    if (r >= lo && r < hi) x[r] = __ldcs(reinterpret_cast<const uint4*>(src + r * p.row_stride));
+    for (int r = 0; r < kRows; ++r) x[r] = __ldcs(reinterpret_cast<const uint4*>(src + r * p.row_stride));
+  } else {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (r >= lo && r < hi) x[r] = __ldcs(reinterpret_cast<const uint4*>(src + r * p.row_stride));
+  }
   uint8_t* rec0 = recs[warp];
   // Where in a record the lane's scale and its two pieces of codes go: K's side by side, V's those of two lanes' operands.
   const int t = j & 3;
@@ -110,9 +117,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) kv_cache_write_kernel(const __
   const uint32_t sel_a = is_v ? 0x7531 : 0x3715;  // 4 bits; the sign bytes of words 0, 2 and of words 1, 3
   const uint32_t sel_c = is_v ? 0x2604 : 0x3210, sel_d = is_v ? 0x3715 : 0x7654;
   const uint32_t sel_8 = is_v ? 0x7531 : 0x3517;
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (r < lo || r >= hi) continue;  // the same for the whole warp
+  auto row = [&](int r) {
     const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
     // The largest magnitude of the group.
     uint32_t top = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
@@ -156,6 +161,14 @@ __global__ void __launch_bounds__(32 * kWarps, 8) kv_cache_write_kernel(const __
             sum | (permute_bytes(w[2 * f], w[2 * f + 1], sel_8) & 0x80808080u);
       }
     }
+  };
+  if (full) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) row(r);
+  } else {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (r >= lo && r < hi) row(r);  // the same for the whole warp
   }
   __syncwarp();
   uint4* dst = reinterpret_cast<uint4*>(p.cache + b * p.cache_batch_stride + h * p.cache_head_stride +
