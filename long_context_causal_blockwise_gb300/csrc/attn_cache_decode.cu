@@ -345,6 +345,27 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
       }
     }
   }
+  uint32_t vw[4][2 * kWords];  // V's words of rows 2t, 2t + 1, 2t + 8, 2t + 9
+  auto load_v = [&] {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* at = rec + key_of(2 * t + (i & 1), i >> 1) * kRec + cache_v_offset(BITS) + 2 * BITS * g;
+      if (BITS == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        vw[i][0] = v.x;
+        vw[i][1] = v.y;
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(at);
+        vw[i][0] = v.x;
+        vw[i][1] = v.y;
+        vw[i][(2 * kWords) - 2] = v.z;
+        vw[i][(2 * kWords) - 1] = v.w;
+      }
+    }
+  };
+  // before the branch with eight rows, so that they arrive during the weights (us, so / after: 8 x 2 tokens of 8 x 20001
+  // keys 36.2 / 37.6; with four rows 8 heads x 524288 101 / 99)
+  if (ROWS == 8) load_v();
   bool raise = false;
 #pragma unroll
   for (int i = 0; i < C::kMine; ++i) raise |= s[0][i] > w.raise_at[i] || s[1][i] > w.raise_at[i];
@@ -391,22 +412,7 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
                                                 : pack_bf16x2(product(2 * nt, c), product(C::kMine > 1 ? 2 * nt + 1 : 0, c)));
   }
   // ---- O^T += V^T P^T
-  uint32_t vw[4][2 * kWords];  // of rows 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint8_t* at = rec + key_of(2 * t + (i & 1), i >> 1) * kRec + cache_v_offset(BITS) + 2 * BITS * g;
-    if (BITS == 4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(at);
-      vw[i][0] = v.x;
-      vw[i][1] = v.y;
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(at);
-      vw[i][0] = v.x;
-      vw[i][1] = v.y;
-      vw[i][(2 * kWords) - 2] = v.z;
-      vw[i][(2 * kWords) - 1] = v.w;
-    }
-  }
+  if (ROWS != 8) load_v();
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t a[4][2];  // the group's four channels: rows 2t, 2t + 1 and 2t + 8, 2t + 9
