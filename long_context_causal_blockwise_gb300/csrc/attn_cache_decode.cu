@@ -408,8 +408,9 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
     for (int c = 0; c < C::kSums; ++c)
 #pragma unroll
       for (int nt = 0; nt < C::kTiles; ++nt)
-        pb[c][nt][h] = transpose_8x8(C::kHalves ? pack_bf16x2(product(0, c), product(0, c + 2))
-                                                : pack_bf16x2(product(2 * nt, c), product(C::kMine > 1 ? 2 * nt + 1 : 0, c)));
+        pb[c][nt][h] = transpose_8x8(
+            C::kHalves ? pack_bf16x2(product(0, c), product(0, c + 2))
+                       : pack_bf16x2(product(2 * nt, c), product(C::kMine > 1 ? 2 * nt + 1 : 0, c)));
   }
   // ---- O^T += V^T P^T
   if (ROWS != 8) load_v();
@@ -675,7 +676,8 @@ __global__ void __launch_bounds__(32 * warps_per_sm(ROWS), 1)
     State<ROWS, BITS> w;
     begin(w, raw, p, a, g, t);
     const int end = walk.off + n;
-    int turn = walk.off + (warp + kWarps - (walk.off - 1 + kDepth) % kWarps) % kWarps;  // the unit after which this warp refills
+    // the unit after which this warp refills
+    int turn = walk.off + (warp + kWarps - (walk.off - 1 + kDepth) % kWarps) % kWarps;
     for (int u = walk.off; u < end; ++u) {
       ok = mbar_wait_warp(&sm.full[at], phase, &sm.abort, p.st, kWhere);
       if (!ok) break;

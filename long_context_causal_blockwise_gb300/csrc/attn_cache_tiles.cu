@@ -99,7 +99,8 @@ struct Smem {  // 1024-byte aligned
 
 // Instruction descriptor, kind::f16, fp32 sums: fp16 operands (format 0).
 constexpr uint32_t idesc_f16(int M, int N, bool transposed_b = false) {
-  return (1u << 4) | (transposed_b ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+  return (1u << 4) | (transposed_b ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
@@ -604,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
               float w[16];
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
-                ffma2(w[k], w[k + 1], __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]), f, f, neg_m, neg_m);
+                ffma2(w[k], w[k + 1], __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]), f, f, neg_m,
+                      neg_m);
                 w[k] = ex2_approx(w[k]), w[k + 1] = ex2_approx(w[k + 1]);
                 fadd2(la, lb, la, lb, w[k], w[k + 1]);
               }

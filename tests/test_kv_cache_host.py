@@ -142,7 +142,8 @@ def test_python_refusals():
     lens = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
         lcb.kv_cache_empty(1, 1, 4, bits=3)
-    for bad in (cache.float(), cache[0], cache[..., :100], cache[:, :, ::2], torch.zeros(2, 2, 16, 288, dtype=torch.uint8)[..., ::2]):
+    for bad in (cache.float(), cache[0], cache[..., :100], cache[:, :, ::2],
+                torch.zeros(2, 2, 16, 288, dtype=torch.uint8)[..., ::2]):
         with pytest.raises(ValueError):
             lcb.kv_cache_write(bad, k, k, lens)
         with pytest.raises(ValueError):
