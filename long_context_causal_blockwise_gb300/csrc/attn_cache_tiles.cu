@@ -19,12 +19,17 @@
 //
 // A pair of codes as they lie is a pair of subnormal numbers (kv_cache.cuh), which
 // one packed multiplication by a scale times the inverse of that smallness makes
-// normal. K goes to fp16 as s n over a power of two that sixteen keys share, which
-// the scores get back: exact in 4 bits (3 bits times a scale's 8) where a scale is
-// above 2^-8 of the largest of the sixteen keys, off by 2^-19 of that key's largest
-// value at most where not. In 8 bits it is two numbers, the magnitude's upper 3
-// bits (so exact) and its lower 4 (off by half a step, 2^-12 of them, 2^-15 of the
-// largest magnitude), and two products. Q as in attn_cache_decode.cu.
+// normal. K goes to fp16 as s n over a power of two, which the scores get back. In 4
+// bits s n has 3 and 8 bits, fp16's eleven. In 8 bits it is two numbers, the
+// magnitude's upper 3 bits (so as exact) and its lower 4 (off by half a step, 2^-12 of
+// them, 2^-15 of the largest magnitude), and two products. What is left is fp16's
+// range. Sixteen keys share the power of two where the exponents of their scales,
+// zeros aside, span 8 at most: s n is a multiple of 2^-24 then, and no bit is lost.
+// Otherwise each key has its own, and two multiplications leave it more room: nothing
+// is lost while a key's own scales span 23 (past that, a channel is off by 2^-31 of
+// the key's largest scale, or twice that in 8 bits). A power of two changes no bit of
+// a score, so that none depends on which keys are neighbours. Q as in
+// attn_cache_decode.cu.
 //
 // V and the weights P are of one type, for each sixteen keys (a product's step) on
 // its own. Where the sixteen keys' scales of V are ordinary (2^-7, in 8 bits 2^-11,
@@ -54,6 +59,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cache_line.cuh"
 
@@ -88,8 +94,10 @@ template <int BITS>
 struct Smem {  // 1024-byte aligned
   uint8_t K[2][kTileBytes], V[2][kTileBytes], Q[kTileBytes];
   uint8_t raw[Raw<BITS>::kStages][Raw<BITS>::kBytes];
-  // by unit modulo 4: the power of two taken from K, for each sixteen keys; below zero where their V and P are bf16
+  // by unit modulo 4: the power of two taken from K, for each sixteen keys (infinity: each of them has its own); below
+  // zero where their V and P are bf16
   float k_factor[4][8];
+  float key_factor[4][kKeys];
   uint2 v_nan[4][8];  // and then, of which scales of V are NaN: bits 2 key + G / 2, G even and odd
   float M[2][kRows], L[2][kRows];
   uint32_t nan[2][kRows];
@@ -161,37 +169,34 @@ __device__ __forceinline__ bool wide_v(const uint8_t* rec, uint2* nan, int lane)
   return wide;
 }
 
-// Sixteen keys of K by a warp: rows row0 .. + 15 of the tile; the first nk of the records exist.
-template <int BITS>
-__device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int row0, int nk, float* factor, uint2* nan,
-                                         int lane, bool& is_wide) {
+// A key's four scales' largest finite one, as bits.
+__device__ __forceinline__ uint32_t top_scale(uint32_t x) {
+  const uint32_t a = x & 0xffffu, b = x >> 16;
+  return max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u);
+}
+
+// The exponent of the largest scale, as bits, that shares a power of two, where it is not so small that nobody writes it.
+__device__ __forceinline__ int top_exponent(uint32_t top) { return max(static_cast<int>(top >> 7) - 127, -110); }
+
+// Sixteen keys of K by a warp: rows row0 .. + 15 of the tile, times powers of two. OWN: each key its own, which go to
+// `own`. Otherwise all of them 2^(-9 - e), e the exponent of their largest scale.
+template <int BITS, bool OWN>
+__device__ __forceinline__ void unpack_k_rows(const uint8_t* rec, uint8_t* tile, int row0, int e, float* own, int lane) {
   constexpr int kRec = cache_row_bytes(BITS);
-  // the largest finite scale of the sixteen keys, as bits
-  uint32_t top = 0;
-  if ((lane >> 1) < nk) {
-    const uint32_t x =
-        *reinterpret_cast<const uint32_t*>(rec + (lane >> 1) * kRec + cache_scale_offset(BITS) + 4 * (lane & 1));
-    const uint32_t a = x & 0xffffu, b = x >> 16;
-    top = max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u);
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  bool wide = wide_v<BITS>(rec, nan, lane);
-  if (!wide && nk < 16) {
-    if (lane == 0) *nan = make_uint2(0, 0);
-    wide = true;
-  }
-  is_wide = wide;
-  // scales are below 2^(e + 1): times 2^(14 - e) they are fp16, and with the codes' 2^-24 they make s n 2^(-10 - e)
-  const int e = max(static_cast<int>(top >> 7) - 127, -100);
-  const float up = exp2_int(14 - e);
-  if (lane == 0) *factor = exp2_int(min(10 + e, 127)) * (wide ? -1.f : 1.f);
   const Lane at(lane);
   const uint8_t* r0 = rec + at.key * kRec;
   const uint32_t first = at.first_chunk(row0);
-#pragma unroll
+  // from the codes' 2^-24 (or 2^-20) to 2^-9, with which s goes up to fp16's end
+  auto code = [](uint32_t x, bool odd) { return OWN ? hmul2_f16(x, odd ? 0x68006800u : 0x78007800u) : x; };
+#pragma unroll(OWN ? 1 : 2)
   for (int round = 0; round < 2; ++round) {
     const uint8_t* r = r0 + round * 8 * kRec;
     const uint2 sc = *reinterpret_cast<const uint2*>(r + cache_scale_offset(BITS));
+    if (OWN) {
+      e = top_exponent(max(top_scale(sc.x), top_scale(sc.y)));
+      if (at.t == 0) own[round * 8 + at.key] = exp2_int(e - 6);
+    }
+    const float up = exp2_int(15 - e);
     uint32_t w[BITS];  // the lane's words
 #pragma unroll
     for (int i = 0; i < BITS / 4; ++i) {
@@ -205,22 +210,50 @@ __device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int 
       const __half2 d = __floats2half2_rn(f, f);
       const uint32_t s = *reinterpret_cast<const uint32_t*>(&d);
       if (BITS == 4) {
-        const uint32_t s16 = hmul2_f16(s, 0x2c002c00u);  // odd fields are 2^4 as large
+        const uint32_t s16 = OWN ? s : hmul2_f16(s, 0x2c002c00u);  // odd fields are 2^4 as large
         const Fields c = k4_fields(w[j]);
-        st_shared16(chunk_of(tile, first, round, j), hmul2_f16(c.pair(0), s), hmul2_f16(c.pair(1), s16),
-                    hmul2_f16(c.pair(2), s), hmul2_f16(c.pair(3), s16));
+        st_shared16(chunk_of(tile, first, round, j), hmul2_f16(code(c.pair(0), false), s),
+                    hmul2_f16(code(c.pair(1), true), s16), hmul2_f16(code(c.pair(2), false), s),
+                    hmul2_f16(code(c.pair(3), true), s16));
       } else {
         const uint32_t w0 = w[(2 * j) % BITS], w1 = w[(2 * j + 1) % BITS];
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           const uint32_t keep = part ? 0x800f800fu : 0x80708070u;
-          st_shared16(chunk_of(tile + part * kTileBytes, first, round, j), hmul2_f16(k8_f16x2(w0, 0) & keep, s),
-                      hmul2_f16(k8_f16x2(w0, 1) & keep, s), hmul2_f16(k8_f16x2(w1, 0) & keep, s),
-                      hmul2_f16(k8_f16x2(w1, 1) & keep, s));
+          auto value = [&](uint32_t w, int f) { return hmul2_f16(code(k8_f16x2(w, f) & keep, false), s); };
+          st_shared16(chunk_of(tile + part * kTileBytes, first, round, j), value(w0, 0), value(w0, 1), value(w1, 0),
+                      value(w1, 1));
         }
       }
     }
   }
+}
+
+// Sixteen keys of K by a warp; the first nk of the records exist.
+template <int BITS>
+__device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int row0, int nk, float* factor, float* own,
+                                         uint2* nan, int lane, bool& is_wide) {
+  constexpr int kRec = cache_row_bytes(BITS);
+  uint32_t x = 0;  // half a key's scales
+  if ((lane >> 1) < nk)
+    x = *reinterpret_cast<const uint32_t*>(rec + (lane >> 1) * kRec + cache_scale_offset(BITS) + 4 * (lane & 1));
+  const uint32_t top = __reduce_max_sync(0xffffffffu, top_scale(x));  // the largest finite scale of the sixteen keys
+  // the smallest one, less 1 so that zeros are none; whether its exponent is more than 8 below
+  const uint32_t low = __reduce_min_sync(0xffffffffu, min((x - 1u) & 0xffffu, ((x >> 16) - 1u) & 0xffffu));
+  const bool each = ((low + 1u) >> 7) + 8u < top >> 7;
+  bool wide = wide_v<BITS>(rec, nan, lane);
+  if (!wide && nk < 16) {
+    if (lane == 0) *nan = make_uint2(0, 0);
+    wide = true;
+  }
+  is_wide = wide;
+  // scales are below 2^(e + 1): times 2^(15 - e) they are fp16, and with the codes' 2^-24 they make s n 2^(-9 - e)
+  const int e = top_exponent(top);
+  if (lane == 0) *factor = (each ? INFINITY : exp2_int(min(9 + e, 127))) * (wide ? -1.f : 1.f);
+  if (each)
+    unpack_k_rows<BITS, true>(rec, tile, row0, 0, own, lane);
+  else
+    unpack_k_rows<BITS, false>(rec, tile, row0, e, nullptr, lane);
 }
 
 // 2^-12 s n of a pair of V's codes, as they lie (magnitudes sh bits to the left). fp16: by one multiplication, by 2^12 s
@@ -300,6 +333,43 @@ __device__ __forceinline__ void unpack_v(const uint8_t* rec, uint8_t* tile, int 
       }
     }
   }
+}
+
+// The largest score of a row in a unit, its scores at tS. OWN: some of the keys have powers of two of their own. Without
+// it, that is seen from top_factor.
+template <bool OWN, class Hidden>
+__device__ __forceinline__ float largest(uint32_t tS, const float* k_factor, const float* key_factor, float c, bool whole,
+                                         Hidden&& hidden, float& top_factor) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t s[32];
+    tmem_ld_x32(tS + ch * 32, s);
+    const float2 kf = *reinterpret_cast<const float2*>(&k_factor[2 * ch]);
+    if (!whole)
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (hidden(32 * ch + k)) s[k] = __float_as_uint(-INFINITY);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float f16 = fabsf(h ? kf.y : kf.x);
+      if (!OWN) top_factor = fmaxf(top_factor, f16);
+      if (OWN && f16 == INFINITY) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          mx = fmaxf(mx, __uint_as_float(s[16 * h + k]) * (c * key_factor[32 * ch + 16 * h + k]));
+        continue;
+      }
+      float y = -INFINITY, z = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) {
+        y = fmax3(y, __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]));
+        z = fmax3(z, __uint_as_float(s[16 * h + k + 2]), __uint_as_float(s[16 * h + k + 3]));
+      }
+      mx = fmaxf(mx, fmaxf(y, z) * (c * f16));
+    }
+  }
+  return mx;
 }
 
 template <int BITS>
@@ -399,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
         if (!ok) break;
         bool wide = true;
         if (mine > 0)
-          unpack_k<BITS>(rec, sm.K[kt], row0, mine, &sm.k_factor[i & 3][w], &sm.v_nan[i & 3][w], lane, wide);
+          unpack_k<BITS>(rec, sm.K[kt], row0, mine, &sm.k_factor[i & 3][w], &sm.key_factor[i & 3][row0],
+                         &sm.v_nan[i & 3][w], lane, wide);
         else if (lane == 0)
           sm.k_factor[i & 3][w] = -1.f, sm.v_nan[i & 3][w] = make_uint2(0, 0);
         fence_to_async();
@@ -548,27 +619,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
             const int j = j0 + k;
             return !(k < nk && j <= pos && (pos - j < p.window || j < p.sinks));
           };
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t s[32];
-            tmem_ld_x32(tS + ch * 32, s);
-            const float2 kf = *reinterpret_cast<const float2*>(&sm.k_factor[i & 3][2 * ch]);
-            if (!whole)
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (hidden(32 * ch + k)) s[k] = __float_as_uint(-INFINITY);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float y = -INFINITY, z = -INFINITY;
-#pragma unroll
-              for (int k = 0; k < 16; k += 4) {
-                y = fmax3(y, __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]));
-                z = fmax3(z, __uint_as_float(s[16 * h + k + 2]), __uint_as_float(s[16 * h + k + 3]));
-              }
-              mx = fmaxf(mx, fmaxf(y, z) * (c * fabsf(h ? kf.y : kf.x)));
-            }
-          }
+          // Some of the keys may have powers of two of their own: copies of the loops, which few units take. (64 rows x 64K
+          // keys, us: without such keys 46.9; with a test in the loops 52.2; so 48.8.)
+          float top_factor = 0.f;
+          float mx = largest<false>(tS, sm.k_factor[i & 3], sm.key_factor[i & 3], c, whole, hidden, top_factor);
+          const bool own = top_factor == INFINITY;
+          if (own) mx = largest<true>(tS, sm.k_factor[i & 3], sm.key_factor[i & 3], c, whole, hidden, top_factor);
           const float m_new = fmaxf(m, mx);
           const bool resc = m_new > m + kRescaleThreshold;
           if (x == first) {
@@ -589,47 +645,56 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
             }
           }
           const float neg_m = m == -INFINITY ? 0.f : kWeightUp - m;
+          auto weights = [&](auto own_factors) {
 #pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t s[32], pk[16];
-            tmem_ld_x32(tS + ch * 32, s);
-            const float2 kf = *reinterpret_cast<const float2*>(&sm.k_factor[i & 3][2 * ch]);
-            if (!whole)
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t s[32], pk[16];
+              tmem_ld_x32(tS + ch * 32, s);
+              const float2 kf = *reinterpret_cast<const float2*>(&sm.k_factor[i & 3][2 * ch]);
+              if (!whole)
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (hidden(32 * ch + k)) s[k] = __float_as_uint(-INFINITY);
-            float la = 0.f, lb = 0.f;
+                for (int k = 0; k < 32; ++k)
+                  if (hidden(32 * ch + k)) s[k] = __float_as_uint(-INFINITY);
+              float la = 0.f, lb = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float f = c * fabsf(h ? kf.y : kf.x);
-              float w[16];
+              for (int h = 0; h < 2; ++h) {
+                const float f16 = fabsf(h ? kf.y : kf.x), f = c * f16;
+                const float* own = &sm.key_factor[i & 3][32 * ch + 16 * h];
+                float w[16];
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                ffma2(w[k], w[k + 1], __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]), f, f, neg_m,
-                      neg_m);
-                w[k] = ex2_approx(w[k]), w[k + 1] = ex2_approx(w[k + 1]);
-                fadd2(la, lb, la, lb, w[k], w[k + 1]);
-              }
-              if ((h ? kf.y : kf.x) < 0.f) {
-                const uint2 nan = sm.v_nan[i & 3][2 * ch + h];
-                if ((nan.x | nan.y) != 0)  // V's NaN, as far as the row sees their keys
+                for (int k = 0; k < 16; k += 2) {
+                  float f0 = f, f1 = f;
+                  if (own_factors.value && f16 == INFINITY) f0 = c * own[k], f1 = c * own[k + 1];
+                  ffma2(w[k], w[k + 1], __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]), f0, f1, neg_m,
+                        neg_m);
+                  w[k] = ex2_approx(w[k]), w[k + 1] = ex2_approx(w[k + 1]);
+                  fadd2(la, lb, la, lb, w[k], w[k + 1]);
+                }
+                if ((h ? kf.y : kf.x) < 0.f) {
+                  const uint2 nan = sm.v_nan[i & 3][2 * ch + h];
+                  if ((nan.x | nan.y) != 0)  // V's NaN, as far as the row sees their keys
 #pragma unroll 1
-                  for (int k = 0; k < 16; ++k)
-                    if (!hidden(32 * ch + 16 * h + k))
-                      row_nan |= spread(nan.x >> 2 * k) | spread(nan.y >> 2 * k) << 1;
+                    for (int k = 0; k < 16; ++k)
+                      if (!hidden(32 * ch + 16 * h + k))
+                        row_nan |= spread(nan.x >> 2 * k) | spread(nan.y >> 2 * k) << 1;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) pk[8 * h + k] = pack_bf16x2(w[2 * k], w[2 * k + 1]);
-              } else {
+                  for (int k = 0; k < 8; ++k) pk[8 * h + k] = pack_bf16x2(w[2 * k], w[2 * k + 1]);
+                } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const __half2 x = __floats2half2_rn(w[2 * k], w[2 * k + 1]);
-                  pk[8 * h + k] = *reinterpret_cast<const uint32_t*>(&x);
+                  for (int k = 0; k < 8; ++k) {
+                    const __half2 x = __floats2half2_rn(w[2 * k], w[2 * k + 1]);
+                    pk[8 * h + k] = *reinterpret_cast<const uint32_t*>(&x);
+                  }
                 }
               }
+              l += la + lb;
+              tmem_st_x16(tS + ch * 16, pk);  // over scores that have been read
             }
-            l += la + lb;
-            tmem_st_x16(tS + ch * 16, pk);  // over scores that have been read
-          }
+          };
+          if (own)
+            weights(std::true_type());
+          else
+            weights(std::false_type());
         }
         tc_fence_before();
         __syncwarp();
