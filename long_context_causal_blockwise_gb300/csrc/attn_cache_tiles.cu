@@ -169,6 +169,10 @@ __device__ __forceinline__ bool wide_v(const uint8_t* rec, uint2* nan, int lane)
   return wide;
 }
 
+// K's factors are kept times 2^-7, and the rows' times 2^7: 2^(9 + e) passes fp32's end where the largest scales (below
+// 2^126, from the largest bf16 over 7) do not, and a row's is 2^126 at most, times the scale.
+constexpr int kFactorDown = 7;
+
 // A key's four scales' largest finite one, as bits.
 __device__ __forceinline__ uint32_t top_scale(uint32_t x) {
   const uint32_t a = x & 0xffffu, b = x >> 16;
@@ -194,7 +198,7 @@ __device__ __forceinline__ void unpack_k_rows(const uint8_t* rec, uint8_t* tile,
     const uint2 sc = *reinterpret_cast<const uint2*>(r + cache_scale_offset(BITS));
     if (OWN) {
       e = top_exponent(max(top_scale(sc.x), top_scale(sc.y)));
-      if (at.t == 0) own[round * 8 + at.key] = exp2_int(e - 6);
+      if (at.t == 0) own[round * 8 + at.key] = exp2_int(e - 6 - kFactorDown);
     }
     const float up = exp2_int(15 - e);
     uint32_t w[BITS];  // the lane's words
@@ -249,7 +253,7 @@ __device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int 
   is_wide = wide;
   // scales are below 2^(e + 1): times 2^(15 - e) they are fp16, and with the codes' 2^-24 they make s n 2^(-9 - e)
   const int e = top_exponent(top);
-  if (lane == 0) *factor = (each ? INFINITY : exp2_int(min(9 + e, 127))) * (wide ? -1.f : 1.f);
+  if (lane == 0) *factor = (each ? INFINITY : exp2_int(min(9 - kFactorDown + e, 127))) * (wide ? -1.f : 1.f);
   if (each)
     unpack_k_rows<BITS, true>(rec, tile, row0, 0, own, lane);
   else
@@ -581,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           }
         const int e = static_cast<int>(top >> 7), up = min(126, 8 + 127 - e);
         const float f = e == 255 ? __int_as_float(0x7fc00000) : exp2_int(up);
-        c = exp2_int(-up) * p.scale_log2;
+        c = exp2_int(kFactorDown - up) * p.scale_log2;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           uint4 v = make_uint4(0u, 0u, 0u, 0u);

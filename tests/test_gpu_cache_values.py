@@ -202,3 +202,15 @@ def test_k_and_its_channels_of_all_sizes(form, B, H, Hkv, T, Smax, bits):
     k = k * torch.exp2(-torch.randint(0, 16, (B, Smax, Hkv, 1), generator=g, device="cuda").float()) * groups
     _check(form, bits, (q / groups).to(BF16), k.to(BF16), v.to(BF16), lens=[Smax - 5 * b - 3 for b in range(B)],
            window=Smax - 99, sinks=5)
+
+
+# ------------------------------------------------------------------ very large K, Q and V
+
+
+@both_bits
+@pytest.mark.parametrize("e", [100, 119, 123])
+@each_form
+def test_very_large_keys(form, B, H, Hkv, T, Smax, e, bits):
+    """K up to 2^125, and Q that makes up for it."""
+    k, v, q = _rand(8, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))
+    _check(form, bits, (q * 2.0 ** -e).to(BF16), (k * 2.0 ** e).to(BF16), v.to(BF16))
