@@ -201,8 +201,8 @@ __device__ __forceinline__ void begin(State<ROWS, BITS>& w, const RawQ<ROWS>& ra
         w.q[nt][4 * c + i] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&y);
       }
     }
-    // the power of two back, and the subnormal codes' 2^24
-    const float back = exp2_int(-up) * 0x1p24f * p.scale_log2;
+    // the power of two back, and the subnormal codes' 2^24; not zero, which times a hidden score's -inf would be NaN
+    const float back = fmaxf(exp2_int(-up) * 0x1p24f * p.scale_log2, kLeastFactor);
     if (C::kHalves) {
       w.c[0] = __shfl_sync(0xffffffffu, back, 8 * t);
     } else {

@@ -339,6 +339,13 @@ __device__ __forceinline__ void unpack_v(const uint8_t* rec, uint8_t* tile, int 
   }
 }
 
+// What products of Q and K as they lie in the tiles are times for scores in base 2: a row's factor times a key's. A score
+// that the mask hides is -inf before that, which times zero would be NaN, and a score of zero times infinity: neither is
+// reached (queries and keys of zeros have the smallest factors that there are).
+__device__ __forceinline__ float score_factor(float row, float key) {
+  return fminf(fmaxf(row * key, kLeastFactor), 0x1.fffffep127f);
+}
+
 // The largest score of a row in a unit, its scores at tS. OWN: some of the keys have powers of two of their own. Without
 // it, that is seen from top_factor.
 template <bool OWN, class Hidden>
@@ -361,7 +368,7 @@ __device__ __forceinline__ float largest(uint32_t tS, const float* k_factor, con
       if (OWN && f16 == INFINITY) {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          mx = fmaxf(mx, __uint_as_float(s[16 * h + k]) * (c * key_factor[32 * ch + 16 * h + k]));
+          mx = fmaxf(mx, __uint_as_float(s[16 * h + k]) * score_factor(c, key_factor[32 * ch + 16 * h + k]));
         continue;
       }
       float y = -INFINITY, z = -INFINITY;
@@ -370,7 +377,7 @@ __device__ __forceinline__ float largest(uint32_t tS, const float* k_factor, con
         y = fmax3(y, __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]));
         z = fmax3(z, __uint_as_float(s[16 * h + k + 2]), __uint_as_float(s[16 * h + k + 3]));
       }
-      mx = fmaxf(mx, fmaxf(y, z) * (c * f16));
+      mx = fmaxf(mx, fmaxf(y, z) * score_factor(c, f16));
     }
   }
   return mx;
@@ -662,13 +669,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
               float la = 0.f, lb = 0.f;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float f16 = fabsf(h ? kf.y : kf.x), f = c * f16;
+                const float f16 = fabsf(h ? kf.y : kf.x), f = score_factor(c, f16);
                 const float* own = &sm.key_factor[i & 3][32 * ch + 16 * h];
                 float w[16];
 #pragma unroll
                 for (int k = 0; k < 16; k += 2) {
                   float f0 = f, f1 = f;
-                  if (own_factors.value && f16 == INFINITY) f0 = c * own[k], f1 = c * own[k + 1];
+                  if (own_factors.value && f16 == INFINITY) f0 = score_factor(c, own[k]), f1 = score_factor(c, own[k + 1]);
                   ffma2(w[k], w[k + 1], __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]), f0, f1, neg_m,
                         neg_m);
                   w[k] = ex2_approx(w[k]), w[k + 1] = ex2_approx(w[k + 1]);

@@ -11,6 +11,7 @@ namespace lcb {
 
 constexpr int kCacheD = 128;
 constexpr int kLineSequences = 1024;  // whose lengths a CTA keeps in shared memory
+constexpr float kLeastFactor = 0x1p-149f;  // of a score: fp32's smallest number
 
 // Contiguous bytes (a multiple of 16, both ends aligned to 16) into shared memory, completing on `bar`.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

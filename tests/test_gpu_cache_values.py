@@ -214,3 +214,40 @@ def test_very_large_keys(form, B, H, Hkv, T, Smax, e, bits):
     """K up to 2^125, and Q that makes up for it."""
     k, v, q = _rand(8, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))
     _check(form, bits, (q * 2.0 ** -e).to(BF16), (k * 2.0 ** e).to(BF16), v.to(BF16))
+
+
+# ------------------------------------------------------------------ zeros
+
+
+@both_bits
+@pytest.mark.parametrize("zero", ["q", "k", "both", "a row", "small q", "some k"])
+@each_form
+def test_zeros(form, B, H, Hkv, T, Smax, zero, bits):
+    """Queries, keys or both of zeros: every visible key has the same weight. Lengths that end inside sixteen keys, and a
+    window that begins inside."""
+    k, v, q = _rand(9, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))
+    if zero in ("q", "both"):
+        q.zero_()
+    if zero in ("k", "both", "small q"):
+        k.zero_()
+    if zero == "a row":
+        q[:, 0].zero_()
+        k.zero_()
+    if zero == "small q":
+        q *= 2.0 ** -100
+    if zero == "some k":
+        q[:, :, ::2].zero_()
+        k[:, ::3].zero_()
+        k[:, -40:].zero_()
+    lens = [Smax - 7 - 20 * b for b in range(B)]
+    for window, sinks in ((None, 0), (Smax - 77, 3)):
+        _check(form, bits, q.to(BF16), k.to(BF16), v.to(BF16), lens, window, sinks)
+
+
+@both_bits
+@each_form
+def test_a_scale_next_to_nothing(form, B, H, Hkv, T, Smax, bits):
+    """scale = 2^-120, with which the scores are zeros in fp32: equal weights, for zero queries too."""
+    k, v, q = _rand(10, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))
+    q[:, 0].zero_()
+    _check(form, bits, q.to(BF16), k.to(BF16), v.to(BF16), [Smax - 5] * B, scale=2.0 ** -120)
