@@ -93,6 +93,12 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -123,11 +129,20 @@ __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static
 constexpr int kUp = 96;            // weights go into the second product times 2^96, which subnormal codes take back
 constexpr int kUpRange = 119 - kUp;  // while V's scales are below 2^23: a weight is 2^8 at most
 
+// A row is far where one fused multiplication does not make weights of its products: where its factor could pass fp32's
+// end (a largest |q| of 2^68 or more), or where its maximum is so large that the rounding of the product it was is no
+// longer small beside 1. Its raise_at stays -inf, so that every step takes the branch that raises a maximum, and there
+// its products become differences from m, by a multiplication and a subtraction, over c. Such a row's c is its factor
+// over 2^24, and its neg_m -0, which no other row's is. (With the factor in a register of its own: 8 heads x 65536
+// keys, sixteen rows, 8 bits 50.4 us for 49.6; 46.8 without far rows.)
+constexpr float kFarScore = 0x1p23f;
+__device__ __forceinline__ bool is_far(float neg_m) { return __float_as_uint(neg_m) == 0x80000000u; }
+
 template <int ROWS, int BITS>
 struct State {
   using C = Cols<ROWS>;
   uint32_t q[C::kTiles][16];    // Q's fragments, in K's channel order
-  float c[C::kMine];            // a row's scores in base 2 are its products times this
+  float c[C::kMine];            // a row's scores in base 2 are its products times this (a far row's 2^24 more)
   int pr[C::kMine];             // its position; -1 past the last row
   float o[8][C::kTiles][4];     // o[2 G + f]: channels 32 G + 4 g + 2 f + {0, 1}, each of columns 2t, 2t + 1
   float m[C::kMine], l[C::kMine];
@@ -201,13 +216,19 @@ __device__ __forceinline__ void begin(State<ROWS, BITS>& w, const RawQ<ROWS>& ra
         w.q[nt][4 * c + i] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&y);
       }
     }
-    // the power of two back, and the subnormal codes' 2^24; not zero, which times a hidden score's -inf would be NaN
-    const float back = fmaxf(exp2_int(-up) * 0x1p24f * p.scale_log2, kLeastFactor);
+    // the power of two back, and the subnormal codes' 2^24
+    auto factor = [&](int i, int up) {
+      const float all = exp2_int(min(24 - up, 127)) * p.scale_log2;
+      const bool far = up < -60 || all >= 0x1p84f;
+      // (zero times a hidden score's -inf would be NaN)
+      w.c[i] = far ? fminf(exp2_int(-up) * p.scale_log2, 0x1p125f) : fmaxf(all, kLeastFactor);
+      w.neg_m[i] = far ? -0.f : 0.f;
+    };
     if (C::kHalves) {
-      w.c[0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      factor(0, __shfl_sync(0xffffffffu, up, 8 * t));
     } else {
-      w.c[2 * nt] = __shfl_sync(0xffffffffu, back, 8 * t);
-      w.c[C::kMine > 1 ? 2 * nt + 1 : 0] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+      factor(2 * nt, __shfl_sync(0xffffffffu, up, 8 * t));
+      factor(C::kMine > 1 ? 2 * nt + 1 : 0, __shfl_sync(0xffffffffu, up, 8 * t + 4));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -219,7 +240,7 @@ __device__ __forceinline__ void begin(State<ROWS, BITS>& w, const RawQ<ROWS>& ra
     const int r = a.r0 + C::row(i, t);
     w.pr[i] = r < p.T * p.G ? a.p0 + (p.G == 1 ? r : r / p.G) : -1;
     w.m[i] = w.raise_at[i] = -INFINITY;
-    w.l[i] = w.neg_m[i] = 0.f;
+    w.l[i] = 0.f;
   }
   w.up = exp2_int(kUp);
   w.up_limit = 0x10001u * ((kUpRange + 127) * 128 - 1);
@@ -375,15 +396,24 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
     lower_up(w, sc);
 #pragma unroll
     for (int i = 0; i < C::kMine; ++i) {
-      float mx = fmaxf(s[0][i], s[1][i]) * w.c[i];
+      const bool was_far = is_far(w.neg_m[i]);
+      float mx = fmaxf(s[0][i], s[1][i]) * w.c[i] * (was_far ? 0x1p24f : 1.f);
 #pragma unroll
       for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
       // each row for itself: no other row's keys change its bits
       mx = mx > w.m[i] + kRescaleThreshold ? mx : w.m[i];
       const float a = weight(w.m[i], mx);
       w.m[i] = mx;
-      w.neg_m[i] = mx == -INFINITY ? 0.f : -mx;
+      w.neg_m[i] = mx == -INFINITY ? 0.f : 0.f - mx;
       w.raise_at[i] = (mx + kRescaleThreshold) / w.c[i];
+      if (was_far || fabsf(w.neg_m[i]) >= kFarScore) {
+        if (!was_far) w.c[i] *= 0x1p-24f;
+        const float inv = rcp_approx(w.c[i]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[h][i] = __fadd_rn(__fmul_rn(s[h][i], w.c[i]) * 0x1p24f, w.neg_m[i]) * inv;
+        w.neg_m[i] = -0.f;
+        w.raise_at[i] = -INFINITY;
+      }
       w.l[i] *= a;
 #pragma unroll
       for (int G = 0; G < 4; ++G)

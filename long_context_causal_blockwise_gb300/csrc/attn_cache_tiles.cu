@@ -70,7 +70,7 @@ constexpr int kD = 128;
 constexpr int kRows = 128, kKeys = 128;  // of a tile, of a unit
 constexpr int kProducts = 16, kRecords = 17, kThreads = 18 * 32;  // warps, threads
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
-constexpr float kRescaleThreshold = 8.0f;
+constexpr float kRescaleThreshold = 8.0f, kFarScore = 0x1p23f;  // in base 2
 constexpr uint32_t kWhere = 10u << 24;
 
 // K's two tiles are those of two units in 4 bits, of one unit's two parts in 8.
@@ -368,7 +368,7 @@ __device__ __forceinline__ float largest(uint32_t tS, const float* k_factor, con
       if (OWN && f16 == INFINITY) {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          mx = fmaxf(mx, __uint_as_float(s[16 * h + k]) * score_factor(c, key_factor[32 * ch + 16 * h + k]));
+          mx = fmaxf(mx, __fmul_rn(__uint_as_float(s[16 * h + k]), score_factor(c, key_factor[32 * ch + 16 * h + k])));
         continue;
       }
       float y = -INFINITY, z = -INFINITY;
@@ -612,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.q_full);
       float m = -INFINITY, l = 0.f;
+      bool any_far = false;
       uint32_t row_nan = 0;  // channel groups in which the row sees a NaN of V
       auto spread = [](uint32_t two) { return (two & 1u) | (two & 2u) << 1; };  // groups 0, 2
       const int first = (i0 & 1) == t ? 0 : 1;  // the stream's first unit of the tile
@@ -638,8 +639,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           if (own) mx = largest<true>(tS, sm.k_factor[i & 3], sm.key_factor[i & 3], c, whole, hidden, top_factor);
           const float m_new = fmaxf(m, mx);
           const bool resc = m_new > m + kRescaleThreshold;
+          // A row whose maximum is so large that the rounding of the product it was is no longer small beside 1: its
+          // weights take a multiplication and a subtraction. Whether the warp has one changes with the maxima alone.
+          auto is_far = [&] { return fabsf(m) >= kFarScore && m != -INFINITY; };
           if (x == first) {
             m = m_new;
+            any_far = __any_sync(0xffffffffu, is_far());
           } else if (__any_sync(0xffffffffu, resc)) {
             const float alpha = resc ? ex2_approx(m - m_new) : 1.f;
 #pragma unroll 1
@@ -654,9 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
               l *= alpha;
               m = m_new;
             }
+            any_far = __any_sync(0xffffffffu, is_far());
           }
           const float neg_m = m == -INFINITY ? 0.f : kWeightUp - m;
-          auto weights = [&](auto own_factors) {
+          auto weights = [&](auto rare) {
 #pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
               uint32_t s[32], pk[16];
@@ -674,10 +680,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
                 float w[16];
 #pragma unroll
                 for (int k = 0; k < 16; k += 2) {
+                  const float s0 = __uint_as_float(s[16 * h + k]), s1 = __uint_as_float(s[16 * h + k + 1]);
                   float f0 = f, f1 = f;
-                  if (own_factors.value && f16 == INFINITY) f0 = score_factor(c, own[k]), f1 = score_factor(c, own[k + 1]);
-                  ffma2(w[k], w[k + 1], __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]), f0, f1, neg_m,
-                        neg_m);
+                  if (rare.value && f16 == INFINITY) f0 = score_factor(c, own[k]), f1 = score_factor(c, own[k + 1]);
+                  ffma2(w[k], w[k + 1], s0, s1, f0, f1, neg_m, neg_m);
+                  if (rare.value && is_far())
+                    w[k] = __fsub_rn(__fmul_rn(s0, f0), m) + kWeightUp, w[k + 1] = __fsub_rn(__fmul_rn(s1, f1), m) + kWeightUp;
                   w[k] = ex2_approx(w[k]), w[k + 1] = ex2_approx(w[k + 1]);
                   fadd2(la, lb, la, lb, w[k], w[k + 1]);
                 }
@@ -702,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
               tmem_st_x16(tS + ch * 16, pk);  // over scores that have been read
             }
           };
-          if (own)
+          if (own || any_far)
             weights(std::true_type());
           else
             weights(std::false_type());

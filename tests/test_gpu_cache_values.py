@@ -251,3 +251,25 @@ def test_a_scale_next_to_nothing(form, B, H, Hkv, T, Smax, bits):
     k, v, q = _rand(10, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))
     q[:, 0].zero_()
     _check(form, bits, q.to(BF16), k.to(BF16), v.to(BF16), [Smax - 5] * B, scale=2.0 ** -120)
+
+
+@both_bits
+@pytest.mark.parametrize("e", [100, 112, 118, 124])
+@each_form
+def test_very_large_queries(form, B, H, Hkv, T, Smax, e, bits):
+    """Q up to 2^126: over K of 2^-95, with a scale that makes up for the rest; then K such that a row's largest score
+    takes it all; one such row among ordinary ones leaves those as they are."""
+    k, v, q = _rand(11, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))
+    small, large, v = (k * 2.0 ** -95).to(BF16), (q * 2.0 ** e).to(BF16), v.to(BF16)
+    lens = [Smax - 3 - 30 * b for b in range(B)]
+    _check(form, bits, large, small, v, lens, Smax - 99, 5, scale=SCALE * 2.0 ** (95 - e))
+    _check(form, bits, large, small, v, lens, all_rows=False)
+    k, q = k.to(BF16), q.to(BF16)
+    want = _check(form, bits, q, k, v, lens)
+    mixed = q.clone()
+    mixed[:, -1, 1] = (mixed[:, -1, 1].float() * 2.0 ** (e - 2)).to(BF16)  # scores below 2^127 for e = 124 too
+    o, lse = _check(form, bits, mixed, k, v, lens, all_rows=False)
+    keep = torch.ones(T, H, dtype=torch.bool, device="cuda")
+    keep[-1, 1] = False
+    assert torch.equal(o[:, keep], want[0][:, keep])
+    assert torch.equal(lse.transpose(1, 2)[:, keep], want[1].transpose(1, 2)[:, keep])
