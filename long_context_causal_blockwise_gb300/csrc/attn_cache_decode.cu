@@ -147,8 +147,8 @@ struct State {
   float o[8][C::kTiles][4];     // o[2 G + f]: channels 32 G + 4 g + 2 f + {0, 1}, each of columns 2t, 2t + 1
   float m[C::kMine], l[C::kMine];
   float neg_m[C::kMine], raise_at[C::kMine];  // -m (0 while nothing is seen); the product above which m is raised
-  float up;                     // what weights go into the second product with: 2^kUp, or less
-  uint32_t up_limit;            // bf16, twice: V's scales above it want a smaller one
+  float up[C::kMine];           // what a row's weights go into the second product with: 2^kUp, or less
+  uint32_t up_limit;            // bf16, twice: V's scales above it want a smaller one, of some row that sees them
   // O of a lane's row i in channel 32 G + 4 g + k, times `up` and a subnormal's factor
   __device__ float& out(int i, int G, int k) {
     const int col = C::kHalves ? G >> 1 : i & 1;
@@ -157,8 +157,9 @@ struct State {
   __device__ float true_out(int i, int G, int k, float down) {
     return out(i, G, k) * (BITS == 4 && (k & 1) ? 0x1p61f : 0x1p65f) * down;
   }
+  __device__ int up_exponent(int i) const { return static_cast<int>(__float_as_uint(up[i]) >> 23) - 127; }
   // 2^68 / up: an exponent of at most 85
-  __device__ float down() const { return exp2_int(68 - (static_cast<int>(__float_as_uint(up) >> 23) - 127)); }
+  __device__ float down(int i) const { return exp2_int(68 - up_exponent(i)); }
 };
 
 // A lane's part of Q as it lies in memory.
@@ -241,36 +242,50 @@ __device__ __forceinline__ void begin(State<ROWS, BITS>& w, const RawQ<ROWS>& ra
     w.pr[i] = r < p.T * p.G ? a.p0 + (p.G == 1 ? r : r / p.G) : -1;
     w.m[i] = w.raise_at[i] = -INFINITY;
     w.l[i] = 0.f;
+    w.up[i] = exp2_int(kUp);
   }
-  w.up = exp2_int(kUp);
   w.up_limit = 0x10001u * ((kUpRange + 127) * 128 - 1);
 }
 
-// V's scales (of the lane's two keys) are so large that weights times `up` would
-// not fit: the smaller `up` that the largest one needs. NaN is none of them.
-template <int ROWS, int BITS>
-__device__ __forceinline__ void lower_up(State<ROWS, BITS>& w, const uint4 (&sc)[2]) {
-  uint32_t top = 0;
+// The largest scale of V, as bits, for which a weight times 2^(119 - range) times it is a number: below 2^range.
+__device__ __forceinline__ uint32_t scale_limit(int range) { return range >= 128 ? 0x7f7fu : (range + 127) * 128 - 1; }
+
+// Some scales of V (of the lane's two keys) are so large that weights times `up` would not fit: for each row, the smaller
+// `up` that the largest one that it sees needs. (A key that it does not see takes nothing of its precision.) NaN is none
+// of them. `sees` tells whether the lane's row i sees its key h.
+template <int ROWS, int BITS, class Sees>
+__device__ __forceinline__ void lower_up(State<ROWS, BITS>& w, const uint4 (&sc)[2], Sees&& sees) {
+  using C = Cols<ROWS>;
+  uint32_t top[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h) {
+    top[h] = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t x = i < 2 ? sc[h].z : sc[h].w, s = i & 1 ? x >> 16 : x & 0xffffu;
-      top = max(top, s < 0x7f80u ? s : 0u);
+      top[h] = max(top[h], s < 0x7f80u ? s : 0u);
     }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (top <= (w.up_limit & 0xffffu)) return;
-  const int e = static_cast<int>(top >> 7) - 126;  // scales below 2^e
-  const int range = min(e + 8, 128);               // room for some growth
-  const float up = exp2_int(119 - range), f = up / w.up;
-  w.up = up;
-  w.up_limit = range >= 128 ? 0x7f7f7f7fu : 0x10001u * ((range + 127) * 128 - 1);
+  }
+  if (__reduce_max_sync(0xffffffffu, max(top[0], top[1])) <= (w.up_limit & 0xffffu)) return;
+  uint32_t limit = 0xffffu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < C::kMine; ++i) {
+    uint32_t seen = max(sees(0, i) ? top[0] : 0u, sees(1, i) ? top[1] : 0u);
+    for (int x = 4; x < 32; x *= 2) seen = max(seen, __shfl_xor_sync(0xffffffffu, seen, x));
+    float f = 1.f;
+    if (seen > scale_limit(119 - w.up_exponent(i))) {
+      const int e = static_cast<int>(seen >> 7) - 126;      // scales below 2^e
+      const float up = exp2_int(119 - min(e + 8, 128));     // room for some growth
+      f = up / w.up[i];
+      w.up[i] = up;
+    }
+    limit = min(limit, scale_limit(119 - w.up_exponent(i)));
 #pragma unroll
-    for (int nt = 0; nt < Cols<ROWS>::kTiles; ++nt)
+    for (int G = 0; G < 4; ++G)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w.o[i][nt][k] *= f;
+      for (int k = 0; k < 4; ++k) w.out(i, G, k) *= f;
+  }
+  w.up_limit = 0x10001u * __reduce_min_sync(0xffffffffu, limit);
 }
 
 // Which of a step's sixteen keys is row x + 8 h of the first product, and so the second one's x + 8 h along the sum: rows
@@ -393,7 +408,7 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
   const uint32_t v_top = max_u16x2(max_u16x2(sc[0].z, sc[0].w), max_u16x2(sc[1].z, sc[1].w));
   raise |= max_u16x2(v_top, w.up_limit) != w.up_limit;
   if (__any_sync(0xffffffffu, raise)) {
-    lower_up(w, sc);
+    lower_up(w, sc, [&](int h, int i) { return !CUT || seen[h][i]; });
 #pragma unroll
     for (int i = 0; i < C::kMine; ++i) {
       const bool was_far = is_far(w.neg_m[i]);
@@ -430,7 +445,7 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
     for (int i = 0; i < C::kMine; ++i) {
       e[i] = ex2_approx(fmaf(s[h][i], w.c[i], w.neg_m[i]));
       w.l[i] += e[i];
-      e[i] *= w.up;
+      e[i] *= w.up[i];
     }
     // a weight times a scale; what belongs to a hidden row may be anything
     auto product = [&](int i, int c) { return CUT && !seen[h][i] ? 0.f : e[i] * v_scale(h, c); };
@@ -481,10 +496,10 @@ __device__ __forceinline__ void join_warps(Parts<ROWS, kWarps>& sm, State<ROWS, 
                                            Emit&& emit) {
   using C = Cols<ROWS>;
   const int g = lane >> 2, t = lane & 3;
-  const float down = w.down();
 #pragma unroll
   for (int i = 0; i < C::kMine; ++i) {
     const int r = C::row(i, t);
+    const float down = w.down(i);
 #pragma unroll
     for (int x = 4; x < 32; x *= 2) w.l[i] += __shfl_xor_sync(0xffffffffu, w.l[i], x);
     if (g == 0) {

@@ -273,3 +273,37 @@ def test_very_large_queries(form, B, H, Hkv, T, Smax, e, bits):
     keep[-1, 1] = False
     assert torch.equal(o[:, keep], want[0][:, keep])
     assert torch.equal(lse.transpose(1, 2)[:, keep], want[1].transpose(1, 2)[:, keep])
+
+
+def _values_that_the_last_token_sees(form, B, H, Hkv, T, Smax, bits):
+    """V up to bf16's largest number, and far below 1, in the newest key: the other tokens' rows keep their bits."""
+    k, v, q = [x.to(BF16) for x in _rand(12, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))]
+    want = _check(form, bits, q, k, v)
+    for x in (2.0 ** -30, 2.0 ** 10, 2.0 ** 100, 2.0 ** 120, torch.finfo(BF16).max):
+        other = v.clone()
+        other[:, -1] = x
+        o, lse = lcb.attn_cache_decode(q, _cache(k, other, bits), _lens(*[Smax] * B))
+        assert torch.equal(o[:, :-1], want[0][:, :-1]), x
+        assert torch.equal(lse, want[1]), x
+
+
+@both_bits
+@pytest.mark.parametrize("form,B,H,Hkv,T,Smax", FORMS[:6])
+def test_a_huge_value_that_only_the_last_token_sees(form, B, H, Hkv, T, Smax, bits):
+    _values_that_the_last_token_sees(form, B, H, Hkv, T, Smax, bits)
+
+
+@both_bits
+@pytest.mark.parametrize("which", ["large", "all sizes", "grows"])
+@each_form
+def test_values_of_all_sizes(form, B, H, Hkv, T, Smax, which, bits):
+    """V whose sizes change at once, from key to key, and along the keys, in every layout."""
+    k, v, q = _rand(13, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))
+    g = torch.Generator(device="cuda").manual_seed(14)
+    if which == "large":
+        v = v * 2.0 ** 95
+    elif which == "all sizes":
+        v = v * torch.exp2(torch.randint(-30, 30, (B, Smax, Hkv, 1), generator=g, device="cuda").float())
+    else:
+        v = v * torch.exp2((torch.arange(Smax, device="cuda") * 130 // Smax - 40).float())[None, :, None, None]
+    _check(form, bits, q.to(BF16), k.to(BF16), v.to(BF16), [Smax - 3 - 30 * b for b in range(B)], Smax - 99, 5)
