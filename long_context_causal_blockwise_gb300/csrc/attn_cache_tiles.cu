@@ -35,9 +35,9 @@
 // its own. Where the sixteen keys' scales of V are ordinary (2^-7, in 8 bits 2^-11,
 // up to 16, or zero) they are fp16: 2^-12 s n, off by 2^-13 of the group's largest
 // value at best, 2^-9 of it at the smallest scales, and 2^7 P, off by 2^-12 down to
-// weights of 2^-21 of the largest. Otherwise, and where fewer than sixteen keys
-// exist, bf16 with the same powers of two: off by half a step, 2^-9 to 2^-8 of each
-// value. (bf16 for all of them: errors 2.8e-3 of the outputs instead of 1.7e-3, which
+// weights of 2^-21 of the largest. Otherwise, and where some row of the tile does not
+// see all sixteen (so that no row's bits depend on V that it does not see), bf16 with
+// the same powers of two: off by half a step, 2^-9 to 2^-8 of each value. (bf16 for all of them: errors 2.8e-3 of the outputs instead of 1.7e-3, which
 // is what rounding these to bf16 costs, and 2 us of 53 less.) NaN of V are zeros in
 // the tile, so that a weight of zero leaves nothing of them; the rows that see one
 // are told by bits, 1 us of 53.
@@ -154,13 +154,14 @@ __device__ __forceinline__ uint8_t* chunk_of(uint8_t* tile, uint32_t first, int 
 
 // Whether a scale of V among the sixteen keys is not one for fp16; if so, which ones are NaN (v_nan; an infinity, which
 // kv_cache_write never leaves, counts as one).
+// `cut` says so beforehand.
 template <int BITS>
-__device__ __forceinline__ bool wide_v(const uint8_t* rec, uint2* nan, int lane) {
+__device__ __forceinline__ bool wide_v(const uint8_t* rec, bool cut, uint2* nan, int lane) {
   const uint32_t x = *reinterpret_cast<const uint32_t*>(rec + (lane >> 1) * cache_row_bytes(BITS) +
                                                         cache_scale_offset(BITS) + 8 + 4 * (lane & 1));
   constexpr uint32_t kLow = (BITS == 4 ? 120u : 116u) << 7, kHigh = 131u << 7;  // 2^-7 or 2^-11, 2^4
   auto out = [](uint32_t a) { return a != 0 && (a < kLow || a >= kHigh); };
-  const bool wide = __any_sync(0xffffffffu, out(x & 0xffffu) || out(x >> 16));
+  const bool wide = __any_sync(0xffffffffu, cut || out(x & 0xffffu) || out(x >> 16));
   if (wide) {
     const uint32_t even = __ballot_sync(0xffffffffu, (x & 0x7f80u) == 0x7f80u);
     const uint32_t odd = __ballot_sync(0xffffffffu, (x & 0x7f800000u) == 0x7f800000u);
@@ -233,10 +234,10 @@ __device__ __forceinline__ void unpack_k_rows(const uint8_t* rec, uint8_t* tile,
   }
 }
 
-// Sixteen keys of K by a warp; the first nk of the records exist.
+// Sixteen keys of K by a warp; the first nk of the records exist. cut: some row of the tile does not see all sixteen.
 template <int BITS>
 __device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int row0, int nk, float* factor, float* own,
-                                         uint2* nan, int lane, bool& is_wide) {
+                                         uint2* nan, bool cut, int lane, bool& is_wide) {
   constexpr int kRec = cache_row_bytes(BITS);
   uint32_t x = 0;  // half a key's scales
   if ((lane >> 1) < nk)
@@ -245,11 +246,7 @@ __device__ __forceinline__ void unpack_k(const uint8_t* rec, uint8_t* tile, int 
   // the smallest one, less 1 so that zeros are none; whether its exponent is more than 8 below
   const uint32_t low = __reduce_min_sync(0xffffffffu, min((x - 1u) & 0xffffu, ((x >> 16) - 1u) & 0xffffu));
   const bool each = ((low + 1u) >> 7) + 8u < top >> 7;
-  bool wide = wide_v<BITS>(rec, nan, lane);
-  if (!wide && nk < 16) {
-    if (lane == 0) *nan = make_uint2(0, 0);
-    wide = true;
-  }
+  const bool wide = wide_v<BITS>(rec, cut, nan, lane);
   is_wide = wide;
   // scales are below 2^(e + 1): times 2^(15 - e) they are fp16, and with the codes' 2^-24 they make s n 2^(-9 - e)
   const int e = top_exponent(top);
@@ -478,10 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           ok = mbar_wait_warp(&bars.k_empty[kt], (BITS == 4 ? ph : static_cast<uint32_t>(i) & 1u) ^ 1u, abort_flag, p.st,
                               kWhere | (3u << 16));
         if (!ok) break;
+        // whether some row of the tile does not see all sixteen
+        const int k0 = j0 + row0, k1 = k0 + 15;
+        const bool cut = mine < 16 || k1 > a.p_min || (k0 <= a.p_max - p.window && k1 >= p.sinks);
         bool wide = true;
         if (mine > 0)
           unpack_k<BITS>(rec, sm.K[kt], row0, mine, &sm.k_factor[i & 3][w], &sm.key_factor[i & 3][row0],
-                         &sm.v_nan[i & 3][w], lane, wide);
+                         &sm.v_nan[i & 3][w], cut, lane, wide);
         else if (lane == 0)
           sm.k_factor[i & 3][w] = -1.f, sm.v_nan[i & 3][w] = make_uint2(0, 0);
         fence_to_async();

@@ -307,3 +307,23 @@ def test_values_of_all_sizes(form, B, H, Hkv, T, Smax, which, bits):
     else:
         v = v * torch.exp2((torch.arange(Smax, device="cuda") * 130 // Smax - 40).float())[None, :, None, None]
     _check(form, bits, q.to(BF16), k.to(BF16), v.to(BF16), [Smax - 3 - 30 * b for b in range(B)], Smax - 99, 5)
+
+
+@both_bits
+@pytest.mark.parametrize("form,B,H,Hkv,T,Smax", FORMS[6:])
+def test_a_huge_value_that_only_the_last_token_sees_tiles(form, B, H, Hkv, T, Smax, bits):
+    _values_that_the_last_token_sees(form, B, H, Hkv, T, Smax, bits)
+
+
+@both_bits
+@each_form
+def test_rows_before_the_last_token_are_those_without_it(form, B, H, Hkv, T, Smax, bits):
+    """The newest key's V at any distance from a multiple of sixteen: the other rows keep their bits."""
+    k, v, q = [x.to(BF16) for x in _rand(15, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))]
+    for back in (0, 1, 7, 15, 16):
+        n, lens = Smax - back, _lens(*[Smax - back] * B)
+        want = lcb.attn_cache_decode(q, _cache(k, v, bits), lens)
+        other = v.clone()
+        other[:, n - 1, :, ::3] = 2.0 ** 9
+        o, lse = lcb.attn_cache_decode(q, _cache(k, other, bits), lens)
+        assert torch.equal(o[:, :-1], want[0][:, :-1]) and torch.equal(lse, want[1]), back
