@@ -787,12 +787,14 @@ def kv_cache_read(cache, n, start=0, lens=None, k=None, v=None):
 
 def attn_cache_decode_workspace_bytes(B, H, Hkv, T, Smax, bits=4, window=None, sinks=0, D=128):
     """Bytes of workspace that attn_cache_decode needs for these sizes on the current device."""
-    return _cache_decode_workspace(torch.cuda.current_device() if torch.cuda.is_available() else -1, B, H, Hkv, T, Smax,
-                                   D, bits, _MOST if window is None else _count(window), _count(sinks))
+    return int(load().attn_cache_decode_workspace_bytes(B, H, Hkv, T, Smax, D, bits,
+                                                        _MOST if window is None else _count(window), _count(sinks)))
 
 
 @functools.lru_cache(maxsize=4096)  # a decoding loop asks for the same sizes over and over
 def _cache_decode_workspace(device, *sizes):
+    """What the library said for these sizes once, on this device: in another context, or after a query of the device
+    that failed, it may say otherwise, so a call that is refused asks again."""
     return int(load().attn_cache_decode_workspace_bytes(*sizes))
 
 
@@ -829,17 +831,26 @@ def attn_cache_decode(q, cache, lens, window=None, sinks=0, scale=None, o=None, 
     dev = q.get_device()
     stream = _raw_stream("attn_cache_decode", dev, (cache, lens, o, lse) if workspace is None else (cache, lens, o, lse,
                                                                                                   workspace))
-    if workspace is None:
-        n = _cache_decode_workspace(dev, B, H, Hkv, T, Smax, D, bits, window, sinks)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    rc = (_LIB or load()).attn_cache_decode(
-        q.data_ptr(), cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, Smax, D, bits,
-        window, sinks, D ** -0.5 if scale is None else float(scale), qr, qb, cb, ch, orr, ob, lh, lb,
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+
+    def call(ws):
+        return (_LIB or load()).attn_cache_decode(
+            q.data_ptr(), cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, Smax, D, bits,
+            window, sinks, D ** -0.5 if scale is None else float(scale), qr, qb, cb, ch, orr, ob, lh, lb,
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), stream)
+
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        rc = call(workspace)
+    else:
+        sizes = dev, B, H, Hkv, T, Smax, D, bits, window, sinks
+        n = _cache_decode_workspace(*sizes)
+        rc = call(torch.empty(n, dtype=torch.uint8, device=q.device) if n else None)
+        if rc == LCB_ERR_ARG:
+            _cache_decode_workspace.cache_clear()
+            now = _cache_decode_workspace(*sizes)
+            if now > n:
+                rc = call(torch.empty(now, dtype=torch.uint8, device=q.device))
     if rc:
         _check("attn_cache_decode", rc)
     return o, lse

@@ -167,3 +167,42 @@ def test_python_refusals():
         lcb.kv_cache_write(cache, k, k, lens)
     with pytest.raises(ValueError):
         lcb.kv_cache_read(cache, 2)
+
+
+class _Library:
+    """Answers as the library does in one device context, whose calls need `need` bytes; queries listed in `says` answer
+    that instead (one that failed: 0)."""
+
+    def __init__(self, need, says=()):
+        self.need, self.says, self.given = need, list(says), []
+        self.attn_status_string = _lib.load().attn_status_string
+
+    def attn_cache_decode_workspace_bytes(self, *sizes):
+        return self.says.pop(0) if self.says else self.need
+
+    def attn_cache_decode(self, *args):
+        self.given.append(args[-2])
+        return OK if args[-2] >= self.need else ERR_ARG
+
+
+def test_a_workspace_size_that_is_out_of_date_is_asked_for_again(monkeypatch):
+    cache = lcb.kv_cache_empty(1, 2, 16, device="cpu")
+    q, lens = torch.zeros(1, 1, 4, 128, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    monkeypatch.setattr(_lib, "_raw_stream", lambda *args: 0)
+    _lib._cache_decode_workspace.cache_clear()
+
+    def calls(lib, n, **kw):
+        monkeypatch.setattr(_lib, "_LIB", lib)
+        for _ in range(n):
+            lcb.attn_cache_decode(q, cache, lens, **kw)
+        return lib.given
+
+    assert calls(_Library(64, says=[0]), 2) == [0, 64, 64]  # the first query failed
+    assert calls(_Library(128), 2) == [64, 128, 128]        # a context with more SMs
+    assert calls(_Library(96), 1) == [128]                  # and one with fewer
+    assert lcb.attn_cache_decode_workspace_bytes(1, 4, 2, 1, 16) == 96  # what is said to the caller is never kept
+    with pytest.raises(lcb.AttnError):                      # a size of the caller's own is refused as it is
+        calls(_Library(256), 1, workspace=torch.empty(128, dtype=torch.uint8))
+    with pytest.raises(lcb.AttnError):
+        calls(_Library(1 << 40, says=[64, 64]), 1)          # still too little: an error, no second attempt
+    _lib._cache_decode_workspace.cache_clear()
