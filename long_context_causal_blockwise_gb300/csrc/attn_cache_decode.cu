@@ -10,8 +10,9 @@
 // rounded. p s^V goes to bf16 for the second product, as P does in the other
 // forms: half a step, up to 2^-8 of each weight, of either sign. Q goes to fp16
 // for the first one, after a division by a power of two that puts a row's
-// largest element into [2^8, 2^9): exact but for elements below 2^-17 of that
-// largest, whose errors are under 2^-28 of it.
+// largest element into [2^15, 2^16), or [2^11, 2^12) in the half of the channels whose
+// 4-bit codes lie 2^4 higher: exact but for elements below 2^-28 of that largest, whose
+// errors are under 2^-36 of it.
 //
 // Every visible record (144 or 272 bytes) is read once for all query rows that
 // share its head, up to 16 of them. HBM bounds it only if little is done per
@@ -130,7 +131,7 @@ constexpr int kUp = 96;            // weights go into the second product times 2
 constexpr int kUpRange = 119 - kUp;  // while V's scales are below 2^23: a weight is 2^8 at most
 
 // A row is far where one fused multiplication does not make weights of its products: where its factor could pass fp32's
-// end (a largest |q| of 2^68 or more), or where its maximum is so large that the rounding of the product it was is no
+// end (a largest |q| of 2^75 or more), or where its maximum is so large that the rounding of the product it was is no
 // longer small beside 1. Its raise_at stays -inf, so that every step takes the branch that raises a maximum, and there
 // its products become differences from m, by a multiplication and a subtraction, over c. Such a row's c is its factor
 // over 2^24, and its neg_m -0, which no other row's is. (With the factor in a register of its own: 8 heads x 65536
@@ -190,7 +191,6 @@ __device__ __forceinline__ void begin(State<ROWS, BITS>& w, const RawQ<ROWS>& ra
                                       int g, int t) {
   using C = Cols<ROWS>;
   constexpr int kLoaded = C::kHalves ? 2 : 4;  // groups that the lane has
-  constexpr int kTop = 8;
 #pragma unroll
   for (int nt = 0; nt < C::kTiles; ++nt) {
     uint32_t top = 0;
@@ -203,7 +203,7 @@ __device__ __forceinline__ void begin(State<ROWS, BITS>& w, const RawQ<ROWS>& ra
 #pragma unroll
     for (int x = 1; x < (C::kHalves ? 8 : 4); x *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
     const int e = static_cast<int>(top >> 7);  // 127 more than the exponent; 255 with infinities or NaN
-    const int up = min(126, kTop + 127 - e);
+    const int up = min(126, kQTop + 127 - e);
     const float f = e == 255 ? __int_as_float(0x7fc00000) : exp2_int(up);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {

@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
 #pragma unroll
             for (int j = 0; j < 4; ++j) top = max(top, max(x[j] & 0x7fffu, x[j] >> 16 & 0x7fffu));
           }
-        const int e = static_cast<int>(top >> 7), up = min(126, 8 + 127 - e);
+        const int e = static_cast<int>(top >> 7), up = min(126, kQTop + 127 - e);
         const float f = e == 255 ? __int_as_float(0x7fc00000) : exp2_int(up);
         c = exp2_int(kFactorDown - up) * p.scale_log2;
 #pragma unroll

@@ -11,6 +11,7 @@ namespace lcb {
 
 constexpr int kCacheD = 128;
 constexpr int kLineSequences = 1024;  // whose lengths a CTA keeps in shared memory
+constexpr int kQTop = 15;  // a row's largest element of Q goes to [2^15, 2^16) in fp16: bf16's largest mantissa fits
 constexpr float kLeastFactor = 0x1p-149f;  // of a score: fp32's smallest number
 
 // Contiguous bytes (a multiple of 16, both ends aligned to 16) into shared memory, completing on `bar`.

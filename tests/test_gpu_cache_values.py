@@ -5,7 +5,8 @@ Q, K and V, and values that a row does not see.
 
 Bounds. A pair's score is off by at most d = 2 * 128 * 2^-24 * scale * |q| |k|
 (window_bounds.py; in 8 bits in the form for many rows 2^-12 of K's lower four bits
-more, test_gpu_kv_cache.py), so its weight by a factor between e^-d and e^d. With
+more, test_gpu_kv_cache.py; and scale * 2^-36 max |q| sum |k|, as Q goes to fp16 with
+its largest element at 2^15, or 2^11 for half of the channels), so its weight by a factor between e^-d and e^d. With
 w = e^d - 1 and z = sum p w + 2^-20 (ex2.approx and the sums), the sum of weights is
 off by z at most, and where z <= 1/2
   |dLSE| <= 2 z + 2^-21 (1 + |LSE|)
@@ -103,7 +104,7 @@ def _compare(q, kd, vd, window, sinks, pos0, scale, o, lse, bits, form, name):
         assert torch.equal(torch.isfinite(lse[h]), seen) and (lse[h][~seen] == -torch.inf).all(), f"{name} LSE: empty rows"
         assert (o[:, h][~seen] == 0).all(), f"{name} O: empty rows"
         qh, kh, vh = qh.abs(), kh.abs(), vh.abs()
-        d = 2 * 128 * 2.0 ** -24 * scale * (qh @ kh.T)
+        d = 2 * 128 * 2.0 ** -24 * scale * (qh @ kh.T) + scale * 2.0 ** -36 * qh.amax(dim=1)[:, None] * kh.sum(dim=1)
         if bits == 8 and form == "tiles":
             top = kh.unflatten(1, (4, 32)).amax(dim=2)
             d = d + scale * (qh.unflatten(1, (4, 32)).sum(dim=2) @ top.T) * 2.0 ** -12 * 15 / 127 * (1 + U)
@@ -327,3 +328,16 @@ def test_rows_before_the_last_token_are_those_without_it(form, B, H, Hkv, T, Sma
         other[:, n - 1, :, ::3] = 2.0 ** 9
         o, lse = lcb.attn_cache_decode(q, _cache(k, other, bits), lens)
         assert torch.equal(o[:, :-1], want[0][:, :-1]) and torch.equal(lse, want[1]), back
+
+
+# ------------------------------------------------------------------ Q whose sizes differ among channels
+
+
+@both_bits
+@pytest.mark.parametrize("form,B,H,Hkv,T,Smax,e", [(*f, e) for f in FORMS for e in (14, 22)] + [(*f, 27) for f in FORMS[:6]])
+def test_small_channels_of_q_over_large_ones_of_k(form, B, H, Hkv, T, Smax, e, bits):
+    """K's second group 2^e times the others, Q's the same below them: all groups count alike."""
+    k, v, q = _rand(16, (B, Smax, Hkv, D), (B, Smax, Hkv, D), (B, T, H, D))
+    k[..., 32:64] *= 2.0 ** e
+    q[..., 32:64] *= 2.0 ** -e
+    _check(form, bits, q.to(BF16), k.to(BF16), v.to(BF16))
