@@ -55,7 +55,6 @@ namespace lcb {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kSms = 152;
 constexpr int kStep = 16;  // keys of a product, and of a warp's turn
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum is raised lazily, P stays <= 256
 constexpr uint32_t kWhere = 9u << 24;
@@ -876,14 +875,14 @@ Plan plan_of(int B, int H, int Hkv, int T, int Smax, int window, int sinks) {
 template <int ROWS, int BITS>
 struct ClusterChoice {
   int warps, cluster;
-  long long in_flight;  // warps of the tiles that the GPU holds at once
+  long long all_warps;  // of the tiles
   ClusterChoice(const Plan& a, const ContextKey& at) {
     const long long units = (a.keys + unit_keys<BITS>() - 1) / unit_keys<BITS>();
     const int c4 = ClusterForm<ROWS, BITS, 4>::one_wave(at, a.tiles, units);
     const int c8 = ROWS == 16 ? 0 : ClusterForm<ROWS, BITS, 8>::one_wave(at, a.tiles, units);
     warps = 4 * c4 >= 8 * c8 ? 4 : 8;
     cluster = std::max(1, warps == 4 ? c4 : c8);
-    in_flight = std::min<long long>(a.tiles * cluster * warps, kSms * warps_per_sm(ROWS));
+    all_warps = a.tiles * cluster * warps;
   }
 };
 
@@ -896,14 +895,14 @@ struct ClusterChoice {
 // 20001, eight rows, 38 / 42; 160 x 32772 127 / 114; 8 x 131072 in 8 bits 69 / 50; 8 x
 // 524288 204 / 99; 1 x 524288 123 / 25; 4 x 100000 33 / 23; 512 x 2000 26 / 36; 80 x
 // 5000 in 8 bits 20 / 24; 40 x 32768 40 / 38; 8 x 65536, eight rows 37 / 26, sixteen
-// 56 / 37. Of 33 sizes four take the slower form, by 3, 4, 12 and 15%.
+// 56 / 37.
 template <int ROWS, int BITS>
 int line_ctas(const Plan& a, const ClusterChoice<ROWS, BITS>& c, const ContextKey& at) {
   const int n = LineForm<ROWS, BITS>::ctas(at);
   const long long units = a.tiles * ((a.keys + Line<ROWS, BITS>::kKeys - 1) / Line<ROWS, BITS>::kKeys + 1);
   if (n <= 0 || a.B > kLineSequences || a.row_tiles > 8 || units + a.tiles * kTileCost<ROWS> >= 1LL << 31) return 0;
   const double hbm_us = static_cast<double>(a.tiles) * a.keys * cache_row_bytes(BITS) / 6.7e6;
-  const double busy = static_cast<double>(c.in_flight) / (kSms * warps_per_sm(ROWS));
+  const double busy = std::min(1.0, static_cast<double>(c.all_warps) / (n * warps_per_sm(ROWS)));  // n: one CTA to an SM
   const double cluster_us = 5 + 1.15 * hbm_us / std::min(1.0, (BITS == 4 ? 1.0 : 1.5) * busy);
   const double more = std::max(0.0, static_cast<double>(a.tiles) / n - 1);
   const double line_us = 12 + (BITS == 4 && ROWS > 4 ? 1.25 : 1.08) * hbm_us + 3.5 * more;
