@@ -59,15 +59,6 @@ constexpr int kStep = 16;  // keys of a product, and of a warp's turn
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum is raised lazily, P stays <= 256
 constexpr uint32_t kWhere = 9u << 24;
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -93,18 +84,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-
 // How a tile of ROWS query rows lies in the eight columns of a product, and
 // what a lane (g, t) has of them.
 //   8, 16: a column is a row; lane t has the rows 2t and 2t + 1 of every eight.
@@ -122,9 +101,6 @@ struct Cols {
   static constexpr int kSums = kHalves ? 2 : 4;              // sums, and operands, per eight columns
   static __device__ int row(int i, int t) { return kHalves ? t : 8 * (i >> 1) + 2 * t + (i & 1); }  // a lane's i-th
 };
-
-// 2^e, e from -126 to 127.
-__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 constexpr int kUp = 96;            // weights go into the second product times 2^96, which subnormal codes take back
 constexpr int kUpRange = 119 - kUp;  // while V's scales are below 2^23: a weight is 2^8 at most

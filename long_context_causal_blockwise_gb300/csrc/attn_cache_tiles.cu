@@ -111,8 +111,6 @@ constexpr uint32_t idesc_f16(int M, int N, bool transposed_b = false) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-
 // Byte offset of 16-byte chunk c (of 8 channels, 16 a row) of row r in a tile with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return static_cast<uint32_t>(c >> 3) * kHalfBytes + static_cast<uint32_t>(r) * 128u +

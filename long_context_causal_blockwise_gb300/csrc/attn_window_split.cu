@@ -45,21 +45,6 @@ constexpr int kKeys = 16;  // keys per warp step
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: the running maximum is raised lazily, P stays <= 256
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -67,9 +52,6 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
                : "l"(p));
   return v;
 }
-
-// Weight of a partial with maximum m in a sum with maximum M >= m (both -inf: the partial is empty, or NaN).
-__device__ __forceinline__ float weight(float m, float M) { return m == M ? 1.f : ex2_approx(m - M); }
 
 // A CTA's shared memory: its warps' partials, joined into slot 0, cM and cL.
 template <int kRows, int kWarps>
@@ -187,8 +169,8 @@ __global__ void __launch_bounds__(32 * kWarps) window_split_kernel(const __grid_
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma_16816(s[nt], kf[0][c].x, kf[1][c].x, kf[0][c].y, kf[1][c].y, qf[nt][2 * c][0], qf[nt][2 * c][1]);
-        mma_16816(s[nt], kf[0][c].z, kf[1][c].z, kf[0][c].w, kf[1][c].w, qf[nt][2 * c + 1][0], qf[nt][2 * c + 1][1]);
+        mma_bf16(s[nt], kf[0][c].x, kf[1][c].x, kf[0][c].y, kf[1][c].y, qf[nt][2 * c][0], qf[nt][2 * c][1]);
+        mma_bf16(s[nt], kf[0][c].z, kf[1][c].z, kf[0][c].w, kf[1][c].w, qf[nt][2 * c + 1][0], qf[nt][2 * c + 1][1]);
       }
     const int next = step + kWarps;
     if (next < end) load_k(next * kKeys);  // the fragments' registers are free: the next keys are on their way
@@ -254,7 +236,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_split_kernel(const __grid_
         const uint32_t a0 = __byte_perm(v0[i], v1[i], 0x5410), a1 = __byte_perm(v0[i], v1[i], 0x7632);
         const uint32_t a2 = __byte_perm(v2[i], v3[i], 0x5410), a3 = __byte_perm(v2[i], v3[i], 0x7632);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816(o[4 * h + i][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_bf16(o[4 * h + i][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
       }
     }
     if (next < end) load_v(next * kKeys);

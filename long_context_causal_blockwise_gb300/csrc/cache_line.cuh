@@ -14,17 +14,6 @@ constexpr int kLineSequences = 1024;  // whose lengths a CTA keeps in shared mem
 constexpr int kQTop = 15;  // a row's largest element of Q goes to [2^15, 2^16) in fp16: bf16's largest mantissa fits
 constexpr float kLeastFactor = 0x1p-149f;  // of a score: fp32's smallest number
 
-// Contiguous bytes (a multiple of 16, both ends aligned to 16) into shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// Weight of a partial with maximum m in a sum with maximum M >= m (both -inf: the partial is empty, or NaN).
-__device__ __forceinline__ float weight(float m, float M) { return m == M ? 1.f : ex2_approx(m - M); }
-
 // Rows of a sequence in the cache.
 __device__ __forceinline__ int length(const CacheDecode& p, int len) { return min(max(len, 0), p.Smax); }
 

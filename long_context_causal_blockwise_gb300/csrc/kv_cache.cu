@@ -49,11 +49,6 @@ __device__ __forceinline__ uint32_t magnitude(float x, float inv) {
 }
 constexpr uint32_t kMagic = 0x4b400000u;  // the bits around it
 
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // The larger magnitudes of two pairs of bf16 (with some sign); NaN where there is one.
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
