@@ -476,7 +476,9 @@ int attn_window_decode(const void* q, const void* k, const void* v, const int* l
  * x_c / s rounded to the nearest whole number, ties away from zero: off by at
  * most s / 2 (and the scale's rounding at the group's largest, 2^-8 of it).
  * A group whose largest magnitude is below 2^-100 holds zeros; one with an
- * infinity or a NaN holds NaN in all 32 channels.
+ * infinity or a NaN holds NaN in all 32 channels. Of a group that has bf16's
+ * largest number, m * s passes bf16's end: lcb_kv_cache_read makes an infinity of
+ * it (attn_cache_decode takes it as it is).
  * A row is one record of lcb_kv_cache_row_bytes(bits) bytes, 144 or 272; the
  * order of the codes in it is the library's (csrc/kv_cache.cuh).
  * cache: [B, Hkv, Smax, row bytes], the rows of a head one after another,
@@ -494,7 +496,10 @@ int lcb_kv_cache_row_bytes(int bits);
  * among them, as in attn_window_decode: token t of sequence b goes to row
  * lens[b] - T + t. A token whose row would lie before 0 or at or past Smax is
  * dropped: a batch of prompts of unequal length, padded on the left, is one
- * call. Other rows are left as they were.
+ * call. Other rows are left as they were. (lens counts as it is, above Smax too,
+ * where attn_cache_decode takes Smax for it: an overfull sequence loses its newest
+ * tokens here, and its queries there stand before the rows that these would have
+ * had. Stop at Smax.)
  */
 int lcb_kv_cache_write(void* cache, const void* k, const void* v, const int* lens, int B, int Hkv, int T, int Smax,
                        int D, int bits, long long cache_batch_stride, long long cache_head_stride,
@@ -536,10 +541,16 @@ int attn_cache_decode_form(int B, int H, int Hkv, int T, int Smax, int D, int bi
  * for all query rows of its head up to 16 of them (T * H / Hkv), or 128 in the
  * form for many rows. Deterministic. Any T; for the hundreds of tokens of a
  * prompt's chunk, lcb_kv_cache_read and attn_window_fwd are faster.
- * What is rounded: weights times V's scales (and O) to bf16; in the form for many
- * rows weights and V, to fp16 where V's scales for sixteen keys on end are
- * ordinary (2^-7 to 16, in 8 bits 2^-11 to 16, or zero), otherwise to bf16;
- * weights in fp16 are also off by up to 2^-32 of a row's largest.
+ * What is rounded beside fp32 sums: weights times V's scales (and O) to bf16; Q's
+ * elements below 2^-28 of their row's largest, by up to 2^-36 of that. In the form
+ * for many rows weights and V, to fp16 for sixteen neighbouring keys that all rows
+ * of a tile (128) see and whose V's scales are ordinary (2^-7 to 16, in 8 bits
+ * 2^-11 to 16, or zero), otherwise to bf16; weights in fp16 also by up to 2^-32 of
+ * a row's largest; of K in 8 bits the magnitudes' lower four bits times their
+ * scale, by 2^-12 of it; and K's channels where a key's own scales lie more than
+ * 2^23 apart, by up to 2^-31 of the largest of them (2^-30 in 8 bits).
+ * A row's bits depend on the keys that it sees, the sizes and the lengths: on no
+ * other key, whatever that holds, and on no other row.
  * A cached NaN makes NaN of those query rows alone that see it (V's in its
  * channels). O is finite where |v| < 2^113 / keys. window, sinks, scale, heads, q,
  * o, lse and their strides as attn_window_decode; the cache as above. workspace:

@@ -736,7 +736,8 @@ def kv_cache_write(cache, k, v, lens):
     lens (CUDA int32 [B]): rows of each sequence with the new ones among them;
     token t goes to row lens[b] - T + t, and is dropped if that is before 0 or
     past the cache (prompts of unequal length, padded on the left, are one
-    call). Per group of 32 channels: scale bf16(max |x| / 7) in 4 bits (/ 127
+    call; lens[b] may not pass the cache if attn_cache_decode is to find the
+    newest tokens, as it takes the cache's end for it). Per group of 32 channels: scale bf16(max |x| / 7) in 4 bits (/ 127
     in 8), x / scale to the nearest whole number, ties away from zero. A group
     with an infinity or NaN reads as NaN."""
     B, Hkv, Smax, bits, cb, ch = _cache(cache, "kv_cache_write")
@@ -813,8 +814,9 @@ def attn_cache_decode(q, cache, lens, window=None, sinks=0, scale=None, o=None, 
     """attn_window_decode over a quantised cache (kv_cache_empty, kv_cache_write); returns (o, lse fp32 [B, H, T]).
 
     q [B, T, H, 128] bf16, the T newest tokens, whose K and V are in the cache
-    already: token t stands at position lens[b] - T + t. window=None: every key
-    up to its own position. Attention is over the values that the cache holds.
+    already: token t stands at position lens[b] - T + t, where a lens[b] past
+    the cache counts as its end. window=None: every key up to its own position.
+    Attention is over the values that the cache holds.
     workspace: uint8 of attn_cache_decode_workspace_bytes (None: allocated
     here)."""
     B, Hkv, Smax, bits, cb, ch = _cache(cache, "attn_cache_decode")

@@ -13,14 +13,14 @@
 // memory, where a lane's codes are scattered over the row, and leave or arrive
 // as contiguous 16-byte accesses: the rows of a head follow one another.
 //
-// 32768 tokens x 32 heads, at 6.7 TB/s 103 us in 4 bits and 123 in 8: read back in
-// 103 and 119, written in 107 and 120. At the memory's rate an SM has 116 issue slots
-// for a written row's 256 numbers, and in 4 bits they are what is short: with K's and
-// V's lanes in branches of their own, a division a group and signs moved one by one
-// it took 203 us, with operands selected instead 143, with the sums of products below
-// 120, and with all eight rows of a warp in one piece of code where they all exist
-// 107 (92 instructions a row). 1777 tokens x 3 x 8 heads in 8 bits: written in 7.8 us,
-// read in 6.7 (of 5.0 by bytes); one token: 2.1 and 1.6.
+// 32768 tokens x 32 heads, 103 us in 4 bits and 123 in 8 at the 6.7 TB/s that a plain
+// copy reaches: read back in 103 and 119, written in 107 and 120. At the memory's rate
+// an SM has 116 issue slots for a written row's 256 numbers, and in 4 bits they are
+// what is short: with K's and V's lanes in branches of their own, a division a group
+// and signs moved one by one it took 203 us, with operands selected instead 143, with
+// the sums of products below 120, and with all eight rows of a warp in one piece of
+// code where they all exist 107 (92 instructions a row). 1777 tokens x 3 x 8 heads in
+// 8 bits: written in 7.8 us, read in 6.7 (of 5.0 by bytes); one token: 2.1 and 1.6.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -41,8 +41,9 @@ constexpr float kTiny = 0x1p-100f;
 
 // |n| of a channel, from |x| / s by one multiplication. bf16 values and scales
 // have 8 significant bits, so x / s is a tie (a whole number and a half) or away
-// from one by more than 2^-11 of itself; a reciprocal that is larger by 2^-20
-// moves ties past the half, and nothing else across one, its own error included.
+// from one by more than 2^-12 of itself up to 7, and 2^-16 up to 127. The reciprocal
+// is off by 2^-23 of itself at most, and times 1 + 2^-20, rounded, too large by
+// 2^-21 to 2^-19: ties move past the half, and nothing else across one.
 // Adding 1.5 * 2^23 leaves the rounded number in the low bits of the result.
 __device__ __forceinline__ uint32_t magnitude(float x, float inv) {
   return __float_as_uint(fmaf(fabsf(x), inv, 12582912.f));

@@ -341,3 +341,27 @@ def test_small_channels_of_q_over_large_ones_of_k(form, B, H, Hkv, T, Smax, e, b
     k[..., 32:64] *= 2.0 ** e
     q[..., 32:64] *= 2.0 ** -e
     _check(form, bits, q.to(BF16), k.to(BF16), v.to(BF16))
+
+
+# ------------------------------------------------------------------ bf16's end
+
+
+@both_bits
+def test_the_largest_number_reads_as_infinity(bits):
+    """A group whose largest magnitude is bf16's largest number holds m s = 7 * 146 * 2^118 or 127 * 129 * 2^114, which
+    bf16 rounds to infinity when it is read; attention takes the held number. The next smaller one reads as a number,
+    the held one rounded as any other is."""
+    end = torch.finfo(BF16).max
+    below = (2.0 - 2.0 ** -6) * 2.0 ** 127
+    x = torch.zeros(1, 4, 1, D, device="cuda", dtype=BF16)
+    x[0, 0, 0, 5], x[0, 1, 0, 40], x[0, 2, 0, 127], x[0, 3, 0, 64] = end, -end, below, -below
+    cache = _cache(x, torch.ones_like(x), bits)
+    k, v = lcb.kv_cache_read(cache, 4)
+    assert k[0, 0, 0, 5] == torch.inf and k[0, 1, 0, 40] == -torch.inf and (v == 1).all()
+    assert k[0, 2, 0, 127] == _held(x, bits)[0, 2, 0, 127].to(BF16) and torch.isfinite(k[0, 2:]).all()
+    assert k[0, 3, 0, 64] == _held(x, bits)[0, 3, 0, 64].to(BF16)
+    held = 7 * 146 * 2.0 ** 118 if bits == 4 else 127 * 129 * 2.0 ** 114
+    q = torch.zeros(1, 1, 1, D, device="cuda", dtype=BF16)
+    q[..., 5] = 2.0 ** -126
+    o, lse = lcb.attn_cache_decode(q, cache, _lens(1))
+    assert (o == 1).all() and abs(lse.item() - SCALE * held * 2.0 ** -126) <= 2.0 ** -21
