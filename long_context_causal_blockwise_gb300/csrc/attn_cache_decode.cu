@@ -935,9 +935,9 @@ struct Launch {
 
 // CTAs of the form with 128-row tiles (attn_cache_tiles.cu), or 0 for one of the
 // forms here, which unpack the keys once for every sixteen rows: two estimates in
-// us. us, those here / 128-row tiles: 8 heads x 65536 keys, 32 rows 61 / 45, 64 rows
-// 104 / 47, in 8 bits 131 / 58; 32 x 20000, 128 rows 201 / 56; 8 x 65536, window 16384,
-// 4000 rows 1237 / 335; 8 x 2000, 56 rows 13 / 17; 8 x 500, 20 rows 9 / 14.
+// us. us, those here / 128-row tiles: 8 heads x 65536 keys, 32 rows 61 / 49, 64 rows
+// 104 / 50, in 8 bits 131 / 62; 32 x 20000, 128 rows 201 / 59; 8 x 65536, window 16384,
+// 4000 rows 1237 / 357; 8 x 2000, 56 rows 13 / 17; 8 x 500, 20 rows 10 / 14.
 static int tiles_ctas(const Plan& a, int T, int G, int bits, const ContextKey& at) {
   const long long R = static_cast<long long>(T) * G;
   if (R <= 16 || a.B > kLineSequences) return 0;

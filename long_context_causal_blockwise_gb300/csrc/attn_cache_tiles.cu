@@ -46,14 +46,16 @@
 // by a second kernel (cache_line.cuh). Streams are joined first, in tensor memory:
 // the warps of both see the same lanes, and take half of the channels each.
 //
-// Bound: 128 keys (a unit) take 2440 clocks. Their two products take the tensor
+// Bound: 128 keys (a unit) take some 2650 clocks. Their two products take the tensor
 // core 1024 of them (a tile has 128 rows whether it uses them or not), 128 rows'
 // weights the exponential unit 1024, HBM 770 in 4 bits. Shared memory has the most
 // to do: 96 KB that the products read, 82 KB that unpacking reads and writes, 18 KB
 // that arrive, 1540 clocks at 128 bytes each; and an unpacking warp's turn (its
-// sixteen keys of K 960 clocks, of V 700, two fences 330, and its waits) leaves no
-// room. 8 heads x 65536 keys, 64 rows: 47 us in 4 bits, 58 in 8; 32 heads x 20000,
-// 128 rows: 56. More warps only share this out (us, when that first was 53): 16
+// sixteen keys of K 960 clocks, of V 700, two fences 330, and its waits, when a unit
+// took 2440) leaves no room. 8 heads x 65536 keys, 64 rows: 50 us in 4 bits, 62 in 8;
+// 32 heads x 20000, 128 rows: 59. (47, 58 and 56 before keys could have powers of two
+// of their own, factors were kept off zero and infinity, and V's type followed what
+// all rows see.) More warps only share this out (us, when the first was 53): 16
 // softmax warps of 64 keys each 56, 16 unpacking warps 69, 12 in turn 60.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
