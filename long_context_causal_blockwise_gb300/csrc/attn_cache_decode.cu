@@ -106,7 +106,7 @@ constexpr int kUp = 96;            // weights go into the second product times 2
 constexpr int kUpRange = 119 - kUp;  // while V's scales are below 2^23: a weight is 2^8 at most
 
 // A row is far where one fused multiplication does not make weights of its products: where its factor could pass fp32's
-// end (a largest |q| of 2^75 or more), or where its maximum is so large that the rounding of the product it was is no
+// end (a largest |q| of 2^76 or more), or where its maximum is so large that the rounding of the product it was is no
 // longer small beside 1. Its raise_at stays -inf, so that every step takes the branch that raises a maximum, and there
 // its products become differences from m, by a multiplication and a subtraction, over c. Such a row's c is its factor
 // over 2^24, and its neg_m -0, which no other row's is. (With the factor in a register of its own: 8 heads x 65536
@@ -394,7 +394,7 @@ __device__ __forceinline__ void step(State<ROWS, BITS>& w, const CacheDecode& p,
       mx = mx > w.m[i] + kRescaleThreshold ? mx : w.m[i];
       const float a = weight(w.m[i], mx);
       w.m[i] = mx;
-      w.neg_m[i] = mx == -INFINITY ? 0.f : 0.f - mx;
+      w.neg_m[i] = mx == -INFINITY ? 0.f : __fsub_rn(0.f, mx);  // never -0
       w.raise_at[i] = (mx + kRescaleThreshold) / w.c[i];
       if (was_far || fabsf(w.neg_m[i]) >= kFarScore) {
         if (!was_far) w.c[i] *= 0x1p-24f;

@@ -37,10 +37,11 @@
 // value at best, 2^-9 of it at the smallest scales, and 2^7 P, off by 2^-12 down to
 // weights of 2^-21 of the largest. Otherwise, and where some row of the tile does not
 // see all sixteen (so that no row's bits depend on V that it does not see), bf16 with
-// the same powers of two: off by half a step, 2^-9 to 2^-8 of each value. (bf16 for all of them: errors 2.8e-3 of the outputs instead of 1.7e-3, which
-// is what rounding these to bf16 costs, and 2 us of 53 less.) NaN of V are zeros in
-// the tile, so that a weight of zero leaves nothing of them; the rows that see one
-// are told by bits, 1 us of 53.
+// the same powers of two: off by half a step, 2^-9 to 2^-8 of each value. (bf16 for
+// all of them: errors 2.8e-3 of the outputs instead of 1.7e-3, which is what rounding
+// these to bf16 costs, and 2 us of 53 less.) NaN of V are zeros in the tile, so that
+// a weight of zero leaves nothing of them; the rows that see one are told by bits, 1
+// us of 53.
 //
 // The units of all tiles are dealt evenly to the CTAs, one to an SM, and joined
 // by a second kernel (cache_line.cuh). Streams are joined first, in tensor memory:
@@ -152,9 +153,8 @@ __device__ __forceinline__ uint8_t* chunk_of(uint8_t* tile, uint32_t first, int 
   return tile + ((first ^ (G & 1 ? 64u : 0u)) + round * 1024 + (G >> 1) * kHalfBytes);
 }
 
-// Whether a scale of V among the sixteen keys is not one for fp16; if so, which ones are NaN (v_nan; an infinity, which
-// kv_cache_write never leaves, counts as one).
-// `cut` says so beforehand.
+// Whether V of sixteen keys is bf16: `cut`, or a scale is not one for fp16. If so, which scales are NaN (v_nan; an
+// infinity, which kv_cache_write never leaves, counts as one).
 template <int BITS>
 __device__ __forceinline__ bool wide_v(const uint8_t* rec, bool cut, uint2* nan, int lane) {
   const uint32_t x = *reinterpret_cast<const uint32_t*>(rec + (lane >> 1) * cache_row_bytes(BITS) +
@@ -171,7 +171,7 @@ __device__ __forceinline__ bool wide_v(const uint8_t* rec, bool cut, uint2* nan,
 }
 
 // K's factors are kept times 2^-7, and the rows' times 2^7: 2^(9 + e) passes fp32's end where the largest scales (below
-// 2^126, from the largest bf16 over 7) do not, and a row's is 2^126 at most, times the scale.
+// 2^126, from the largest bf16 over 7) do not, and a row's is 2^119 at most, times the scale.
 constexpr int kFactorDown = 7;
 
 // A key's four scales' largest finite one, as bits.
@@ -180,7 +180,7 @@ __device__ __forceinline__ uint32_t top_scale(uint32_t x) {
   return max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u);
 }
 
-// The exponent of the largest scale, as bits, that shares a power of two, where it is not so small that nobody writes it.
+// The exponent of a largest scale given as bits (kv_cache_write leaves none below 2^-107, but zero).
 __device__ __forceinline__ int top_exponent(uint32_t top) { return max(static_cast<int>(top >> 7) - 127, -110); }
 
 // Sixteen keys of K by a warp: rows row0 .. + 15 of the tile, times powers of two. OWN: each key its own, which go to
@@ -684,8 +684,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
                   float f0 = f, f1 = f;
                   if (rare.value && f16 == INFINITY) f0 = score_factor(c, own[k]), f1 = score_factor(c, own[k + 1]);
                   ffma2(w[k], w[k + 1], s0, s1, f0, f1, neg_m, neg_m);
-                  if (rare.value && is_far())
-                    w[k] = __fsub_rn(__fmul_rn(s0, f0), m) + kWeightUp, w[k + 1] = __fsub_rn(__fmul_rn(s1, f1), m) + kWeightUp;
+                  if (rare.value && is_far()) {
+                    w[k] = __fsub_rn(__fmul_rn(s0, f0), m) + kWeightUp;
+                    w[k + 1] = __fsub_rn(__fmul_rn(s1, f1), m) + kWeightUp;
+                  }
                   w[k] = ex2_approx(w[k]), w[k + 1] = ex2_approx(w[k + 1]);
                   fadd2(la, lb, la, lb, w[k], w[k + 1]);
                 }
