@@ -833,26 +833,25 @@ def attn_cache_decode(q, cache, lens, window=None, sinks=0, scale=None, o=None, 
     dev = q.get_device()
     stream = _raw_stream("attn_cache_decode", dev, (cache, lens, o, lse) if workspace is None else (cache, lens, o, lse,
                                                                                                   workspace))
-
-    def call(ws):
-        return (_LIB or load()).attn_cache_decode(
-            q.data_ptr(), cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, Smax, D, bits,
-            window, sinks, D ** -0.5 if scale is None else float(scale), qr, qb, cb, ch, orr, ob, lh, lb,
-            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), stream)
-
-    if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        rc = call(workspace)
-    else:
+    kept = workspace is None
+    if kept:
         sizes = dev, B, H, Hkv, T, Smax, D, bits, window, sinks
         n = _cache_decode_workspace(*sizes)
-        rc = call(torch.empty(n, dtype=torch.uint8, device=q.device) if n else None)
-        if rc == LCB_ERR_ARG:
-            _cache_decode_workspace.cache_clear()
-            now = _cache_decode_workspace(*sizes)
-            if now > n:
-                rc = call(torch.empty(now, dtype=torch.uint8, device=q.device))
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    args = (q.data_ptr(), cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hkv, T, Smax, D, bits,
+            window, sinks, D ** -0.5 if scale is None else float(scale), qr, qb, cb, ch, orr, ob, lh, lb)
+    fn = (_LIB or load()).attn_cache_decode
+    rc = fn(*args, None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+    if rc == LCB_ERR_ARG and kept:
+        _cache_decode_workspace.cache_clear()
+        now = _cache_decode_workspace(*sizes)
+        if now > n:
+            workspace = torch.empty(now, dtype=torch.uint8, device=q.device)
+            rc = fn(*args, workspace.data_ptr(), now, stream)
     if rc:
         _check("attn_cache_decode", rc)
     return o, lse
